@@ -4,7 +4,9 @@ Argument marshalling only.  Every step of the path runs in the CUDA kernels
 of libmsa.so (include/msa.h); there is no fallback.  If the library is not
 built, loading raises.  Tensors are torch CUDA tensors with 2-byte elements
 (bf16, int16 or uint16 holding bf16 bit patterns) in the layouts msa.h
-states; q_start and kv_len are host sequences of B ints.
+states (the codes and exponents of an 8-bit cache have 1-byte elements);
+q_start and kv_len are host sequences of B ints, or positions() of one, which
+saves the conversion on every call.
 """
 import ctypes
 import math
@@ -18,7 +20,11 @@ __all__ = ["MsaParams", "MsaError", "params", "load", "msa_workspace_bytes", "ms
            "msa_quality_workspace_bytes", "msa_selection_quality", "quality_workspace",
            "msa_cache_append", "msa_forward_paged", "msa_dense_workspace_bytes",
            "msa_dense_attn", "dense_workspace", "msa_index_kl_workspace_bytes", "msa_index_kl",
-           "kl_workspace",
+           "kl_workspace", "msa_cache_append_q8", "msa_q8_workspace_bytes", "q8_workspace",
+           "msa_sparse_attn_q8", "msa_forward_q8", "msa_window_workspace_bytes",
+           "window_workspace", "msa_window_attn", "msa_window_attn_q8", "MsaPool", "pools",
+           "msa_pages_workspace_bytes", "pages_workspace", "msa_pages_copy", "msa_pages_fork",
+           "msa_pages_free", "msa_pages_alloc", "msa_pages_compact", "positions",
            "workspace", "BLOCK", "TOPK"]
 
 BLOCK = 128
@@ -29,7 +35,11 @@ EXPORTS = ("msa_workspace_bytes", "msa_index_topk", "msa_sparse_attn", "msa_forw
            "msa_index_topk_noalloc", "msa_debug_set_wait_polls", "msa_quality_workspace_bytes",
            "msa_selection_quality", "msa_cache_append", "msa_forward_paged",
            "msa_dense_workspace_bytes", "msa_dense_attn", "msa_index_kl_workspace_bytes",
-           "msa_index_kl")
+           "msa_index_kl", "msa_cache_append_q8", "msa_q8_workspace_bytes",
+           "msa_sparse_attn_q8", "msa_forward_q8", "msa_window_workspace_bytes",
+           "msa_window_attn", "msa_window_attn_q8", "msa_pages_workspace_bytes",
+           "msa_pages_copy", "msa_pages_fork", "msa_pages_free", "msa_pages_alloc",
+           "msa_pages_compact")
 
 
 class MsaError(RuntimeError):
@@ -43,6 +53,11 @@ class MsaParams(ctypes.Structure):
                 ("G", ctypes.c_int), ("D", ctypes.c_int), ("Di", ctypes.c_int),
                 ("block", ctypes.c_int), ("topk", ctypes.c_int), ("max_blocks", ctypes.c_int),
                 ("scale", ctypes.c_float), ("kernels", ctypes.c_int)]
+
+
+class MsaPool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t),
+                ("per_token", ctypes.c_int)]
 
 
 def params(B, T, H, G, D, Di, max_blocks, scale=None, kernels="auto"):
@@ -83,6 +98,23 @@ def load(path=None):
     L.msa_quality_workspace_bytes.argtypes = [PP]
     L.msa_quality_workspace_bytes.restype = sz
     L.msa_selection_quality.argtypes = [PP, P, P, P, P, P, P, P, P, P, P, sz, P]
+    pool = ctypes.POINTER(MsaPool)
+    for name in ("msa_q8_workspace_bytes", "msa_window_workspace_bytes"):
+        getattr(L, name).argtypes = [PP]
+    L.msa_pages_workspace_bytes.argtypes = [ci]
+    L.msa_cache_append_q8.argtypes = [PP, P, ci] + [P] * 10 + [sz, P]
+    L.msa_sparse_attn_q8.argtypes = [PP, P, ci] + [P] * 10 + [sz, P]
+    L.msa_forward_q8.argtypes = [PP, P, ci] + [P] * 12 + [sz, P]
+    L.msa_window_attn.argtypes = [PP, P, ci, ci, ci] + [P] * 7 + [sz, P]
+    L.msa_window_attn_q8.argtypes = [PP, P, ci, ci, ci] + [P] * 9 + [sz, P]
+    L.msa_pages_copy.argtypes = [pool, ci, ci, P, P, ci, P, sz, P]
+    L.msa_pages_fork.argtypes = [pool, ci, ci, P, ci, ci, P, P, P, P, ci, P, sz, P]
+    for name in ("msa_pages_free", "msa_pages_alloc"):
+        getattr(L, name).argtypes = [ci, P, ci, ci, P, P, P, P, ci, P, sz, P]
+    L.msa_pages_compact.argtypes = [pool, ci, ci, P, ci, ci, P, P, P, P, P, sz, P]
+    for name in ("msa_q8_workspace_bytes", "msa_window_workspace_bytes",
+                 "msa_pages_workspace_bytes"):
+        getattr(L, name).restype = sz
     L.msa_debug_set_wait_polls.argtypes = [ctypes.c_uint32]
     L.msa_debug_set_wait_polls.restype = None
     L.msa_kernel_launch_count.argtypes = []
@@ -91,7 +123,10 @@ def load(path=None):
     L.msa_status_string.restype = ctypes.c_char_p
     for f in ("msa_index_topk", "msa_sparse_attn", "msa_forward", "msa_workspace_status",
               "msa_index_topk_noalloc", "msa_selection_quality", "msa_cache_append",
-              "msa_forward_paged", "msa_dense_attn", "msa_index_kl"):
+              "msa_forward_paged", "msa_dense_attn", "msa_index_kl", "msa_cache_append_q8",
+              "msa_sparse_attn_q8", "msa_forward_q8", "msa_window_attn", "msa_window_attn_q8",
+              "msa_pages_copy", "msa_pages_fork", "msa_pages_free", "msa_pages_alloc",
+              "msa_pages_compact"):
         getattr(L, f).restype = ci
     if path == _build.LIBMSA:
         _lib = L
@@ -117,7 +152,18 @@ def _stream(stream):
     return ctypes.c_void_p(getattr(stream, "cuda_stream", stream))
 
 
+def positions(x):
+    """A host array of ints (positions, lengths, row numbers) in the form that
+    the library reads; every call also takes it in place of a sequence."""
+    vals = [int(v) for v in x]
+    return (ctypes.c_int32 * len(vals))(*vals)
+
+
 def _host_i32(x, B):
+    if isinstance(x, ctypes.Array) and x._type_ is ctypes.c_int32:
+        if len(x) != B:
+            raise ValueError("expected %d positions, got %d" % (B, len(x)))
+        return x
     vals = [int(v) for v in (x if hasattr(x, "__len__") else [x] * B)]
     if len(vals) != B:
         raise ValueError("expected %d positions, got %d" % (B, len(vals)))
@@ -269,6 +315,156 @@ def msa_forward_paged(p, block_table, num_pool_blocks, q_idx, k_idx_pool, q, k_p
                                    _ptr(sel_out), _ptr(out), _ptr(ws),
                                    ws.numel() * ws.element_size(), _stream(stream)),
           "msa_forward_paged")
+
+
+def _scratch(n, what, device):
+    import torch
+    if n == 0:
+        raise MsaError(-2, what)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _nbytes(ws):
+    return ws.numel() * ws.element_size()
+
+
+def msa_q8_workspace_bytes(p):
+    return int(load().msa_q8_workspace_bytes(ctypes.byref(p)))
+
+
+def q8_workspace(p, device="cuda"):
+    """A device scratch buffer of msa_q8_workspace_bytes(p) bytes."""
+    return _scratch(msa_q8_workspace_bytes(p), "msa_q8_workspace_bytes", device)
+
+
+def msa_cache_append_q8(p, k_new, v_new, k_idx_new, q_start, k_cache, v_cache, k_exp, v_exp,
+                        k_idx_cache, ws, block_table=None, num_pool_blocks=0, stream=None):
+    """msa_cache_append into an 8-bit cache: e4m3 codes and one exponent per
+    (block, KV head), see msa.h."""
+    _call(load().msa_cache_append_q8(ctypes.byref(p), _ptr(block_table), int(num_pool_blocks),
+                                     _ptr(k_new), _ptr(v_new), _ptr(k_idx_new),
+                                     _host_i32(q_start, p.B), _ptr(k_cache), _ptr(v_cache),
+                                     _ptr(k_exp), _ptr(v_exp), _ptr(k_idx_cache), _ptr(ws),
+                                     _nbytes(ws), _stream(stream)), "msa_cache_append_q8")
+
+
+def msa_sparse_attn_q8(p, q, k_cache, v_cache, k_exp, v_exp, sel, q_start, kv_len, out, ws,
+                       block_table=None, num_pool_blocks=0, stream=None):
+    """msa_sparse_attn on an 8-bit cache (see msa.h)."""
+    _call(load().msa_sparse_attn_q8(ctypes.byref(p), _ptr(block_table), int(num_pool_blocks),
+                                    _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp),
+                                    _ptr(v_exp), _ptr(sel), _host_i32(q_start, p.B),
+                                    _host_i32(kv_len, p.B), _ptr(out), _ptr(ws), _nbytes(ws),
+                                    _stream(stream)), "msa_sparse_attn_q8")
+
+
+def msa_forward_q8(p, q_idx, k_idx, q, k_cache, v_cache, k_exp, v_exp, q_start, kv_len, out, ws,
+                   sel_out=None, block_table=None, num_pool_blocks=0, stream=None):
+    """msa_forward on an 8-bit cache (see msa.h)."""
+    _call(load().msa_forward_q8(ctypes.byref(p), _ptr(block_table), int(num_pool_blocks),
+                                _ptr(q_idx), _ptr(k_idx), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                _ptr(k_exp), _ptr(v_exp), _host_i32(q_start, p.B),
+                                _host_i32(kv_len, p.B), _ptr(sel_out), _ptr(out), _ptr(ws),
+                                _nbytes(ws), _stream(stream)), "msa_forward_q8")
+
+
+def msa_window_workspace_bytes(p):
+    return int(load().msa_window_workspace_bytes(ctypes.byref(p)))
+
+
+def window_workspace(p, device="cuda"):
+    """A device scratch buffer of msa_window_workspace_bytes(p) bytes."""
+    return _scratch(msa_window_workspace_bytes(p), "msa_window_workspace_bytes", device)
+
+
+def msa_window_attn(p, window, sinks, q, k_cache, v_cache, q_start, kv_len, out, ws,
+                    block_table=None, num_pool_blocks=0, stream=None):
+    """GQA attention over the last `window` and the first `sinks` tokens (see msa.h)."""
+    _call(load().msa_window_attn(ctypes.byref(p), _ptr(block_table), int(num_pool_blocks),
+                                 int(window), int(sinks), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                 _host_i32(q_start, p.B), _host_i32(kv_len, p.B), _ptr(out),
+                                 _ptr(ws), _nbytes(ws), _stream(stream)), "msa_window_attn")
+
+
+def msa_window_attn_q8(p, window, sinks, q, k_cache, v_cache, k_exp, v_exp, q_start, kv_len, out,
+                       ws, block_table=None, num_pool_blocks=0, stream=None):
+    """msa_window_attn on an 8-bit cache (see msa.h)."""
+    _call(load().msa_window_attn_q8(ctypes.byref(p), _ptr(block_table), int(num_pool_blocks),
+                                    int(window), int(sinks), _ptr(q), _ptr(k_cache),
+                                    _ptr(v_cache), _ptr(k_exp), _ptr(v_exp),
+                                    _host_i32(q_start, p.B), _host_i32(kv_len, p.B), _ptr(out),
+                                    _ptr(ws), _nbytes(ws), _stream(stream)), "msa_window_attn_q8")
+
+
+def pools(tensors):
+    """The pools that move together in a page operation.  Each is a contiguous
+    tensor [pages][...]; one of shape [pages][128][...] holds token rows.  Keep
+    the tensors alive as long as the result is used."""
+    a = (MsaPool * len(tensors))()
+    for d, t in zip(a, tensors):
+        if not t.is_contiguous():
+            raise ValueError("a pool must be contiguous")
+        d.base = t.data_ptr()
+        d.page_bytes = t[0].numel() * t.element_size()
+        d.per_token = int(t.dim() > 2 and t.shape[1] == BLOCK)
+    return a
+
+
+def msa_pages_workspace_bytes(num_pool_blocks):
+    return int(load().msa_pages_workspace_bytes(int(num_pool_blocks)))
+
+
+def pages_workspace(num_pool_blocks, device="cuda"):
+    """A device scratch buffer of msa_pages_workspace_bytes(num_pool_blocks) bytes."""
+    return _scratch(msa_pages_workspace_bytes(num_pool_blocks), "msa_pages_workspace_bytes", device)
+
+
+def msa_pages_copy(pools, num_pool_blocks, src, dst, ws, stream=None):
+    """Page dst[i] of every pool becomes a copy of page src[i] (device int32 lists)."""
+    _call(load().msa_pages_copy(pools, len(pools), int(num_pool_blocks), _ptr(src), _ptr(dst),
+                                src.numel(), _ptr(ws), _nbytes(ws), _stream(stream)),
+          "msa_pages_copy")
+
+
+def msa_pages_fork(pools, num_pool_blocks, block_table, refs, src_rows, dst_rows, lens, ws,
+                   stream=None):
+    """Rows dst_rows take the first lens tokens of rows src_rows: complete pages
+    shared, the last one copied (see msa.h)."""
+    n = len(src_rows)
+    _call(load().msa_pages_fork(pools, len(pools), int(num_pool_blocks), _ptr(block_table),
+                                block_table.shape[0], block_table.shape[1], _ptr(refs),
+                                _host_i32(src_rows, n), _host_i32(dst_rows, n),
+                                _host_i32(lens, n), n, _ptr(ws), _nbytes(ws), _stream(stream)),
+          "msa_pages_fork")
+
+
+def _ranges(fn, what, num_pool_blocks, block_table, refs, rows, first, last, ws, stream):
+    n = len(rows)
+    _call(fn(int(num_pool_blocks), _ptr(block_table), block_table.shape[0], block_table.shape[1],
+             _ptr(refs), _host_i32(rows, n), _host_i32(first, n), _host_i32(last, n), n, _ptr(ws),
+             _nbytes(ws), _stream(stream)), what)
+
+
+def msa_pages_free(num_pool_blocks, block_table, refs, rows, first, last, ws, stream=None):
+    """Unmap blocks [first[j], last[j]) of row rows[j] (see msa.h)."""
+    _ranges(load().msa_pages_free, "msa_pages_free", num_pool_blocks, block_table, refs, rows,
+            first, last, ws, stream)
+
+
+def msa_pages_alloc(num_pool_blocks, block_table, refs, rows, first, last, ws, stream=None):
+    """Map the unmapped blocks of [first[j], last[j]) of row rows[j] to the lowest
+    free pages (see msa.h)."""
+    _ranges(load().msa_pages_alloc, "msa_pages_alloc", num_pool_blocks, block_table, refs, rows,
+            first, last, ws, stream)
+
+
+def msa_pages_compact(pools, num_pool_blocks, block_table, refs, table_out, refs_out, live, ws,
+                      stream=None):
+    """Move the pages in use to the front of the pools (see msa.h)."""
+    _call(load().msa_pages_compact(pools, len(pools), int(num_pool_blocks), _ptr(block_table),
+                                   block_table.shape[0], block_table.shape[1], _ptr(refs),
+                                   _ptr(table_out), _ptr(refs_out), _ptr(live), _ptr(ws),
+                                   _nbytes(ws), _stream(stream)), "msa_pages_compact")
 
 
 def msa_workspace_status(ws, stream=None):

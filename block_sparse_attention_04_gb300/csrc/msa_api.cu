@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "msa_internal.h"
+#include "msa_serve.h"
 #include "msa_tc.h"
 
 namespace msa {
@@ -63,6 +64,15 @@ Shape shape_of(const msa_params* p, const int32_t* block_table, int pool_blocks)
   return s;
 }
 
+// A pool of num_pool_blocks 128-token blocks: its rows (tensor-copy
+// coordinates) must fit 32 bits, like those of per-sequence caches.
+int validate_pool(const int32_t* block_table, int num_pool_blocks) {
+  if (!block_table || num_pool_blocks < 1) return MSA_ERR_INVALID_ARG;
+  if (((uintptr_t)block_table & 3u) != 0) return MSA_ERR_INVALID_ARG;
+  if ((int64_t)num_pool_blocks * MSA_BLOCK + MSA_BLOCK >= ((int64_t)1 << 31))
+    return MSA_ERR_UNSUPPORTED;
+  return MSA_OK;
+}
 
 namespace {
 
@@ -199,16 +209,6 @@ DensePlan dense_plan_for(const msa_params* p) {
   return d;
 }
 
-// A pool of num_pool_blocks 128-token blocks: its rows (tensor-copy
-// coordinates) must fit 32 bits, like those of per-sequence caches.
-int validate_pool(const int32_t* block_table, int num_pool_blocks) {
-  if (!block_table || num_pool_blocks < 1) return MSA_ERR_INVALID_ARG;
-  if (((uintptr_t)block_table & 3u) != 0) return MSA_ERR_INVALID_ARG;
-  if ((int64_t)num_pool_blocks * MSA_BLOCK + MSA_BLOCK >= ((int64_t)1 << 31))
-    return MSA_ERR_UNSUPPORTED;
-  return MSA_OK;
-}
-
 // Steps 1-4 for msa_forward and msa_forward_paged (s carries the block table,
 // or none); p is validated.
 int forward(const msa_params* p, const Shape& s, const uint16_t* q_idx, const uint16_t* k_idx,
@@ -233,6 +233,16 @@ int forward(const msa_params* p, const Shape& s, const uint16_t* q_idx, const ui
 }
 
 }  // namespace
+
+int run_index_in(const msa_params* p, const Shape& s, const Positions& pos, const uint16_t* q_idx,
+                 const uint16_t* k_idx, int32_t* sel, void* ws, cudaStream_t st) {
+  const Workspace w = carve(p, plan_for(p), ws);
+  if (cudaMemsetAsync(w.status, 0, sizeof(int), st) != cudaSuccess) return MSA_ERR_CUDA;
+  return run_index(p, s, pos, q_idx, k_idx, sel, w, st);
+}
+
+bool prefill_sized(const msa_params* p) { return use_tc_attn(p); }
+
 }  // namespace msa
 
 using namespace msa;
@@ -442,6 +452,7 @@ int msa_workspace_status(const void* ws, cudaStream_t stream) {
   if (cudaMemcpy(&v, ws, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return MSA_ERR_CUDA;
   if (v == kDevTimeout) return MSA_ERR_TIMEOUT;
   if (v == kDevInvalid) return MSA_ERR_INVALID_ARG;
+  if (v == kDevNoPages) return MSA_ERR_PAGES;
   return v == 0 ? MSA_OK : MSA_ERR_CUDA;
 }
 
@@ -459,6 +470,7 @@ const char* msa_status_string(int status) {
     case MSA_ERR_WORKSPACE: return "workspace too small";
     case MSA_ERR_CUDA: return "CUDA error";
     case MSA_ERR_TIMEOUT: return "kernel wait timed out";
+    case MSA_ERR_PAGES: return "no free page left";
     default: return "unknown status";
   }
 }

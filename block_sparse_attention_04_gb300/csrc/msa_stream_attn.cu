@@ -1,0 +1,742 @@
+// Streaming attention over cached blocks: a caller's selection on an 8-bit
+// cache (msa_sparse_attn_q8) and a sliding window with sinks on either cache
+// (msa_window_attn, msa_window_attn_q8), for decode-sized calls; any shape.
+//
+// Mathematics: for query (b, t) and head h of KV group g, over the visible
+// tokens j of the unit's blocks, s_j = scale q.k_j, o = sum 2^(x_j - m) v_j /
+// sum 2^(x_j - m) with x = s log2(e).  An 8-bit cache holds k = ck 2^ek and
+// v = cv 2^ev (ck, cv e4m3 codes, one exponent per block and KV head): ek
+// scales the block's scores, and 2^ev is folded into the exponential,
+// p'_j = 2^(x_j + ev - m'), so that p' bounds the value's size rather than the
+// weight's; the block adds 2^-ev sum p' to the normaliser.
+//
+// A persistent CTA per SM walks items (unit (b, t, g), part): a part is `spp`
+// consecutive blocks of the unit's list.  Warp 8 copies K and V of each block
+// (128 tokens of one KV head) into a ring of stages by TMA and runs ahead by
+// its depth.  Warps 0-7 take 16 tokens of every block each and never wait for
+// one another inside an item: S = Q K^T with mma.sync m16n8k16 (rows: the
+// group's heads), softmax in registers, P straight from the accumulator
+// layout into the A operand of O += P V.  The order of the contraction's
+// terms is free, so dims (for S) and output columns (for O) are dealt to
+// threads such that every thread reads whole 16-byte chunks of the swizzled
+// rows; pairs of tokens of V are put together with byte permutes.  e4m3 codes
+// become f16 (exact) by one conversion per pair; Q is scaled by a power of two
+// per row to fit f16 (exact but for elements 2^-27 below the row's maximum,
+// which round at 2^-38 of it), and P rounds to f16 (2^-11).  With a bf16 cache
+// the products are bf16 and P rounds to bf16 (2^-8).
+// At an item's end the eight warps' (O, m, l) are joined in shared memory;
+// a unit of one part is written out directly, others leave one partial per
+// part that stream_finish_kernel joins.
+#include "msa_q8.cuh"
+#include "msa_tma.h"
+
+namespace msa {
+namespace {
+
+constexpr int kConsWarps = 8;
+constexpr int kConsumers = 32 * kConsWarps;
+constexpr int kThreads = kConsumers + 32;
+constexpr int kQBufs = 2;
+constexpr int kMaxStages = 8;
+constexpr int kExtraItems = 2048;    // items beyond one per unit
+constexpr int kMaxCtas = 512;        // error words in the workspace
+constexpr int kPassRows = 2048;      // (sequence, query) rows per pass
+constexpr float kLazy = 8.f;         // log2 growth of p tolerated before O is rescaled
+constexpr int kSmemMax = 227 * 1024;
+
+struct StreamArgs {
+  Shape s;
+  int32_t q_start[kMaxBatch];
+  int32_t item0[kMaxBatch + 1];   // first item of each sequence
+  int t0, Tp, spp, nitems, stages;
+  int window, sinks;
+  const int32_t* sel;
+  const uint16_t* q;
+  const int8_t* k_exp;
+  const int8_t* v_exp;
+  float* part_o;                  // [item][H/G][D], O relative to m
+  float2* part_ml;                // [item][H/G] (m in log2 units, l)
+  uint16_t* out;
+  int* errs;                      // [gridDim.x]
+  int* status;
+  bool first_pass;
+  uint32_t wait_polls;
+};
+
+struct Unit {
+  int b, i, g, part, nparts, t;
+};
+
+__device__ __forceinline__ Unit unit_of(const StreamArgs& a, int item) {
+  int lo = 0, hi = a.s.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.item0[mid] <= item) lo = mid; else hi = mid;
+  }
+  Unit u;
+  u.b = lo;
+  const int r = item - a.item0[lo];
+  u.nparts = (a.item0[lo + 1] - a.item0[lo]) / (a.Tp * a.s.G);
+  u.part = r % u.nparts;
+  const int ig = r / u.nparts;
+  u.g = ig % a.s.G;
+  u.i = a.t0 + ig / a.s.G;
+  u.t = a.q_start[lo] + u.i;
+  return u;
+}
+
+// The blocks of a unit's list: all 16 slots of a selection, or the blocks
+// that hold a visible token (sink blocks first).
+struct BlockList {
+  int len, nsink, first;          // window: list position p is block p (p < nsink) or first + p
+};
+__device__ __forceinline__ BlockList list_of(const StreamArgs& a, int t) {
+  if (a.sel) return BlockList{kTopk, 0, 0};
+  const int lo = max(0, t - a.window + 1) / kBlock;
+  const int ns = min((a.sinks + kBlock - 1) / kBlock, lo);
+  return BlockList{ns + t / kBlock - lo + 1, ns, lo - ns};
+}
+
+template <int D, bool Q8>
+struct Cfg {
+  static constexpr int kTile = kBlock * D * (Q8 ? 1 : 2);   // K (or V) of one block and head
+  static constexpr int kStage = 2 * kTile;
+};
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const __grid_constant__ StreamArgs a) {
+  using C = Cfg<D, Q8>;
+  constexpr int NS = D / 16;       // k-steps of S
+  constexpr int NO = D / 8;        // n-tiles of O
+  extern __shared__ uint8_t dsm_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], q_full[kQBufs], q_empty[kQBufs];
+  __shared__ int meta_kb[kMaxStages], meta_ke[kMaxStages], meta_ve[kMaxStages];
+  __shared__ float sm_m[kConsWarps][16], sm_l[kConsWarps][16];
+  __shared__ int err;
+  const Shape& s = a.s;
+  const int H = s.H, G = s.G, hpg = H / G, S = a.stages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint16_t* qbuf = reinterpret_cast<uint16_t*>(sm + S * C::kStage);       // [kQBufs][hpg][D]
+  float* red = reinterpret_cast<float*>(qbuf + kQBufs * hpg * D);         // [8][hpg][D]
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kConsWarps);
+    }
+    for (int i = 0; i < kQBufs; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], kConsWarps);
+    }
+    err = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == kConsWarps) {
+    // ------------------------------------------------------------ producer
+    const uint64_t pol = l2_policy_evict_first();
+    const uint32_t qbytes = (uint32_t)(hpg * D * 2);
+    int st = 0, k = 0;              // next stage, items begun
+    uint32_t ph = 1;                // phase parity that frees the stage (first lap: free)
+    uint32_t used = 0, loaded = 0;  // stages ever loaded / parity of each stage's last load
+    int nq = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x, ++k) {
+      const Unit u = unit_of(a, item);
+      const int qs = k % kQBufs;
+      ok = __all_sync(0xffffffffu, k < kQBufs || mbar_wait(&q_empty[qs], ((k / kQBufs) - 1) & 1,
+                                                           &err, a.wait_polls));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[qs], qbytes);
+        bulk_load(smem_u32(qbuf + qs * hpg * D),
+                  a.q + (((int64_t)u.b * s.T + u.i) * H + (int64_t)u.g * hpg) * D, qbytes,
+                  &q_full[qs]);
+      }
+      ++nq;
+      const BlockList bl = list_of(a, u.t);
+      const int p0 = u.part * a.spp, p1 = min(p0 + a.spp, bl.len);
+      const int32_t* srow =
+          a.sel ? a.sel + (((int64_t)u.b * s.T + u.i) * G + u.g) * kTopk : nullptr;
+      for (int pc = p0; pc < p1 && ok; pc += 32) {
+        // one list position per lane: its block, cache block and exponents
+        int kb = -1, ke = 0, ve = 0, row = 0;
+        const int p = pc + lane;
+        if (p < p1) {
+          kb = srow ? srow[p] : (p < bl.nsink ? p : bl.first + p);
+          if (srow && kb >= 0 && (kb > u.t / kBlock || kb >= s.max_blocks)) {
+            flag_invalid(&err);
+            kb = -1;
+          }
+          if (kb >= 0) {
+            const int64_t pb = cache_block(s, u.b, kb, &err);
+            if (pb < 0) {
+              kb = -1;
+            } else {
+              row = (int)(pb * kBlock);
+              if (Q8) {
+                ke = clamp_exp(a.k_exp[pb * G + u.g]);
+                ve = clamp_exp(a.v_exp[pb * G + u.g]);
+              }
+            }
+          }
+        }
+        const int n = min(32, p1 - pc);
+        for (int j = 0; j < n; ++j) {
+          const int kbj = __shfl_sync(0xffffffffu, kb, j), rowj = __shfl_sync(0xffffffffu, row, j);
+          const int kej = __shfl_sync(0xffffffffu, ke, j), vej = __shfl_sync(0xffffffffu, ve, j);
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph, &err, a.wait_polls));
+          if (!ok) break;
+          if (lane == 0) {
+            meta_kb[st] = kbj;
+            meta_ke[st] = kej;
+            meta_ve[st] = vej;
+            if (kbj < 0) {
+              mbar_arrive(&full[st]);
+            } else {
+              mbar_arrive_expect_tx(&full[st], C::kStage);
+              const uint32_t kd = smem_u32(sm + st * C::kStage), vd = kd + C::kTile;
+              if constexpr (Q8) {
+                tma_load_3d_hint(kd, &tm_k, &full[st], 0, u.g, rowj, pol);
+                tma_load_3d_hint(vd, &tm_v, &full[st], 0, u.g, rowj, pol);
+              } else {
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                  tma_load_3d_hint(kd + h * 16384, &tm_k, &full[st], h * 64, u.g, rowj, pol);
+                  tma_load_3d_hint(vd + h * 16384, &tm_v, &full[st], h * 64, u.g, rowj, pol);
+                }
+              }
+            }
+          }
+          used |= 1u << st;
+          loaded = (loaded & ~(1u << st)) | ((ph ^ 1u) << st);
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    }
+    // no copy may still be landing when the CTA exits (wall-clock bound only)
+    if (lane == 0) {
+      for (int i = 0; i < S; ++i)
+        if (used >> i & 1) mbar_wait(&full[i], (loaded >> i) & 1, nullptr);
+      for (int m = nq - 1; m >= 0 && m >= nq - kQBufs; --m)
+        mbar_wait(&q_full[m % kQBufs], (m / kQBufs) & 1, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------- consumers
+    const int g4 = lane >> 2, t4 = lane & 3;   // row (head or token) and column quad of a fragment
+    const float qk = s.scale * kLog2e;
+    int st = 0, k = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < a.nitems; item += gridDim.x, ++k) {
+      const Unit u = unit_of(a, item);
+      const BlockList bl = list_of(a, u.t);
+      const int nblk = max(0, min(a.spp, bl.len - u.part * a.spp));
+      const int lo = a.sel ? 0 : max(0, u.t - a.window + 1);   // visible: j <= t and
+      const int sinks = a.sel ? 0 : a.sinks;                   // (j >= lo or j < sinks)
+      const int qs = k % kQBufs;
+      ok = __all_sync(0xffffffffu,
+                      ok && mbar_wait(&q_full[qs], (k / kQBufs) & 1, &err, a.wait_polls));
+      // Q fragments: rows g4 and g4 + 8, the four dims per k-step that this
+      // thread's 16-byte chunks of a K row hold (see the reads of K below)
+      uint32_t qa[NS][4];
+      float fq[2] = {qk, qk};          // score factor of the two rows
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const int h = g4 + 8 * rr;
+        const uint32_t qrow = smem_u32(qbuf + (qs * hpg + min(h, hpg - 1)) * D);
+        uint2 w[NS];
+#pragma unroll
+        for (int ks = 0; ks < NS; ++ks) {
+          int dim;
+          if constexpr (Q8)
+            dim = D == 128 ? (2 * t4 + (ks >> 2)) * 16 + (ks & 3) * 4 : t4 * 16 + ks * 4;
+          else
+            dim = (ks >> 2) * 64 + (2 * t4 + ((ks >> 1) & 1)) * 8 + (ks & 1) * 4;
+          w[ks] = h < hpg && ok ? lds64(qrow + dim * 2) : make_uint2(0, 0);
+        }
+        if constexpr (Q8) {
+          // scale the row by a power of two: its largest magnitude to [2^13, 2^14)
+          uint32_t mx = 0;
+#pragma unroll
+          for (int ks = 0; ks < NS; ++ks) {
+            mx = max(max(mx, w[ks].x & 0x7FFFu), max(w[ks].x >> 16 & 0x7FFFu, w[ks].y & 0x7FFFu));
+            mx = max(mx, w[ks].y >> 16 & 0x7FFFu);
+          }
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          int e = (int)(mx >> 7) - 127;                   // floor(log2 max); inf, NaN: 128
+          e = mx == 0 || e == 128 ? 0 : max(e, -100);
+          const float f = pow2i(13 - e);
+          fq[rr] = qk * pow2i(e - 13);
+#pragma unroll
+          for (int ks = 0; ks < NS; ++ks) {
+            qa[ks][rr] = pack_f16(bf16lo(w[ks].x) * f, bf16hi(w[ks].x) * f);
+            qa[ks][2 + rr] = pack_f16(bf16lo(w[ks].y) * f, bf16hi(w[ks].y) * f);
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < NS; ++ks) {
+            qa[ks][rr] = w[ks].x;
+            qa[ks][2 + rr] = w[ks].y;
+          }
+        }
+      }
+      float o[NO][4];
+#pragma unroll
+      for (int j = 0; j < NO; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+      for (int blk = 0; blk < nblk; ++blk) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[st], ph, &err, a.wait_polls));
+        if (!ok) break;
+        const int kb = meta_kb[st];
+        if (kb >= 0) {
+          const int tok0 = kb * kBlock;
+          const int w0 = tok0 + warp * 16;              // this warp's first token
+          const bool whole = tok0 + kBlock - 1 <= u.t && (tok0 >= lo || tok0 + kBlock - 1 < sinks);
+          const bool any = w0 <= u.t && (w0 + 15 >= lo || w0 < sinks);
+          if (any) {
+            const uint32_t kbase = smem_u32(sm + st * C::kStage), vbase = kbase + C::kTile;
+            // ---- S = Q K^T of 16 tokens (two n-tiles of 8)
+            float sc[2][4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const int r = warp * 16 + nt * 8 + g4;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
+              if constexpr (Q8) {
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) {
+                  const uint4 w = D == 128
+                                      ? lds128(kbase + r * 128 + (((2 * t4 + j) ^ (r & 7)) << 4))
+                                      : lds128(kbase + r * 64 + ((t4 ^ ((r >> 1) & 3)) << 4));
+                  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    const int ks = j * 4 + x;
+                    mma_f16_16816(sc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3],
+                                  e4m3x2_to_f16x2(ww[x] & 0xFFFFu), e4m3x2_to_f16x2(ww[x] >> 16));
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int hj = 0; hj < D / 32; ++hj) {    // 64-dim half, chunk of it
+                  const uint4 w = lds128(kbase + (hj >> 1) * 16384 + r * 128 +
+                                         (((2 * t4 + (hj & 1)) ^ (r & 7)) << 4));
+                  const int ks = hj * 2;
+                  mma_bf16_16816(sc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], w.x, w.y);
+                  mma_bf16_16816(sc[nt], qa[ks + 1][0], qa[ks + 1][1], qa[ks + 1][2],
+                                 qa[ks + 1][3], w.z, w.w);
+                }
+              }
+            }
+            // ---- x = s log2(e) + ev, masked; row maxima
+            float f[2] = {fq[0], fq[1]}, ev = 0.f, back = 1.f;
+            if constexpr (Q8) {
+              const float fk = pow2i(meta_ke[st]);
+              f[0] = fminf(fmaxf(fq[0] * fk, -3e38f), 3e38f);
+              f[1] = fminf(fmaxf(fq[1] * fk, -3e38f), 3e38f);
+              ev = (float)meta_ve[st];
+              back = pow2i(-meta_ve[st]);
+            }
+            bool vis[4] = {true, true, true, true};      // tokens (nt, e) = w0 + nt*8 + 2*t4 + e
+            if (!whole) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int tok = w0 + (j >> 1) * 8 + 2 * t4 + (j & 1);
+                vis[j] = tok <= u.t && (tok >= lo || tok < sinks);
+              }
+            }
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float x = fmaf(sc[nt][c], f[c >> 1], ev);
+                sc[nt][c] = vis[nt * 2 + (c & 1)] ? x : -INFINITY;
+                mx[c >> 1] = fmaxf(mx[c >> 1], sc[nt][c]);
+              }
+            bool grow = false;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+              mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+              grow |= mx[r] > m[r] + kLazy;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const float mn = fmaxf(m[r], mx[r]);
+                const float al = m[r] == -INFINITY ? 0.f : ex2(m[r] - mn);
+                m[r] = mn;
+                l[r] *= al;
+#pragma unroll
+                for (int j = 0; j < NO; ++j) {
+                  o[j][2 * r] *= al;
+                  o[j][2 * r + 1] *= al;
+                }
+              }
+            }
+            // ---- p' = 2^(x - m): A fragment of O += P V
+            uint32_t pa[4];
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const float mr = m[r] == -INFINITY ? 0.f : m[r];
+                const float p0 = ex2(sc[nt][2 * r] - mr), p1 = ex2(sc[nt][2 * r + 1] - mr);
+                sum[r] += p0 + p1;
+                pa[nt * 2 + r] = Q8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+              }
+            l[0] = fmaf(sum[0], back, l[0]);
+            l[1] = fmaf(sum[1], back, l[1]);
+            // ---- V: tokens w0 + {2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4}, the
+            // dims of this thread's chunks; rows that the query does not see
+            // (they may hold anything) as zeros
+            const int r0 = warp * 16 + 2 * t4;
+            constexpr int kHalves = Q8 ? 1 : D / 64;      // boxes of a row
+            constexpr int kDimsPer = Q8 ? D / 8 : 8;      // dims of this thread in a box
+#pragma unroll
+            for (int hb = 0; hb < kHalves; ++hb) {
+              constexpr int W = Q8 ? D / 32 : 4;          // words per token
+              uint32_t vw[4][W];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int r = r0 + (j >> 1) * 8 + (j & 1);
+                if constexpr (Q8 && D == 64) {
+                  const uint2 w = lds64(vbase + r * 64 + (((g4 >> 1) ^ ((r >> 1) & 3)) << 4) +
+                                        (g4 & 1) * 8);
+                  vw[j][0] = w.x;
+                  vw[j][1] = w.y;
+                } else {
+                  const uint4 w = lds128(vbase + hb * 16384 + r * 128 + ((g4 ^ (r & 7)) << 4));
+                  vw[j][0] = w.x;
+                  vw[j][1] = w.y;
+                  vw[j][W > 2 ? 2 : 0] = w.z;
+                  vw[j][W > 2 ? 3 : 0] = w.w;
+                }
+                if (!whole && !vis[j]) {
+#pragma unroll
+                  for (int x = 0; x < W; ++x) vw[j][x] = 0u;
+                }
+              }
+#pragma unroll
+              for (int x = 0; x < W; ++x) {
+                if constexpr (Q8) {
+#pragma unroll
+                  for (int y = 0; y < 2; ++y) {           // dims 4x + 2y, 4x + 2y + 1
+                    const uint32_t sel = y ? 0x7362u : 0x5140u;
+                    const uint32_t c0 = __byte_perm(vw[0][x], vw[1][x], sel);
+                    const uint32_t c1 = __byte_perm(vw[2][x], vw[3][x], sel);
+                    const int j = 4 * x + 2 * y;
+                    mma_f16_16816(o[j], pa[0], pa[1], pa[2], pa[3], e4m3x2_to_f16x2(c0 & 0xFFFFu),
+                                  e4m3x2_to_f16x2(c1 & 0xFFFFu));
+                    mma_f16_16816(o[j + 1], pa[0], pa[1], pa[2], pa[3], e4m3x2_to_f16x2(c0 >> 16),
+                                  e4m3x2_to_f16x2(c1 >> 16));
+                  }
+                } else {                                  // dims 2x, 2x + 1 of the box's chunk
+                  const int j = hb * kDimsPer + 2 * x;
+                  mma_bf16_16816(o[j], pa[0], pa[1], pa[2], pa[3],
+                                 __byte_perm(vw[0][x], vw[1][x], 0x5410),
+                                 __byte_perm(vw[2][x], vw[3][x], 0x5410));
+                  mma_bf16_16816(o[j + 1], pa[0], pa[1], pa[2], pa[3],
+                                 __byte_perm(vw[0][x], vw[1][x], 0x7632),
+                                 __byte_perm(vw[2][x], vw[3][x], 0x7632));
+                }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_empty[qs]);
+
+      // ---- join the warps: O relative to each warp's own m
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      }
+      if (!named_bar_and(1, kConsumers, ok)) {   // also: the last item's sums have been read
+        ok = false;
+        break;
+      }
+      if (t4 == 0) {
+        sm_m[warp][g4] = m[0];
+        sm_l[warp][g4] = l[0];
+        sm_m[warp][g4 + 8] = m[1];
+        sm_l[warp][g4 + 8] = l[1];
+      }
+      // column n = 2 t4 + c of n-tile j is the dim of chunk n, element j
+#pragma unroll
+      for (int j = 0; j < NO; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int n = 2 * t4 + (c & 1), h = g4 + 8 * (c >> 1);
+          const int dim = Q8 ? n * (D / 8) + j : (j >> 3) * 64 + n * 8 + (j & 7);
+          if (h < hpg) red[(warp * hpg + h) * D + dim] = o[j][c];
+        }
+      named_bar_sync(1, kConsumers);
+      for (int e = threadIdx.x * 2; e < hpg * D; e += kConsumers * 2) {
+        const int h = e / D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, sm_m[w][h]);
+        float L = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kConsWarps; ++w) {
+          const float mw = sm_m[w][h];
+          const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
+          const float2 v = *reinterpret_cast<const float2*>(&red[w * hpg * D + e]);
+          if (f != 0.f) {
+            L = fmaf(sm_l[w][h], f, L);
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
+          }
+        }
+        if (u.nparts == 1) {
+          const float inv = L == 0.f ? 0.f : 1.f / L;     // nothing visible: zeros
+          uint16_t* dst = a.out + (((int64_t)u.b * s.T + u.i) * H + (int64_t)u.g * hpg) * D + e;
+          *reinterpret_cast<uint32_t*>(dst) = pack_bf16(x * inv, y * inv);
+        } else {
+          *reinterpret_cast<float2*>(a.part_o + (int64_t)item * hpg * D + e) = make_float2(x, y);
+          if (e % D == 0) a.part_ml[(int64_t)item * hpg + h] = make_float2(M, L);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) a.errs[blockIdx.x] = err;
+}
+
+// The worse of two error words (a timeout before an invalid block).
+__device__ __forceinline__ int worse(int x, int y) {
+  if (x == kDevTimeout || y == kDevTimeout) return kDevTimeout;
+  return max(x, y);
+}
+
+// Joins the partials of units with several parts: one warp per (pass row,
+// head).  The first CTA also turns the CTAs' error words into the status.
+template <int D>
+__global__ void __launch_bounds__(256) stream_finish_kernel(const __grid_constant__ StreamArgs a,
+                                                            int nctas) {
+  constexpr int PER = D / 32;
+  const Shape& s = a.s;
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
+    int e = 0;
+    for (int c = lane; c < nctas; c += 32) e = worse(e, a.errs[c]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) e = worse(e, __shfl_xor_sync(0xffffffffu, e, x));
+    if (lane == 0) *a.status = a.first_pass ? e : worse(e, *a.status);
+  }
+  const int gw = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (gw >= s.B * a.Tp * s.H) return;
+  const int row = gw / s.H, h = gw % s.H;
+  const int b = row / a.Tp, i = row % a.Tp;
+  const int hpg = s.H / s.G, g = h / hpg;
+  const int nparts = (a.item0[b + 1] - a.item0[b]) / (a.Tp * s.G);
+  if (nparts == 1) return;                       // written by the unit's CTA
+  const int64_t item = a.item0[b] + (int64_t)(i * s.G + g) * nparts;
+  const float2* ml = a.part_ml + item * hpg + h % hpg;
+  float M = -INFINITY;
+  for (int j = lane; j < nparts; j += 32) M = fmaxf(M, ml[(int64_t)j * hpg].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  float L = 0.f, acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  const float* po = a.part_o + (item * hpg + h % hpg) * D + lane * PER;
+  for (int j = 0; j < nparts; ++j) {
+    const float2 v = ml[(int64_t)j * hpg];
+    const float w = v.x == -INFINITY ? 0.f : ex2(v.x - M);
+    if (w == 0.f) continue;
+    L = fmaf(w, v.y, L);
+    float x[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) x[e] = po[(int64_t)j * hpg * D + e];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint16_t* dst = a.out + (((int64_t)b * s.T + a.t0 + i) * s.H + h) * D + lane * PER;
+#pragma unroll
+  for (int e = 0; e < PER; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+}
+
+int list_len(const Visible& vis, int t) {
+  if (vis.sel) return kTopk;
+  const int lo = (t - vis.window + 1 > 0 ? t - vis.window + 1 : 0) / kBlock;
+  const int sb = (vis.sinks + kBlock - 1) / kBlock;
+  return (sb < lo ? sb : lo) + t / kBlock - lo + 1;
+}
+
+// Blocks per part: of the candidates, the one whose deal over the CTAs leaves
+// the busiest one the least work, a block counted as 8 and an item's own cost
+// (its query, the join of its warps, its partial) as `kItemCost`.
+constexpr int kItemCost = 6;
+int pick_spp(const int* len, int B, int units_per_b, int ctas, int max_items) {
+  int most = 1;
+  for (int b = 0; b < B; ++b) most = len[b] > most ? len[b] : most;
+  int best = most;
+  int64_t best_load = INT64_MAX;
+  for (int spp = most;; spp = spp > 16 ? spp * 3 / 4 : spp - 1) {
+    if (spp < 1) break;
+    int64_t items = 0;
+    for (int b = 0; b < B; ++b) items += (int64_t)((len[b] + spp - 1) / spp) * units_per_b;
+    if (items > max_items) break;
+    const int64_t load = (items + ctas - 1) / ctas * (8 * spp + kItemCost);
+    if (load < best_load) {
+      best_load = load;
+      best = spp;
+    }
+  }
+  return best;
+}
+
+bool encode_codes_map(CUtensorMap* map, const void* base, const Shape& s) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)s.D, (cuuint64_t)s.G, (cuuint64_t)(s.cache_blocks() * kBlock)};
+  cuuint64_t strides[2] = {(cuuint64_t)s.D, (cuuint64_t)s.G * s.D};
+  cuuint32_t box[3] = {(cuuint32_t)s.D, 1, (cuuint32_t)kBlock};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            s.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_bf16_cache_map(CUtensorMap* map, const void* base, const Shape& s) {
+  cuuint64_t dims[3] = {(cuuint64_t)s.D, (cuuint64_t)s.G, (cuuint64_t)(s.cache_blocks() * kBlock)};
+  cuuint64_t strides[2] = {(cuuint64_t)s.D * 2, (cuuint64_t)s.G * s.D * 2};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)kBlock};
+  return encode_bf16_map(map, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D, bool Q8>
+cudaError_t launch_impl(const CacheView& c, StreamArgs& a, cudaStream_t st) {
+  using C = Cfg<D, Q8>;
+  const int hpg = a.s.H / a.s.G;
+  CUtensorMap tm_k, tm_v;
+  if constexpr (Q8) {
+    if (!encode_codes_map(&tm_k, c.k, a.s) || !encode_codes_map(&tm_v, c.v, a.s))
+      return cudaErrorInvalidValue;
+  } else {
+    if (!encode_bf16_cache_map(&tm_k, c.k, a.s) || !encode_bf16_cache_map(&tm_v, c.v, a.s))
+      return cudaErrorInvalidValue;
+  }
+  const int fixed = 1024 + kQBufs * hpg * D * 2 + kConsWarps * hpg * D * 4;
+  // static shared memory (barriers, row statistics) takes under 2 KiB
+  a.stages = (kSmemMax - 2048 - fixed) / C::kStage;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  const int smem = fixed + a.stages * C::kStage;
+  cudaError_t e = cudaFuncSetAttribute(stream_attn_kernel<D, Q8>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int ctas = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+  const int grid = a.nitems < ctas ? a.nitems : ctas;
+  note_launches(2);
+  stream_attn_kernel<D, Q8><<<grid, kThreads, smem, st>>>(tm_k, tm_v, a);
+  const bool joined = a.nitems == a.s.B * a.Tp * a.s.G;   // every unit has one part
+  const int warps = joined ? 1 : a.s.B * a.Tp * a.s.H;
+  stream_finish_kernel<D><<<(warps + 7) / 8, 256, 0, st>>>(a, grid);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int stream_pass_rows(const Shape& s) {
+  int tp = kPassRows / s.B;
+  if (tp < 1) tp = 1;
+  return tp < s.T ? tp : (s.T > 0 ? s.T : 1);
+}
+
+StreamPlan stream_plan(const Shape& s) {
+  StreamPlan p{};
+  auto al = [](size_t x) { return (x + 255) / 256 * 256; };
+  p.max_items = s.B * stream_pass_rows(s) * s.G + kExtraItems;
+  const size_t rows = (size_t)p.max_items * (s.H / s.G);
+  size_t o = 0;
+  p.errs_off = o;     o += al(kMaxCtas * sizeof(int));
+  p.part_ml_off = o;  o += al(rows * sizeof(float2));
+  p.part_o_off = o;   o += al(rows * s.D * sizeof(float));
+  p.total = o;
+  return p;
+}
+
+cudaError_t launch_stream_attn(const Shape& s, const Positions& pos, const CacheView& c,
+                               const Visible& vis, const uint16_t* q, uint16_t* out, int* status,
+                               bool join_status, char* base, cudaStream_t st) {
+  const StreamPlan pl = stream_plan(s);
+  const int tp = stream_pass_rows(s);
+  const int ctas = sm_count();
+  StreamArgs a;
+  a.s = s;
+  for (int b = 0; b < s.B; ++b) a.q_start[b] = pos.q_start[b];
+  a.window = vis.window;
+  a.sinks = vis.sinks;
+  a.sel = vis.sel;
+  a.q = q;
+  a.k_exp = c.k_exp;
+  a.v_exp = c.v_exp;
+  a.part_o = reinterpret_cast<float*>(base + pl.part_o_off);
+  a.part_ml = reinterpret_cast<float2*>(base + pl.part_ml_off);
+  a.errs = reinterpret_cast<int*>(base + pl.errs_off);
+  a.out = out;
+  a.status = status;
+  a.wait_polls = debug_wait_polls();
+  for (int t0 = 0; t0 < s.T; t0 += tp) {
+    a.t0 = t0;
+    a.Tp = tp < s.T - t0 ? tp : s.T - t0;
+    a.first_pass = t0 == 0 && !join_status;
+    int len[kMaxBatch];
+    for (int b = 0; b < s.B; ++b) {
+      // the longest list of the pass: of the last query, or (a window that
+      // ends inside a block) of one of the 128 before it
+      len[b] = 1;
+      const int last = pos.q_start[b] + t0 + a.Tp - 1;
+      const int from = a.Tp > kBlock ? last - kBlock + 1 : last - a.Tp + 1;
+      for (int t = from; t <= last; ++t) {
+        const int n = list_len(vis, t);
+        len[b] = n > len[b] ? n : len[b];
+        if (vis.sel) break;
+      }
+    }
+    const int upb = a.Tp * s.G;
+    a.spp = pick_spp(len, s.B, upb, ctas, s.B * upb + kExtraItems);
+    a.item0[0] = 0;
+    for (int b = 0; b < s.B; ++b)
+      a.item0[b + 1] = a.item0[b] + upb * ((len[b] + a.spp - 1) / a.spp);
+    a.nitems = a.item0[s.B];
+    cudaError_t e;
+    if (s.D == 128)
+      e = c.kv8 ? launch_impl<128, true>(c, a, st) : launch_impl<128, false>(c, a, st);
+    else
+      e = c.kv8 ? launch_impl<64, true>(c, a, st) : launch_impl<64, false>(c, a, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace msa

@@ -69,6 +69,9 @@ extern "C" {
 #define MSA_TOPK 16
 #define MSA_MAX_BATCH 256
 #define MSA_NOALLOC_SCRATCH_BYTES (16u << 20)
+#define MSA_Q8_MIN_EXP (-126) /* exponents of an 8-bit cache's block scales */
+#define MSA_Q8_MAX_EXP 119
+#define MSA_MAX_POOLS 8       /* pools that move together in a page operation */
 
 typedef enum {
   MSA_OK = 0,
@@ -76,7 +79,8 @@ typedef enum {
   MSA_ERR_UNSUPPORTED = -2, /* a shape outside the supported set              */
   MSA_ERR_WORKSPACE = -3,   /* ws too small                                   */
   MSA_ERR_CUDA = -4,        /* a CUDA launch or driver call failed            */
-  MSA_ERR_TIMEOUT = -5      /* a kernel's bounded wait ran out (read from ws) */
+  MSA_ERR_TIMEOUT = -5,     /* a kernel's bounded wait ran out (read from ws) */
+  MSA_ERR_PAGES = -6        /* no free page was left (read from ws)           */
 } msa_status;
 
 /* Which kernels run the prefill steps.  MSA_KERNELS_AUTO picks by shape: the
@@ -275,12 +279,154 @@ int msa_selection_quality(const msa_params *p, const uint16_t *q, const uint16_t
                           float *coverage, float *best_coverage, int32_t *dense_sel,
                           int32_t *hits, void *ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ---- 8-bit caches ---------------------------------------------------------
+ * K and V held as 8-bit floating-point codes (e4m3: 1 sign, 4 exponent and 3
+ * mantissa bits, largest value 448, no infinities) with one power-of-two scale
+ * per (cache block, KV head), for K and for V:
+ *     k_cache, v_cache  [blocks][128][G][D]   uint8 codes
+ *     k_exp, v_exp      [blocks][G]           int8 exponents e
+ *     value = code * 2^e
+ * blocks are B * max_blocks consecutive ones (block_table NULL: each sequence
+ * owns max_blocks) or a pool of num_pool_blocks (paged, as above).  K_idx and
+ * the selections stay as they are (bf16, exact).  Readers take any exponent,
+ * those outside [MSA_Q8_MIN_EXP, MSA_Q8_MAX_EXP] as the nearer end.  Half the
+ * bytes of a bf16 cache; a value is within 2^-4 of its own size of the bf16
+ * one, or within 2^-10 * 2^e where it is smaller than 2^-6 * 2^e. */
+
+/* msa_cache_append into an 8-bit cache (the same tokens, positions and K_idx
+ * rows).  For every block that the call's rows touch, KV head, and K or V:
+ *   need = the smallest exponent with |x| <= 448 * 2^need for all finite new
+ *          values of the block (MSA_Q8_MIN_EXP if they are all zero)
+ *   e    = need, if the block's first new row is its row 0; otherwise
+ *          max(need, the stored exponent), and if that is larger than the
+ *          stored one, the codes of the rows before are rounded again to 2^e
+ *          (exact unless a code becomes subnormal)
+ * Codes round to nearest even; NaN and infinities are stored as NaN; values
+ * above 448 * 2^MSA_Q8_MAX_EXP saturate.  Rows of the block behind the new
+ * ones keep their bytes.  A block must not be written by two sequences of one
+ * call (as after msa_pages_fork, which copies the page that is still filled). */
+int msa_cache_append_q8(const msa_params *p, const int32_t *block_table, int num_pool_blocks,
+                        const uint16_t *k_new, const uint16_t *v_new, const uint16_t *k_idx_new,
+                        const int32_t *q_start, uint8_t *k_cache, uint8_t *v_cache, int8_t *k_exp,
+                        int8_t *v_exp, uint16_t *k_idx_cache, void *ws, size_t ws_bytes,
+                        cudaStream_t stream);
+
+/* Step 4 (msa_sparse_attn) and steps 1-4 (msa_forward) on an 8-bit cache, per
+ * sequence (block_table NULL) or paged.  The attention of the cached values is
+ * computed as for a bf16 cache (fp32 accumulation, bf16 output); a row whose
+ * selection holds no visible token is written as zeros.  Cache rows that no
+ * query may see (behind the last query) may hold anything.  ws: at least
+ * msa_q8_workspace_bytes(p) bytes, 256-byte aligned. */
+size_t msa_q8_workspace_bytes(const msa_params *p);
+int msa_sparse_attn_q8(const msa_params *p, const int32_t *block_table, int num_pool_blocks,
+                       const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache,
+                       const int8_t *k_exp, const int8_t *v_exp, const int32_t *sel,
+                       const int32_t *q_start, const int32_t *kv_len, uint16_t *out, void *ws,
+                       size_t ws_bytes, cudaStream_t stream);
+int msa_forward_q8(const msa_params *p, const int32_t *block_table, int num_pool_blocks,
+                   const uint16_t *q_idx, const uint16_t *k_idx, const uint16_t *q,
+                   const uint8_t *k_cache, const uint8_t *v_cache, const int8_t *k_exp,
+                   const int8_t *v_exp, const int32_t *q_start, const int32_t *kv_len,
+                   int32_t *sel_out, uint16_t *out, void *ws, size_t ws_bytes,
+                   cudaStream_t stream);
+
+/* ---- Sliding-window attention ----------------------------------------------
+ * GQA attention on the same caches (per sequence or paged, bf16 or 8-bit) in
+ * which the query at position t sees the tokens
+ *     j <= t  with  j > t - window  or  j < sinks
+ * i.e. the last `window` tokens, itself among them, and the first `sinks`
+ * tokens of the sequence.  window >= 1, sinks >= 0; a window of at least
+ * kv_len is dense causal attention.  Blocks that hold no visible token are
+ * not read, nor are their block-table entries (a serving engine can free
+ * pages that the window has left: msa_pages_free).  Rows of a block that no
+ * query of the call sees may hold anything; a NaN or an infinity in V of a
+ * token that one query of a prefill-sized call sees also reaches outputs of
+ * the queries up to 127 positions from that one.  p->topk and p->Di are
+ * checked but not used.  out is bf16 (round to nearest even) from fp32
+ * accumulation.  ws: at least msa_window_workspace_bytes(p) bytes, 256-byte
+ * aligned. */
+size_t msa_window_workspace_bytes(const msa_params *p);
+int msa_window_attn(const msa_params *p, const int32_t *block_table, int num_pool_blocks,
+                    int window, int sinks, const uint16_t *q, const uint16_t *k_cache,
+                    const uint16_t *v_cache, const int32_t *q_start, const int32_t *kv_len,
+                    uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream);
+int msa_window_attn_q8(const msa_params *p, const int32_t *block_table, int num_pool_blocks,
+                       int window, int sinks, const uint16_t *q, const uint8_t *k_cache,
+                       const uint8_t *v_cache, const int8_t *k_exp, const int8_t *v_exp,
+                       const int32_t *q_start, const int32_t *kv_len, uint16_t *out, void *ws,
+                       size_t ws_bytes, cudaStream_t stream);
+
+/* ---- Page operations --------------------------------------------------------
+ * Bookkeeping of paged pools on the device: a block table
+ * block_table[rows][max_blocks] (-1: unmapped) and refs[num_pool_blocks], the
+ * number of table entries that map each page (0: the page is free).  Row
+ * numbers, token counts and block ranges are HOST arrays of n entries, n <=
+ * MSA_MAX_BATCH.  The calls only enqueue work and give the same result in any
+ * order of execution.  Table entries outside [0, num_pool_blocks) other than
+ * -1, and mappings of pages whose count is 0, are reported
+ * (MSA_ERR_INVALID_ARG in ws); a call that runs out of free pages maps what it
+ * can, leaves the rest at -1 and reports MSA_ERR_PAGES (msa_workspace_status).
+ * ws: at least msa_pages_workspace_bytes(num_pool_blocks), 256-byte aligned.
+ *
+ * The pools that move together are described by up to MSA_MAX_POOLS entries:
+ * page i is the page_bytes bytes at base + i * page_bytes (device memory).
+ * per_token != 0: the page is 128 rows of page_bytes / 128 bytes (K, V, K_idx),
+ * of which a copy of a partly filled page moves only the used ones; 0: the
+ * page is moved whole (exponents). */
+typedef struct {
+  void *base;
+  size_t page_bytes;
+  int per_token;
+} msa_pool;
+
+size_t msa_pages_workspace_bytes(int num_pool_blocks);
+
+/* Page dst[i] of every pool becomes a copy of page src[i], i < n (src, dst:
+ * device arrays; any n >= 0).  The pages of dst must be distinct and none of
+ * them may be in src, but for pairs with src[i] == dst[i], which do nothing. */
+int msa_pages_copy(const msa_pool *pools, int npools, int num_pool_blocks, const int32_t *src,
+                   const int32_t *dst, int n, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* For each pair j in order: row dst_rows[j] lets go of the pages it maps, then
+ * maps the first len[j] tokens of row src_rows[j]: the pages that they fill
+ * completely are shared (their counts rise), a partly filled last one is
+ * copied to the lowest free page (its used rows), and the row's other entries
+ * become -1.  dst_rows are distinct and none is in src_rows. */
+int msa_pages_fork(const msa_pool *pools, int npools, int num_pool_blocks, int32_t *block_table,
+                   int rows, int max_blocks, int32_t *refs, const int32_t *src_rows,
+                   const int32_t *dst_rows, const int32_t *len, int n, void *ws, size_t ws_bytes,
+                   cudaStream_t stream);
+
+/* Unmaps blocks [first[j], last[j]) of row row[j]: a whole sequence, the
+ * blocks that a window has left, or a rejected tail.  Overlapping ranges count
+ * once. */
+int msa_pages_free(int num_pool_blocks, int32_t *block_table, int rows, int max_blocks,
+                   int32_t *refs, const int32_t *row, const int32_t *first, const int32_t *last,
+                   int n, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Maps the unmapped blocks of [first[j], last[j]) of row row[j], in order of j
+ * and block, to the lowest free pages.  The rows are distinct. */
+int msa_pages_alloc(int num_pool_blocks, int32_t *block_table, int rows, int max_blocks,
+                    int32_t *refs, const int32_t *row, const int32_t *first, const int32_t *last,
+                    int n, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Moves the pages in use to the front of the pools: with live[0] (device,
+ * written) pages in use, the i-th one at or behind that index goes to the i-th
+ * free page before it.  table_out and refs_out receive the table and counts
+ * after the move (they may be block_table and refs themselves).  The bytes of
+ * the pages that were moved away stay behind. */
+int msa_pages_compact(const msa_pool *pools, int npools, int num_pool_blocks,
+                      const int32_t *block_table, int rows, int max_blocks, const int32_t *refs,
+                      int32_t *table_out, int32_t *refs_out, int32_t *live, void *ws,
+                      size_t ws_bytes, cudaStream_t stream);
+
 /* Waits for `stream`, then returns the status the last call on ws left in
  * it: MSA_OK; MSA_ERR_TIMEOUT if a kernel's bounded wait ran out (its
  * outputs are then incomplete; this takes precedence over the next case);
  * MSA_ERR_INVALID_ARG if msa_sparse_attn met a selected id outside [0, lb]
- * or beyond max_blocks (that id was skipped, never read).  MSA_ERR_CUDA if
- * the read itself fails. */
+ * or beyond max_blocks (that id was skipped, never read); MSA_ERR_PAGES if a
+ * page operation ran out of free pages.  MSA_ERR_CUDA if the read itself
+ * fails. */
 int msa_workspace_status(const void *ws, cudaStream_t stream);
 
 /* A static, human-readable name of a status code. */
