@@ -24,11 +24,9 @@ struct Visible {
   int window, sinks;
 };
 
-// Scratch of the streaming attention: partials of at most `items` (unit,
-// part) items and one error word per CTA.
+// Scratch of the streaming attention: two partials and one error word per CTA.
 struct StreamPlan {
   size_t part_o_off, part_ml_off, errs_off, total;
-  int max_items;
 };
 StreamPlan stream_plan(const Shape& s);
 int stream_pass_rows(const Shape& s);

@@ -10,11 +10,11 @@
 // p'_j = 2^(x_j + ev - m'), so that p' bounds the value's size rather than the
 // weight's; the block adds 2^-ev sum p' to the normaliser.
 //
-// A persistent CTA per SM walks items (unit (b, t, g), part): a part is `spp`
-// consecutive blocks of the unit's list.  Warp 8 copies K and V of each block
-// (128 tokens of one KV head) into a ring of stages by TMA and runs ahead by
-// its depth.  Warps 0-7 take 16 tokens of every block each and never wait for
-// one another inside an item: S = Q K^T with mma.sync m16n8k16 (rows: the
+// The call's work is one sequence of (unit, block) steps, unit (b, t, g) after
+// unit, cut into equal runs, one per CTA and SM; a run's share of one unit is a
+// segment.  Warp 8 copies K and V of each block (128 tokens of one KV head)
+// into a ring of stages by TMA and runs ahead by its depth.  Warps 0-7 take 16
+// tokens of every block each and never wait for one another inside a segment: S = Q K^T with mma.sync m16n8k16 (rows: the
 // group's heads), softmax in registers, P straight from the accumulator
 // layout into the A operand of O += P V.  The order of the contraction's
 // terms is free, so dims (for S) and output columns (for O) are dealt to
@@ -24,9 +24,10 @@
 // per row to fit f16 (exact but for elements 2^-27 below the row's maximum,
 // which round at 2^-38 of it), and P rounds to f16 (2^-11).  With a bf16 cache
 // the products are bf16 and P rounds to bf16 (2^-8).
-// At an item's end the eight warps' (O, m, l) are joined in shared memory;
-// a unit of one part is written out directly, others leave one partial per
-// part that stream_finish_kernel joins.
+// At a segment's end the eight warps' (O, m, l) are joined in shared memory; a
+// whole unit is written out directly, a cut one leaves a partial per CTA (at
+// most two: the unit its run begins inside, the one it ends inside) that
+// stream_finish_kernel joins.
 #include "msa_q8.cuh"
 #include "msa_tma.h"
 
@@ -38,8 +39,7 @@ constexpr int kConsumers = 32 * kConsWarps;
 constexpr int kThreads = kConsumers + 32;
 constexpr int kQBufs = 2;
 constexpr int kMaxStages = 8;
-constexpr int kExtraItems = 2048;    // items beyond one per unit
-constexpr int kMaxCtas = 512;        // error words in the workspace
+constexpr int kMaxCtas = 512;        // partials and error words in the workspace
 constexpr int kPassRows = 2048;      // (sequence, query) rows per pass
 constexpr float kLazy = 8.f;         // log2 growth of p tolerated before O is rescaled
 constexpr int kSmemMax = 227 * 1024;
@@ -47,38 +47,47 @@ constexpr int kSmemMax = 227 * 1024;
 struct StreamArgs {
   Shape s;
   int32_t q_start[kMaxBatch];
-  int32_t item0[kMaxBatch + 1];   // first item of each sequence
-  int t0, Tp, spp, nitems, stages;
+  int32_t step0[kMaxBatch + 1];   // first step of each sequence; [B]: all steps
+  int t0, Tp, nctas, stages;
   int window, sinks;
   const int32_t* sel;
   const uint16_t* q;
   const int8_t* k_exp;
   const int8_t* v_exp;
-  float* part_o;                  // [item][H/G][D], O relative to m
-  float2* part_ml;                // [item][H/G] (m in log2 units, l)
+  float* part_o;                  // [2 * CTA + slot][H/G][D], O relative to m
+  float2* part_ml;                // [2 * CTA + slot][H/G] (m in log2 units, l)
   uint16_t* out;
-  int* errs;                      // [gridDim.x]
+  int* errs;                      // [nctas]
   int* status;
   bool first_pass;
   uint32_t wait_polls;
 };
 
+// CTA c's run of steps begins at floor(c * steps / nctas).
+__host__ __device__ __forceinline__ int run_begin(int steps, int nctas, int c) {
+  return (int)((int64_t)c * steps / nctas);
+}
+__device__ __forceinline__ int run_of(int steps, int nctas, int step) {
+  return (int)((((int64_t)step + 1) * nctas - 1) / steps);
+}
+
+// The unit that a step belongs to: its first step, its steps (the longest
+// list of its sequence in this pass) and its query.
 struct Unit {
-  int b, i, g, part, nparts, t;
+  int b, i, g, t, first, len;
 };
 
-__device__ __forceinline__ Unit unit_of(const StreamArgs& a, int item) {
+__device__ __forceinline__ Unit unit_of(const StreamArgs& a, int step) {
   int lo = 0, hi = a.s.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (a.item0[mid] <= item) lo = mid; else hi = mid;
+    if (a.step0[mid] <= step) lo = mid; else hi = mid;
   }
   Unit u;
   u.b = lo;
-  const int r = item - a.item0[lo];
-  u.nparts = (a.item0[lo + 1] - a.item0[lo]) / (a.Tp * a.s.G);
-  u.part = r % u.nparts;
-  const int ig = r / u.nparts;
+  u.len = (a.step0[lo + 1] - a.step0[lo]) / (a.Tp * a.s.G);
+  const int ig = (step - a.step0[lo]) / u.len;
+  u.first = a.step0[lo] + ig * u.len;
   u.g = ig % a.s.G;
   u.i = a.t0 + ig / a.s.G;
   u.t = a.q_start[lo] + u.i;
@@ -101,6 +110,7 @@ template <int D, bool Q8>
 struct Cfg {
   static constexpr int kTile = kBlock * D * (Q8 ? 1 : 2);   // K (or V) of one block and head
   static constexpr int kStage = 2 * kTile;
+  static constexpr int kRedRow = D + 8;                     // padded row of the join buffer (floats)
 };
 
 template <int D, bool Q8>
@@ -121,7 +131,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
   const int H = s.H, G = s.G, hpg = H / G, S = a.stages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint16_t* qbuf = reinterpret_cast<uint16_t*>(sm + S * C::kStage);       // [kQBufs][hpg][D]
-  float* red = reinterpret_cast<float*>(qbuf + kQBufs * hpg * D);         // [8][hpg][D]
+  const uint32_t red = smem_u32(qbuf + kQBufs * hpg * D);                 // [8][hpg][kRedRow] float
+  const int steps = a.step0[s.B];
+  const int run0 = run_begin(steps, a.nctas, blockIdx.x);
+  const int run1 = run_begin(steps, a.nctas, blockIdx.x + 1);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -141,13 +154,14 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
     // ------------------------------------------------------------ producer
     const uint64_t pol = l2_policy_evict_first();
     const uint32_t qbytes = (uint32_t)(hpg * D * 2);
-    int st = 0, k = 0;              // next stage, items begun
+    int st = 0, k = 0;              // next stage, segments begun
     uint32_t ph = 1;                // phase parity that frees the stage (first lap: free)
     uint32_t used = 0, loaded = 0;  // stages ever loaded / parity of each stage's last load
     int nq = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x, ++k) {
-      const Unit u = unit_of(a, item);
+    for (int step = run0, next; step < run1 && ok; step = next, ++k) {
+      const Unit u = unit_of(a, step);
+      next = min(run1, u.first + u.len);
       const int qs = k % kQBufs;
       ok = __all_sync(0xffffffffu, k < kQBufs || mbar_wait(&q_empty[qs], ((k / kQBufs) - 1) & 1,
                                                            &err, a.wait_polls));
@@ -160,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
       }
       ++nq;
       const BlockList bl = list_of(a, u.t);
-      const int p0 = u.part * a.spp, p1 = min(p0 + a.spp, bl.len);
+      const int p0 = step - u.first, p1 = min(next - u.first, bl.len);
       const int32_t* srow =
           a.sel ? a.sel + (((int64_t)u.b * s.T + u.i) * G + u.g) * kTopk : nullptr;
       for (int pc = p0; pc < p1 && ok; pc += 32) {
@@ -237,10 +251,11 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
     int st = 0, k = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < a.nitems; item += gridDim.x, ++k) {
-      const Unit u = unit_of(a, item);
+    for (int step = run0, next; step < run1; step = next, ++k) {
+      const Unit u = unit_of(a, step);
+      next = min(run1, u.first + u.len);
       const BlockList bl = list_of(a, u.t);
-      const int nblk = max(0, min(a.spp, bl.len - u.part * a.spp));
+      const int nblk = min(next - u.first, bl.len) - (step - u.first);
       const int lo = a.sel ? 0 : max(0, u.t - a.window + 1);   // visible: j <= t and
       const int sinks = a.sel ? 0 : a.sinks;                   // (j >= lo or j < sinks)
       const int qs = k % kQBufs;
@@ -476,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       }
-      if (!named_bar_and(1, kConsumers, ok)) {   // also: the last item's sums have been read
+      if (!named_bar_and(1, kConsumers, ok)) {   // also: the last segment's sums have been read
         ok = false;
         break;
       }
@@ -486,18 +501,19 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
         sm_m[warp][g4 + 8] = m[1];
         sm_l[warp][g4 + 8] = l[1];
       }
-      // column n = 2 t4 + c of n-tile j is the dim of chunk n, element j
+      // fragment order: columns 2 t4, 2 t4 + 1 of n-tile j side by side
 #pragma unroll
-      for (int j = 0; j < NO; ++j)
+      for (int r = 0; r < 2; ++r)
+        if (g4 + 8 * r < hpg) {
+          const uint32_t row = red + ((warp * hpg + g4 + 8 * r) * C::kRedRow + 2 * t4) * 4;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int n = 2 * t4 + (c & 1), h = g4 + 8 * (c >> 1);
-          const int dim = Q8 ? n * (D / 8) + j : (j >> 3) * 64 + n * 8 + (j & 7);
-          if (h < hpg) red[(warp * hpg + h) * D + dim] = o[j][c];
+          for (int j = 0; j < NO; ++j) sts_f2(row + j * 32, o[j][2 * r], o[j][2 * r + 1]);
         }
       named_bar_sync(1, kConsumers);
-      for (int e = threadIdx.x * 2; e < hpg * D; e += kConsumers * 2) {
-        const int h = e / D;
+      const bool whole_unit = step == u.first && next == u.first + u.len;
+      const int64_t slot = 2 * blockIdx.x + (step == u.first);
+      for (int e = threadIdx.x; e < hpg * NO * 4; e += kConsumers) {
+        const int h = e / (NO * 4), j = e / 4 % NO;        // one head per warp and step
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, sm_m[w][h]);
@@ -506,20 +522,26 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
         for (int w = 0; w < kConsWarps; ++w) {
           const float mw = sm_m[w][h];
           const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-          const float2 v = *reinterpret_cast<const float2*>(&red[w * hpg * D + e]);
+          const float2 v = lds_f2(red + ((w * hpg + h) * C::kRedRow + (e % (NO * 4)) * 2) * 4);
           if (f != 0.f) {
             L = fmaf(sm_l[w][h], f, L);
             x = fmaf(v.x, f, x);
             y = fmaf(v.y, f, y);
           }
         }
-        if (u.nparts == 1) {
-          const float inv = L == 0.f ? 0.f : 1.f / L;     // nothing visible: zeros
-          uint16_t* dst = a.out + (((int64_t)u.b * s.T + u.i) * H + (int64_t)u.g * hpg) * D + e;
-          *reinterpret_cast<uint32_t*>(dst) = pack_bf16(x * inv, y * inv);
+        // dims j, j + 1 of one column: the lane of the other j holds the pair's other half
+        const bool odd = j & 1;
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 4);
+        const float d0 = odd ? other : x, d1 = odd ? y : other;
+        const int n = 2 * (e & 3) + odd, je = j & ~1;
+        const int dim = Q8 ? n * (D / 8) + je : (je >> 3) * 64 + n * 8 + (je & 7);
+        if (whole_unit) {
+          const float inv = L == 0.f ? 0.f : 1.f / L;      // nothing visible: zeros
+          uint16_t* dst = a.out + (((int64_t)u.b * s.T + u.i) * H + (int64_t)u.g * hpg + h) * D + dim;
+          *reinterpret_cast<uint32_t*>(dst) = pack_bf16(d0 * inv, d1 * inv);
         } else {
-          *reinterpret_cast<float2*>(a.part_o + (int64_t)item * hpg * D + e) = make_float2(x, y);
-          if (e % D == 0) a.part_ml[(int64_t)item * hpg + h] = make_float2(M, L);
+          *reinterpret_cast<float2*>(a.part_o + (slot * hpg + h) * D + dim) = make_float2(d0, d1);
+          if (e % (NO * 4) == 0) a.part_ml[slot * hpg + h] = make_float2(M, L);
         }
       }
     }
@@ -534,51 +556,55 @@ __device__ __forceinline__ int worse(int x, int y) {
   return max(x, y);
 }
 
-// Joins the partials of units with several parts: one warp per (pass row,
-// head).  The first CTA also turns the CTAs' error words into the status.
+// Joins the partials of the units that a run's end cuts: one warp per (run,
+// head), for the first run that begins inside a unit.  The first CTA also
+// turns the CTAs' error words into the status.
 template <int D>
-__global__ void __launch_bounds__(256) stream_finish_kernel(const __grid_constant__ StreamArgs a,
-                                                            int nctas) {
+__global__ void __launch_bounds__(256) stream_finish_kernel(const __grid_constant__ StreamArgs a) {
   constexpr int PER = D / 32;
   const Shape& s = a.s;
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x < 32) {
     int e = 0;
-    for (int c = lane; c < nctas; c += 32) e = worse(e, a.errs[c]);
+    for (int c = lane; c < a.nctas; c += 32) e = worse(e, a.errs[c]);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) e = worse(e, __shfl_xor_sync(0xffffffffu, e, x));
     if (lane == 0) *a.status = a.first_pass ? e : worse(e, *a.status);
   }
+  const int hpg = s.H / s.G;
   const int gw = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (gw >= s.B * a.Tp * s.H) return;
-  const int row = gw / s.H, h = gw % s.H;
-  const int b = row / a.Tp, i = row % a.Tp;
-  const int hpg = s.H / s.G, g = h / hpg;
-  const int nparts = (a.item0[b + 1] - a.item0[b]) / (a.Tp * s.G);
-  if (nparts == 1) return;                       // written by the unit's CTA
-  const int64_t item = a.item0[b] + (int64_t)(i * s.G + g) * nparts;
-  const float2* ml = a.part_ml + item * hpg + h % hpg;
+  const int run = gw / hpg + 1, h = gw % hpg, steps = a.step0[s.B];
+  if (run >= a.nctas) return;
+  const int begin = run_begin(steps, a.nctas, run);
+  const Unit u = unit_of(a, begin);
+  const int r0 = run_of(steps, a.nctas, u.first);
+  if (begin == u.first || run != r0 + 1) return;
+  const int r1 = run_of(steps, a.nctas, u.first + u.len - 1);
+  // run r0 ends inside the unit (its slot 1), runs r0 + 1 ... r1 begin inside it (slot 0)
   float M = -INFINITY;
-  for (int j = lane; j < nparts; j += 32) M = fmaxf(M, ml[(int64_t)j * hpg].x);
+  for (int r = r0 + lane; r <= r1; r += 32)
+    M = fmaxf(M, a.part_ml[(int64_t)(2 * r + (r == r0)) * hpg + h].x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   float L = 0.f, acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  const float* po = a.part_o + (item * hpg + h % hpg) * D + lane * PER;
-  for (int j = 0; j < nparts; ++j) {
-    const float2 v = ml[(int64_t)j * hpg];
+#pragma unroll 4
+  for (int r = r0; r <= r1; ++r) {
+    const int64_t p = (int64_t)(2 * r + (r == r0)) * hpg + h;
+    const float2 v = a.part_ml[p];
     const float w = v.x == -INFINITY ? 0.f : ex2(v.x - M);
-    if (w == 0.f) continue;
-    L = fmaf(w, v.y, L);
     float x[PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) x[e] = po[(int64_t)j * hpg * D + e];
+    for (int e = 0; e < PER; ++e) x[e] = a.part_o[p * D + lane * PER + e];
+    if (w == 0.f) continue;
+    L = fmaf(w, v.y, L);
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, x[e], acc[e]);
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint16_t* dst = a.out + (((int64_t)b * s.T + a.t0 + i) * s.H + h) * D + lane * PER;
+  uint16_t* dst =
+      a.out + (((int64_t)u.b * s.T + u.i) * s.H + (int64_t)u.g * hpg + h) * D + lane * PER;
 #pragma unroll
   for (int e = 0; e < PER; e += 2)
     *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
@@ -589,29 +615,6 @@ int list_len(const Visible& vis, int t) {
   const int lo = (t - vis.window + 1 > 0 ? t - vis.window + 1 : 0) / kBlock;
   const int sb = (vis.sinks + kBlock - 1) / kBlock;
   return (sb < lo ? sb : lo) + t / kBlock - lo + 1;
-}
-
-// Blocks per part: of the candidates, the one whose deal over the CTAs leaves
-// the busiest one the least work, a block counted as 8 and an item's own cost
-// (its query, the join of its warps, its partial) as `kItemCost`.
-constexpr int kItemCost = 6;
-int pick_spp(const int* len, int B, int units_per_b, int ctas, int max_items) {
-  int most = 1;
-  for (int b = 0; b < B; ++b) most = len[b] > most ? len[b] : most;
-  int best = most;
-  int64_t best_load = INT64_MAX;
-  for (int spp = most;; spp = spp > 16 ? spp * 3 / 4 : spp - 1) {
-    if (spp < 1) break;
-    int64_t items = 0;
-    for (int b = 0; b < B; ++b) items += (int64_t)((len[b] + spp - 1) / spp) * units_per_b;
-    if (items > max_items) break;
-    const int64_t load = (items + ctas - 1) / ctas * (8 * spp + kItemCost);
-    if (load < best_load) {
-      best_load = load;
-      best = spp;
-    }
-  }
-  return best;
 }
 
 bool encode_codes_map(CUtensorMap* map, const void* base, const Shape& s) {
@@ -646,7 +649,7 @@ cudaError_t launch_impl(const CacheView& c, StreamArgs& a, cudaStream_t st) {
     if (!encode_bf16_cache_map(&tm_k, c.k, a.s) || !encode_bf16_cache_map(&tm_v, c.v, a.s))
       return cudaErrorInvalidValue;
   }
-  const int fixed = 1024 + kQBufs * hpg * D * 2 + kConsWarps * hpg * D * 4;
+  const int fixed = 1024 + kQBufs * hpg * D * 2 + kConsWarps * hpg * C::kRedRow * 4;
   // static shared memory (barriers, row statistics) takes under 2 KiB
   a.stages = (kSmemMax - 2048 - fixed) / C::kStage;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
@@ -654,13 +657,10 @@ cudaError_t launch_impl(const CacheView& c, StreamArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(stream_attn_kernel<D, Q8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int ctas = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
-  const int grid = a.nitems < ctas ? a.nitems : ctas;
   note_launches(2);
-  stream_attn_kernel<D, Q8><<<grid, kThreads, smem, st>>>(tm_k, tm_v, a);
-  const bool joined = a.nitems == a.s.B * a.Tp * a.s.G;   // every unit has one part
-  const int warps = joined ? 1 : a.s.B * a.Tp * a.s.H;
-  stream_finish_kernel<D><<<(warps + 7) / 8, 256, 0, st>>>(a, grid);
+  stream_attn_kernel<D, Q8><<<a.nctas, kThreads, smem, st>>>(tm_k, tm_v, a);
+  const int warps = (a.nctas - 1) * hpg;
+  stream_finish_kernel<D><<<warps > 0 ? (warps + 7) / 8 : 1, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -675,8 +675,7 @@ int stream_pass_rows(const Shape& s) {
 StreamPlan stream_plan(const Shape& s) {
   StreamPlan p{};
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
-  p.max_items = s.B * stream_pass_rows(s) * s.G + kExtraItems;
-  const size_t rows = (size_t)p.max_items * (s.H / s.G);
+  const size_t rows = (size_t)2 * kMaxCtas * (s.H / s.G);
   size_t o = 0;
   p.errs_off = o;     o += al(kMaxCtas * sizeof(int));
   p.part_ml_off = o;  o += al(rows * sizeof(float2));
@@ -690,7 +689,7 @@ cudaError_t launch_stream_attn(const Shape& s, const Positions& pos, const Cache
                                bool join_status, char* base, cudaStream_t st) {
   const StreamPlan pl = stream_plan(s);
   const int tp = stream_pass_rows(s);
-  const int ctas = sm_count();
+  const int ctas = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
   StreamArgs a;
   a.s = s;
   for (int b = 0; b < s.B; ++b) a.q_start[b] = pos.q_start[b];
@@ -723,12 +722,10 @@ cudaError_t launch_stream_attn(const Shape& s, const Positions& pos, const Cache
         if (vis.sel) break;
       }
     }
-    const int upb = a.Tp * s.G;
-    a.spp = pick_spp(len, s.B, upb, ctas, s.B * upb + kExtraItems);
-    a.item0[0] = 0;
-    for (int b = 0; b < s.B; ++b)
-      a.item0[b + 1] = a.item0[b] + upb * ((len[b] + a.spp - 1) / a.spp);
-    a.nitems = a.item0[s.B];
+    a.step0[0] = 0;
+    for (int b = 0; b < s.B; ++b) a.step0[b + 1] = a.step0[b] + a.Tp * s.G * len[b];
+    const int steps = a.step0[s.B];
+    a.nctas = steps < ctas ? steps : ctas;
     cudaError_t e;
     if (s.D == 128)
       e = c.kv8 ? launch_impl<128, true>(c, a, st) : launch_impl<128, false>(c, a, st);
