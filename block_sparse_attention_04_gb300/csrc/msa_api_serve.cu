@@ -63,6 +63,9 @@ int run_window(const msa_params* p, const int32_t* block_table, int num_pool_blo
   const Visible vis{nullptr, window < cap ? window : cap, sinks < cap ? sinks : cap};
   const Shape s = shape_of(p, block_table, num_pool_blocks);
   char* base = static_cast<char*>(ws);
+  if (prefill_sized(p))
+    return cuda_status(launch_window_tc(s, pos, c, vis.window, vis.sinks, q, out,
+                                        reinterpret_cast<int*>(base), st));
   return cuda_status(launch_stream_attn(s, pos, c, vis, q, out, reinterpret_cast<int*>(base),
                                         false, base + kAlign, st));
 }

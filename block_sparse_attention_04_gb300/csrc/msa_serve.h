@@ -39,6 +39,12 @@ cudaError_t launch_stream_attn(const Shape& s, const Positions& pos, const Cache
                                const Visible& vis, const uint16_t* q, uint16_t* out, int* status,
                                bool join_status, char* base, cudaStream_t st);
 
+// Sliding-window attention of every query of the call on tensor cores
+// (prefill shapes).  status: the status word and the word after it.
+cudaError_t launch_window_tc(const Shape& s, const Positions& pos, const CacheView& c, int window,
+                             int sinks, const uint16_t* q, uint16_t* out, int* status,
+                             cudaStream_t st);
+
 // Appends tokens to an 8-bit cache (layouts of msa_cache_append_q8).
 cudaError_t launch_cache_append_q8(const Shape& s, const Positions& pos, const uint16_t* k_new,
                                    const uint16_t* v_new, const uint16_t* kidx_new, uint8_t* k,

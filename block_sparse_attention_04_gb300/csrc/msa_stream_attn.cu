@@ -6,9 +6,11 @@
 // tokens j of the unit's blocks, s_j = scale q.k_j, o = sum 2^(x_j - m) v_j /
 // sum 2^(x_j - m) with x = s log2(e).  An 8-bit cache holds k = ck 2^ek and
 // v = cv 2^ev (ck, cv e4m3 codes, one exponent per block and KV head): ek
-// scales the block's scores, and 2^ev is folded into the exponential,
-// p'_j = 2^(x_j + ev - m'), so that p' bounds the value's size rather than the
-// weight's; the block adds 2^-ev sum p' to the normaliser.
+// scales the block's scores, and 2^ev is folded into the exponential that
+// multiplies V, p'_j = 2^(x_j + ev - m') with m' the running maximum of x + ev.
+// The normaliser keeps its own exponentials and maximum, l = sum 2^(x_j - n):
+// a block of zeros has the smallest ev, and p' of it would vanish beside other
+// blocks while its weights count.  The result is O / l * 2^(m' - n).
 //
 // The call's work is one sequence of (unit, block) steps, unit (b, t, g) after
 // unit, cut into equal runs, one per CTA and SM; a run's share of one unit is a
@@ -55,7 +57,7 @@ struct StreamArgs {
   const int8_t* k_exp;
   const int8_t* v_exp;
   float* part_o;                  // [2 * CTA + slot][H/G][D], O relative to m
-  float2* part_ml;                // [2 * CTA + slot][H/G] (m in log2 units, l)
+  float4* part_ml;                // [2 * CTA + slot][H/G] (m, n in log2 units, l)
   uint16_t* out;
   int* errs;                      // [nctas]
   int* status;
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], q_full[kQBufs], q_empty[kQBufs];
   __shared__ int meta_kb[kMaxStages], meta_ke[kMaxStages], meta_ve[kMaxStages];
-  __shared__ float sm_m[kConsWarps][16], sm_l[kConsWarps][16];
+  __shared__ float sm_m[kConsWarps][16], sm_n[kConsWarps][16], sm_l[kConsWarps][16];
   __shared__ int err;
   const Shape& s = a.s;
   const int H = s.H, G = s.G, hpg = H / G, S = a.stages;
@@ -311,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
       for (int j = 0; j < NO; ++j)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      // running maxima of x + ev (of O's terms) and x (of l's; the same without ev)
+      float m[2] = {-INFINITY, -INFINITY}, n[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
       for (int blk = 0; blk < nblk; ++blk) {
         ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[st], ph, &err, a.wait_polls));
@@ -357,14 +360,13 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
                 }
               }
             }
-            // ---- x = s log2(e) + ev, masked; row maxima
-            float f[2] = {fq[0], fq[1]}, ev = 0.f, back = 1.f;
+            // ---- x = s log2(e), masked; row maxima
+            float f[2] = {fq[0], fq[1]}, ev = 0.f;
             if constexpr (Q8) {
               const float fk = pow2i(meta_ke[st]);
               f[0] = fminf(fmaxf(fq[0] * fk, -3e38f), 3e38f);
               f[1] = fminf(fmaxf(fq[1] * fk, -3e38f), 3e38f);
               ev = (float)meta_ve[st];
-              back = pow2i(-meta_ve[st]);
             }
             bool vis[4] = {true, true, true, true};      // tokens (nt, e) = w0 + nt*8 + 2*t4 + e
             if (!whole) {
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                const float x = fmaf(sc[nt][c], f[c >> 1], ev);
+                const float x = sc[nt][c] * f[c >> 1];
                 sc[nt][c] = vis[nt * 2 + (c & 1)] ? x : -INFINITY;
                 mx[c >> 1] = fmaxf(mx[c >> 1], sc[nt][c]);
               }
@@ -388,15 +390,21 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
             for (int r = 0; r < 2; ++r) {
               mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
               mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-              grow |= mx[r] > m[r] + kLazy;
+              grow |= mx[r] + ev > m[r] + kLazy || (Q8 && mx[r] > n[r] + kLazy);
             }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                const float mn = fmaxf(m[r], mx[r]);
+                const float mn = fmaxf(m[r], mx[r] + ev);
                 const float al = m[r] == -INFINITY ? 0.f : ex2(m[r] - mn);
                 m[r] = mn;
-                l[r] *= al;
+                if constexpr (Q8) {
+                  const float nn = fmaxf(n[r], mx[r]);
+                  l[r] *= n[r] == -INFINITY ? 0.f : ex2(n[r] - nn);
+                  n[r] = nn;
+                } else {
+                  l[r] *= al;
+                }
 #pragma unroll
                 for (int j = 0; j < NO; ++j) {
                   o[j][2 * r] *= al;
@@ -411,13 +419,18 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                const float mr = m[r] == -INFINITY ? 0.f : m[r];
+                const float mr = m[r] == -INFINITY ? 0.f : m[r] - ev;
                 const float p0 = ex2(sc[nt][2 * r] - mr), p1 = ex2(sc[nt][2 * r + 1] - mr);
-                sum[r] += p0 + p1;
                 pa[nt * 2 + r] = Q8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+                if constexpr (Q8) {
+                  const float nr = n[r] == -INFINITY ? 0.f : n[r];
+                  sum[r] += ex2(sc[nt][2 * r] - nr) + ex2(sc[nt][2 * r + 1] - nr);
+                } else {
+                  sum[r] += p0 + p1;
+                }
               }
-            l[0] = fmaf(sum[0], back, l[0]);
-            l[1] = fmaf(sum[1], back, l[1]);
+            l[0] += sum[0];
+            l[1] += sum[1];
             // ---- V: tokens w0 + {2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4}, the
             // dims of this thread's chunks; rows that the query does not see
             // (they may hold anything) as zeros
@@ -496,10 +509,12 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
         break;
       }
       if (t4 == 0) {
-        sm_m[warp][g4] = m[0];
-        sm_l[warp][g4] = l[0];
-        sm_m[warp][g4 + 8] = m[1];
-        sm_l[warp][g4 + 8] = l[1];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          sm_m[warp][g4 + 8 * r] = m[r];
+          sm_n[warp][g4 + 8 * r] = Q8 ? n[r] : m[r];
+          sm_l[warp][g4 + 8 * r] = l[r];
+        }
       }
       // fragment order: columns 2 t4, 2 t4 + 1 of n-tile j side by side
 #pragma unroll
@@ -514,20 +529,22 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
       const int64_t slot = 2 * blockIdx.x + (step == u.first);
       for (int e = threadIdx.x; e < hpg * NO * 4; e += kConsumers) {
         const int h = e / (NO * 4), j = e / 4 % NO;        // one head per warp and step
-        float M = -INFINITY;
+        float M = -INFINITY, N = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, sm_m[w][h]);
+        for (int w = 0; w < kConsWarps; ++w) {
+          M = fmaxf(M, sm_m[w][h]);
+          N = fmaxf(N, sm_n[w][h]);
+        }
         float L = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
         for (int w = 0; w < kConsWarps; ++w) {
           const float mw = sm_m[w][h];
           const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
           const float2 v = lds_f2(red + ((w * hpg + h) * C::kRedRow + (e % (NO * 4)) * 2) * 4);
-          if (f != 0.f) {
-            L = fmaf(sm_l[w][h], f, L);
-            x = fmaf(v.x, f, x);
-            y = fmaf(v.y, f, y);
-          }
+          const float nw = sm_n[w][h];
+          L = fmaf(sm_l[w][h], nw == -INFINITY ? 0.f : ex2(nw - N), L);
+          x = fmaf(v.x, f, x);
+          y = fmaf(v.y, f, y);
         }
         // dims j, j + 1 of one column: the lane of the other j holds the pair's other half
         const bool odd = j & 1;
@@ -536,12 +553,12 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
         const int n = 2 * (e & 3) + odd, je = j & ~1;
         const int dim = Q8 ? n * (D / 8) + je : (je >> 3) * 64 + n * 8 + (je & 7);
         if (whole_unit) {
-          const float inv = L == 0.f ? 0.f : 1.f / L;      // nothing visible: zeros
+          const float inv = L == 0.f ? 0.f : ex2(M - N) / L;      // nothing visible: zeros
           uint16_t* dst = a.out + (((int64_t)u.b * s.T + u.i) * H + (int64_t)u.g * hpg + h) * D + dim;
           *reinterpret_cast<uint32_t*>(dst) = pack_bf16(d0 * inv, d1 * inv);
         } else {
           *reinterpret_cast<float2*>(a.part_o + (slot * hpg + h) * D + dim) = make_float2(d0, d1);
-          if (e % (NO * 4) == 0) a.part_ml[slot * hpg + h] = make_float2(M, L);
+          if (e % (NO * 4) == 0) a.part_ml[slot * hpg + h] = make_float4(M, N, L, 0.f);
         }
       }
     }
@@ -581,28 +598,33 @@ __global__ void __launch_bounds__(256) stream_finish_kernel(const __grid_constan
   if (begin == u.first || run != r0 + 1) return;
   const int r1 = run_of(steps, a.nctas, u.first + u.len - 1);
   // run r0 ends inside the unit (its slot 1), runs r0 + 1 ... r1 begin inside it (slot 0)
-  float M = -INFINITY;
-  for (int r = r0 + lane; r <= r1; r += 32)
-    M = fmaxf(M, a.part_ml[(int64_t)(2 * r + (r == r0)) * hpg + h].x);
+  float M = -INFINITY, N = -INFINITY;
+  for (int r = r0 + lane; r <= r1; r += 32) {
+    const float4 v = a.part_ml[(int64_t)(2 * r + (r == r0)) * hpg + h];
+    M = fmaxf(M, v.x);
+    N = fmaxf(N, v.y);
+  }
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  for (int x = 16; x > 0; x >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    N = fmaxf(N, __shfl_xor_sync(0xffffffffu, N, x));
+  }
   float L = 0.f, acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
 #pragma unroll 4
   for (int r = r0; r <= r1; ++r) {
     const int64_t p = (int64_t)(2 * r + (r == r0)) * hpg + h;
-    const float2 v = a.part_ml[p];
+    const float4 v = a.part_ml[p];
     const float w = v.x == -INFINITY ? 0.f : ex2(v.x - M);
     float x[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) x[e] = a.part_o[p * D + lane * PER + e];
-    if (w == 0.f) continue;
-    L = fmaf(w, v.y, L);
+    L = fmaf(v.y == -INFINITY ? 0.f : ex2(v.y - N), v.z, L);
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, x[e], acc[e]);
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const float inv = L == 0.f ? 0.f : ex2(M - N) / L;
   uint16_t* dst =
       a.out + (((int64_t)u.b * s.T + u.i) * s.H + (int64_t)u.g * hpg + h) * D + lane * PER;
 #pragma unroll
@@ -678,7 +700,7 @@ StreamPlan stream_plan(const Shape& s) {
   const size_t rows = (size_t)2 * kMaxCtas * (s.H / s.G);
   size_t o = 0;
   p.errs_off = o;     o += al(kMaxCtas * sizeof(int));
-  p.part_ml_off = o;  o += al(rows * sizeof(float2));
+  p.part_ml_off = o;  o += al(rows * sizeof(float4));
   p.part_o_off = o;   o += al(rows * s.D * sizeof(float));
   p.total = o;
   return p;
@@ -700,7 +722,7 @@ cudaError_t launch_stream_attn(const Shape& s, const Positions& pos, const Cache
   a.k_exp = c.k_exp;
   a.v_exp = c.v_exp;
   a.part_o = reinterpret_cast<float*>(base + pl.part_o_off);
-  a.part_ml = reinterpret_cast<float2*>(base + pl.part_ml_off);
+  a.part_ml = reinterpret_cast<float4*>(base + pl.part_ml_off);
   a.errs = reinterpret_cast<int*>(base + pl.errs_off);
   a.out = out;
   a.status = status;

@@ -253,6 +253,30 @@ def test_sparse_q8_spread_exponents_and_negative_scale(msa, kernels):
         sr.check(out, want, bound)
 
 
+@pytest.mark.parametrize("kernels", KERNELS)
+@pytest.mark.parametrize("zero", ["first", "last", "most"])
+def test_sparse_q8_blocks_of_zeros_keep_their_weight(msa, kernels, zero):
+    # a block of zero values is stored with the smallest exponent; its weights
+    # count in full beside blocks of ordinary (and of large) values
+    lens, T, H, G, D = [1900, 700], 3, 12, 2, 128
+    c = Cache(lens, G, D, 15, seed=27)
+    page = c.table[0].long()
+    pick = {"first": page[:1], "last": page[14:15], "most": page[1:14]}[zero]
+    c.codes[1][pick] = c.codes[1][pick] & 0x7F
+    c.codes[1][pick] = torch.where(c.codes[1][pick] == 0x7F, c.codes[1][pick], 0)
+    c.exps[1][pick] = -126
+    c.exps[1][page[3]] = 90
+    q = torch.randn(2, T, H, D, device="cuda").to(torch.bfloat16)
+    q_start = [n - T for n in lens]
+    sel = random_sel(2, T, G, q_start, 28)
+    k, v = c.values()
+    for scale in (0.01, 0.5):
+        out = run_sparse(msa, c, q, sel, q_start, lens, 15, 32, kernels, scale=scale)
+        want, bound = sr.attend_call(q, k, v, q_start, sr.sel_seen(sel, 15 * 128, "cuda"), scale,
+                                     2 * sr.U_BF16)
+        sr.check(out, want, bound)
+
+
 @pytest.mark.parametrize("e", [-128, -126, 119, 127])
 def test_exponents_outside_the_range_read_as_its_ends(msa, e):
     lens, H, G, D = [300], 4, 2, 64

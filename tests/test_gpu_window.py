@@ -61,8 +61,8 @@ def run(msa, c, q8, q, q_start, kv_len, nb, window, sinks, kernels, scale=None, 
 
 
 def u_of(q8, kernels):
-    # weights round to f16 in the streaming kernel of an 8-bit cache, else to bf16
-    return sr.U_F16 if q8 and kernels == "streaming" else sr.U_BF16
+    # weights round to f16 beside an 8-bit cache, to bf16 beside a bf16 one
+    return sr.U_F16 if q8 else sr.U_BF16
 
 
 def make(lens, T, H, G, D, seed, extra=0, nb=None):
@@ -151,6 +151,24 @@ def test_window_q8_spread_exponents(msa, kernels):
     want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, 700, 9, "cuda"),
                                  64 ** -0.5, u_of(True, kernels))
     sr.check(out, want, bound)
+
+
+@pytest.mark.parametrize("kernels", KERNELS)
+@pytest.mark.parametrize("T", [1, 140])
+def test_window_q8_blocks_of_zeros_keep_their_weight(msa, kernels, T):
+    c, q, q_start = make([1100], T, 12, 2, 128, seed=87)
+    nb = c.table.shape[1]
+    for i in (0, 5, 8):
+        page = c.table[0, i].long()
+        c.codes[1][page] = torch.where(c.codes[1][page] == 0x7F, c.codes[1][page], 0)
+        c.exps[1][page] = -126
+    c.exps[1][c.table[0, 6].long()] = 60
+    for scale in (0.01, 0.3):
+        out = run(msa, c, True, q, q_start, [1100], nb, 800, 9, kernels, scale=scale)
+        k, v = c.values()
+        want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, 800, 9, "cuda"),
+                                     scale, u_of(True, kernels))
+        sr.check(out, want, bound)
 
 
 @pytest.mark.parametrize("q8", [False, True])
