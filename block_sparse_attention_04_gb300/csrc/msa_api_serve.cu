@@ -5,6 +5,7 @@
 
 #include "msa_pages.h"
 #include "msa_serve.h"
+#include "msa_tc.h"
 
 namespace msa {
 namespace {
@@ -30,12 +31,15 @@ int check_call(const msa_params* p, const int32_t* block_table, int num_pool_blo
 }
 
 // Workspace of the attention calls: the status word, then their scratch.
-size_t attn_scratch(const msa_params* p) { return align_up(stream_plan(shape_of(p)).total); }
+size_t stream_scratch(const msa_params* p) { return align_up(stream_plan(shape_of(p)).total); }
+size_t sparse_scratch(const msa_params* p) {
+  return prefill_sized(p) ? align_up(tc_attn_workspace_bytes(shape_of(p))) : stream_scratch(p);
+}
 
 // ... of an 8-bit call: msa_forward's index scratch follows msa_workspace_bytes'
 // own layout in the same bytes (the steps run in order), then the selection.
 size_t q8_sel_off(const msa_params* p) {
-  const size_t idx = msa_workspace_bytes(p), att = kAlign + attn_scratch(p);
+  const size_t idx = msa_workspace_bytes(p), att = kAlign + sparse_scratch(p);
   return align_up(idx > att ? idx : att);
 }
 
@@ -43,6 +47,11 @@ int run_attn_q8(const msa_params* p, const Shape& s, const Positions& pos, const
                 const CacheView& c, const int32_t* sel, uint16_t* out, bool join_status, void* ws,
                 cudaStream_t st) {
   char* base = static_cast<char*>(ws);
+  if (prefill_sized(p)) {
+    if (!join_status && cudaMemsetAsync(ws, 0, sizeof(int), st) != cudaSuccess) return MSA_ERR_CUDA;
+    return cuda_status(launch_attn_tc_q8(s, pos, q, c, sel, out, reinterpret_cast<int*>(base),
+                                         base + kAlign, st));
+  }
   return cuda_status(launch_stream_attn(s, pos, c, Visible{sel, 0, 0}, q, out,
                                         reinterpret_cast<int*>(base), join_status, base + kAlign, st));
 }
@@ -199,7 +208,7 @@ int msa_forward_q8(const msa_params* p, const int32_t* block_table, int num_pool
 
 size_t msa_window_workspace_bytes(const msa_params* p) {
   if (validate_params(p) != MSA_OK) return 0;
-  return kAlign + attn_scratch(p);
+  return kAlign + stream_scratch(p);
 }
 
 int msa_window_attn(const msa_params* p, const int32_t* block_table, int num_pool_blocks,

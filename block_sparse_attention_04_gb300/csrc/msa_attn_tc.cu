@@ -23,9 +23,15 @@
 //   warps 11-18   O as an unnormalised bf16 partial, one warpgroup per chain
 // Each (query, head, slot) partial (O, m, l) is combined by a log-sum-exp
 // merge into the bf16 output.
+//
+// An 8-bit cache (kernels with Q8 set) has four more warps in place of warp 1:
+// they read a list's codes, convert them to bf16 (exact) and write them into
+// the same rings.  A tile has one KV block, so its exponents are two numbers:
+// 2^ek scales the scores, 2^ev the partial O; both travel in the tile's
+// descriptor.  Rows of V behind the call's last query are zeroed on the way.
 #include <climits>
 
-#include "msa_device.cuh"
+#include "msa_q8.cuh"
 #include "msa_tc.h"
 #include "msa_tma.h"
 
@@ -35,6 +41,9 @@ namespace {
 // warps: Q TMA, K/V TMA, MMA, 2 softmax warpgroups, 2 O-epilogue warpgroups
 constexpr int kQWarp = 0, kKVWarp = 1, kMmaWarp = 2, kSoftWarp0 = 3, kEpiWarp0 = 11;
 constexpr int kAttnThreads = 32 * 19;
+constexpr int kConvWarp0 = 19, kConv = 128;  // converters of an 8-bit cache
+template <bool Q8>
+constexpr int attn_threads() { return kAttnThreads + (Q8 ? kConv : 0); }
 constexpr int kPassRows = 8192;    // (sequence, query) rows per pass
 
 struct AttnPass {
@@ -50,11 +59,16 @@ struct AttnPass {
   int32_t* off;          // [nlists + 1]   entry offsets
   int32_t* tile_off;     // [nlists + 1]   tile offsets; tile_off[nlists] = total
   int32_t* entries;      // packed (i - t0) * 16 + slot
-  int4* tile_desc;       // per tile: list, first entry, entries, kb | g << 15 | b << 18
+  int4* tile_desc;       // per tile: list, first entry, entries (| (ek + 128) << 8 |
+                         // (ev + 128) << 16 for an 8-bit cache), kb | g << 15 | b << 18
   uint16_t* part_o;      // [B*Tp*H*16][D] bf16, O = sum 2^(s-m) v (unnormalised)
   float2* part_ml;       // [B*Tp*H*16] (m in log2 units, l)
   int* status;
   uint32_t wait_polls;   // poll cap of the pipeline waits (0: wall-clock bound only)
+  const uint8_t* k8;     // an 8-bit cache's codes and exponents (null: bf16 cache)
+  const uint8_t* v8;
+  const int8_t* k_exp;
+  const int8_t* v_exp;
 };
 
 // Lists are ordered group-major, list (b, kb, g) at index (g*B + b)*nbl + kb:
@@ -242,9 +256,18 @@ __global__ void __launch_bounds__(kCsrThreads) csr_fill_kernel(AttnPass a, int s
     if (t0 == t1) continue;
     const int kb = (lo + k) % a.nbl, b = (lo + k) / a.nbl;
     const int cnt = a.count[L], o = a.off[L];
+    int exps = 0;
+    if (a.k_exp) {
+      // a table entry outside the pool is flagged where its block is read
+      const int64_t pb = cache_block(a.s, b, kb, nullptr);
+      const int ek = pb < 0 ? 0 : clamp_exp(a.k_exp[pb * a.s.G + g]);
+      const int ev = pb < 0 ? 0 : clamp_exp(a.v_exp[pb * a.s.G + g]);
+      exps = (ek + 128) << 8 | (ev + 128) << 16;
+    }
     for (int t = t0; t < t1; ++t) {
       const int e0 = (t - t0) * a.R;
-      a.tile_desc[t] = make_int4((int)L, o + e0, min(a.R, cnt - e0), kb | (g << 15) | (b << 18));
+      a.tile_desc[t] =
+          make_int4((int)L, o + e0, min(a.R, cnt - e0) | exps, kb | (g << 15) | (b << 18));
     }
   }
 }
@@ -275,8 +298,8 @@ struct AttnCfg {
   static constexpr uint32_t kTmemCols = 512;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+template <int D, bool Q8>
+__global__ void __launch_bounds__(attn_threads<Q8>(), 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const AttnPass a) {
   using C = AttnCfg<D>;
@@ -307,9 +330,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < kKVStages; ++i) {
-      mbar_init(&k_full[i], 1);
+      mbar_init(&k_full[i], Q8 ? kConv : 1);
       mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
+      mbar_init(&v_full[i], Q8 ? kConv : 1);
       mbar_init(&v_empty[i], 1);
     }
     for (int c = 0; c < 2; ++c) {
@@ -322,8 +345,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
+    if constexpr (!Q8) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
   }
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, C::kTmemCols);
   tc_fence_before();
@@ -367,7 +392,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int t = 0; t < n; ++t) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // warp-uniform
       const int4 d = desc[t];
-      const int ne = d.z;
+      const int ne = d.z & 0xFF;
       int qrow = 0;
       if (box_e < ne) {
         const int il = a.entries[d.y + box_e] >> 4;
@@ -400,7 +425,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // One K and one V block per list change, through a kKVStages ring; a
     // buffer is refilled once the last tile of its previous list is through
     // S (K) or P.V (V).  L2 policy: evict first (used once, from smem).
-    if (lane == 0) {
+    if (!Q8 && lane == 0) {
       const uint64_t pol_kv = l2_policy_evict_first();
       int kv = -1, prev = -1;
       int k_last[kKVStages], v_last[kKVStages];   // last list loaded into each slot
@@ -539,13 +564,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int quad = warp & 3;
     const int r = quad * 32 + lane;  // tile row = TMEM lane
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + c * 128;
-    const float sl = a.s.scale * kLog2e;
+    float sl = a.s.scale * kLog2e;
     for (int t = c; t < n; t += 2) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // warp-uniform
       const int4 d = desc[t];
       const int kb = d.w & 0x7FFF, g = (d.w >> 15) & 7, b = d.w >> 18;
       const int e = r >> rshift, hh = r & (a.rpe - 1);
-      const bool valid = e < d.z && hh < hpg;
+      const bool valid = e < (d.z & 0xFF) && hh < hpg;
+      if constexpr (Q8) {
+        sl = a.s.scale * kLog2e * pow2i((d.z >> 8 & 0xFF) - 128);
+        sl = fminf(fmaxf(sl, -3e38f), 3e38f);
+      }
       int il = 0, slot = 0;
       if (valid) {
         const int en = a.entries[d.y + e];
@@ -637,7 +666,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __stcs(a.part_ml + prow, make_float2(m, l0 + l1));
       }
     }
-  } else {
+  } else if (!Q8 || warp < kConvWarp0) {
     // ------------------------------------ O epilogue (2 warpgroups, one per chain)
     // O = P.V (unnormalised) as a bf16 partial; the merge divides by the
     // combined sum.
@@ -650,7 +679,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int4 d = desc[t];
       const int g = (d.w >> 15) & 7, b = d.w >> 18;
       const int e = r >> rshift, hh = r & (a.rpe - 1);
-      const bool valid = e < d.z && hh < hpg;
+      const bool valid = e < (d.z & 0xFF) && hh < hpg;
+      const float fo = Q8 ? pow2i((d.z >> 16 & 0xFF) - 128) : 1.f;
       size_t prow = 0;
       if (valid) {
         const int en = a.entries[d.y + e];
@@ -667,6 +697,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         uint32_t h[16];
         tmem_ld16(lane_base + cc * 16, h);
         tmem_ld_wait();
+        if constexpr (Q8) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) h[k] = __float_as_uint(__uint_as_float(h[k]) * fo);
+        }
         if (valid) {
 #pragma unroll
           for (int e8 = 0; e8 < 2; ++e8) {
@@ -682,6 +716,71 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tc_fence_before();
       mbar_arrive(&o_empty[c]);
     }
+  } else if constexpr (Q8) {
+    // -------------------------------- converters (four warps, 8-bit cache)
+    // One K and one V block per list change, as the K/V warp of a bf16 cache.
+    // Each warp looks at 32 descriptors at a time for the lists that begin.
+    const int tid = threadIdx.x - kConvWarp0 * 32;
+    constexpr int NL = D / 16;               // 16-byte chunks of codes per thread and block
+    // chunk u of this thread: row tid / 4 + 32 (u % 4), chunk 4 (u / 4) + tid % 4
+    const int row0 = tid >> 2, c4 = tid & 3;
+    const int64_t pitch = (int64_t)a.s.G * D;
+    uint4 reg[NL];
+    auto load = [&](const uint8_t* base, int64_t off) {
+#pragma unroll
+      for (int u = 0; u < NL; ++u)
+        reg[u] = off < 0 ? make_uint4(0, 0, 0, 0)
+                         : __ldg(reinterpret_cast<const uint4*>(
+                               base + off + (row0 + 32 * (u & 3)) * pitch + (4 * (u >> 2) + c4) * 16));
+    };
+    auto store = [&](uint32_t tile, int last) {   // rows behind `last` as zeros
+#pragma unroll
+      for (int u = 0; u < NL; ++u) {
+        const int row = row0 + 32 * (u & 3), ch = 4 * (u >> 2) + c4;
+        const uint32_t w[4] = {reg[u].x, reg[u].y, reg[u].z, reg[u].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h[2 * j] = row > last ? 0u : e4m3x2_to_bf16x2(w[j] & 0xFFFFu);
+          h[2 * j + 1] = row > last ? 0u : e4m3x2_to_bf16x2(w[j] >> 16);
+        }
+        sts128(tile + tile_off(row, 2 * ch), make_uint4(h[0], h[1], h[2], h[3]));
+        sts128(tile + tile_off(row, 2 * ch + 1), make_uint4(h[4], h[5], h[6], h[7]));
+      }
+    };
+    int kv = -1, prev = -1;
+    bool ok = true;
+    for (int t0 = 0; t0 < n && ok; t0 += 32) {
+      const bool in = t0 + lane < n;
+      const int4 d = in ? desc[t0 + lane] : make_int4(-1, 0, 0, 0);
+      int before = __shfl_up_sync(0xffffffffu, d.x, 1);
+      if (lane == 0) before = prev;
+      prev = __shfl_sync(0xffffffffu, d.x, min(31, n - 1 - t0));
+      for (uint32_t m = __ballot_sync(0xffffffffu, in && d.x != before); m != 0; m &= m - 1) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const int w = __shfl_sync(0xffffffffu, d.w, __ffs(m) - 1);
+        const int kb = w & 0x7FFF, g = (w >> 15) & 7, b = w >> 18;
+        const int64_t pb = cache_block(a.s, b, kb, a.status);
+        const int64_t off = pb < 0 ? -1 : (pb * kBlock * a.s.G + g) * D;
+        ++kv;
+        const int ks = kv % kKVStages;
+        const uint32_t par = ((uint32_t)(kv / kKVStages) & 1) ^ 1;
+        load(a.k8, off);
+        ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[ks], par, a.status, a.wait_polls));
+        if (!ok) break;
+        store(smem_u32(sK + ks * C::kSmemK), kBlock);
+        fence_async();
+        mbar_arrive(&k_full[ks]);
+        load(a.v8, off);
+        ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[ks], par, a.status, a.wait_polls));
+        if (!ok) break;
+        const int64_t last = (int64_t)a.pos.q_start[b] + a.s.T - 1 - (int64_t)kb * kBlock;
+        store(smem_u32(sV + ks * C::kSmemK), last < kBlock ? (int)last : kBlock);
+        fence_async();
+        mbar_arrive(&v_full[ks]);
+      }
+    }
+    if (!ok) *abort_flag = 1;
   }
 
   tc_fence_before();
@@ -743,7 +842,8 @@ __global__ void __launch_bounds__(256) attn_tc_merge_kernel(AttnPass a, uint16_t
     }
   }
   uint16_t* dst = out + (((size_t)b * a.s.T + i) * H + h) * D + lane * PER;
-  const float inv = 1.f / W;
+  // a selection without a visible token: zeros (8-bit calls)
+  const float inv = a.k_exp && W == 0.f ? 0.f : 1.f / W;
 #pragma unroll
   for (int e = 0; e < PER; e += 2)
     *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
@@ -772,10 +872,10 @@ AttnLayout attn_layout(const Shape& s) {
   return L;
 }
 
-template <int D>
+template <int D, bool Q8>
 cudaError_t launch_attn_tc_impl(const Shape& s, const Positions& pos, const uint16_t* q,
-                                const uint16_t* k, const uint16_t* v, const int32_t* sel,
-                                uint16_t* out, const Workspace& ws, cudaStream_t st) {
+                                const CacheView& cv, const int32_t* sel, uint16_t* out,
+                                const Workspace& ws, cudaStream_t st) {
   using C = AttnCfg<D>;
   const AttnLayout lay = attn_layout(s);
   char* base = ws.tc_base;
@@ -791,19 +891,21 @@ cudaError_t launch_attn_tc_impl(const Shape& s, const Positions& pos, const uint
     if (!encode_bf16_map(&tm_q, q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
-  {
+  if constexpr (Q8) {
+    tm_k = tm_v = tm_q;   // not used
+  } else {
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)s.G, (cuuint64_t)(s.cache_blocks() * kBlock)};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)s.G * D * 2};
     cuuint32_t box[3] = {64, 1, (cuuint32_t)kBlock};
-    if (!encode_bf16_map(&tm_k, k, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_bf16_map(&tm_v, v, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_bf16_map(&tm_k, cv.k, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_bf16_map(&tm_v, cv.v, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D>,
+  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, Q8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   // one CTA per SM: all 512 TMEM columns and ~225 KiB of shared memory
-  cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  cudaFuncSetAttribute(attn_tc_kernel<D, Q8>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if ((e = cudaFuncSetAttribute(csr_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kCsrMaxLists * 4)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(csr_fill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -832,6 +934,10 @@ cudaError_t launch_attn_tc_impl(const Shape& s, const Positions& pos, const uint
     a.part_ml = reinterpret_cast<float2*>(base + lay.pml_off);
     a.status = ws.status;
     a.wait_polls = debug_wait_polls();
+    a.k8 = Q8 ? static_cast<const uint8_t*>(cv.k) : nullptr;
+    a.v8 = Q8 ? static_cast<const uint8_t*>(cv.v) : nullptr;
+    a.k_exp = cv.k_exp;
+    a.v_exp = cv.v_exp;
     const CsrGrid cg = csr_grid(s, a.nbl);
     const unsigned csr_ctas = (unsigned)(s.G * cg.per_group);
     const size_t csr_smem = (size_t)cg.span * 4;
@@ -839,7 +945,7 @@ cudaError_t launch_attn_tc_impl(const Shape& s, const Positions& pos, const uint
     csr_count_kernel<<<csr_ctas, kCsrThreads, csr_smem, st>>>(a, cg.span, cg.per_group);
     csr_scan_kernel<<<1, 1024, 0, st>>>(a);
     csr_fill_kernel<<<csr_ctas, kCsrThreads, csr_smem, st>>>(a, cg.span, cg.per_group);
-    attn_tc_kernel<D><<<grid, kAttnThreads, C::kSmem, st>>>(tm_q, tm_k, tm_v, a);
+    attn_tc_kernel<D, Q8><<<grid, attn_threads<Q8>(), C::kSmem, st>>>(tm_q, tm_k, tm_v, a);
     const int64_t warps = (int64_t)s.B * a.Tp * s.H;
     note_launches(1);
     attn_tc_merge_kernel<D><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a, out);
@@ -861,8 +967,19 @@ size_t tc_attn_workspace_bytes(const Shape& s) { return attn_layout(s).total; }
 cudaError_t launch_attn_tc(const Shape& s, const Positions& pos, const uint16_t* q,
                            const uint16_t* k, const uint16_t* v, const int32_t* sel,
                            uint16_t* out, const Workspace& ws, cudaStream_t st) {
-  if (s.D == 128) return launch_attn_tc_impl<128>(s, pos, q, k, v, sel, out, ws, st);
-  return launch_attn_tc_impl<64>(s, pos, q, k, v, sel, out, ws, st);
+  const CacheView cv{k, v, nullptr, nullptr, false};
+  if (s.D == 128) return launch_attn_tc_impl<128, false>(s, pos, q, cv, sel, out, ws, st);
+  return launch_attn_tc_impl<64, false>(s, pos, q, cv, sel, out, ws, st);
+}
+
+cudaError_t launch_attn_tc_q8(const Shape& s, const Positions& pos, const uint16_t* q,
+                              const CacheView& cv, const int32_t* sel, uint16_t* out, int* status,
+                              char* base, cudaStream_t st) {
+  Workspace ws{};
+  ws.status = status;
+  ws.tc_base = base;
+  if (s.D == 128) return launch_attn_tc_impl<128, true>(s, pos, q, cv, sel, out, ws, st);
+  return launch_attn_tc_impl<64, true>(s, pos, q, cv, sel, out, ws, st);
 }
 
 }  // namespace msa

@@ -39,6 +39,12 @@ cudaError_t launch_stream_attn(const Shape& s, const Positions& pos, const Cache
                                const Visible& vis, const uint16_t* q, uint16_t* out, int* status,
                                bool join_status, char* base, cudaStream_t st);
 
+// Step 4 of an 8-bit call on tensor cores (prefill shapes).  base: scratch of
+// tc_attn_workspace_bytes(s) bytes; *status is cleared by the caller.
+cudaError_t launch_attn_tc_q8(const Shape& s, const Positions& pos, const uint16_t* q,
+                              const CacheView& c, const int32_t* sel, uint16_t* out, int* status,
+                              char* base, cudaStream_t st);
+
 // Sliding-window attention of every query of the call on tensor cores
 // (prefill shapes).  status: the status word and the word after it.
 cudaError_t launch_window_tc(const Shape& s, const Positions& pos, const CacheView& c, int window,

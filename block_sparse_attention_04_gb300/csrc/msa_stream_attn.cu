@@ -16,16 +16,16 @@
 // unit, cut into equal runs, one per CTA and SM; a run's share of one unit is a
 // segment.  Warp 8 copies K and V of each block (128 tokens of one KV head)
 // into a ring of stages by TMA and runs ahead by its depth.  Warps 0-7 take 16
-// tokens of every block each and never wait for one another inside a segment: S = Q K^T with mma.sync m16n8k16 (rows: the
-// group's heads), softmax in registers, P straight from the accumulator
-// layout into the A operand of O += P V.  The order of the contraction's
-// terms is free, so dims (for S) and output columns (for O) are dealt to
-// threads such that every thread reads whole 16-byte chunks of the swizzled
-// rows; pairs of tokens of V are put together with byte permutes.  e4m3 codes
-// become f16 (exact) by one conversion per pair; Q is scaled by a power of two
-// per row to fit f16 (exact but for elements 2^-27 below the row's maximum,
-// which round at 2^-38 of it), and P rounds to f16 (2^-11).  With a bf16 cache
-// the products are bf16 and P rounds to bf16 (2^-8).
+// tokens of every block each and never wait for one another inside a segment:
+// S^T = K Q^T (tokens x heads) with mma.sync m16n8k16, softmax in registers,
+// P^T transposed inside the warp into the B operand of O^T += V^T P^T.  The
+// order of the contraction's terms is free, so dims are dealt to threads such
+// that every thread reads whole 16-byte chunks of the swizzled rows; pairs of
+// tokens of V are put together with byte permutes.  e4m3 codes of K become f16
+// (exact), Q is scaled by a power of two per row to fit f16 (exact but for
+// elements 2^-27 below the row's maximum, which round at 2^-38 of it).  Codes
+// of V become bf16 (exact), like P (2^-8): the largest p' may belong to values
+// that cancel or vanish, so the others need bf16's range.
 // At a segment's end the eight warps' (O, m, l) are joined in shared memory; a
 // whole unit is written out directly, a cut one leaves a partial per CTA (at
 // most two: the unit its run begins inside, the one it ends inside) that
@@ -112,16 +112,16 @@ template <int D, bool Q8>
 struct Cfg {
   static constexpr int kTile = kBlock * D * (Q8 ? 1 : 2);   // K (or V) of one block and head
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kRedRow = D + 8;                     // padded row of the join buffer (floats)
+  static constexpr int kRedRow = D + 4;                     // padded row of the join buffer (floats)
 };
 
-template <int D, bool Q8>
+template <int D, bool Q8, int NTH>
 __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ StreamArgs a) {
   using C = Cfg<D, Q8>;
   constexpr int NS = D / 16;       // k-steps of S
-  constexpr int NO = D / 8;        // n-tiles of O
+  constexpr int MT = D / 16;       // m-tiles of O^T
   extern __shared__ uint8_t dsm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
     __syncwarp();
   } else {
     // ----------------------------------------------------------- consumers
-    const int g4 = lane >> 2, t4 = lane & 3;   // row (head or token) and column quad of a fragment
+    // S^T = K Q^T (tokens x heads) and O^T += V^T P^T (dims x heads)
+    const int g4 = lane >> 2, t4 = lane & 3;   // row group and column pair of a fragment
     const float qk = s.scale * kLog2e;
     int st = 0, k = 0;
     uint32_t ph = 0;
@@ -263,15 +264,14 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
       const int qs = k % kQBufs;
       ok = __all_sync(0xffffffffu,
                       ok && mbar_wait(&q_full[qs], (k / kQBufs) & 1, &err, a.wait_polls));
-      // Q fragments: rows g4 and g4 + 8, the four dims per k-step that this
+      // Q^T fragments: head nt * 8 + g4, per k-step the four dims that this
       // thread's 16-byte chunks of a K row hold (see the reads of K below)
-      uint32_t qa[NS][4];
-      float fq[2] = {qk, qk};          // score factor of the two rows
+      uint32_t qb[NTH][NS][2];
+      float fq[NTH][2];                // score factors of heads nt * 8 + 2 t4 + {0, 1}
 #pragma unroll
-      for (int rr = 0; rr < 2; ++rr) {
-        const int h = g4 + 8 * rr;
+      for (int nt = 0; nt < NTH; ++nt) {
+        const int h = nt * 8 + g4;
         const uint32_t qrow = smem_u32(qbuf + (qs * hpg + min(h, hpg - 1)) * D);
-        uint2 w[NS];
 #pragma unroll
         for (int ks = 0; ks < NS; ++ks) {
           int dim;
@@ -279,42 +279,52 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
             dim = D == 128 ? (2 * t4 + (ks >> 2)) * 16 + (ks & 3) * 4 : t4 * 16 + ks * 4;
           else
             dim = (ks >> 2) * 64 + (2 * t4 + ((ks >> 1) & 1)) * 8 + (ks & 1) * 4;
-          w[ks] = h < hpg && ok ? lds64(qrow + dim * 2) : make_uint2(0, 0);
+          const uint2 w = h < hpg && ok ? lds64(qrow + dim * 2) : make_uint2(0, 0);
+          qb[nt][ks][0] = w.x;
+          qb[nt][ks][1] = w.y;
         }
+        float f = qk;
         if constexpr (Q8) {
           // scale the row by a power of two: its largest magnitude to [2^13, 2^14)
           uint32_t mx = 0;
 #pragma unroll
-          for (int ks = 0; ks < NS; ++ks) {
-            mx = max(max(mx, w[ks].x & 0x7FFFu), max(w[ks].x >> 16 & 0x7FFFu, w[ks].y & 0x7FFFu));
-            mx = max(mx, w[ks].y >> 16 & 0x7FFFu);
-          }
+          for (int ks = 0; ks < NS; ++ks)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              mx = max(max(mx, qb[nt][ks][x] & 0x7FFFu), qb[nt][ks][x] >> 16 & 0x7FFFu);
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           int e = (int)(mx >> 7) - 127;                   // floor(log2 max); inf, NaN: 128
           e = mx == 0 || e == 128 ? 0 : max(e, -100);
-          const float f = pow2i(13 - e);
-          fq[rr] = qk * pow2i(e - 13);
+          const float up = pow2i(13 - e);
+          f = qk * pow2i(e - 13);
 #pragma unroll
-          for (int ks = 0; ks < NS; ++ks) {
-            qa[ks][rr] = pack_f16(bf16lo(w[ks].x) * f, bf16hi(w[ks].x) * f);
-            qa[ks][2 + rr] = pack_f16(bf16lo(w[ks].y) * f, bf16hi(w[ks].y) * f);
-          }
-        } else {
+          for (int ks = 0; ks < NS; ++ks)
 #pragma unroll
-          for (int ks = 0; ks < NS; ++ks) {
-            qa[ks][rr] = w[ks].x;
-            qa[ks][2 + rr] = w[ks].y;
-          }
+            for (int x = 0; x < 2; ++x)
+              qb[nt][ks][x] = pack_f16(bf16lo(qb[nt][ks][x]) * up, bf16hi(qb[nt][ks][x]) * up);
         }
+        fq[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t4);       // a lane of head 2 t4
+        fq[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
       }
-      float o[NO][4];
+      // O^T: rows (dims) 2j and 2j + 1 of this thread's chunk of V, heads 2 t4 + {0, 1}
+      float o[NTH][MT][4];
 #pragma unroll
-      for (int j = 0; j < NO; ++j)
+      for (int nt = 0; nt < NTH; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
-      // running maxima of x + ev (of O's terms) and x (of l's; the same without ev)
-      float m[2] = {-INFINITY, -INFINITY}, n[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[nt][j][c] = 0.f;
+      // per head, the same in all lanes of a column: running maxima of x + ev
+      // (of O's terms) and x (of l's; the same without ev); l: this thread's tokens
+      float m[NTH][2], n[NTH][2], l[NTH][2];
+#pragma unroll
+      for (int nt = 0; nt < NTH; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m[nt][e] = n[nt][e] = -INFINITY;
+          l[nt][e] = 0.f;
+        }
 
       for (int blk = 0; blk < nblk; ++blk) {
         ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[st], ph, &err, a.wait_polls));
@@ -327,123 +337,134 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
           const bool any = w0 <= u.t && (w0 + 15 >= lo || w0 < sinks);
           if (any) {
             const uint32_t kbase = smem_u32(sm + st * C::kStage), vbase = kbase + C::kTile;
-            // ---- S = Q K^T of 16 tokens (two n-tiles of 8)
-            float sc[2][4];
+            // ---- S^T of 16 tokens: rows g4 and g4 + 8
+            const int r0 = warp * 16 + g4;                // r0 & 7 == (r0 + 8) & 7
+            float sc[NTH][4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const int r = warp * 16 + nt * 8 + g4;
+            for (int nt = 0; nt < NTH; ++nt)
 #pragma unroll
               for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
-              if constexpr (Q8) {
+            if constexpr (Q8) {
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j) {
-                  const uint4 w = D == 128
-                                      ? lds128(kbase + r * 128 + (((2 * t4 + j) ^ (r & 7)) << 4))
-                                      : lds128(kbase + r * 64 + ((t4 ^ ((r >> 1) & 3)) << 4));
-                  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+              for (int j = 0; j < D / 64; ++j) {
+                const uint32_t at = D == 128 ? kbase + r0 * 128 + (((2 * t4 + j) ^ (r0 & 7)) << 4)
+                                             : kbase + r0 * 64 + ((t4 ^ ((r0 >> 1) & 3)) << 4);
+                const uint4 x0 = lds128(at), x1 = lds128(at + 8 * D);
+                const uint32_t ya[4] = {x0.x, x0.y, x0.z, x0.w}, yb[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    const int ks = j * 4 + x;
-                    mma_f16_16816(sc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3],
-                                  e4m3x2_to_f16x2(ww[x] & 0xFFFFu), e4m3x2_to_f16x2(ww[x] >> 16));
-                  }
+                for (int x = 0; x < 4; ++x) {
+                  const uint32_t a0 = e4m3x2_to_f16x2(ya[x] & 0xFFFFu), a2 = e4m3x2_to_f16x2(ya[x] >> 16);
+                  const uint32_t a1 = e4m3x2_to_f16x2(yb[x] & 0xFFFFu), a3 = e4m3x2_to_f16x2(yb[x] >> 16);
+#pragma unroll
+                  for (int nt = 0; nt < NTH; ++nt)
+                    mma_f16_16816(sc[nt], a0, a1, a2, a3, qb[nt][j * 4 + x][0], qb[nt][j * 4 + x][1]);
                 }
-              } else {
+              }
+            } else {
 #pragma unroll
-                for (int hj = 0; hj < D / 32; ++hj) {    // 64-dim half, chunk of it
-                  const uint4 w = lds128(kbase + (hj >> 1) * 16384 + r * 128 +
-                                         (((2 * t4 + (hj & 1)) ^ (r & 7)) << 4));
-                  const int ks = hj * 2;
-                  mma_bf16_16816(sc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], w.x, w.y);
-                  mma_bf16_16816(sc[nt], qa[ks + 1][0], qa[ks + 1][1], qa[ks + 1][2],
-                                 qa[ks + 1][3], w.z, w.w);
+              for (int hj = 0; hj < D / 32; ++hj) {      // 64-dim half, chunk of it
+                const uint32_t at = kbase + (hj >> 1) * 16384 + r0 * 128 +
+                                    (((2 * t4 + (hj & 1)) ^ (r0 & 7)) << 4);
+                const uint4 x0 = lds128(at), x1 = lds128(at + 1024);
+#pragma unroll
+                for (int nt = 0; nt < NTH; ++nt) {
+                  mma_bf16_16816(sc[nt], x0.x, x1.x, x0.y, x1.y, qb[nt][hj * 2][0], qb[nt][hj * 2][1]);
+                  mma_bf16_16816(sc[nt], x0.z, x1.z, x0.w, x1.w, qb[nt][hj * 2 + 1][0],
+                                 qb[nt][hj * 2 + 1][1]);
                 }
               }
             }
-            // ---- x = s log2(e), masked; row maxima
-            float f[2] = {fq[0], fq[1]}, ev = 0.f;
+            // ---- x = s log2(e), masked; the maxima move only when one grew
+            float fk = 1.f, ev = 0.f;
             if constexpr (Q8) {
-              const float fk = pow2i(meta_ke[st]);
-              f[0] = fminf(fmaxf(fq[0] * fk, -3e38f), 3e38f);
-              f[1] = fminf(fmaxf(fq[1] * fk, -3e38f), 3e38f);
+              fk = pow2i(meta_ke[st]);
               ev = (float)meta_ve[st];
             }
-            bool vis[4] = {true, true, true, true};      // tokens (nt, e) = w0 + nt*8 + 2*t4 + e
+            bool vis[2] = {true, true};                   // tokens w0 + g4, w0 + g4 + 8
             if (!whole) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int tok = w0 + (j >> 1) * 8 + 2 * t4 + (j & 1);
+              for (int j = 0; j < 2; ++j) {
+                const int tok = w0 + g4 + 8 * j;
                 vis[j] = tok <= u.t && (tok >= lo || tok < sinks);
               }
             }
-            float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float x = sc[nt][c] * f[c >> 1];
-                sc[nt][c] = vis[nt * 2 + (c & 1)] ? x : -INFINITY;
-                mx[c >> 1] = fmaxf(mx[c >> 1], sc[nt][c]);
-              }
+            float mx[NTH][2];
             bool grow = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-              mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-              grow |= mx[r] + ev > m[r] + kLazy || (Q8 && mx[r] > n[r] + kLazy);
-            }
+            for (int nt = 0; nt < NTH; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float f = Q8 ? fminf(fmaxf(fq[nt][e] * fk, -3e38f), 3e38f) : fq[nt][e];
+                sc[nt][e] = vis[0] ? sc[nt][e] * f : -INFINITY;
+                sc[nt][2 + e] = vis[1] ? sc[nt][2 + e] * f : -INFINITY;
+                mx[nt][e] = fmaxf(sc[nt][e], sc[nt][2 + e]);
+                grow |= mx[nt][e] + ev > m[nt][e] + kLazy || (Q8 && mx[nt][e] > n[nt][e] + kLazy);
+              }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const float mn = fmaxf(m[r], mx[r] + ev);
-                const float al = m[r] == -INFINITY ? 0.f : ex2(m[r] - mn);
-                m[r] = mn;
-                if constexpr (Q8) {
-                  const float nn = fmaxf(n[r], mx[r]);
-                  l[r] *= n[r] == -INFINITY ? 0.f : ex2(n[r] - nn);
-                  n[r] = nn;
-                } else {
-                  l[r] *= al;
-                }
+              for (int nt = 0; nt < NTH; ++nt)
 #pragma unroll
-                for (int j = 0; j < NO; ++j) {
-                  o[j][2 * r] *= al;
-                  o[j][2 * r + 1] *= al;
+                for (int e = 0; e < 2; ++e) {
+                  float x = mx[nt][e];
+#pragma unroll
+                  for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+                  const float mn = fmaxf(m[nt][e], x + ev);
+                  const float al = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mn);
+                  m[nt][e] = mn;
+                  if constexpr (Q8) {
+                    const float nn = fmaxf(n[nt][e], x);
+                    l[nt][e] *= n[nt][e] == -INFINITY ? 0.f : ex2(n[nt][e] - nn);
+                    n[nt][e] = nn;
+                  } else {
+                    l[nt][e] *= al;
+                  }
+#pragma unroll
+                  for (int j = 0; j < MT; ++j) {
+                    o[nt][j][e] *= al;
+                    o[nt][j][2 + e] *= al;
+                  }
                 }
-              }
             }
-            // ---- p' = 2^(x - m): A fragment of O += P V
-            uint32_t pa[4];
-            float sum[2] = {0.f, 0.f};
+            // ---- P^T: p' = 2^(x + ev - m) as bf16, transposed into B fragments
+            // (tokens 2 t4, 2 t4 + 1 and 8 + ... of head g4)
+            uint32_t pb[NTH][2];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int nt = 0; nt < NTH; ++nt) {
+              float p[4];
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const float mr = m[r] == -INFINITY ? 0.f : m[r] - ev;
-                const float p0 = ex2(sc[nt][2 * r] - mr), p1 = ex2(sc[nt][2 * r + 1] - mr);
-                pa[nt * 2 + r] = Q8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+              for (int e = 0; e < 2; ++e) {
+                const float mr = m[nt][e] == -INFINITY ? 0.f : m[nt][e] - ev;
+                p[e] = ex2(sc[nt][e] - mr);
+                p[2 + e] = ex2(sc[nt][2 + e] - mr);
                 if constexpr (Q8) {
-                  const float nr = n[r] == -INFINITY ? 0.f : n[r];
-                  sum[r] += ex2(sc[nt][2 * r] - nr) + ex2(sc[nt][2 * r + 1] - nr);
+                  const float nr = n[nt][e] == -INFINITY ? 0.f : n[nt][e];
+                  l[nt][e] += ex2(sc[nt][e] - nr) + ex2(sc[nt][2 + e] - nr);
                 } else {
-                  sum[r] += p0 + p1;
+                  l[nt][e] += p[e] + p[2 + e];
                 }
               }
-            l[0] += sum[0];
-            l[1] += sum[1];
-            // ---- V: tokens w0 + {2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4}, the
+              pb[nt][0] = movmatrix_trans(pack_bf16(p[0], p[1]));
+              pb[nt][1] = movmatrix_trans(pack_bf16(p[2], p[3]));
+            }
+            // ---- V^T: tokens w0 + {2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4}, the
             // dims of this thread's chunks; rows that the query does not see
             // (they may hold anything) as zeros
-            const int r0 = warp * 16 + 2 * t4;
-            constexpr int kHalves = Q8 ? 1 : D / 64;      // boxes of a row
-            constexpr int kDimsPer = Q8 ? D / 8 : 8;      // dims of this thread in a box
+            const int v0 = warp * 16 + 2 * t4;
+            bool dead[4] = {false, false, false, false};
+            if (!whole) {
 #pragma unroll
-            for (int hb = 0; hb < kHalves; ++hb) {
-              constexpr int W = Q8 ? D / 32 : 4;          // words per token
+              for (int j = 0; j < 4; ++j) {
+                const int tok = tok0 + v0 + (j >> 1) * 8 + (j & 1);
+                dead[j] = !(tok <= u.t && (tok >= lo || tok < sinks));
+              }
+            }
+#pragma unroll
+            for (int hb = 0; hb < (Q8 ? 1 : D / 64); ++hb) {    // boxes of a row
+              constexpr int W = Q8 ? D / 32 : 4;          // words per token and box
               uint32_t vw[4][W];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const int r = r0 + (j >> 1) * 8 + (j & 1);
+                const int r = v0 + (j >> 1) * 8 + (j & 1);
                 if constexpr (Q8 && D == 64) {
                   const uint2 w = lds64(vbase + r * 64 + (((g4 >> 1) ^ ((r >> 1) & 3)) << 4) +
                                         (g4 & 1) * 8);
@@ -456,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
                   vw[j][W > 2 ? 2 : 0] = w.z;
                   vw[j][W > 2 ? 3 : 0] = w.w;
                 }
-                if (!whole && !vis[j]) {
+                if (!whole && dead[j]) {
 #pragma unroll
                   for (int x = 0; x < W; ++x) vw[j][x] = 0u;
                 }
@@ -465,24 +486,23 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
               for (int x = 0; x < W; ++x) {
                 if constexpr (Q8) {
 #pragma unroll
-                  for (int y = 0; y < 2; ++y) {           // dims 4x + 2y, 4x + 2y + 1
-                    const uint32_t sel = y ? 0x7362u : 0x5140u;
-                    const uint32_t c0 = __byte_perm(vw[0][x], vw[1][x], sel);
-                    const uint32_t c1 = __byte_perm(vw[2][x], vw[3][x], sel);
-                    const int j = 4 * x + 2 * y;
-                    mma_f16_16816(o[j], pa[0], pa[1], pa[2], pa[3], e4m3x2_to_f16x2(c0 & 0xFFFFu),
-                                  e4m3x2_to_f16x2(c1 & 0xFFFFu));
-                    mma_f16_16816(o[j + 1], pa[0], pa[1], pa[2], pa[3], e4m3x2_to_f16x2(c0 >> 16),
-                                  e4m3x2_to_f16x2(c1 >> 16));
+                  for (int y = 0; y < 2; ++y) {           // dims 4x + 2y, 4x + 2y + 1: m-tile 2x + y
+                    const uint32_t c0 = __byte_perm(vw[0][x], vw[1][x], y ? 0x7362u : 0x5140u);
+                    const uint32_t c1 = __byte_perm(vw[2][x], vw[3][x], y ? 0x7362u : 0x5140u);
+                    const uint32_t a0 = e4m3x2_to_bf16x2(c0 & 0xFFFFu), a1 = e4m3x2_to_bf16x2(c0 >> 16);
+                    const uint32_t a2 = e4m3x2_to_bf16x2(c1 & 0xFFFFu), a3 = e4m3x2_to_bf16x2(c1 >> 16);
+#pragma unroll
+                    for (int nt = 0; nt < NTH; ++nt)
+                      mma_bf16_16816(o[nt][2 * x + y], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
                   }
                 } else {                                  // dims 2x, 2x + 1 of the box's chunk
-                  const int j = hb * kDimsPer + 2 * x;
-                  mma_bf16_16816(o[j], pa[0], pa[1], pa[2], pa[3],
-                                 __byte_perm(vw[0][x], vw[1][x], 0x5410),
-                                 __byte_perm(vw[2][x], vw[3][x], 0x5410));
-                  mma_bf16_16816(o[j + 1], pa[0], pa[1], pa[2], pa[3],
-                                 __byte_perm(vw[0][x], vw[1][x], 0x7632),
-                                 __byte_perm(vw[2][x], vw[3][x], 0x7632));
+                  const uint32_t a0 = __byte_perm(vw[0][x], vw[1][x], 0x5410);
+                  const uint32_t a1 = __byte_perm(vw[0][x], vw[1][x], 0x7632);
+                  const uint32_t a2 = __byte_perm(vw[2][x], vw[3][x], 0x5410);
+                  const uint32_t a3 = __byte_perm(vw[2][x], vw[3][x], 0x7632);
+#pragma unroll
+                  for (int nt = 0; nt < NTH; ++nt)
+                    mma_bf16_16816(o[nt][hb * 4 + x], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
                 }
               }
             }
@@ -500,35 +520,38 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
 
       // ---- join the warps: O relative to each warp's own m
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      }
+      for (int nt = 0; nt < NTH; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1)
+            l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], w);
       if (!named_bar_and(1, kConsumers, ok)) {   // also: the last segment's sums have been read
         ok = false;
         break;
       }
-      if (t4 == 0) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          sm_m[warp][g4 + 8 * r] = m[r];
-          sm_n[warp][g4 + 8 * r] = Q8 ? n[r] : m[r];
-          sm_l[warp][g4 + 8 * r] = l[r];
-        }
-      }
-      // fragment order: columns 2 t4, 2 t4 + 1 of n-tile j side by side
+      for (int nt = 0; nt < NTH; ++nt)
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        if (g4 + 8 * r < hpg) {
-          const uint32_t row = red + ((warp * hpg + g4 + 8 * r) * C::kRedRow + 2 * t4) * 4;
+        for (int e = 0; e < 2; ++e) {
+          const int h = nt * 8 + 2 * t4 + e;
+          if (g4 == 0) {
+            sm_m[warp][h] = m[nt][e];
+            sm_n[warp][h] = Q8 ? n[nt][e] : m[nt][e];
+            sm_l[warp][h] = l[nt][e];
+          }
+          // pairs of dims in fragment order: m-tile j, row group g4
+          if (h < hpg) {
+            const uint32_t row = red + ((warp * hpg + h) * C::kRedRow + 2 * g4) * 4;
 #pragma unroll
-          for (int j = 0; j < NO; ++j) sts_f2(row + j * 32, o[j][2 * r], o[j][2 * r + 1]);
+            for (int j = 0; j < MT; ++j) sts_f2(row + j * 64, o[nt][j][e], o[nt][j][2 + e]);
+          }
         }
       named_bar_sync(1, kConsumers);
       const bool whole_unit = step == u.first && next == u.first + u.len;
       const int64_t slot = 2 * blockIdx.x + (step == u.first);
-      for (int e = threadIdx.x; e < hpg * NO * 4; e += kConsumers) {
-        const int h = e / (NO * 4), j = e / 4 % NO;        // one head per warp and step
+      for (int e = threadIdx.x; e < hpg * (D / 2); e += kConsumers) {
+        const int h = e / (D / 2), pr = e % (D / 2);       // one head per warp and step
         float M = -INFINITY, N = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kConsWarps; ++w) {
@@ -540,25 +563,21 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
         for (int w = 0; w < kConsWarps; ++w) {
           const float mw = sm_m[w][h];
           const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-          const float2 v = lds_f2(red + ((w * hpg + h) * C::kRedRow + (e % (NO * 4)) * 2) * 4);
+          const float2 v = lds_f2(red + ((w * hpg + h) * C::kRedRow + pr * 2) * 4);
           const float nw = sm_n[w][h];
           L = fmaf(sm_l[w][h], nw == -INFINITY ? 0.f : ex2(nw - N), L);
           x = fmaf(v.x, f, x);
           y = fmaf(v.y, f, y);
         }
-        // dims j, j + 1 of one column: the lane of the other j holds the pair's other half
-        const bool odd = j & 1;
-        const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 4);
-        const float d0 = odd ? other : x, d1 = odd ? y : other;
-        const int n = 2 * (e & 3) + odd, je = j & ~1;
-        const int dim = Q8 ? n * (D / 8) + je : (je >> 3) * 64 + n * 8 + (je & 7);
+        const int j = pr >> 3, c = pr & 7;                 // m-tile, chunk of V
+        const int dim = Q8 ? c * (D / 8) + 2 * j : (j >> 2) * 64 + c * 8 + 2 * (j & 3);
         if (whole_unit) {
           const float inv = L == 0.f ? 0.f : ex2(M - N) / L;      // nothing visible: zeros
           uint16_t* dst = a.out + (((int64_t)u.b * s.T + u.i) * H + (int64_t)u.g * hpg + h) * D + dim;
-          *reinterpret_cast<uint32_t*>(dst) = pack_bf16(d0 * inv, d1 * inv);
+          *reinterpret_cast<uint32_t*>(dst) = pack_bf16(x * inv, y * inv);
         } else {
-          *reinterpret_cast<float2*>(a.part_o + (slot * hpg + h) * D + dim) = make_float2(d0, d1);
-          if (e % (NO * 4) == 0) a.part_ml[slot * hpg + h] = make_float4(M, N, L, 0.f);
+          *reinterpret_cast<float2*>(a.part_o + (slot * hpg + h) * D + dim) = make_float2(x, y);
+          if (pr == 0) a.part_ml[slot * hpg + h] = make_float4(M, N, L, 0.f);
         }
       }
     }
@@ -659,7 +678,7 @@ bool encode_bf16_cache_map(CUtensorMap* map, const void* base, const Shape& s) {
   return encode_bf16_map(map, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, int NTH>
 cudaError_t launch_impl(const CacheView& c, StreamArgs& a, cudaStream_t st) {
   using C = Cfg<D, Q8>;
   const int hpg = a.s.H / a.s.G;
@@ -676,11 +695,11 @@ cudaError_t launch_impl(const CacheView& c, StreamArgs& a, cudaStream_t st) {
   a.stages = (kSmemMax - 2048 - fixed) / C::kStage;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   const int smem = fixed + a.stages * C::kStage;
-  cudaError_t e = cudaFuncSetAttribute(stream_attn_kernel<D, Q8>,
+  cudaError_t e = cudaFuncSetAttribute(stream_attn_kernel<D, Q8, NTH>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   note_launches(2);
-  stream_attn_kernel<D, Q8><<<a.nctas, kThreads, smem, st>>>(tm_k, tm_v, a);
+  stream_attn_kernel<D, Q8, NTH><<<a.nctas, kThreads, smem, st>>>(tm_k, tm_v, a);
   const int warps = (a.nctas - 1) * hpg;
   stream_finish_kernel<D><<<warps > 0 ? (warps + 7) / 8 : 1, 256, 0, st>>>(a);
   return cudaGetLastError();
@@ -748,11 +767,16 @@ cudaError_t launch_stream_attn(const Shape& s, const Positions& pos, const Cache
     for (int b = 0; b < s.B; ++b) a.step0[b + 1] = a.step0[b] + a.Tp * s.G * len[b];
     const int steps = a.step0[s.B];
     a.nctas = steps < ctas ? steps : ctas;
+    const bool wide = s.H / s.G > 8;    // heads of a group in one or two n-tiles of 8
     cudaError_t e;
-    if (s.D == 128)
-      e = c.kv8 ? launch_impl<128, true>(c, a, st) : launch_impl<128, false>(c, a, st);
+    if (s.D == 128 && c.kv8)
+      e = wide ? launch_impl<128, true, 2>(c, a, st) : launch_impl<128, true, 1>(c, a, st);
+    else if (s.D == 128)
+      e = wide ? launch_impl<128, false, 2>(c, a, st) : launch_impl<128, false, 1>(c, a, st);
+    else if (c.kv8)
+      e = wide ? launch_impl<64, true, 2>(c, a, st) : launch_impl<64, true, 1>(c, a, st);
     else
-      e = c.kv8 ? launch_impl<64, true>(c, a, st) : launch_impl<64, false>(c, a, st);
+      e = wide ? launch_impl<64, false, 2>(c, a, st) : launch_impl<64, false, 1>(c, a, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

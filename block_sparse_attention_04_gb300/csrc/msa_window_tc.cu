@@ -22,11 +22,13 @@
 //   warps 3-10    one warpgroup per chain, a row per thread: mask, maximum,
 //                 P = 2^(x - m) over S, row sum; at the item's end O / l
 //   warps 11-14   8-bit cache, in place of warp 1: codes of the next block to
-//                 registers, converted to f16 (exact) into the same rings; Q
-//                 tiles to f16 in place, each row scaled by a power of two to
-//                 [2^13, 2^14) (exact but for elements 2^-27 below the row's
-//                 maximum).  P rounds to f16 (2^-11) there, to bf16 (2^-8)
-//                 beside a bf16 cache.
+//                 registers, converted into the same rings: K to f16 and V to
+//                 bf16 (both exact); Q tiles to f16 in place, each row scaled by
+//                 a power of two to [2^13, 2^14) (exact but for elements 2^-27
+//                 below the row's maximum).  f16 takes a third of the
+//                 conversion's instructions; V needs bf16's range, because P
+//                 (bf16, 2^-8) is relative to the largest p', which may belong
+//                 to values that cancel or vanish.
 // An 8-bit block's exponents: 2^ek scales the scores, 2^ev is folded into the
 // exponential that multiplies V (p' = 2^(x + ev - m), m the maximum of x + ev),
 // while the normaliser counts 2^(x - n) with its own maximum n.  p' gives the
@@ -110,21 +112,6 @@ __device__ __forceinline__ int block_at(const Item& d, int p) { return p < d.nsi
 // Instruction descriptor of kind::f16 with f16 A and B (format 0), f32 D.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
   return idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
-}
-
-__device__ __forceinline__ void sts128(uint32_t saddr, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "r"(v.x), "r"(v.y), "r"(v.z),
-               "r"(v.w)
-               : "memory");
-}
-// Shared-memory writes of this thread before later accesses of the async proxy.
-__device__ __forceinline__ void fence_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// Byte offset of 16-byte chunk c (8 dims of 16 bits) of row r in a tile.
-__device__ __forceinline__ uint32_t tile_off(int r, int c) {
-  return (uint32_t)((c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 // Bits [0, n) of word w of a 128-bit mask.
@@ -312,7 +299,7 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
     // The whole warp runs the loop; one elected lane issues and commits.
     constexpr uint32_t idesc_s =
         Q8 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
-    constexpr uint32_t idesc_o = Q8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
+    constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
     const uint64_t qdesc0 = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
     const uint64_t kdesc0 = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
     const uint64_t vdesc0 = smem_desc(smem_u32(sV), C::kHalf, 1024, kSwizzle128B);
@@ -567,7 +554,7 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
                   pp.y = vw >> (hf * 16 + 2 * u + 1) & 1 ? pp.y : 0.f;
                 }
                 lsum = fadd2(lsum, pp);
-                wv[hf * 8 + u] = Q8 ? pack_f16(pp.x, pp.y) : pack_bf16(pp.x, pp.y);
+                wv[hf * 8 + u] = pack_bf16(pp.x, pp.y);
               }
             }
             tmem_st16(s_base + cc * 16, wv);
@@ -645,7 +632,8 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
                          : __ldg(reinterpret_cast<const uint4*>(base + x.off + r * pitch + ch * 16));
       }
     };
-    auto store = [&](uint32_t tile, const uint4 (&v)[NL], int hi, int lo, int sk) {
+    auto store = [&](const bool is_v, uint32_t tile, const uint4 (&v)[NL], int hi, int lo,
+                     int sk) {
 #pragma unroll
       for (int u = 0; u < NL; ++u) {
         const int r = row0 + 32 * (u & 3), ch = 4 * (u >> 2) + c4;
@@ -654,8 +642,9 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         uint32_t h[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          h[2 * j] = dead ? 0u : e4m3x2_to_f16x2(w[j] & 0xFFFFu);
-          h[2 * j + 1] = dead ? 0u : e4m3x2_to_f16x2(w[j] >> 16);
+          const uint32_t c0 = w[j] & 0xFFFFu, c1 = w[j] >> 16;
+          h[2 * j] = !is_v ? e4m3x2_to_f16x2(c0) : dead ? 0u : e4m3x2_to_bf16x2(c0);
+          h[2 * j + 1] = !is_v ? e4m3x2_to_f16x2(c1) : dead ? 0u : e4m3x2_to_bf16x2(c1);
         }
         sts128(tile + tile_off(r, 2 * ch), make_uint4(h[0], h[1], h[2], h[3]));
         sts128(tile + tile_off(r, 2 * ch + 1), make_uint4(h[4], h[5], h[6], h[7]));
@@ -731,14 +720,14 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[ks], (w & 1) ^ 1, a.status, a.wait_polls));
         if (!ok) break;
         if (tid == 0) meta[n % kMetaRing] = make_int2(cur.ek, cur.ev);
-        store(smem_u32(sK + ks * C::kTile), kreg, kBlock, 0, 0);
+        store(false, smem_u32(sK + ks * C::kTile), kreg, kBlock, 0, 0);
         fence_async();
         mbar_arrive(&k_full[ks]);
         if (p == 0 && !convert_q(k)) { ok = false; break; }
         if (more) load(a.k8, nxt, kreg);
         ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[ks], (w & 1) ^ 1, a.status, a.wait_polls));
         if (!ok) break;
-        store(smem_u32(sV + ks * C::kTile), vreg, d.t_last - cur.tok0, d.lo - cur.tok0,
+        store(true, smem_u32(sV + ks * C::kTile), vreg, d.t_last - cur.tok0, d.lo - cur.tok0,
               a.sinks - cur.tok0);
         fence_async();
         mbar_arrive(&v_full[ks]);

@@ -3,8 +3,8 @@ that the kernels are held to (torch float64, any device).
 
 Attention bound.  Write w_j for the exact softmax weights of a row and
 A = sum_j w_j |v_j| (per output element).  A kernel rounds
-  - each weight p to 16 bits before the product with V: u_p = 2^-8 (bf16) or
-    2^-11 (f16 products of an 8-bit cache), relative, contributing u_p A;
+  - each weight p to bf16 before the product with V: u_p = 2^-8, relative,
+    contributing u_p A;
   - each score: D products summed in fp32 by the tensor cores, whose adders may
     truncate (2^-23 per term), and an 8-bit call's Q to f16 after scaling the
     row's maximum to 2^13 (elements below 2^-14 round at 2^-25 absolute, i.e.
@@ -21,7 +21,7 @@ import torch
 
 BLOCK = 128
 MIN_EXP, MAX_EXP = -126, 119
-U_BF16, U_F16 = 2.0 ** -8, 2.0 ** -11
+U_BF16 = 2.0 ** -8
 
 
 def codes_to_f64(codes):

@@ -20,6 +20,11 @@ def msa():
     return m
 
 
+def randq(*shape, seed=77):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+
 def bf16(x):
     return torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(torch.bfloat16)
 
@@ -225,9 +230,9 @@ def test_sparse_q8(msa, kernels, lens, T, H, G, D, Di):
     sel = random_sel(B, T, G, q_start, 6, empty)
     out = run_sparse(msa, c, q, sel, q_start, lens, nb, Di, kernels)
     k, v = c.values()
-    # the tensor-core kernels round weights to bf16 and keep one bf16 partial
+    # weights round to bf16; the tensor-core kernels also keep one bf16 partial
     # per selected block: 2^-8 of A twice
-    u = sr.U_F16 if kernels == "streaming" else 2 * sr.U_BF16
+    u = sr.U_BF16 if kernels == "streaming" else 2 * sr.U_BF16
     want, bound = sr.attend_call(q, k, v, q_start, sr.sel_seen(sel, nb * 128, "cuda"), D ** -0.5, u)
     sr.check(out, want, bound)
     for b, i, gg in empty:
@@ -241,8 +246,9 @@ def test_sparse_q8_spread_exponents_and_negative_scale(msa, kernels):
     # and the other way round
     lens, T, H, G, D = [1900, 900], 2, 16, 2, 64
     c = Cache(lens, G, D, 15, seed=21, exp_lo=-60, exp_hi=-9)
-    c.exps[1] = torch.randint(-40, 30, c.exps[1].shape, device="cuda", dtype=torch.int8)
-    q = torch.randn(2, T, H, D, device="cuda").to(torch.bfloat16)
+    g = torch.Generator(device="cuda").manual_seed(20)
+    c.exps[1] = torch.randint(-40, 30, c.exps[1].shape, generator=g, device="cuda", dtype=torch.int8)
+    q = randq(2, T, H, D)
     q_start = [n - T for n in lens]
     sel = random_sel(2, T, G, q_start, 22)
     k, v = c.values()
@@ -254,19 +260,22 @@ def test_sparse_q8_spread_exponents_and_negative_scale(msa, kernels):
 
 
 @pytest.mark.parametrize("kernels", KERNELS)
-@pytest.mark.parametrize("zero", ["first", "last", "most"])
+@pytest.mark.parametrize("zero", ["first", "last", "most", "loud"])
 def test_sparse_q8_blocks_of_zeros_keep_their_weight(msa, kernels, zero):
     # a block of zero values is stored with the smallest exponent; its weights
-    # count in full beside blocks of ordinary (and of large) values
+    # count in full beside blocks of ordinary (and of large) values.  "loud":
+    # zeros under a large exponent (a block whose largest token was overwritten)
     lens, T, H, G, D = [1900, 700], 3, 12, 2, 128
     c = Cache(lens, G, D, 15, seed=27)
     page = c.table[0].long()
-    pick = {"first": page[:1], "last": page[14:15], "most": page[1:14]}[zero]
+    pick = {"first": page[:1], "last": page[14:15], "most": page[1:14],
+            "loud": page[4:6]}[zero]
     c.codes[1][pick] = c.codes[1][pick] & 0x7F
     c.codes[1][pick] = torch.where(c.codes[1][pick] == 0x7F, c.codes[1][pick], 0)
-    c.exps[1][pick] = -126
-    c.exps[1][page[3]] = 90
-    q = torch.randn(2, T, H, D, device="cuda").to(torch.bfloat16)
+    c.exps[1][pick] = 40 if zero == "loud" else -126
+    if zero != "loud":
+        c.exps[1][page[3]] = 90
+    q = randq(2, T, H, D)
     q_start = [n - T for n in lens]
     sel = random_sel(2, T, G, q_start, 28)
     k, v = c.values()
@@ -284,7 +293,7 @@ def test_exponents_outside_the_range_read_as_its_ends(msa, e):
     c.exps[0].fill_(-6)
     c.exps[1].fill_(e)
     c.codes[1] = torch.where(c.codes[1] == 0x7F, c.codes[1], c.codes[1] & 0x87)   # small values
-    q = torch.randn(1, 1, H, D, device="cuda").to(torch.bfloat16)
+    q = randq(1, 1, H, D)
     sel = random_sel(1, 1, G, [299], 24)
     out = run_sparse(msa, c, q, sel, [299], lens, 3, 32)
     c2 = Cache(lens, G, D, 3, seed=23)
@@ -292,7 +301,7 @@ def test_exponents_outside_the_range_read_as_its_ends(msa, e):
     out2 = run_sparse(msa, c2, q, sel, [299], lens, 3, 32)
     assert torch.equal(out, out2)
     k, v = c.values()
-    want, bound = sr.attend_call(q, k, v, [299], sr.sel_seen(sel, 384, "cuda"), D ** -0.5, sr.U_F16)
+    want, bound = sr.attend_call(q, k, v, [299], sr.sel_seen(sel, 384, "cuda"), D ** -0.5, sr.U_BF16)
     # bf16 outputs keep 2^-134 at the small end
     sr.check(out, want, bound + 2.0 ** -133)
 
@@ -301,7 +310,7 @@ def test_exponents_outside_the_range_read_as_its_ends(msa, e):
 def test_sparse_q8_per_sequence_equals_paged(msa, kernels):
     lens, T, H, G, D = [1500, 1100], 5, 12, 4, 128
     c = Cache(lens, G, D, 12, seed=31)
-    q = torch.randn(2, T, H, D, device="cuda").to(torch.bfloat16)
+    q = randq(2, T, H, D)
     q_start = [n - T for n in lens]
     sel = random_sel(2, T, G, q_start, 32)
     a = run_sparse(msa, c, q, sel, q_start, lens, 12, 64, kernels)
@@ -349,7 +358,7 @@ def test_forward_q8_selects_like_the_bf16_forward(msa, kernels):
 def test_q8_bad_blocks_are_reported_and_skipped(msa, kernels):
     lens, T, H, G, D, nb = [900], 2, 4, 1, 64, 8
     c = Cache(lens, G, D, nb, seed=51)
-    q = torch.randn(1, T, H, D, device="cuda").to(torch.bfloat16)
+    q = randq(1, T, H, D)
     q_start = [898]
     sel = random_sel(1, T, G, q_start, 52)
     good = sel.clone()

@@ -60,11 +60,6 @@ def run(msa, c, q8, q, q_start, kv_len, nb, window, sinks, kernels, scale=None, 
     return out
 
 
-def u_of(q8, kernels):
-    # weights round to f16 beside an 8-bit cache, to bf16 beside a bf16 one
-    return sr.U_F16 if q8 else sr.U_BF16
-
-
 def make(lens, T, H, G, D, seed, extra=0, nb=None):
     c = Cache([n + extra for n in lens], G, D, nb or max(-(-(n + extra) // 128) for n in lens) + 1,
               seed)
@@ -101,7 +96,7 @@ def test_window(msa, lens, T, H, G, D, window, sinks, kernels, q8):
     out = run(msa, c, q8, q, q_start, lens, nb, window, sinks, kernels)
     k, v = c.values()
     want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, window, sinks, "cuda"),
-                                 D ** -0.5, u_of(q8, kernels))
+                                 D ** -0.5, sr.U_BF16)
     sr.check(out, want, bound)
 
 
@@ -115,7 +110,7 @@ def test_window_past_the_context_is_dense_attention(msa, kernels, q8):
     out = run(msa, c, q8, q, q_start, kv_len, nb, 1 << 30, 1 << 30, kernels)
     k, v = c.values()
     want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, 1 << 30, 0, "cuda"),
-                                 128 ** -0.5, u_of(q8, kernels))
+                                 128 ** -0.5, sr.U_BF16)
     sr.check(out, want, bound)
     if not q8:
         p = msa.params(2, 300, 12, 4, 128, 32, nb, kernels=kernels)
@@ -135,7 +130,7 @@ def test_window_scales(msa, kernels, q8, scale):
     out = run(msa, c, q8, q, q_start, [800, 333], nb, 200, 9, kernels, scale=scale)
     k, v = c.values()
     want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, 200, 9, "cuda"), scale,
-                                 u_of(q8, kernels))
+                                 sr.U_BF16)
     sr.check(out, want, bound)
 
 
@@ -149,7 +144,7 @@ def test_window_q8_spread_exponents(msa, kernels):
     out = run(msa, c, True, q, q_start, [1300, 800], nb, 700, 9, kernels)
     k, v = c.values()
     want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, 700, 9, "cuda"),
-                                 64 ** -0.5, u_of(True, kernels))
+                                 64 ** -0.5, sr.U_BF16)
     sr.check(out, want, bound)
 
 
@@ -163,11 +158,13 @@ def test_window_q8_blocks_of_zeros_keep_their_weight(msa, kernels, T):
         c.codes[1][page] = torch.where(c.codes[1][page] == 0x7F, c.codes[1][page], 0)
         c.exps[1][page] = -126
     c.exps[1][c.table[0, 6].long()] = 60
+    loud = c.table[0, 3].long()                 # zeros under a large exponent
+    c.codes[1][loud], c.exps[1][loud] = 0, 30
     for scale in (0.01, 0.3):
         out = run(msa, c, True, q, q_start, [1100], nb, 800, 9, kernels, scale=scale)
         k, v = c.values()
         want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, 800, 9, "cuda"),
-                                     scale, u_of(True, kernels))
+                                     scale, sr.U_BF16)
         sr.check(out, want, bound)
 
 

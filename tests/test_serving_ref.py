@@ -58,8 +58,8 @@ def test_unseen_rows_never_matter():
     k = torch.randn(200, 1, 64, generator=g, dtype=torch.float64)
     v = torch.randn(200, 1, 64, generator=g, dtype=torch.float64)
     seen = sr.window_seen(200, 10, 1, "cpu")
-    want, _ = sr.attend_call(q, [k], [v], [100], seen, 1.0, sr.U_F16)
+    want, _ = sr.attend_call(q, [k], [v], [100], seen, 1.0, sr.U_BF16)
     k2, v2 = k.clone(), v.clone()
     k2[1:91], v2[103:] = torch.nan, torch.inf
-    got, _ = sr.attend_call(q, [k2], [v2], [100], seen, 1.0, sr.U_F16)
+    got, _ = sr.attend_call(q, [k2], [v2], [100], seen, 1.0, sr.U_BF16)
     assert torch.equal(got, want)
