@@ -741,8 +741,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
         uint32_t h[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          h[2 * j] = row > last ? 0u : e4m3x2_to_bf16x2(w[j] & 0xFFFFu);
-          h[2 * j + 1] = row > last ? 0u : e4m3x2_to_bf16x2(w[j] >> 16);
+          e4m3x4_to_bf16(row > last ? 0u : w[j], h[2 * j], h[2 * j + 1]);
         }
         sts128(tile + tile_off(row, 2 * ch), make_uint4(h[0], h[1], h[2], h[3]));
         sts128(tile + tile_off(row, 2 * ch + 1), make_uint4(h[4], h[5], h[6], h[7]));

@@ -92,8 +92,9 @@ __global__ void __launch_bounds__(kAppThreads) cache_append_q8_kernel(
       uint32_t res[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const float2 lo = unpack_f16(e4m3x2_to_f16x2(in[u] & 0xFFFFu));
-        const float2 hi = unpack_f16(e4m3x2_to_f16x2(in[u] >> 16));
+        uint32_t hl, hh;
+        e4m3x4_to_f16(in[u], hl, hh);
+        const float2 lo = unpack_f16(hl), hi = unpack_f16(hh);
         res[u] = f32x2_to_e4m3x2(lo.x * f, lo.y * f) | f32x2_to_e4m3x2(hi.x * f, hi.y * f) << 16;
       }
       o.x = res[0];

@@ -11,21 +11,25 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 // A stored exponent as the readers use it: any byte is defined.
 __device__ __forceinline__ int clamp_exp(int e) { return min(max(e, kMinExp), kMaxExp); }
 
-// Two e4m3 codes (low byte first) -> two f16, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  uint32_t r;
-  asm("{\n .reg .b16 c;\n cvt.u16.u32 c, %1;\n cvt.rn.f16x2.e4m3x2 %0, c;\n}" : "=r"(r) : "r"(codes));
-  return r;
+// Four e4m3 codes (low byte first) -> two pairs of f16, exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 
-// Two e4m3 codes (low byte first) -> two bf16, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
-  const uint32_t h = e4m3x2_to_f16x2(codes);
-  float lo, hi;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
-      : "=f"(lo), "=f"(hi)
-      : "r"(h));
-  return pack_bf16(lo, hi);
+// Four e4m3 codes (low byte first) -> two pairs of bf16, exact; NaN stays NaN.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  float a, b, c, d;
+  asm("{\n .reg .b16 l, h;\n .reg .b32 x, y;\n mov.b32 {l, h}, %4;\n"
+      " cvt.rn.f16x2.e4m3x2 x, l;\n cvt.rn.f16x2.e4m3x2 y, h;\n"
+      " mov.b32 {l, h}, x;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n"
+      " mov.b32 {l, h}, y;\n cvt.f32.f16 %2, l;\n cvt.f32.f16 %3, h;\n}"
+      : "=f"(a), "=f"(b), "=f"(c), "=f"(d)
+      : "r"(codes));
+  lo = pack_bf16(a, b);
+  hi = pack_bf16(c, d);
 }
 
 // Two fp32 -> two e4m3 codes (round to nearest even, saturating; NaN stays

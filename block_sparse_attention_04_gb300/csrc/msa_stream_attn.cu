@@ -14,7 +14,7 @@
 //
 // The call's work is one sequence of (unit, block) steps, unit (b, t, g) after
 // unit, cut into equal runs, one per CTA and SM; a run's share of one unit is a
-// segment.  Warp 8 copies K and V of each block (128 tokens of one KV head)
+// segment.  The last warp copies K and V of each block (128 tokens of one KV head)
 // into a ring of stages by TMA and runs ahead by its depth.  Warps 0-7 take 16
 // tokens of every block each and never wait for one another inside a segment:
 // S^T = K Q^T (tokens x heads) with mma.sync m16n8k16, softmax in registers,
@@ -36,9 +36,12 @@
 namespace msa {
 namespace {
 
-constexpr int kConsWarps = 8;
-constexpr int kConsumers = 32 * kConsWarps;
-constexpr int kThreads = kConsumers + 32;
+constexpr int kTeam = 8;             // consumer warps that share a block, 16 tokens each
+// Teams: the blocks of an 8-bit cache take more instructions per byte, and two
+// teams on alternate blocks hide their latency (measured, 4 x 64K tokens: one
+// team 116 us, two TWOTEAM us); a bf16 cache keeps HBM busy with one.
+template <bool Q8, int NTH>
+constexpr int teams() { return Q8 && NTH == 1 ? 2 : 1; }
 constexpr int kQBufs = 2;
 constexpr int kMaxStages = 8;
 constexpr int kMaxCtas = 512;        // partials and error words in the workspace
@@ -108,18 +111,23 @@ __device__ __forceinline__ BlockList list_of(const StreamArgs& a, int t) {
   return BlockList{ns + t / kBlock - lo + 1, ns, lo - ns};
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, int NTH>
 struct Cfg {
+  static constexpr int kTeams = teams<Q8, NTH>();
+  static constexpr int kWarps = kTeam * kTeams;
+  static constexpr int kConsumers = 32 * kWarps;
+  static constexpr int kThreads = kConsumers + 32;          // and the producer warp
   static constexpr int kTile = kBlock * D * (Q8 ? 1 : 2);   // K (or V) of one block and head
   static constexpr int kStage = 2 * kTile;
   static constexpr int kRedRow = D + 4;                     // padded row of the join buffer (floats)
 };
 
 template <int D, bool Q8, int NTH>
-__global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
+__global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ StreamArgs a) {
-  using C = Cfg<D, Q8>;
+  using C = Cfg<D, Q8, NTH>;
+  constexpr int kWarps = C::kWarps, kConsumers = C::kConsumers;
   constexpr int NS = D / 16;       // k-steps of S
   constexpr int MT = D / 16;       // m-tiles of O^T
   extern __shared__ uint8_t dsm_raw[];
@@ -127,13 +135,13 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], q_full[kQBufs], q_empty[kQBufs];
   __shared__ int meta_kb[kMaxStages], meta_ke[kMaxStages], meta_ve[kMaxStages];
-  __shared__ float sm_m[kConsWarps][16], sm_n[kConsWarps][16], sm_l[kConsWarps][16];
+  __shared__ float sm_m[kWarps][NTH * 8], sm_n[kWarps][NTH * 8], sm_l[kWarps][NTH * 8];
   __shared__ int err;
   const Shape& s = a.s;
   const int H = s.H, G = s.G, hpg = H / G, S = a.stages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint16_t* qbuf = reinterpret_cast<uint16_t*>(sm + S * C::kStage);       // [kQBufs][hpg][D]
-  const uint32_t red = smem_u32(qbuf + kQBufs * hpg * D);                 // [8][hpg][kRedRow] float
+  const uint32_t red = smem_u32(qbuf + kQBufs * hpg * D);                 // [kWarps][hpg][kRedRow] float
   const int steps = a.step0[s.B];
   const int run0 = run_begin(steps, a.nctas, blockIdx.x);
   const int run1 = run_begin(steps, a.nctas, blockIdx.x + 1);
@@ -141,18 +149,18 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kConsWarps);
+      mbar_init(&empty[i], kTeam);
     }
     for (int i = 0; i < kQBufs; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], kConsWarps);
+      mbar_init(&q_empty[i], kWarps);
     }
     err = 0;
     fence_mbar_init();
   }
   __syncthreads();
 
-  if (warp == kConsWarps) {
+  if (warp == kWarps) {
     // ------------------------------------------------------------ producer
     const uint64_t pol = l2_policy_evict_first();
     const uint32_t qbytes = (uint32_t)(hpg * D * 2);
@@ -251,7 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
     // S^T = K Q^T (tokens x heads) and O^T += V^T P^T (dims x heads)
     const int g4 = lane >> 2, t4 = lane & 3;   // row group and column pair of a fragment
     const float qk = s.scale * kLog2e;
-    int st = 0, k = 0;
+    const int wt = warp % kTeam;               // this warp's 16 tokens of a block
+    int st = 0, k = 0, turn = warp / kTeam;    // turn 0: the next block is this team's
     uint32_t ph = 0;
     bool ok = true;
     for (int step = run0, next; step < run1; step = next, ++k) {
@@ -327,18 +336,22 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
         }
 
       for (int blk = 0; blk < nblk; ++blk) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[st], ph, &err, a.wait_polls));
-        if (!ok) break;
-        const int kb = meta_kb[st];
+        const bool mine = turn == 0;
+        turn = mine ? C::kTeams - 1 : turn - 1;
+        if (mine) {
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[st], ph, &err, a.wait_polls));
+          if (!ok) break;
+        }
+        const int kb = mine ? meta_kb[st] : -1;
         if (kb >= 0) {
           const int tok0 = kb * kBlock;
-          const int w0 = tok0 + warp * 16;              // this warp's first token
+          const int w0 = tok0 + wt * 16;              // this warp's first token
           const bool whole = tok0 + kBlock - 1 <= u.t && (tok0 >= lo || tok0 + kBlock - 1 < sinks);
           const bool any = w0 <= u.t && (w0 + 15 >= lo || w0 < sinks);
           if (any) {
             const uint32_t kbase = smem_u32(sm + st * C::kStage), vbase = kbase + C::kTile;
             // ---- S^T of 16 tokens: rows g4 and g4 + 8
-            const int r0 = warp * 16 + g4;                // r0 & 7 == (r0 + 8) & 7
+            const int r0 = wt * 16 + g4;                // r0 & 7 == (r0 + 8) & 7
             float sc[NTH][4];
 #pragma unroll
             for (int nt = 0; nt < NTH; ++nt)
@@ -353,8 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
                 const uint32_t ya[4] = {x0.x, x0.y, x0.z, x0.w}, yb[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                  const uint32_t a0 = e4m3x2_to_f16x2(ya[x] & 0xFFFFu), a2 = e4m3x2_to_f16x2(ya[x] >> 16);
-                  const uint32_t a1 = e4m3x2_to_f16x2(yb[x] & 0xFFFFu), a3 = e4m3x2_to_f16x2(yb[x] >> 16);
+                  uint32_t a0, a1, a2, a3;
+                  e4m3x4_to_f16(ya[x], a0, a2);
+                  e4m3x4_to_f16(yb[x], a1, a3);
 #pragma unroll
                   for (int nt = 0; nt < NTH; ++nt)
                     mma_f16_16816(sc[nt], a0, a1, a2, a3, qb[nt][j * 4 + x][0], qb[nt][j * 4 + x][1]);
@@ -449,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
             // ---- V^T: tokens w0 + {2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4}, the
             // dims of this thread's chunks; rows that the query does not see
             // (they may hold anything) as zeros
-            const int v0 = warp * 16 + 2 * t4;
+            const int v0 = wt * 16 + 2 * t4;
             bool dead[4] = {false, false, false, false};
             if (!whole) {
 #pragma unroll
@@ -487,10 +501,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
                 if constexpr (Q8) {
 #pragma unroll
                   for (int y = 0; y < 2; ++y) {           // dims 4x + 2y, 4x + 2y + 1: m-tile 2x + y
-                    const uint32_t c0 = __byte_perm(vw[0][x], vw[1][x], y ? 0x7362u : 0x5140u);
-                    const uint32_t c1 = __byte_perm(vw[2][x], vw[3][x], y ? 0x7362u : 0x5140u);
-                    const uint32_t a0 = e4m3x2_to_bf16x2(c0 & 0xFFFFu), a1 = e4m3x2_to_bf16x2(c0 >> 16);
-                    const uint32_t a2 = e4m3x2_to_bf16x2(c1 & 0xFFFFu), a3 = e4m3x2_to_bf16x2(c1 >> 16);
+                    const uint32_t pick = y ? 0x7362u : 0x5140u;
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_bf16(__byte_perm(vw[0][x], vw[1][x], pick), a0, a1);
+                    e4m3x4_to_bf16(__byte_perm(vw[2][x], vw[3][x], pick), a2, a3);
 #pragma unroll
                     for (int nt = 0; nt < NTH; ++nt)
                       mma_bf16_16816(o[nt][2 * x + y], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
+        if (mine && lane == 0) mbar_arrive(&empty[st]);
         if (++st == S) {
           st = 0;
           ph ^= 1;
@@ -554,13 +568,13 @@ __global__ void __launch_bounds__(kThreads, 1) stream_attn_kernel(
         const int h = e / (D / 2), pr = e % (D / 2);       // one head per warp and step
         float M = -INFINITY, N = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kConsWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
           M = fmaxf(M, sm_m[w][h]);
           N = fmaxf(N, sm_n[w][h]);
         }
         float L = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
-        for (int w = 0; w < kConsWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
           const float mw = sm_m[w][h];
           const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
           const float2 v = lds_f2(red + ((w * hpg + h) * C::kRedRow + pr * 2) * 4);
@@ -668,7 +682,7 @@ bool encode_codes_map(CUtensorMap* map, const void* base, const Shape& s) {
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE,
             s.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_bf16_cache_map(CUtensorMap* map, const void* base, const Shape& s) {
@@ -680,7 +694,7 @@ bool encode_bf16_cache_map(CUtensorMap* map, const void* base, const Shape& s) {
 
 template <int D, bool Q8, int NTH>
 cudaError_t launch_impl(const CacheView& c, StreamArgs& a, cudaStream_t st) {
-  using C = Cfg<D, Q8>;
+  using C = Cfg<D, Q8, NTH>;
   const int hpg = a.s.H / a.s.G;
   CUtensorMap tm_k, tm_v;
   if constexpr (Q8) {
@@ -690,16 +704,20 @@ cudaError_t launch_impl(const CacheView& c, StreamArgs& a, cudaStream_t st) {
     if (!encode_bf16_cache_map(&tm_k, c.k, a.s) || !encode_bf16_cache_map(&tm_v, c.v, a.s))
       return cudaErrorInvalidValue;
   }
-  const int fixed = 1024 + kQBufs * hpg * D * 2 + kConsWarps * hpg * C::kRedRow * 4;
+  const int fixed = 1024 + kQBufs * hpg * D * 2 + C::kWarps * hpg * C::kRedRow * 4;
   // static shared memory (barriers, row statistics) takes under 2 KiB
   a.stages = (kSmemMax - 2048 - fixed) / C::kStage;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
+  // a stage always serves the same team, whose waits on it then alternate in
+  // parity (a team that met a stage every other lap would take the phase
+  // before last for its own)
+  a.stages -= a.stages % C::kTeams;
   const int smem = fixed + a.stages * C::kStage;
   cudaError_t e = cudaFuncSetAttribute(stream_attn_kernel<D, Q8, NTH>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   note_launches(2);
-  stream_attn_kernel<D, Q8, NTH><<<a.nctas, kThreads, smem, st>>>(tm_k, tm_v, a);
+  stream_attn_kernel<D, Q8, NTH><<<a.nctas, C::kThreads, smem, st>>>(tm_k, tm_v, a);
   const int warps = (a.nctas - 1) * hpg;
   stream_finish_kernel<D><<<warps > 0 ? (warps + 7) / 8 : 1, 256, 0, st>>>(a);
   return cudaGetLastError();

@@ -642,9 +642,8 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         uint32_t h[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t c0 = w[j] & 0xFFFFu, c1 = w[j] >> 16;
-          h[2 * j] = !is_v ? e4m3x2_to_f16x2(c0) : dead ? 0u : e4m3x2_to_bf16x2(c0);
-          h[2 * j + 1] = !is_v ? e4m3x2_to_f16x2(c1) : dead ? 0u : e4m3x2_to_bf16x2(c1);
+          if (is_v) e4m3x4_to_bf16(dead ? 0u : w[j], h[2 * j], h[2 * j + 1]);
+          else e4m3x4_to_f16(w[j], h[2 * j], h[2 * j + 1]);
         }
         sts128(tile + tile_off(r, 2 * ch), make_uint4(h[0], h[1], h[2], h[3]));
         sts128(tile + tile_off(r, 2 * ch + 1), make_uint4(h[4], h[5], h[6], h[7]));

@@ -101,6 +101,21 @@ def test_window(msa, lens, T, H, G, D, window, sinks, kernels, q8):
 
 
 @pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("H,G,D", [(48, 8, 128), (24, 8, 64), (64, 4, 128), (8, 8, 128)])
+def test_long_decode_laps_every_ring(msa, H, G, D, q8):
+    # about 30 blocks per CTA: every stage of the block ring is reused several
+    # times, by both teams of warps where there are two
+    lens = [18000, 17000, 16500, 11111]
+    c, q, q_start = make(lens, 1, H, G, D, seed=73)
+    nb = c.table.shape[1]
+    out = run(msa, c, q8, q, q_start, lens, nb, 1 << 22, 0, "streaming")
+    k, v = c.values()
+    want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, 1 << 22, 0, "cuda"),
+                                 D ** -0.5, sr.U_BF16)
+    sr.check(out, want, bound)
+
+
+@pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("kernels", KERNELS)
 def test_window_past_the_context_is_dense_attention(msa, kernels, q8):
     # kv_len beyond the last query: the tokens behind it are not seen
