@@ -157,7 +157,6 @@ int msa_cache_append_q8(const msa_params* p, const int32_t* block_table, int num
   if ((rc = check_ws(ws, ws_bytes, kAlign))) return rc;
   if (p->T == 0) return MSA_OK;
   int* status = static_cast<int*>(ws);
-  if (cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return MSA_ERR_CUDA;
   return cuda_status(launch_cache_append_q8(shape_of(p, block_table, num_pool_blocks), pos, k_new,
                                             v_new, k_idx_new, k_cache, v_cache, k_exp, v_exp,
                                             k_idx_cache, status, stream));

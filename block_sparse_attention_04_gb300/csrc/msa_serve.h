@@ -51,7 +51,8 @@ cudaError_t launch_window_tc(const Shape& s, const Positions& pos, const CacheVi
                              int sinks, const uint16_t* q, uint16_t* out, int* status,
                              cudaStream_t st);
 
-// Appends tokens to an 8-bit cache (layouts of msa_cache_append_q8).
+// Appends tokens to an 8-bit cache (layouts of msa_cache_append_q8) and writes
+// the status word.
 cudaError_t launch_cache_append_q8(const Shape& s, const Positions& pos, const uint16_t* k_new,
                                    const uint16_t* v_new, const uint16_t* kidx_new, uint8_t* k,
                                    uint8_t* v, int8_t* k_exp, int8_t* v_exp, uint16_t* kidx,
