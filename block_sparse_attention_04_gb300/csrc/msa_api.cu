@@ -450,6 +450,17 @@ int msa_workspace_status(const void* ws, cudaStream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return MSA_ERR_CUDA;
   int v = 0;
   if (cudaMemcpy(&v, ws, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return MSA_ERR_CUDA;
+  if (v > 0 && (v & kDevWords)) {
+    int words[kMaxStatusWords];
+    const int n = v & ~kDevWords;
+    if (n > kMaxStatusWords) return MSA_ERR_CUDA;
+    if (cudaMemcpy(words, static_cast<const char*>(ws) + kAlign, n * sizeof(int),
+                   cudaMemcpyDeviceToHost) != cudaSuccess)
+      return MSA_ERR_CUDA;
+    v = 0;
+    for (int i = 0; i < n; ++i)     // a timeout before an invalid block
+      v = v == kDevTimeout || words[i] == kDevTimeout ? kDevTimeout : (words[i] > v ? words[i] : v);
+  }
   if (v == kDevTimeout) return MSA_ERR_TIMEOUT;
   if (v == kDevInvalid) return MSA_ERR_INVALID_ARG;
   if (v == kDevNoPages) return MSA_ERR_PAGES;

@@ -14,6 +14,9 @@ constexpr int kCand = MSA_TOPK - 1;   // ranked candidates besides the local blo
 constexpr int kMaxBatch = MSA_MAX_BATCH;
 constexpr int kDevTimeout = 1;        // status word value: a bounded wait ran out
 constexpr int kDevInvalid = 2;        // status word value: a selected id out of range
+constexpr int kDevWords = 1 << 30;    // flag of a status word that stands for the N words (its
+                                      // low bits) at byte 256 of the workspace, one per CTA
+constexpr int kMaxStatusWords = 512;
 constexpr int kDevNoPages = 3;        // status word value: no free page left
 
 // Poll cap of the kernels' pipeline waits (0: the wall-clock bound alone);

@@ -83,6 +83,21 @@ __device__ __forceinline__ uint2 lds64(uint32_t saddr) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(saddr));
   return v;
 }
+// Barrier over the cluster's CTAs (all threads), ordering their memory accesses.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Two floats at `saddr` in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t saddr, int rank) {
+  float2 v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %2, %3;\n"
+      " ld.shared::cluster.v2.f32 {%0, %1}, [a];\n}"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(saddr), "r"(rank));
+  return v;
+}
 __device__ __forceinline__ void sts128(uint32_t saddr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)

@@ -29,7 +29,9 @@
 // At a segment's end the eight warps' (O, m, l) are joined in shared memory; a
 // whole unit is written out directly, a cut one leaves a partial per CTA (at
 // most two: the unit its run begins inside, the one it ends inside) that
-// stream_finish_kernel joins.
+// stream_finish_kernel joins.  Small calls, where a launch counts, give every
+// unit a cluster of CTAs instead, which joins its parts through distributed
+// shared memory.
 #include "msa_q8.cuh"
 #include "msa_tma.h"
 
@@ -44,7 +46,7 @@ template <bool Q8, int NTH>
 constexpr int teams() { return Q8 && NTH == 1 ? 2 : 1; }
 constexpr int kQBufs = 2;
 constexpr int kMaxStages = 8;
-constexpr int kMaxCtas = 512;        // partials and error words in the workspace
+constexpr int kMaxCtas = kMaxStatusWords;        // partials and error words in the workspace
 constexpr int kPassRows = 2048;      // (sequence, query) rows per pass
 constexpr float kLazy = 8.f;         // log2 growth of p tolerated before O is rescaled
 constexpr int kSmemMax = 227 * 1024;
@@ -65,6 +67,7 @@ struct StreamArgs {
   int* errs;                      // [nctas]
   int* status;
   bool first_pass;
+  int parts;                      // > 0: a cluster of this many CTAs per unit
   uint32_t wait_polls;
 };
 
@@ -96,6 +99,18 @@ __device__ __forceinline__ Unit unit_of(const StreamArgs& a, int step) {
   u.g = ig % a.s.G;
   u.i = a.t0 + ig / a.s.G;
   u.t = a.q_start[lo] + u.i;
+  return u;
+}
+
+// The segment of a CTA in cluster form: part `rank` of unit blockIdx.x / parts
+// (units in order of sequence, query, group), list positions [p0, p1).
+__device__ __forceinline__ Unit unit_of_cluster(const StreamArgs& a) {
+  Unit u;
+  const int unit = (int)blockIdx.x / a.parts;
+  u.g = unit % a.s.G;
+  u.i = unit / a.s.G % a.Tp;
+  u.b = unit / a.s.G / a.Tp;
+  u.t = a.q_start[u.b] + u.i;
   return u;
 }
 
@@ -143,8 +158,26 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
   uint16_t* qbuf = reinterpret_cast<uint16_t*>(sm + S * C::kStage);       // [kQBufs][hpg][D]
   const uint32_t red = smem_u32(qbuf + kQBufs * hpg * D);                 // [kWarps][hpg][kRedRow] float
   const int steps = a.step0[s.B];
-  const int run0 = run_begin(steps, a.nctas, blockIdx.x);
-  const int run1 = run_begin(steps, a.nctas, blockIdx.x + 1);
+  // steps of this CTA; in cluster form one segment, numbered from 0
+  const int run0 = a.parts ? 0 : run_begin(steps, a.nctas, blockIdx.x);
+  const int run1 = a.parts ? 1 : run_begin(steps, a.nctas, blockIdx.x + 1);
+  // the segment that begins at `step`: its unit and list positions; the next step
+  auto segment = [&](int step, Unit& u, BlockList& bl, int& p0, int& p1) -> int {
+    if (a.parts) {
+      u = unit_of_cluster(a);
+      bl = list_of(a, u.t);
+      const int rank = (int)blockIdx.x % a.parts;
+      p0 = rank * bl.len / a.parts;
+      p1 = (rank + 1) * bl.len / a.parts;
+      return 1;
+    }
+    u = unit_of(a, step);
+    bl = list_of(a, u.t);
+    const int next = min(run1, u.first + u.len);
+    p0 = step - u.first;
+    p1 = min(next - u.first, bl.len);
+    return next;
+  };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -170,8 +203,10 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
     int nq = 0;
     bool ok = true;
     for (int step = run0, next; step < run1 && ok; step = next, ++k) {
-      const Unit u = unit_of(a, step);
-      next = min(run1, u.first + u.len);
+      Unit u;
+      BlockList bl;
+      int p0, p1;
+      next = segment(step, u, bl, p0, p1);
       const int qs = k % kQBufs;
       ok = __all_sync(0xffffffffu, k < kQBufs || mbar_wait(&q_empty[qs], ((k / kQBufs) - 1) & 1,
                                                            &err, a.wait_polls));
@@ -183,8 +218,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
                   &q_full[qs]);
       }
       ++nq;
-      const BlockList bl = list_of(a, u.t);
-      const int p0 = step - u.first, p1 = min(next - u.first, bl.len);
       const int32_t* srow =
           a.sel ? a.sel + (((int64_t)u.b * s.T + u.i) * G + u.g) * kTopk : nullptr;
       for (int pc = p0; pc < p1 && ok; pc += 32) {
@@ -264,10 +297,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
     uint32_t ph = 0;
     bool ok = true;
     for (int step = run0, next; step < run1; step = next, ++k) {
-      const Unit u = unit_of(a, step);
-      next = min(run1, u.first + u.len);
-      const BlockList bl = list_of(a, u.t);
-      const int nblk = min(next - u.first, bl.len) - (step - u.first);
+      Unit u;
+      BlockList bl;
+      int p0, p1;
+      next = segment(step, u, bl, p0, p1);
+      const int nblk = p1 - p0;
       const int lo = a.sel ? 0 : max(0, u.t - a.window + 1);   // visible: j <= t and
       const int sinks = a.sel ? 0 : a.sinks;                   // (j >= lo or j < sinks)
       const int qs = k % kQBufs;
@@ -562,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
           }
         }
       named_bar_sync(1, kConsumers);
-      const bool whole_unit = step == u.first && next == u.first + u.len;
+      const bool whole_unit = a.parts ? a.parts == 1 : step == u.first && next == u.first + u.len;
       const int64_t slot = 2 * blockIdx.x + (step == u.first);
       for (int e = threadIdx.x; e < hpg * (D / 2); e += kConsumers) {
         const int h = e / (D / 2), pr = e % (D / 2);       // one head per warp and step
@@ -589,6 +623,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
           const float inv = L == 0.f ? 0.f : ex2(M - N) / L;      // nothing visible: zeros
           uint16_t* dst = a.out + (((int64_t)u.b * s.T + u.i) * H + (int64_t)u.g * hpg + h) * D + dim;
           *reinterpret_cast<uint32_t*>(dst) = pack_bf16(x * inv, y * inv);
+        } else if (a.parts) {
+          // over the ring, whose blocks are all consumed
+          sts_f2(smem_u32(sm) + (h * D + dim) * 4, x, y);
+          if (pr == 0) sts128(smem_u32(sm) + (hpg * D + h * 4) * 4,
+                              make_uint4(__float_as_uint(M), __float_as_uint(N), __float_as_uint(L), 0));
         } else {
           *reinterpret_cast<float2*>(a.part_o + (slot * hpg + h) * D + dim) = make_float2(x, y);
           if (pr == 0) a.part_ml[slot * hpg + h] = make_float4(M, N, L, 0.f);
@@ -597,7 +636,43 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0) a.errs[blockIdx.x] = err;
+  if (a.parts > 1) {
+    // join the unit's parts: every CTA of the cluster takes a share of the
+    // outputs and reads all parts' sums from their shared memory
+    cluster_sync();
+    const Unit u = unit_of_cluster(a);
+    const int rank = (int)blockIdx.x % a.parts;
+    const uint32_t base = smem_u32(sm);
+    for (int e = rank * C::kThreads + threadIdx.x; e < hpg * (D / 2); e += a.parts * C::kThreads) {
+      const int h = e / (D / 2);
+      float M = -INFINITY, N = -INFINITY;
+      for (int r = 0; r < a.parts; ++r) {
+        const float2 mn = ld_cluster_f2(base + (hpg * D + h * 4) * 4, r);
+        M = fmaxf(M, mn.x);
+        N = fmaxf(N, mn.y);
+      }
+      float L = 0.f, x = 0.f, y = 0.f;
+#pragma unroll 4
+      for (int r = 0; r < a.parts; ++r) {
+        const float2 mn = ld_cluster_f2(base + (hpg * D + h * 4) * 4, r);
+        const float2 l = ld_cluster_f2(base + (hpg * D + h * 4 + 2) * 4, r);
+        const float2 v = ld_cluster_f2(base + e * 8, r);
+        const float f = mn.x == -INFINITY ? 0.f : ex2(mn.x - M);
+        L = fmaf(l.x, mn.y == -INFINITY ? 0.f : ex2(mn.y - N), L);
+        x = fmaf(v.x, f, x);
+        y = fmaf(v.y, f, y);
+      }
+      const float inv = L == 0.f ? 0.f : ex2(M - N) / L;
+      uint16_t* dst = a.out + (((int64_t)u.b * s.T + u.i) * H + (int64_t)u.g * hpg) * D + e * 2;
+      *reinterpret_cast<uint32_t*>(dst) = pack_bf16(x * inv, y * inv);
+    }
+    cluster_sync();   // no CTA leaves while its sums are read
+  }
+  if (threadIdx.x == 0) {
+    a.errs[blockIdx.x] = err;
+    // cluster form: no kernel follows that joins the words; the reader does
+    if (a.parts && blockIdx.x == 0) *a.status = kDevWords | (int)gridDim.x;
+  }
 }
 
 // The worse of two error words (a timeout before an invalid block).
@@ -665,6 +740,18 @@ __global__ void __launch_bounds__(256) stream_finish_kernel(const __grid_constan
     *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
 }
 
+// CTAs per unit in cluster form, 0: runs.  A cluster joins its parts itself,
+// which saves the second launch (about 3 us, the time of kSpare blocks), but
+// gives a CTA ceil(longest list / parts) blocks where runs give it the average.
+// A cluster's CTAs (one per SM) share one of the 8 GPCs, of at least 16 SMs.
+constexpr int kMaxCluster = 8, kSpare = 4, kGpcs = 8, kGpcSms = 16;
+int cluster_parts(int units, int longest, int64_t steps, int ctas) {
+  int parts = longest < kMaxCluster ? longest : kMaxCluster;
+  while (parts > 0 && units > kGpcs * (kGpcSms / parts)) --parts;
+  if (parts == 0) return 0;
+  return (longest + parts - 1) / parts <= steps / ctas + kSpare ? parts : 0;
+}
+
 int list_len(const Visible& vis, int t) {
   if (vis.sel) return kTopk;
   const int lo = (t - vis.window + 1 > 0 ? t - vis.window + 1 : 0) / kBlock;
@@ -716,6 +803,21 @@ cudaError_t launch_impl(const CacheView& c, StreamArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(stream_attn_kernel<D, Q8, NTH>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  if (a.parts) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.s.B * a.Tp * a.s.G * a.parts);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = a.parts;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    note_launches(1);
+    return cudaLaunchKernelEx(&cfg, stream_attn_kernel<D, Q8, NTH>, tm_k, tm_v, a);
+  }
   note_launches(2);
   stream_attn_kernel<D, Q8, NTH><<<a.nctas, C::kThreads, smem, st>>>(tm_k, tm_v, a);
   const int warps = (a.nctas - 1) * hpg;
@@ -785,6 +887,12 @@ cudaError_t launch_stream_attn(const Shape& s, const Positions& pos, const Cache
     for (int b = 0; b < s.B; ++b) a.step0[b + 1] = a.step0[b] + a.Tp * s.G * len[b];
     const int steps = a.step0[s.B];
     a.nctas = steps < ctas ? steps : ctas;
+    a.parts = 0;
+    if (a.Tp == s.T && !join_status) {
+      int longest = 1;
+      for (int b = 0; b < s.B; ++b) longest = len[b] > longest ? len[b] : longest;
+      a.parts = cluster_parts(s.B * a.Tp * s.G, longest, steps, ctas);
+    }
     const bool wide = s.H / s.G > 8;    // heads of a group in one or two n-tiles of 8
     cudaError_t e;
     if (s.D == 128 && c.kv8)
