@@ -14,9 +14,11 @@
 // bound by the tensor cores and, next to them, by the exponentials.
 //   warp 0        takes items from a shared counter; TMA of the Q tiles
 //   warp 1        bf16 cache: TMA of K and V blocks, 2-deep rings
-//   warp 2        tcgen05.mma, per block: P.V(c0, n-1), S(c0, n), P.V(c1, n-1),
-//                 S(c1, n); S and P share TMEM columns [128c, 128c + 128), O is
-//                 at [256 + 128c, ...).  Rows of V that no query of the item
+//   warp 2        tcgen05.mma, per block n: P.V(c0, n-1), S(c0, n), P.V(c1, n-1),
+//                 S(c1, n), also across items (each chain's Q tile is reloaded
+//                 when its last S is done, so the next item's first S follows
+//                 the last P.V); S and P share TMEM columns [128c, 128c + 128),
+//                 O is at [256 + 128c, ...).  Rows of V that no query of the item
 //                 sees (they may hold anything) are zeroed before their first
 //                 use: a weight of 0 does not cancel a NaN.
 //   warps 3-10    one warpgroup per chain, a row per thread: mask, maximum,
@@ -35,8 +37,6 @@
 // latter by one factor per row and block, 2^(m - ev - n), unless that factor is
 // so large that p' may have vanished (blocks whose scale is 2^80 below the
 // others', such as blocks of zeros): then it is summed by exponentials of its own.
-#include <type_traits>
-
 #include "msa_q8.cuh"
 #include "msa_serve.h"
 #include "msa_tma.h"
@@ -132,10 +132,10 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
   uint8_t* sV = sK + kStages * C::kTile;      // [kStages] V blocks
   float* q_scale = reinterpret_cast<float*>(sV + kStages * C::kTile);   // [2][chain][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(q_scale + 2 * 2 * 128);
-  uint64_t* q_full = bars;                    // both Q tiles of the item landed
-  uint64_t* q_ready = q_full + 1;             // ... and are in f16 (8-bit cache)
-  uint64_t* q_empty = q_ready + 1;            // the item's last S MMAs are done
-  uint64_t* k_full = q_empty + 1;             // kStages
+  uint64_t* q_full = bars;                    // per chain: the item's Q tile landed
+  uint64_t* q_ready = q_full + 2;             // ... and is in f16 (8-bit cache)
+  uint64_t* q_empty = q_ready + 2;            // per chain: the item's last S is done
+  uint64_t* k_full = q_empty + 2;             // kStages
   uint64_t* k_empty = k_full + kStages;
   uint64_t* v_full = k_empty + kStages;
   uint64_t* v_empty = v_full + kStages;
@@ -153,9 +153,6 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = a.s.T, H = a.s.H, hpg = H / a.s.G, nq = a.nq;
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_ready, kConv);
-    mbar_init(q_empty, 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&k_full[i], Q8 ? kConv : 1);
       mbar_init(&k_empty[i], 1);
@@ -163,6 +160,9 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
       mbar_init(&v_empty[i], 1);
     }
     for (int c = 0; c < 2; ++c) {
+      mbar_init(&q_full[c], 1);
+      mbar_init(&q_ready[c], kConv);
+      mbar_init(&q_empty[c], 1);
       mbar_init(&s_full[c], 1);
       mbar_init(&p_full[c], 128);
       mbar_init(&o_full[c], 1);
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
       if (cur >= a.nitems) cur = -1;
       item_ring[0] = cur;
       mbar_arrive(&it_full[0]);
-      int k = 0;
+      int k = 0, loads[2] = {0, 0};
       for (; cur >= 0; ++k) {
         const int r = k + 1, slot = r % kItemRing;
         if (r >= kItemRing &&
@@ -223,26 +223,34 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         item_ring[slot] = nx;
         mbar_arrive(&it_full[slot]);
         const Item d = item_of(a, cur);
-        if (k > 0 && !mbar_wait(q_empty, (k - 1) & 1, a.status, a.wait_polls)) {
-          *abort_flag = 1;
-          break;
-        }
         // a tile that begins behind the last query is loaded from the first
         // one instead: its rows are computed and never written
-        mbar_arrive_expect_tx(q_full, 2 * rows * D * 2);
+        bool ok = true;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+          if (k > 0 && !mbar_wait(&q_empty[c], (k - 1) & 1, a.status, a.wait_polls)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&q_full[c], rows * D * 2);
+          loads[c] = k + 1;
           const int i = d.i0 + c * nq;
           const int z = d.b * T + (i < T ? i : d.i0);
 #pragma unroll
           for (int h = 0; h < C::kNHalf; ++h)
-            tma_load_3d_hint(smem_u32(sQ + c * C::kTile + h * C::kHalf), &tm_q, q_full, h * 64,
+            tma_load_3d_hint(smem_u32(sQ + c * C::kTile + h * C::kHalf), &tm_q, &q_full[c], h * 64,
                              d.g * hpg, z, pol);
+        }
+        if (!ok) {
+          *abort_flag = 1;
+          break;
         }
         cur = nx;
       }
       // no copy may still be landing when the CTA exits
-      if (k > 0) mbar_wait(q_full, (k - 1) & 1, nullptr);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (loads[c] > 0) mbar_wait(&q_full[c], (loads[c] - 1) & 1, nullptr);
     }
   } else if (warp == kKVWarp) {
     // ----------------------------------------------------- K/V TMA (warp 1)
@@ -303,88 +311,100 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
     const uint64_t qdesc0 = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
     const uint64_t kdesc0 = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
     const uint64_t vdesc0 = smem_desc(smem_u32(sV), C::kHalf, 1024, kSwizzle128B);
-    int n = 0, k = 0;
-    bool ok = true;
-    for (; ok; ++k) {
+    int n = 0, k = 0, p = 0;         // block steps issued, items begun, block of the item
+    bool ok = true, has_s = true, has_pv = false;
+    Item d;
+    d.nblk = 0;
+    // the block whose P.V is due: stage, wait parity, visible rows, first / last of its item
+    int pks = 0, phi = 0, plo = 0, psk = 0;
+    uint32_t pw = 0;
+    bool pfirst = false, plast = false;
+    while (ok) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
-      const int it = take_item(k);
-      if (it < 0) {
-        ok = it == -1;
-        break;
-      }
-      const Item d = item_of(a, it);
-      ok = __all_sync(0xffffffffu,
-                      mbar_wait(Q8 ? q_ready : q_full, k & 1, a.status, a.wait_polls));
-      if (!ok) break;
-      int pks = 0;
-      uint32_t pw = 0;
-      for (int p = 0; p <= d.nblk && ok; ++p) {
-        const bool has_s = p < d.nblk;
-        const int ks = n % kStages;
-        const uint32_t w = (uint32_t)(n / kStages);
-        bool okl = !has_s || mbar_wait(&k_full[ks], w & 1, a.status, a.wait_polls);
-        if (p > 0) okl = okl && mbar_wait(&v_full[pks], pw & 1, a.status, a.wait_polls);
-        ok = __all_sync(0xffffffffu, okl);
-        if (!ok) break;
-        if (!Q8 && p > 0) {
-          // rows of V that no query of the item sees
-          const int tok0 = block_at(d, p - 1) * kBlock;
-          const int hi = d.t_last - tok0, lo = d.lo - tok0, sk = a.sinks - tok0;
-          if (hi < kBlock - 1 || (lo > 0 && sk < kBlock)) {
-            const uint32_t v = smem_u32(sV + pks * C::kTile);
-            for (int e = lane; e < kBlock * (D / 8); e += 32) {
-              const int r = e / (D / 8);
-              if (r > hi || (r < lo && r >= sk))
-                sts128(v + tile_off(r, e % (D / 8)), make_uint4(0, 0, 0, 0));
-            }
-            fence_async();
-            __syncwarp();
-          }
+      if (has_s && p == d.nblk) {    // the next item
+        const int it = take_item(k);
+        if (it == -2) { ok = false; break; }
+        has_s = it >= 0;
+        if (has_s) {
+          d = item_of(a, it);
+          p = 0;
+          ++k;
         }
-        for (int c = 0; c < 2; ++c) {
-          if (p > 0) {
-            // ---- P.V(c, p - 1): P in TMEM columns [128c, 128c + 64)
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait(&p_full[c], (uint32_t)(n - 1) & 1, a.status, a.wait_polls));
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t vd = vdesc0 + (uint64_t)((pks * C::kTile) >> 4);
-            if (elect_one()) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                tc_mma_f16_ts(tmem + 256 + c * 128, tmem + c * 128 + j * 8,
-                              vd + (uint64_t)((j * 2048) >> 4), idesc_o, (p > 1 || j > 0) ? 1u : 0u);
-              if (!has_s) tc_commit(&o_full[c]);
-              if (c == 1) tc_commit(&v_empty[pks]);
-            }
-            __syncwarp();
+      }
+      if (!has_s && !has_pv) break;
+      const int ks = n % kStages;
+      const uint32_t w = (uint32_t)(n / kStages);
+      if (has_pv) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&v_full[pks], pw & 1, a.status, a.wait_polls));
+        if (!ok) break;
+        if (!Q8 && (phi < kBlock - 1 || (plo > 0 && psk < kBlock))) {
+          // rows of V that no query of the item sees
+          const uint32_t v = smem_u32(sV + pks * C::kTile);
+          for (int e = lane; e < kBlock * (D / 8); e += 32) {
+            const int r = e / (D / 8);
+            if (r > phi || (r < plo && r >= psk))
+              sts128(v + tile_off(r, e % (D / 8)), make_uint4(0, 0, 0, 0));
           }
-          if (has_s) {
-            // ---- S(c, p) = Q_c K_p^T
-            tc_fence_after();
-            const uint64_t qd = qdesc0 + (uint64_t)((c * C::kTile) >> 4);
-            const uint64_t kd = kdesc0 + (uint64_t)((ks * C::kTile) >> 4);
-            if (elect_one()) {
+          fence_async();
+          __syncwarp();
+        }
+      }
+      for (int c = 0; c < 2; ++c) {
+        if (has_pv) {
+          // ---- P.V(c, n - 1): P in TMEM columns [128c, 128c + 64)
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&p_full[c], (uint32_t)(n - 1) & 1, a.status, a.wait_polls));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = vdesc0 + (uint64_t)((pks * C::kTile) >> 4);
+          if (elect_one()) {
 #pragma unroll
-              for (int j = 0; j < D / 16; ++j)  // 16 dims: (j & 3) * 32 bytes within a 64-dim half
-                tc_mma_f16(tmem + c * 128,
-                           qd + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4),
-                           kd + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4), idesc_s,
-                           j > 0 ? 1u : 0u);
-              tc_commit(&s_full[c]);
-              if (c == 1) {
-                tc_commit(&k_empty[ks]);
-                if (p + 1 == d.nblk) tc_commit(q_empty);
-              }
-            }
-            __syncwarp();
+            for (int j = 0; j < 8; ++j)
+              tc_mma_f16_ts(tmem + 256 + c * 128, tmem + c * 128 + j * 8,
+                            vd + (uint64_t)((j * 2048) >> 4), idesc_o, (!pfirst || j > 0) ? 1u : 0u);
+            if (plast) tc_commit(&o_full[c]);
+            if (c == 1) tc_commit(&v_empty[pks]);
           }
+          __syncwarp();
         }
         if (has_s) {
-          pks = ks;
-          pw = w;
-          ++n;
+          // ---- S(c, n) = Q_c K^T
+          bool okl = true;
+          if (p == 0)
+            okl = mbar_wait(Q8 ? &q_ready[c] : &q_full[c], (k - 1) & 1, a.status, a.wait_polls);
+          if (c == 0) okl = okl && mbar_wait(&k_full[ks], w & 1, a.status, a.wait_polls);
+          ok = __all_sync(0xffffffffu, okl);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t qd = qdesc0 + (uint64_t)((c * C::kTile) >> 4);
+          const uint64_t kd = kdesc0 + (uint64_t)((ks * C::kTile) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)  // 16 dims: (j & 3) * 32 bytes within a 64-dim half
+              tc_mma_f16(tmem + c * 128,
+                         qd + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4),
+                         kd + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4), idesc_s,
+                         j > 0 ? 1u : 0u);
+            tc_commit(&s_full[c]);
+            if (c == 1) tc_commit(&k_empty[ks]);
+            if (p + 1 == d.nblk) tc_commit(&q_empty[c]);
+          }
+          __syncwarp();
         }
+      }
+      if (!ok) break;
+      has_pv = has_s;
+      if (has_s) {
+        const int tok0 = block_at(d, p) * kBlock;
+        pks = ks;
+        pw = w;
+        phi = d.t_last - tok0;
+        plo = d.lo - tok0;
+        psk = a.sinks - tok0;
+        pfirst = p == 0;
+        plast = p + 1 == d.nblk;
+        ++p;
+        ++n;
       }
     }
     if (!ok && lane == 0) *abort_flag = 1;
@@ -432,50 +452,74 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
           f = fminf(fmaxf(fr * pow2i(e.x), -3e38f), 3e38f);
           ev = (float)e.y;
         }
-        // visible columns: [lo, hi] and [0, sk)
+        // visible columns: [lo, hi] and [0, sk).  Of a masked block's four
+        // chunks of 32 columns, those that all rows of the warp see take the
+        // unmasked path and those that none sees are skipped.
         const int tok0 = block_at(d, p) * kBlock;
         const int hi = tq - tok0, lo = tlo - tok0, sk = a.sinks - tok0;
         const bool masked =
             __any_sync(0xffffffffu, hi < kBlock - 1 || (lo > 0 && sk < kBlock));
         uint32_t vis[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) vis[w] = below(hi + 1, w) & (~below(lo, w) | below(sk, w));
-        // pass 1: row maximum of x = f s (of the smallest s when f < 0);
-        // unmasked blocks: reduced by the loads
-        float mx = -INFINITY;
+        int full = 0xF, empty = 0;       // chunks that all rows, no row sees
         if (masked) {
+          full = 0;
 #pragma unroll
-          for (int cc = 0; cc < 8; ++cc) {
-            uint32_t h[16];
-            tmem_ld16(s_base + cc * 16, h);
-            tmem_ld_wait();
-            const uint32_t vw = vis[cc >> 1] >> ((cc & 1) * 16);
+          for (int w = 0; w < 4; ++w) {
+            vis[w] = below(hi + 1, w) & (~below(lo, w) | below(sk, w));
+            full |= (__all_sync(0xffffffffu, vis[w] == 0xFFFFFFFFu) ? 1 : 0) << w;
+            empty |= (__all_sync(0xffffffffu, vis[w] == 0u) ? 1 : 0) << w;
+          }
+        }
+        // pass 1: row maximum of x = f s; whole chunks are reduced by the
+        // loads (to the smallest s when f < 0)
+        const bool up = __all_sync(0xffffffffu, f >= 0.f);
+        float mx = -INFINITY;
+        if (!masked) {
+          if (up) {
+            float s = -INFINITY;
+#pragma unroll 1
+            for (int cc = 0; cc < 8; cc += 2) {
+              const float r0 = tmem_ld16_red<true>(s_base + cc * 16);
+              const float r1 = tmem_ld16_red<true>(s_base + cc * 16 + 16);
+              tmem_ld_wait();
+              s = fmax3(s, r0, r1);
+            }
+            mx = s * f;
+          } else {
+            float s = INFINITY;
+#pragma unroll 1
+            for (int cc = 0; cc < 8; cc += 2) {
+              const float r0 = tmem_ld16_red<false>(s_base + cc * 16);
+              const float r1 = tmem_ld16_red<false>(s_base + cc * 16 + 16);
+              tmem_ld_wait();
+              s = fmin3(s, r0, r1);
+            }
+            mx = s * f;
+          }
+        } else {
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            if (empty >> cc & 1) continue;
+            if (full >> cc & 1) {
+              const float r0 = up ? tmem_ld16_red<true>(s_base + cc * 32)
+                                  : tmem_ld16_red<false>(s_base + cc * 32);
+              const float r1 = up ? tmem_ld16_red<true>(s_base + cc * 32 + 16)
+                                  : tmem_ld16_red<false>(s_base + cc * 32 + 16);
+              tmem_ld_wait();
+              mx = fmaxf(mx, fmaxf(r0 * f, r1 * f));
+            } else {
+              const uint32_t vw = cc == 0 ? vis[0] : cc == 1 ? vis[1] : cc == 2 ? vis[2] : vis[3];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = __uint_as_float(h[e]) * f;
-              mx = fmaxf(mx, vw >> e & 1 ? x : -INFINITY);
+              for (int hf = 0; hf < 2; ++hf) {
+                uint32_t h[16];
+                tmem_ld16(s_base + cc * 32 + hf * 16, h);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  mx = fmaxf(mx, vw >> (hf * 16 + e) & 1 ? __uint_as_float(h[e]) * f : -INFINITY);
+              }
             }
           }
-        } else if (__all_sync(0xffffffffu, f >= 0.f)) {
-          float s = -INFINITY;
-#pragma unroll 1
-          for (int cc = 0; cc < 8; cc += 2) {
-            const float r0 = tmem_ld16_red<true>(s_base + cc * 16);
-            const float r1 = tmem_ld16_red<true>(s_base + cc * 16 + 16);
-            tmem_ld_wait();
-            s = fmax3(s, r0, r1);
-          }
-          mx = s * f;
-        } else {
-          float s = INFINITY;
-#pragma unroll 1
-          for (int cc = 0; cc < 8; cc += 2) {
-            const float r0 = tmem_ld16_red<false>(s_base + cc * 16);
-            const float r1 = tmem_ld16_red<false>(s_base + cc * 16 + 16);
-            tmem_ld_wait();
-            s = fmin3(s, r0, r1);
-          }
-          mx = s * f;
         }
         // lazy rescale: a new reference only when the maximum grew by more
         // than kLazy (always at the row's first visible token)
@@ -515,11 +559,13 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
             float ls = 0.f;
 #pragma unroll 1
             for (int cc = 0; cc < 8; ++cc) {
+              if (empty >> (cc >> 1) & 1) continue;
               uint32_t h[16];
               tmem_ld16(s_base + cc * 16, h);
               tmem_ld_wait();
-              const uint32_t vw = (cc < 2 ? vis[0] : cc < 4 ? vis[1] : cc < 6 ? vis[2] : vis[3]) >>
-                                  ((cc & 1) * 16);
+              uint32_t vw = 0xFFFFFFFFu;
+              if (!(full >> (cc >> 1) & 1))
+                vw = (cc < 2 ? vis[0] : cc < 4 ? vis[1] : cc < 6 ? vis[2] : vis[3]) >> ((cc & 1) * 16);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 ls += vw >> e & 1 ? ex2(fmaf(__uint_as_float(h[e]), f, -nn)) : 0.f;
@@ -532,35 +578,61 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         // [16cc, 16cc + 16), already read, are written); row sum
         const float2 f2 = make_float2(f, f), nm2 = make_float2(-mn, -mn);
         float2 lsum = make_float2(0.f, 0.f);
-        auto pass2 = [&](auto mask_tag) {
-          constexpr bool kMask = decltype(mask_tag)::value;
+        // columns [32cc, 32cc + 32) that every row sees
+        auto whole_chunk = [&](int cc, uint32_t (&wv)[16]) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t h[16];
+            tmem_ld16(s_base + cc * 32 + hf * 16, h);
+            tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const float2 x = ffma2(
+                  make_float2(__uint_as_float(h[2 * u]), __uint_as_float(h[2 * u + 1])), f2, nm2);
+              const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+              lsum = fadd2(lsum, pp);
+              wv[hf * 8 + u] = pack_bf16(pp.x, pp.y);
+            }
+          }
+        };
+        if (!masked) {
 #pragma unroll 1
           for (int cc = 0; cc < 4; ++cc) {
             uint32_t wv[16];
-            const uint32_t vw = !kMask ? 0u : cc == 0 ? vis[0] : cc == 1 ? vis[1]
-                                                  : cc == 2 ? vis[2] : vis[3];
+            whole_chunk(cc, wv);
+            tmem_st16(s_base + cc * 16, wv);
+          }
+        } else {
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t wv[16];
+            if (empty >> cc & 1) {
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              uint32_t h[16];
-              tmem_ld16(s_base + cc * 32 + hf * 16, h);
-              tmem_ld_wait();
+              for (int u = 0; u < 16; ++u) wv[u] = 0u;
+            } else if (full >> cc & 1) {
+              whole_chunk(cc, wv);
+            } else {
+              const uint32_t vw = cc == 0 ? vis[0] : cc == 1 ? vis[1] : cc == 2 ? vis[2] : vis[3];
 #pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                const float2 x = ffma2(
-                    make_float2(__uint_as_float(h[2 * u]), __uint_as_float(h[2 * u + 1])), f2, nm2);
-                float2 pp = make_float2(ex2(x.x), ex2(x.y));
-                if constexpr (kMask) {
-                  pp.x = vw >> (hf * 16 + 2 * u) & 1 ? pp.x : 0.f;
-                  pp.y = vw >> (hf * 16 + 2 * u + 1) & 1 ? pp.y : 0.f;
+              for (int hf = 0; hf < 2; ++hf) {
+                uint32_t h[16];
+                tmem_ld16(s_base + cc * 32 + hf * 16, h);
+                tmem_ld_wait();
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                  const float2 x = ffma2(
+                      make_float2(__uint_as_float(h[2 * u]), __uint_as_float(h[2 * u + 1])), f2, nm2);
+                  float2 pp;
+                  pp.x = vw >> (hf * 16 + 2 * u) & 1 ? ex2(x.x) : 0.f;
+                  pp.y = vw >> (hf * 16 + 2 * u + 1) & 1 ? ex2(x.y) : 0.f;
+                  lsum = fadd2(lsum, pp);
+                  wv[hf * 8 + u] = pack_bf16(pp.x, pp.y);
                 }
-                lsum = fadd2(lsum, pp);
-                wv[hf * 8 + u] = pack_bf16(pp.x, pp.y);
               }
             }
             tmem_st16(s_base + cc * 16, wv);
           }
-        };
-        if (masked) pass2(std::true_type{}); else pass2(std::false_type{});
+        }
         const float ls = lsum.x + lsum.y;
         if constexpr (Q8) {
           if (!apart) l = fmaf(ls, ex2(mn - nn), l);
@@ -651,10 +723,10 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
     };
     // Q tiles of item k to f16, each row scaled to a maximum in [2^13, 2^14)
     auto convert_q = [&](int k) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(q_full, (uint32_t)k & 1, a.status, a.wait_polls)))
-        return false;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&q_full[c], (uint32_t)k & 1, a.status, a.wait_polls)))
+          return false;
         const uint32_t tile = smem_u32(sQ + c * C::kTile);
         uint32_t mx = 0;
 #pragma unroll 4
@@ -677,9 +749,9 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
                             pack_f16(bf16lo(v.w) * f, bf16hi(v.w) * f)));
         }
         q_scale[((k & 1) * 2 + c) * 128 + tid] = pow2i(e - 13);
+        fence_async();
+        mbar_arrive(&q_ready[c]);
       }
-      fence_async();
-      mbar_arrive(q_ready);
       return true;
     };
     int n = 0, k = 0;
