@@ -5,14 +5,16 @@
 //
 // Every operation gives the same result whatever order its threads run in:
 // counts change by integer atomics, table entries are claimed by exchanges,
-// and pages are dealt by rank (the lowest free id first).  A list of free
-// pages is made by CTAs that each count the free pages before their own chunk
-// (reading the counts once more costs less than a second launch up to about
-// a million pages).  Page contents move in 16-byte chunks, four per thread in
-// flight; copying is bound by HBM, 2 bytes per byte moved, the rest by launch
-// latency.
-#include "msa_device.cuh"
+// and pages are dealt by rank (the lowest free id first).  The bookkeeping is
+// bound by launch latency, so each operation does all of it in one launch: one
+// cluster of CTAs whose steps are separated by cluster barriers, and whose
+// error words are joined at the end into the status (no clearing launch).
+// Fork of 32 sequences: four launches and a clearing FORKOLD us, now FORKNEW us.
+// Page contents move in 16-byte chunks, four per thread in flight, by a grid of
+// their own; copying is bound by HBM, 2 bytes per byte moved (COMPACTBW TB/s in
+// the compaction of 4096 pages of 278 KB).
 #include "msa_pages.h"
+#include "msa_q8.cuh"
 #include "msa_tma.h"
 
 namespace msa {
@@ -20,33 +22,50 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kSeg = kThreads * 16 * 4;   // bytes of a page copied by one CTA step
-constexpr int kMaxListCtas = 128;
-constexpr int kChunk = 1024;              // least pages of a free-list CTA
+constexpr int kBook = 1024;               // threads of a bookkeeping CTA
+constexpr int kBookCtas = 8;              // CTAs of the bookkeeping cluster
 
-// The workspace: status word; then per-page words of the free list, or of a
-// compaction the holes, the pages that fill them and each page's fate.
+// The workspace: status word; then per-page words: the free list (and fork's
+// source and destination pages), or of a compaction the holes, the pages that
+// fill them and each page's fate.
 constexpr size_t kWsHead = 256;
 struct PageWs {
   int* status;
-  int32_t* count;   // pages listed (free list) or moved (compaction)
-  int32_t* live;
+  int32_t* count;   // pages that a compaction moves
   int32_t* x;       // free list, or holes
-  int32_t* y;       // movers
-  int32_t* z;       // fates
+  int32_t* y;       // source pages, or movers
+  int32_t* z;       // destination pages, or fates
 };
 PageWs carve(char* ws, int pages) {
   int32_t* w = reinterpret_cast<int32_t*>(ws);
   PageWs p;
   p.status = w;
   p.count = w + 1;
-  p.live = w + 2;
   p.x = w + kWsHead / 4;
-  p.y = p.x + pages;
-  p.z = p.y + pages;
+  const int n = pages > kMaxBatch ? pages : kMaxBatch;
+  p.y = p.x + n;
+  p.z = p.y + n;
   return p;
 }
 
-__device__ __forceinline__ void flag(int* status, int code) { atomicMax(status, code); }
+// The worse of two codes (no page left before an invalid entry).
+__device__ __forceinline__ int worse(int x, int y) { return max(x, y); }
+
+// Joins every thread's code over the cluster and writes the status; a barrier
+// over the cluster.
+__device__ __forceinline__ void write_status(int code, int* status) {
+  __shared__ int sm_code;
+  if (threadIdx.x == 0) sm_code = 0;
+  __syncthreads();
+  if (code) atomicMax(&sm_code, code);
+  cluster_sync();
+  if (cluster_rank() == 0 && threadIdx.x == 0) {
+    int c = 0;
+    for (int r = 0; r < kBookCtas; ++r) c = worse(c, ld_cluster_int(&sm_code, r));
+    *status = c;
+  }
+  cluster_sync();   // no CTA leaves while its word is read
+}
 
 // ---- page contents ---------------------------------------------------------
 struct CopyPlan {
@@ -98,65 +117,31 @@ __global__ void __launch_bounds__(kThreads) pages_copy_kernel(const __grid_const
                                                               const int32_t* __restrict__ src,
                                                               const int32_t* __restrict__ dst,
                                                               int n, int* status) {
+  auto bad = [&](int j) {
+    const int s = src[j], d = dst[j];
+    return s < 0 || s >= pages || d < 0 || d >= pages;
+  };
+  if (blockIdx.x == 0) {   // the first CTA looks all pairs over and writes the status
+    bool any = false;
+    for (int j = threadIdx.x; j < n; j += kThreads) any |= bad(j);
+    any = __syncthreads_or(any);
+    if (threadIdx.x == 0) *status = any ? kDevInvalid : 0;
+  }
   const int segs = c.seg0[c.ps.n];
   for (int64_t w = blockIdx.x; w < (int64_t)n * segs; w += gridDim.x) {
     const int j = (int)(w / segs), seg = (int)(w % segs);
-    const int s = src[j], d = dst[j];
-    if (s < 0 || s >= pages || d < 0 || d >= pages) {
-      if (threadIdx.x == 0) flag(status, kDevInvalid);
-      continue;
-    }
-    if (s != d) copy_segment(c, seg, s, d, kBlock);
+    if (!bad(j) && src[j] != dst[j]) copy_segment(c, seg, src[j], dst[j], kBlock);
   }
 }
 
 // ---- reference counts --------------------------------------------------------
-// One mapping of page e less; a page that no entry mapped is flagged and kept at 0.
-__device__ __forceinline__ void release(const PageTable& pt, int e, int* status) {
-  if (e == -1) return;
-  if (e < 0 || e >= pt.pages) {
-    flag(status, kDevInvalid);
-    return;
-  }
-  if (atomicSub(pt.refs + e, 1) <= 0) {
-    atomicAdd(pt.refs + e, 1);
-    flag(status, kDevInvalid);
-  }
-}
-
-__global__ void __launch_bounds__(256) pages_free_kernel(PageTable pt,
-                                                         const __grid_constant__ RowList rl,
-                                                         int* status) {
-  const int j = blockIdx.y;
-  int32_t* row = pt.table + (int64_t)rl.a[j] * pt.max_blocks;
-  for (int kb = rl.b[j] + blockIdx.x * blockDim.x + threadIdx.x; kb < rl.c[j];
-       kb += gridDim.x * blockDim.x)
-    release(pt, atomicExch(row + kb, -1), status);
-}
-
-// Fork, step 1: the destination row lets go of its pages and takes the
-// source's complete ones.
-__global__ void __launch_bounds__(256) pages_share_kernel(PageTable pt,
-                                                          const __grid_constant__ RowList rl,
-                                                          int* status) {
-  const int j = blockIdx.y, whole = rl.c[j] / kBlock;
-  const int32_t* src = pt.table + (int64_t)rl.a[j] * pt.max_blocks;
-  int32_t* dst = pt.table + (int64_t)rl.b[j] * pt.max_blocks;
-  for (int kb = blockIdx.x * blockDim.x + threadIdx.x; kb < pt.max_blocks;
-       kb += gridDim.x * blockDim.x) {
-    int e = -1;
-    if (kb < whole) {
-      e = src[kb];
-      if (e < 0 || e >= pt.pages) {
-        flag(status, kDevInvalid);
-        e = -1;
-      } else {
-        atomicAdd(pt.refs + e, 1);
-      }
-    }
-    release(pt, dst[kb], status);
-    dst[kb] = e;
-  }
+// One mapping of page e less; a page that no entry mapped is reported and kept at 0.
+__device__ __forceinline__ int release(const PageTable& pt, int e) {
+  if (e == -1) return 0;
+  if (e < 0 || e >= pt.pages) return kDevInvalid;
+  if (atomicSub(pt.refs + e, 1) > 0) return 0;
+  atomicAdd(pt.refs + e, 1);
+  return kDevInvalid;
 }
 
 // Sum of v over the CTA (every thread gets it).
@@ -184,95 +169,182 @@ __device__ __forceinline__ int cta_rank(bool f, int* sm, int* total) {
   *total = all;
   return before + __popc(m & ((1u << lane) - 1));
 }
-// Pages of [lo, hi) in use, counted by the CTA.
+// Pages of [lo, hi) in use, counted by the CTA (past L1: the counts may have
+// changed in this launch).
 __device__ __forceinline__ int cta_live(const int32_t* refs, int lo, int hi, int* sm) {
   int n = 0;
-  for (int i = lo + threadIdx.x; i < hi; i += blockDim.x) n += refs[i] > 0;
+  for (int i = lo + threadIdx.x; i < hi; i += blockDim.x) n += __ldcg(refs + i) > 0;
   return cta_sum(n, sm);
 }
 
-// Free pages in ascending order; CTA c lists those of chunk c.
-__global__ void __launch_bounds__(1024) pages_list_kernel(const int32_t* __restrict__ refs, int pages,
-                                                          int chunk, PageWs w) {
-  __shared__ int sm[32];
-  const int lo = blockIdx.x * chunk, hi = min(pages, lo + chunk);
-  int r = lo - cta_live(refs, 0, lo, sm);
-  for (int i0 = lo; i0 < hi; i0 += blockDim.x) {
+// This CTA's share of the cluster's pages.
+__device__ __forceinline__ void page_range(int pages, int& lo, int& hi) {
+  const int chunk = (pages + kBookCtas - 1) / kBookCtas;
+  lo = min(pages, cluster_rank() * chunk);
+  hi = min(pages, lo + chunk);
+}
+
+// The first `most` free pages in ascending order into list, by the cluster;
+// returns how many there are.  A barrier over the cluster before and after.
+__device__ __forceinline__ int list_free(const PageTable& pt, int most, int32_t* list, int* sm) {
+  __shared__ int sm_free;
+  int lo, hi;
+  cluster_sync();
+  page_range(pt.pages, lo, hi);
+  const int live = cta_live(pt.refs, lo, hi, sm);
+  if (threadIdx.x == 0) sm_free = hi - lo - live;
+  cluster_sync();
+  int r = 0, all = 0;
+  for (int c = 0; c < kBookCtas; ++c) {
+    const int f = ld_cluster_int(&sm_free, c);
+    r += c < cluster_rank() ? f : 0;
+    all += f;
+  }
+  for (int i0 = lo; i0 < hi && r < most; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x;
-    const bool f = i < hi && refs[i] <= 0;
+    const bool f = i < hi && __ldcg(pt.refs + i) <= 0;
     int total;
-    const int k = cta_rank(f, sm, &total);
-    if (f) w.x[r + k] = i;
+    const int k = r + cta_rank(f, sm, &total);
+    if (f && k < most) list[k] = i;
     r += total;
   }
-  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *w.count = r;
+  cluster_sync();
+  return min(all, most);
 }
 
-// Fork, step 3: pair j with a partly filled last page takes free page number
-// (pairs with one before j) and the used rows of the source's page.
-__global__ void __launch_bounds__(kThreads) pages_fork_copy_kernel(
-    const __grid_constant__ CopyPlan c, PageTable pt, const __grid_constant__ RowList rl, PageWs w) {
-  const int segs = c.seg0[c.ps.n];
-  const int j = blockIdx.y, rows = rl.c[j] % kBlock, kb = rl.c[j] / kBlock;
-  if (rows == 0) return;
-  int f = 0;
-  for (int k = 0; k < j; ++k) f += rl.c[k] % kBlock != 0;
-  const int from = pt.table[(int64_t)rl.a[j] * pt.max_blocks + kb];
-  const bool bad = from < 0 || from >= pt.pages, none = f >= *w.count;
-  const int to = none ? -1 : w.x[f];
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    if (bad) flag(w.status, kDevInvalid);
-    if (none) flag(w.status, kDevNoPages);
-    if (!bad && !none) {
-      pt.table[(int64_t)rl.b[j] * pt.max_blocks + kb] = to;
-      pt.refs[to] = 1;
-    }
+// Unmaps ranges of blocks.
+__global__ void __launch_bounds__(kBook) pages_free_kernel(PageTable pt,
+                                                           const __grid_constant__ RowList rl,
+                                                           PageWs w) {
+  int code = 0;
+  for (int j = 0; j < rl.n; ++j) {
+    int32_t* row = pt.table + (int64_t)rl.a[j] * pt.max_blocks;
+    for (int kb = rl.b[j] + blockIdx.x * kBook + threadIdx.x; kb < rl.c[j]; kb += kBookCtas * kBook)
+      code = worse(code, release(pt, atomicExch(row + kb, -1)));
   }
-  if (bad || none) return;
-  for (int seg = blockIdx.x; seg < segs; seg += gridDim.x) copy_segment(c, seg, from, to, rows);
+  write_status(code, w.status);
 }
 
-// Maps the unmapped blocks of the ranges, in order, to the listed pages.
-__global__ void __launch_bounds__(1024) pages_alloc_kernel(PageTable pt,
+// Fork: every destination row lets go of its pages and takes the source's
+// complete ones; then the pairs with a partly filled last page take free pages
+// in order.  Pair j's source and destination page go to w.y and w.z (-1: none).
+__global__ void __launch_bounds__(kBook) pages_fork_kernel(PageTable pt,
                                                            const __grid_constant__ RowList rl,
                                                            PageWs w) {
   __shared__ int sm[32];
-  int r = 0;
-  const int n = *w.count;
-  for (int j = 0; j < rl.n; ++j) {
-    int32_t* row = pt.table + (int64_t)rl.a[j] * pt.max_blocks;
-    for (int k0 = rl.b[j]; k0 < rl.c[j]; k0 += blockDim.x) {
-      const int kb = k0 + threadIdx.x;
-      const int e = kb < rl.c[j] ? row[kb] : 0;
-      if (e < -1 || e >= pt.pages) flag(w.status, kDevInvalid);
-      int total;
-      const int k = r + cta_rank(e == -1, sm, &total);
-      if (e == -1) {
-        if (k < n) {
-          row[kb] = w.x[k];
-          pt.refs[w.x[k]] = 1;
-        } else {
-          flag(w.status, kDevNoPages);
-        }
+  int code = 0;
+  const int64_t entries = (int64_t)rl.n * pt.max_blocks;
+  for (int64_t x = (int64_t)blockIdx.x * kBook + threadIdx.x; x < entries; x += kBookCtas * kBook) {
+    const int j = (int)(x / pt.max_blocks), kb = (int)(x % pt.max_blocks);
+    int32_t* dst = pt.table + (int64_t)rl.b[j] * pt.max_blocks + kb;
+    int e = -1;
+    if (kb < rl.c[j] / kBlock) {
+      e = pt.table[(int64_t)rl.a[j] * pt.max_blocks + kb];
+      if (e < 0 || e >= pt.pages) {
+        code = worse(code, kDevInvalid);
+        e = -1;
+      } else {
+        atomicAdd(pt.refs + e, 1);
       }
-      r += total;
+    }
+    code = worse(code, release(pt, *dst));
+    *dst = e;
+  }
+  // pair j of thread j: does its last page need a copy, and which free page is its
+  const int j = threadIdx.x;
+  const bool part = j < rl.n && rl.c[j] % kBlock != 0;
+  int need;
+  const int f = cta_rank(part, sm, &need);
+  const int got = need ? list_free(pt, need, w.x, sm) : 0;
+  if (blockIdx.x == 0 && j < rl.n) {
+    int from = -1, to = -1;
+    if (part) {
+      const int kb = rl.c[j] / kBlock;
+      const int e = pt.table[(int64_t)rl.a[j] * pt.max_blocks + kb];
+      if (e < 0 || e >= pt.pages) {
+        code = worse(code, kDevInvalid);
+      } else if (f >= got) {
+        code = worse(code, kDevNoPages);
+      } else {
+        from = e;
+        to = __ldcg(w.x + f);
+        pt.table[(int64_t)rl.b[j] * pt.max_blocks + kb] = to;
+        pt.refs[to] = 1;
+      }
+    }
+    w.y[j] = from;
+    w.z[j] = to;
+  }
+  write_status(code, w.status);
+}
+
+// The used rows of the partly filled pages.
+__global__ void __launch_bounds__(kThreads) pages_fork_copy_kernel(
+    const __grid_constant__ CopyPlan c, const __grid_constant__ RowList rl, PageWs w) {
+  const int j = blockIdx.y, rows = rl.c[j] % kBlock, to = w.z[j];
+  if (to < 0) return;
+  for (int seg = blockIdx.x; seg < c.seg0[c.ps.n]; seg += gridDim.x)
+    copy_segment(c, seg, w.y[j], to, rows);
+}
+
+// Maps the unmapped blocks of the ranges, in order, to the lowest free pages.
+__global__ void __launch_bounds__(kBook) pages_alloc_kernel(PageTable pt,
+                                                            const __grid_constant__ RowList rl,
+                                                            PageWs w) {
+  __shared__ int sm[32];
+  int code = 0;
+  const int n = list_free(pt, pt.pages, w.x, sm);
+  if (blockIdx.x == 0) {
+    int r = 0;
+    for (int j = 0; j < rl.n; ++j) {
+      int32_t* row = pt.table + (int64_t)rl.a[j] * pt.max_blocks;
+      for (int k0 = rl.b[j]; k0 < rl.c[j]; k0 += kBook) {
+        const int kb = k0 + threadIdx.x;
+        const int e = kb < rl.c[j] ? row[kb] : 0;
+        if (e < -1 || e >= pt.pages) code = worse(code, kDevInvalid);
+        int total;
+        const int k = r + cta_rank(e == -1, sm, &total);
+        if (e == -1) {
+          if (k < n) {
+            const int pg = __ldcg(w.x + k);
+            row[kb] = pg;
+            pt.refs[pg] = 1;
+          } else {
+            code = worse(code, kDevNoPages);
+          }
+        }
+        r += total;
+      }
     }
   }
+  write_status(code, w.status);
 }
 
 // ---- compaction ------------------------------------------------------------
 constexpr int kStays = -1, kDead = INT32_MIN;   // fates; a mover holds its rank, hole h holds -2 - h
 
-__global__ void __launch_bounds__(1024) pages_plan_kernel(const int32_t* __restrict__ refs, int pages,
-                                                          int chunk, PageWs w, int32_t* live_out) {
+__global__ void __launch_bounds__(kBook) pages_plan_kernel(PageTable pt, PageWs w, int32_t* live_out) {
   __shared__ int sm[32];
-  const int lo = blockIdx.x * chunk, hi = min(pages, lo + chunk);
-  const int live = cta_live(refs, 0, pages, sm);
-  const int low = cta_live(refs, 0, live, sm);    // live pages already below `live`
-  int r = cta_live(refs, 0, lo, sm);              // live pages before i
-  for (int i0 = lo; i0 < hi; i0 += blockDim.x) {
+  __shared__ int sm_live, sm_low;
+  int lo, hi;
+  page_range(pt.pages, lo, hi);
+  const int mine = cta_live(pt.refs, lo, hi, sm);
+  if (threadIdx.x == 0) sm_live = mine;
+  cluster_sync();
+  int r = 0, live = 0;                            // live pages before lo, in all
+  for (int c = 0; c < kBookCtas; ++c) {
+    const int n = ld_cluster_int(&sm_live, c);
+    r += c < cluster_rank() ? n : 0;
+    live += n;
+  }
+  const int mylow = cta_live(pt.refs, lo, max(lo, min(hi, live)), sm);
+  if (threadIdx.x == 0) sm_low = mylow;
+  cluster_sync();
+  int low = 0;                                    // live pages already below `live`
+  for (int c = 0; c < kBookCtas; ++c) low += ld_cluster_int(&sm_low, c);
+  for (int i0 = lo; i0 < hi; i0 += kBook) {
     const int i = i0 + threadIdx.x;
-    const bool f = i < hi && refs[i] > 0;
+    const bool f = i < hi && pt.refs[i] > 0;
     int total;
     const int k = r + cta_rank(f, sm, &total);
     if (i < hi) {
@@ -292,10 +364,11 @@ __global__ void __launch_bounds__(1024) pages_plan_kernel(const int32_t* __restr
     r += total;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *w.status = 0;                                // for the next kernel's reports
     *w.count = live - low;
-    *w.live = live;
     *live_out = live;
   }
+  cluster_sync();                                 // no CTA leaves while its words are read
 }
 
 __global__ void __launch_bounds__(kThreads) pages_move_kernel(const __grid_constant__ CopyPlan c,
@@ -310,9 +383,9 @@ __global__ void __launch_bounds__(kThreads) pages_move_kernel(const __grid_const
     if (e >= 0 && e < pt.pages) {
       const int fate = w.z[e];
       if (fate >= 0) e = w.x[fate];
-      else if (fate != kStays) flag(w.status, kDevInvalid);   // maps a page nobody counts
+      else if (fate != kStays) atomicMax(w.status, kDevInvalid);   // maps a page nobody counts
     } else if (e != -1) {
-      flag(w.status, kDevInvalid);
+      atomicMax(w.status, kDevInvalid);
     }
     table_out[i] = e;
   }
@@ -336,33 +409,35 @@ __global__ void __launch_bounds__(kThreads) pages_move_kernel(const __grid_const
   }
 }
 
-int list_chunk(int pages) {
-  const int c = (pages + kMaxListCtas - 1) / kMaxListCtas;
-  return c < kChunk ? kChunk : c;
-}
-
-cudaError_t clear_status(const PageWs& w, cudaStream_t st) {
-  return cudaMemsetAsync(w.status, 0, sizeof(int), st);
-}
-
-cudaError_t launch_list(const PageTable& pt, const PageWs& w, cudaStream_t st) {
-  const int chunk = list_chunk(pt.pages);
+template <typename... A>
+cudaError_t launch_book(void (*kernel)(A...), cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kBookCtas);
+  cfg.blockDim = dim3(kBook);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kBookCtas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   note_launches(1);
-  pages_list_kernel<<<(pt.pages + chunk - 1) / chunk, 1024, 0, st>>>(pt.refs, pt.pages, chunk, w);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
 
-size_t pages_workspace_bytes(int pages) { return kWsHead + (size_t)pages * 3 * sizeof(int32_t); }
+size_t pages_workspace_bytes(int pages) {
+  // at least one word per row of a list (fork's pairs)
+  const size_t n = pages > kMaxBatch ? pages : kMaxBatch;
+  return kWsHead + n * 3 * sizeof(int32_t);
+}
 
 cudaError_t launch_pages_copy(const PoolSet& ps, int pages, const int32_t* src, const int32_t* dst,
                               int n, char* ws, cudaStream_t st) {
   const PageWs w = carve(ws, pages);
   const CopyPlan c = copy_plan(ps);
   const int64_t work = (int64_t)n * c.seg0[ps.n], most = sm_count() * 4;
-  cudaError_t e = clear_status(w, st);
-  if (e != cudaSuccess) return e;
   note_launches(1);
   pages_copy_kernel<<<(unsigned)(work < most ? work : most), kThreads, 0, st>>>(c, pages, src, dst, n,
                                                                               w.status);
@@ -373,52 +448,33 @@ cudaError_t launch_pages_fork(const PoolSet& ps, const PageTable& pt, const RowL
                               cudaStream_t st) {
   const PageWs w = carve(ws, pt.pages);
   const CopyPlan c = copy_plan(ps);
-  cudaError_t e = clear_status(w, st);
+  cudaError_t e = launch_book(pages_fork_kernel, st, pt, rows, w);
   if (e != cudaSuccess) return e;
-  const int cols = (pt.max_blocks + 255) / 256;
-  note_launches(1);
-  pages_share_kernel<<<dim3(cols < 8 ? cols : 8, rows.n), 256, 0, st>>>(pt, rows, w.status);
   bool part = false;
   for (int j = 0; j < rows.n; ++j) part |= rows.c[j] % kBlock != 0;
-  if (part) {
-    if ((e = launch_list(pt, w, st)) != cudaSuccess) return e;
+  const int segs = c.seg0[ps.n];
+  if (part && segs > 0) {
     note_launches(1);
-    const int segs = c.seg0[ps.n] > 0 ? c.seg0[ps.n] : 1;
-    pages_fork_copy_kernel<<<dim3(segs < 64 ? segs : 64, rows.n), kThreads, 0, st>>>(c, pt, rows, w);
+    pages_fork_copy_kernel<<<dim3(segs < 64 ? segs : 64, rows.n), kThreads, 0, st>>>(c, rows, w);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_pages_free(const PageTable& pt, const RowList& rows, char* ws, cudaStream_t st) {
-  const PageWs w = carve(ws, pt.pages);
-  cudaError_t e = clear_status(w, st);
-  if (e != cudaSuccess) return e;
-  const int cols = (pt.max_blocks + 255) / 256;
-  note_launches(1);
-  pages_free_kernel<<<dim3(cols < 8 ? cols : 8, rows.n), 256, 0, st>>>(pt, rows, w.status);
-  return cudaGetLastError();
+  return launch_book(pages_free_kernel, st, pt, rows, carve(ws, pt.pages));
 }
 
 cudaError_t launch_pages_alloc(const PageTable& pt, const RowList& rows, char* ws, cudaStream_t st) {
-  const PageWs w = carve(ws, pt.pages);
-  cudaError_t e = clear_status(w, st);
-  if (e != cudaSuccess) return e;
-  if ((e = launch_list(pt, w, st)) != cudaSuccess) return e;
-  note_launches(1);
-  pages_alloc_kernel<<<1, 1024, 0, st>>>(pt, rows, w);
-  return cudaGetLastError();
+  return launch_book(pages_alloc_kernel, st, pt, rows, carve(ws, pt.pages));
 }
 
 cudaError_t launch_pages_compact(const PoolSet& ps, const PageTable& pt, int32_t* table_out,
                                  int32_t* refs_out, int32_t* live, char* ws, cudaStream_t st) {
   const PageWs w = carve(ws, pt.pages);
   const CopyPlan c = copy_plan(ps);
-  cudaError_t e = clear_status(w, st);
+  const cudaError_t e = launch_book(pages_plan_kernel, st, pt, w, live);
   if (e != cudaSuccess) return e;
-  const int chunk = list_chunk(pt.pages);
-  note_launches(2);
-  pages_plan_kernel<<<(pt.pages + chunk - 1) / chunk, 1024, 0, st>>>(pt.refs, pt.pages, chunk, w,
-                                                                    live);
+  note_launches(1);
   pages_move_kernel<<<sm_count() * 4, kThreads, 0, st>>>(c, pt, table_out, refs_out, w);
   return cudaGetLastError();
 }

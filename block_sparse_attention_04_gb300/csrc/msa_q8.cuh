@@ -98,6 +98,21 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t saddr, int rank) {
       : "r"(saddr), "r"(rank));
   return v;
 }
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+// The int at this CTA's shared address `p` in the shared memory of CTA `rank`.
+__device__ __forceinline__ int ld_cluster_int(const int* p, int rank) {
+  int v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.b32 %0, [a];\n}"
+      : "=r"(v)
+      : "r"(smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
+}
 __device__ __forceinline__ void sts128(uint32_t saddr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
