@@ -565,22 +565,23 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
     const int r = quad * 32 + lane;  // tile row = TMEM lane
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + c * 128;
     float sl = a.s.scale * kLog2e;
+    const int e = r >> rshift, hh = r & (a.rpe - 1);
+    // the next tile's descriptor and this row's entry of it are loaded a tile
+    // ahead: the two loads depend on each other and would stand before every S
+    int4 nd = c < n ? desc[c] : make_int4(0, 0, 0, 0);
+    int nen = c < n && e < (nd.z & 0xFF) ? a.entries[nd.y + e] : 0;
     for (int t = c; t < n; t += 2) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // warp-uniform
-      const int4 d = desc[t];
+      const int4 d = nd;
+      const int en = nen;
+      if (t + 2 < n) nd = desc[t + 2];
       const int kb = d.w & 0x7FFF, g = (d.w >> 15) & 7, b = d.w >> 18;
-      const int e = r >> rshift, hh = r & (a.rpe - 1);
       const bool valid = e < (d.z & 0xFF) && hh < hpg;
       if constexpr (Q8) {
         sl = a.s.scale * kLog2e * pow2i((d.z >> 8 & 0xFF) - 128);
         sl = fminf(fmaxf(sl, -3e38f), 3e38f);
       }
-      int il = 0, slot = 0;
-      if (valid) {
-        const int en = a.entries[d.y + e];
-        il = en >> 4;
-        slot = en & 15;
-      }
+      const int il = valid ? en >> 4 : 0, slot = valid ? en & 15 : 0;
       const int64_t tq = (int64_t)a.pos.q_start[b] + a.t0 + il;
       // tokens kb*128 + col with col > lim are masked (only in the local block)
       const int lim = (int)(tq - (int64_t)kb * kBlock);
@@ -590,6 +591,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
         break;
       }
       tc_fence_after();
+      if (t + 2 < n && e < (nd.z & 0xFF)) nen = a.entries[nd.y + e];
       // TMEM is read in 16-column loads, each waited before the next: small
       // loads leave the MMAs of the other chain more of tensor memory than
       // larger ones (measured).
@@ -628,6 +630,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
       // loads) before columns [16cc, 16cc+16) are written, and those belong to
       // chunks already read; row sum
       float l0 = 0.f, l1 = 0.f;
+      float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         uint32_t wv[16];
@@ -640,6 +643,19 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
           for (int u = 0; u < 8; ++u) {
             const int k = 2 * u;
             const int uu = hf * 8 + u;
+            if constexpr (Q8) {
+              // every exponential on the MUFU unit, the rest two lanes at a time
+              const float2 x = ffma2(make_float2(__uint_as_float(h[k]), __uint_as_float(h[k + 1])),
+                                     make_float2(sl, sl), make_float2(-m, -m));
+              float2 pp = make_float2(ex2(x.x), ex2(x.y));
+              if (masked) {
+                pp.x = cc * 32 + hf * 16 + k <= lim ? pp.x : 0.f;
+                pp.y = cc * 32 + hf * 16 + k + 1 <= lim ? pp.y : 0.f;
+              }
+              l2 = fadd2(l2, pp);
+              wv[uu] = pack_bf16(pp.x, pp.y);
+              continue;
+            }
             // 6 of 16 pairs on the FMA pipe, the rest on the MUFU unit
             constexpr unsigned kPolyPairs = 0x4925u;  // uu = 0, 2, 5, 8, 11, 14
             const bool poly = (kPolyPairs >> uu) & 1u;
@@ -663,7 +679,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
       mbar_arrive(&p_full[c]);
       if (valid) {
         const size_t prow = (((size_t)b * a.Tp + il) * H + (size_t)g * hpg + hh) * kTopk + slot;
-        __stcs(a.part_ml + prow, make_float2(m, l0 + l1));
+        __stcs(a.part_ml + prow, make_float2(m, Q8 ? l2.x + l2.y : l0 + l1));
       }
     }
   } else if (!Q8 || warp < kConvWarp0) {
@@ -674,23 +690,25 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
     const int quad = warp & 3;
     const int r = quad * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + 256 + c * 128;
+    const int e = r >> rshift, hh = r & (a.rpe - 1);
+    int4 nd = c < n ? desc[c] : make_int4(0, 0, 0, 0);     // a tile ahead, as above
+    int nen = c < n && e < (nd.z & 0xFF) ? a.entries[nd.y + e] : 0;
     for (int t = c; t < n; t += 2) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // warp-uniform
-      const int4 d = desc[t];
+      const int4 d = nd;
+      const int en = nen;
+      if (t + 2 < n) nd = desc[t + 2];
       const int g = (d.w >> 15) & 7, b = d.w >> 18;
-      const int e = r >> rshift, hh = r & (a.rpe - 1);
       const bool valid = e < (d.z & 0xFF) && hh < hpg;
       const float fo = Q8 ? pow2i((d.z >> 16 & 0xFF) - 128) : 1.f;
-      size_t prow = 0;
-      if (valid) {
-        const int en = a.entries[d.y + e];
-        prow = (((size_t)b * a.Tp + (en >> 4)) * H + (size_t)g * hpg + hh) * kTopk + (en & 15);
-      }
+      const size_t prow =
+          valid ? (((size_t)b * a.Tp + (en >> 4)) * H + (size_t)g * hpg + hh) * kTopk + (en & 15) : 0;
       if (!__all_sync(0xffffffffu, mbar_wait(&o_full[c], (uint32_t)(t >> 1) & 1, a.status, a.wait_polls))) {
         *abort_flag = 1;
         break;
       }
       tc_fence_after();
+      if (t + 2 < n && e < (nd.z & 0xFF)) nen = a.entries[nd.y + e];
       uint16_t* dst = a.part_o + prow * D;
 #pragma unroll 1
       for (int cc = 0; cc < D / 16; ++cc) {
@@ -699,7 +717,12 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
         tmem_ld_wait();
         if constexpr (Q8) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) h[k] = __float_as_uint(__uint_as_float(h[k]) * fo);
+          for (int k = 0; k < 16; k += 2) {
+            const float2 o = fmul2(make_float2(__uint_as_float(h[k]), __uint_as_float(h[k + 1])),
+                                   make_float2(fo, fo));
+            h[k] = __float_as_uint(o.x);
+            h[k + 1] = __float_as_uint(o.y);
+          }
         }
         if (valid) {
 #pragma unroll
