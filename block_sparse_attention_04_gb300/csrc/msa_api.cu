@@ -241,8 +241,6 @@ int run_index_in(const msa_params* p, const Shape& s, const Positions& pos, cons
   return run_index(p, s, pos, q_idx, k_idx, sel, w, st);
 }
 
-bool prefill_sized(const msa_params* p) { return use_tc_attn(p); }
-
 }  // namespace msa
 
 using namespace msa;

@@ -1,6 +1,7 @@
 // libmsa C ABI, serving operators (include/msa.h): 8-bit caches, sliding-window
 // attention and page operations.  Argument checks, workspace layout and the
 // choice of kernels; nothing is enqueued before every check has passed.
+#include <cmath>
 #include <cstring>
 
 #include "msa_pages.h"
@@ -33,7 +34,70 @@ int check_call(const msa_params* p, const int32_t* block_table, int num_pool_blo
 // Workspace of the attention calls: the status word, then their scratch.
 size_t stream_scratch(const msa_params* p) { return align_up(stream_plan(shape_of(p)).total); }
 size_t sparse_scratch(const msa_params* p) {
-  return prefill_sized(p) ? align_up(tc_attn_workspace_bytes(shape_of(p))) : stream_scratch(p);
+  const size_t tc = tc_attn_workspace_bytes(shape_of(p)), stream = stream_scratch(p);
+  return align_up(tc > stream ? tc : stream);
+}
+
+// ---- which kernels run an attention call (MSA_KERNELS_AUTO) ---------------
+// The time of both families in microseconds, from what a step of each took on
+// GB300 (graph replays, 152 SMs, contexts of 16K, 1 and 16 sequences of 1 to 256
+// queries, both head layouts; the estimates are within about 25 % of the
+// measurements behind them).
+constexpr double kSms = 152;
+
+// Streaming: 0.8 us per (unit, block) step and CTA and 1.6 us per unit (the
+// join of its warps), or the blocks' bytes where they do not stay in L2 between
+// the queries that read them.
+double stream_us(double units, double steps, double step_bytes, double distinct_bytes) {
+  const double compute = steps / kSms * 0.8 + units / kSms * 1.6;
+  const double memory = distinct_bytes > 64e6 ? steps * step_bytes / 6.6e6 : 0.0;
+  return 6.0 + (compute > memory ? compute : memory);
+}
+
+// Window on tensor cores: a step is one block for two tiles.  16 x 8 queries of
+// a 512-token window, 48/8 heads: 44 us streaming, 22 us here; one decode token
+// of 16 sequences, window 8000: 84 us streaming, 116 us here.
+bool window_on_tc(const msa_params* p, const Shape& s, const Positions& pos, const Visible& vis,
+                  bool kv8) {
+  if (p->kernels != MSA_KERNELS_AUTO) return p->kernels == MSA_KERNELS_TENSORCORE;
+  double blocks = 0;
+  for (int b = 0; b < s.B; ++b) {
+    const int t = pos.q_start[b] + s.T - 1;
+    const int lo = (t - vis.window + 1 > 0 ? t - vis.window + 1 : 0) / kBlock;
+    const int sb = (vis.sinks + kBlock - 1) / kBlock;
+    blocks += (sb < lo ? sb : lo) + t / kBlock - lo + 1;
+  }
+  const double block_bytes = 2.0 * kBlock * s.D * (kv8 ? 1 : 2);
+  const double steps = blocks * s.G;
+  const double stream = stream_us((double)s.B * s.T * s.G, steps * s.T, block_bytes, steps * block_bytes);
+  const int nq = 128 / (s.H / s.G);
+  const double items = (double)((s.T + 2 * nq - 1) / (2 * nq)) * s.B * s.G;
+  const int splits = window_splits(s, pos, vis.window, vis.sinks);
+  const double longest = window_list_len(s, pos, vis.window, vis.sinks);
+  const double step = s.D == 128 ? (kv8 ? 2.2 : 1.65) : (kv8 ? 1.8 : 1.55);
+  const double tc = 10.0 + std::ceil(items * splits / kSms) * std::ceil(longest / splits) * step +
+                    (splits > 1 ? 6.0 : 0.0);
+  return tc < stream;
+}
+
+// Selected blocks of an 8-bit cache: the streaming kernel reads 16 blocks per
+// (query, group); the KV-outer kernels read a block once per list and work in
+// tiles of 128 query-head rows, of which a list has at least one: 256 queries
+// of one sequence at 16K, 48/8 heads, 203 us streaming, 74 us KV-outer; 16 x 8
+// queries 111 and 203 us.
+bool sparse_on_tc(const msa_params* p, const Shape& s, const Positions& pos) {
+  if (p->kernels != MSA_KERNELS_AUTO) return p->kernels == MSA_KERNELS_TENSORCORE;
+  const double entries = (double)s.B * s.T * s.G * MSA_TOPK;
+  double lists = 0;
+  for (int b = 0; b < s.B; ++b) lists += (pos.q_start[b] + s.T - 1) / kBlock + 1;
+  lists *= s.G;
+  const double block_bytes = 2.0 * kBlock * s.D;
+  const double stream = stream_us(entries / MSA_TOPK, entries, block_bytes, lists * block_bytes);
+  const int rows = s.H / s.G <= 8 ? 8 : 16;
+  // lists that at least one of `entries` random choices meets, and full tiles
+  const double tiles = lists * (1.0 - std::exp(-entries / lists)) + entries / (128 / rows);
+  const double tc = 27.0 + tiles / kSms * (s.D == 128 ? 2.3 : 1.6);
+  return tc < stream;
 }
 
 // ... of an 8-bit call: msa_forward's index scratch follows msa_workspace_bytes'
@@ -47,7 +111,7 @@ int run_attn_q8(const msa_params* p, const Shape& s, const Positions& pos, const
                 const CacheView& c, const int32_t* sel, uint16_t* out, bool join_status, void* ws,
                 cudaStream_t st) {
   char* base = static_cast<char*>(ws);
-  if (prefill_sized(p)) {
+  if (sparse_on_tc(p, s, pos)) {
     if (!join_status && cudaMemsetAsync(ws, 0, sizeof(int), st) != cudaSuccess) return MSA_ERR_CUDA;
     return cuda_status(launch_attn_tc_q8(s, pos, q, c, sel, out, reinterpret_cast<int*>(base),
                                          base + kAlign, st));
@@ -72,9 +136,9 @@ int run_window(const msa_params* p, const int32_t* block_table, int num_pool_blo
   const Visible vis{nullptr, window < cap ? window : cap, sinks < cap ? sinks : cap};
   const Shape s = shape_of(p, block_table, num_pool_blocks);
   char* base = static_cast<char*>(ws);
-  if (prefill_sized(p))
+  if (window_on_tc(p, s, pos, vis, c.kv8))
     return cuda_status(launch_window_tc(s, pos, c, vis.window, vis.sinks, q, out,
-                                        reinterpret_cast<int*>(base), st));
+                                        reinterpret_cast<int*>(base), base + kAlign, st));
   return cuda_status(launch_stream_attn(s, pos, c, vis, q, out, reinterpret_cast<int*>(base),
                                         false, base + kAlign, st));
 }
@@ -207,7 +271,8 @@ int msa_forward_q8(const msa_params* p, const int32_t* block_table, int num_pool
 
 size_t msa_window_workspace_bytes(const msa_params* p) {
   if (validate_params(p) != MSA_OK) return 0;
-  return kAlign + stream_scratch(p);
+  const size_t tc = window_tc_scratch_bytes(shape_of(p)), stream = stream_scratch(p);
+  return kAlign + align_up(tc > stream ? tc : stream);
 }
 
 int msa_window_attn(const msa_params* p, const int32_t* block_table, int num_pool_blocks,

@@ -46,9 +46,13 @@ cudaError_t launch_attn_tc_q8(const Shape& s, const Positions& pos, const uint16
                               char* base, cudaStream_t st);
 
 // Sliding-window attention of every query of the call on tensor cores
-// (prefill shapes).  status: the status word and the word after it.
+// (prefill shapes).  status: the status word and the word after it; base:
+// scratch of window_tc_scratch_bytes(s) bytes.
+size_t window_tc_scratch_bytes(const Shape& s);
+int window_splits(const Shape& s, const Positions& pos, int window, int sinks);
+int window_list_len(const Shape& s, const Positions& pos, int window, int sinks);
 cudaError_t launch_window_tc(const Shape& s, const Positions& pos, const CacheView& c, int window,
-                             int sinks, const uint16_t* q, uint16_t* out, int* status,
+                             int sinks, const uint16_t* q, uint16_t* out, int* status, char* base,
                              cudaStream_t st);
 
 // Appends tokens to an 8-bit cache (layouts of msa_cache_append_q8) and writes
@@ -62,8 +66,6 @@ cudaError_t launch_cache_append_q8(const Shape& s, const Positions& pos, const u
 // msa_index_topk); positions and pointers are validated by the caller.
 int run_index_in(const msa_params* p, const Shape& s, const Positions& pos, const uint16_t* q_idx,
                  const uint16_t* k_idx, int32_t* sel, void* ws, cudaStream_t st);
-// Whether prefill-sized kernels run this call (the choice of msa_sparse_attn).
-bool prefill_sized(const msa_params* p);
 int validate_pool(const int32_t* block_table, int num_pool_blocks);
 
 }  // namespace msa

@@ -31,6 +31,10 @@
 //                 conversion's instructions; V needs bf16's range, because P
 //                 (bf16, 2^-8) is relative to the largest p', which may belong
 //                 to values that cancel or vanish.
+// When the items are fewer than the SMs, each block list is split over several
+// items, whose O, maxima and sums go to the workspace and are joined by
+// window_join_kernel (64 queries of one sequence at 16K tokens, window 8000,
+// 48/8 heads: 116 us in one part, 36 us).
 // An 8-bit block's exponents: 2^ek scales the scores, 2^ev is folded into the
 // exponential that multiplies V (p' = 2^(x + ev - m), m the maximum of x + ev),
 // while the normaliser counts 2^(x - n) with its own maximum n.  p' gives the
@@ -50,6 +54,7 @@ constexpr int kStages = 2;            // K and V blocks in flight
 constexpr float kLazy = 8.f;          // log2 growth of P tolerated before O is rescaled
 constexpr float kFoldMax = 80.f;      // log2 of the largest factor from p' to the normaliser
 constexpr int kItemRing = 4;          // item ids published by the Q warp, ahead of use
+constexpr int kSplitItems = 152;      // most parts of split calls (an SM each)
 constexpr int kMetaRing = 4;          // exponents of the blocks in flight
 
 template <bool Q8>
@@ -65,7 +70,10 @@ struct WinArgs {
   int window, sinks;
   int nq;          // queries per tile: 128 / (H/G)
   int npair;       // items per (sequence, group): ceil(T / (2 nq))
-  int nitems;
+  int splits;      // items that share a block list
+  int nitems;      // npair * B * G * splits
+  float* part_o;   // splits > 1: [item][chain][128][D] O relative to m
+  float4* part_ml; // ... (m, n in log2 units, l)
   int* next_item;  // shared counter of taken items (zeroed with the status word)
   const uint8_t* k8;
   const uint8_t* v8;
@@ -90,11 +98,13 @@ struct Item {
   int b, g, i0;          // queries i0 ... i0 + 2 nq - 1 of sequence b (those below T)
   int t_first, t_last;   // their first and last position
   int lo;                // first token of the first query's window
-  int nblk, nsink, first;  // block p of the list is p (p < nsink) or first + p
+  int p0, nblk;          // the item's blocks: list positions p0 ... p0 + nblk - 1
+  int nsink, first;      // block p of the list is p (p < nsink) or first + p
 };
 __device__ __forceinline__ Item item_of(const WinArgs& a, int it) {
   Item d;
-  const int per = a.s.B * a.s.G;
+  const int per = a.s.B * a.s.G, split = it % a.splits;
+  it /= a.splits;
   const int pair = a.npair - 1 - it / per, r = it % per;
   d.g = r % a.s.G;
   d.b = r / a.s.G;
@@ -104,10 +114,15 @@ __device__ __forceinline__ Item item_of(const WinArgs& a, int it) {
   d.lo = max(0, d.t_first - a.window + 1);
   d.nsink = min((a.sinks + kBlock - 1) / kBlock, d.lo / kBlock);
   d.first = d.lo / kBlock - d.nsink;
-  d.nblk = d.nsink + d.t_last / kBlock - d.lo / kBlock + 1;
+  const int len = d.nsink + d.t_last / kBlock - d.lo / kBlock + 1;
+  d.p0 = split * len / a.splits;
+  d.nblk = (split + 1) * len / a.splits - d.p0;    // 0: a list shorter than the splits
   return d;
 }
-__device__ __forceinline__ int block_at(const Item& d, int p) { return p < d.nsink ? p : d.first + p; }
+__device__ __forceinline__ int block_at(const Item& d, int p) {
+  p += d.p0;
+  return p < d.nsink ? p : d.first + p;
+}
 
 // Instruction descriptor of kind::f16 with f16 A and B (format 0), f32 D.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
@@ -210,8 +225,8 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
       if (cur >= a.nitems) cur = -1;
       item_ring[0] = cur;
       mbar_arrive(&it_full[0]);
-      int k = 0, loads[2] = {0, 0};
-      for (; cur >= 0; ++k) {
+      int loads[2] = {0, 0};
+      for (int k = 0; cur >= 0; ++k) {
         const int r = k + 1, slot = r % kItemRing;
         if (r >= kItemRing &&
             !mbar_wait(&it_empty[slot], ((r / kItemRing) - 1) & 1, a.status, a.wait_polls)) {
@@ -227,13 +242,14 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         // one instead: its rows are computed and never written
         bool ok = true;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (k > 0 && !mbar_wait(&q_empty[c], (k - 1) & 1, a.status, a.wait_polls)) {
+        for (int c = 0; c < 2 && d.nblk > 0; ++c) {
+          if (loads[c] > 0 &&
+              !mbar_wait(&q_empty[c], (loads[c] - 1) & 1, a.status, a.wait_polls)) {
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(&q_full[c], rows * D * 2);
-          loads[c] = k + 1;
+          ++loads[c];
           const int i = d.i0 + c * nq;
           const int z = d.b * T + (i < T ? i : d.i0);
 #pragma unroll
@@ -311,7 +327,8 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
     const uint64_t qdesc0 = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
     const uint64_t kdesc0 = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
     const uint64_t vdesc0 = smem_desc(smem_u32(sV), C::kHalf, 1024, kSwizzle128B);
-    int n = 0, k = 0, p = 0;         // block steps issued, items begun, block of the item
+    // block steps issued, items taken, items begun (those with blocks), block of the item
+    int n = 0, ki = 0, k = 0, p = 0;
     bool ok = true, has_s = true, has_pv = false;
     Item d;
     d.nblk = 0;
@@ -322,11 +339,14 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
     while (ok) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
       if (has_s && p == d.nblk) {    // the next item
-        const int it = take_item(k);
+        int it;
+        do {
+          it = take_item(ki++);
+          if (it >= 0) d = item_of(a, it);
+        } while (it >= 0 && d.nblk == 0);
         if (it == -2) { ok = false; break; }
         has_s = it >= 0;
         if (has_s) {
-          d = item_of(a, it);
           p = 0;
           ++k;
         }
@@ -421,10 +441,10 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
     const uint32_t o_base = tmem + ((uint32_t)(quad * 32) << 16) + 256 + c * 128;
     const float sl = a.s.scale * kLog2e;
     const int rq = r / hpg, rh = r - rq * hpg;
-    int n = 0, k = 0;
+    int n = 0, k = 0;                // block steps, items with blocks
     bool ok = true;
-    for (; ok; ++k) {
-      const int it = take_item(k);
+    for (int ki = 0; ok; ++ki) {
+      const int it = take_item(ki);
       if (it < 0) {
         ok = it == -1;
         break;
@@ -432,6 +452,10 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
       const Item d = item_of(a, it);
       const int i = d.i0 + c * nq + rq;
       const bool valid = rq < nq && i < T;
+      if (d.nblk == 0) {
+        a.part_ml[(it * 2 + c) * 128 + r] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        continue;
+      }
       const int tq = a.pos.q_start[d.b] + i;
       const int tlo = max(0, tq - a.window + 1);
       float fr = sl;                   // score factor of the row
@@ -650,6 +674,24 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         break;
       }
       tc_fence_after();
+      ++k;
+      if (a.splits > 1) {
+        const int prow = (it * 2 + c) * 128 + r;     // below 2^16: at most kSplitItems items
+        if (valid) a.part_ml[prow] = make_float4(m_ref, Q8 ? n_ref : m_ref, l, 0.f);
+#pragma unroll 1
+        for (int cc = 0; cc < D / 16; ++cc) {
+          uint32_t h[16];
+          tmem_ld16(o_base + cc * 16, h);
+          tmem_ld_wait();
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(a.part_o + (int64_t)prow * D + cc * 16 + e * 4) =
+                  make_uint4(h[e * 4], h[e * 4 + 1], h[e * 4 + 2], h[e * 4 + 3]);
+          }
+        }
+        continue;
+      }
       const float inv = l == 0.f ? 0.f : (Q8 ? ex2(m_ref - n_ref) : 1.f) / l;
       uint16_t* dst =
           a.out + (((int64_t)d.b * T + (valid ? i : 0)) * H + d.g * hpg + rh) * D;
@@ -754,15 +796,22 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
       }
       return true;
     };
-    int n = 0, k = 0;
-    bool ok = true;
-    int it = take_item(0);
-    ok = it != -2;
+    int n = 0, ki = 0, k = 0;        // block steps, items taken, items with blocks
+    // the next item that has blocks
+    auto next_item = [&](Item& d) -> int {
+      int it;
+      do {
+        it = take_item(ki++);
+        if (it >= 0) d = item_of(a, it);
+      } while (it >= 0 && d.nblk == 0);
+      return it;
+    };
     uint4 kreg[NL], vreg[NL];
     Item d;
     Step cur;
+    int it = next_item(d);
+    bool ok = it != -2;
     if (it >= 0) {
-      d = item_of(a, it);
       cur = resolve(d, 0);
       load(a.k8, cur, kreg);
     }
@@ -778,13 +827,10 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         if (p + 1 < d.nblk) {
           nxt = resolve(d, p + 1);
         } else {
-          nit = take_item(k + 1);
+          nit = next_item(nd);
           if (nit == -2) { ok = false; break; }
           more = nit >= 0;
-          if (more) {
-            nd = item_of(a, nit);
-            nxt = resolve(nd, 0);
-          }
+          if (more) nxt = resolve(nd, 0);
         }
         const int ks = n % kStages;
         const uint32_t w = (uint32_t)(n / kStages);
@@ -823,9 +869,54 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
   }
 }
 
+// Joins the parts of split block lists: one warp per (sequence, query, head).
+template <int D>
+__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WinArgs a) {
+  constexpr int PER = D / 32;
+  const Shape& s = a.s;
+  const int lane = threadIdx.x & 31, hpg = s.H / s.G;
+  const int64_t gw = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (gw >= (int64_t)s.B * s.T * s.H) return;
+  const int h = (int)(gw % s.H), g = h / hpg;
+  const int i = (int)(gw / s.H % s.T), b = (int)(gw / s.H / s.T);
+  const int pair = i / (2 * a.nq), j = i % (2 * a.nq);           // item, query in it
+  const int64_t item = ((int64_t)(a.npair - 1 - pair) * s.B * s.G + b * s.G + g) * a.splits;
+  const int row = (j / a.nq) * 128 + j % a.nq * hpg + h % hpg;   // chain, tile row
+  float M = -INFINITY, N = -INFINITY;
+  for (int p = lane; p < a.splits; p += 32) {
+    const float4 v = a.part_ml[(item + p) * 256 + row];
+    M = fmaxf(M, v.x);
+    N = fmaxf(N, v.y);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    N = fmaxf(N, __shfl_xor_sync(0xffffffffu, N, x));
+  }
+  float L = 0.f, acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < a.splits; ++p) {
+    const float4 v = a.part_ml[(item + p) * 256 + row];
+    if (v.z == 0.f) continue;        // no visible token (or no block): nothing written
+    const float w = v.x == -INFINITY ? 0.f : ex2(v.x - M);
+    L = fmaf(v.y == -INFINITY ? 0.f : ex2(v.y - N), v.z, L);
+    const float* o = a.part_o + ((item + p) * 256 + row) * D + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, o[e], acc[e]);
+  }
+  const float inv = L == 0.f ? 0.f : ex2(M - N) / L;
+  uint16_t* dst = a.out + gw * D + lane * PER;
+#pragma unroll
+  for (int e = 0; e < PER; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+}
+
 template <int D, bool Q8>
 cudaError_t launch_impl(const Shape& s, const Positions& pos, const CacheView& c, int window,
-                        int sinks, const uint16_t* q, uint16_t* out, int* status, cudaStream_t st) {
+                        int sinks, const uint16_t* q, uint16_t* out, int* status, char* base,
+                        cudaStream_t st) {
   using C = WinCfg<D>;
   // the item counter sits in the word after the status word; both are zeroed
   if (cudaMemsetAsync(status, 0, 2 * sizeof(int), st) != cudaSuccess) return cudaErrorUnknown;
@@ -837,7 +928,10 @@ cudaError_t launch_impl(const Shape& s, const Positions& pos, const CacheView& c
   a.sinks = sinks;
   a.nq = 128 / hpg;
   a.npair = (s.T + 2 * a.nq - 1) / (2 * a.nq);
-  a.nitems = a.npair * s.B * s.G;
+  a.splits = window_splits(s, pos, window, sinks);
+  a.nitems = a.npair * s.B * s.G * a.splits;
+  a.part_ml = reinterpret_cast<float4*>(base);
+  a.part_o = reinterpret_cast<float*>(base + (size_t)kSplitItems * 256 * sizeof(float4));
   a.next_item = status + 1;
   a.k8 = static_cast<const uint8_t*>(c.k);
   a.v8 = static_cast<const uint8_t*>(c.v);
@@ -873,19 +967,60 @@ cudaError_t launch_impl(const Shape& s, const Positions& pos, const CacheView& c
   note_launches(1);
   window_tc_kernel<D, Q8><<<a.nitems < ctas ? a.nitems : ctas, threads<Q8>(), C::kSmem, st>>>(
       tm_q, tm_k, tm_v, a);
+  if (a.splits > 1) {
+    const int64_t warps = (int64_t)s.B * s.T * s.H;
+    note_launches(1);
+    window_join_kernel<D><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a);
+  }
   return cudaGetLastError();
 }
 
 }  // namespace
 
+// Items of at most kSplitItems parts in all: no workspace grows with the call.
+// A part keeps at least kMinBlocks blocks of the longest list (a part costs
+// about 3 us of its own: Q, the output, the join).
+size_t window_tc_scratch_bytes(const Shape& s) {
+  const int nq = 128 / (s.H / s.G);
+  const int64_t items = (int64_t)((s.T + 2 * nq - 1) / (2 * nq)) * s.B * s.G;
+  if (items * 2 > kSplitItems) return 0;
+  return (size_t)kSplitItems * 256 * (sizeof(float4) + s.D * sizeof(float));
+}
+
+int window_splits(const Shape& s, const Positions& pos, int window, int sinks) {
+  constexpr int kMinBlocks = 4;
+  const int nq = 128 / (s.H / s.G);
+  const int64_t items = (int64_t)((s.T + 2 * nq - 1) / (2 * nq)) * s.B * s.G;
+  if (items * 2 > kSplitItems) return 1;
+  const int longest = window_list_len(s, pos, window, sinks);
+  int n = (int)(kSplitItems / items);
+  if (n > longest / kMinBlocks) n = longest / kMinBlocks;
+  return n < 1 ? 1 : n;
+}
+
+int window_list_len(const Shape& s, const Positions& pos, int window, int sinks) {
+  const int nq = 128 / (s.H / s.G);
+  int longest = 1;
+  for (int b = 0; b < s.B; ++b) {
+    // the last item's queries see the longest list, or one block less
+    const int t1 = pos.q_start[b] + s.T - 1;
+    const int t0 = pos.q_start[b] + (s.T - 1) / (2 * nq) * (2 * nq);
+    const int lo = (t0 - window + 1 > 0 ? t0 - window + 1 : 0) / kBlock;
+    const int sb = (sinks + kBlock - 1) / kBlock;
+    const int n = (sb < lo ? sb : lo) + t1 / kBlock - lo + 1;
+    longest = n > longest ? n : longest;
+  }
+  return longest;
+}
+
 cudaError_t launch_window_tc(const Shape& s, const Positions& pos, const CacheView& c, int window,
-                             int sinks, const uint16_t* q, uint16_t* out, int* status,
+                             int sinks, const uint16_t* q, uint16_t* out, int* status, char* base,
                              cudaStream_t st) {
   if (s.D == 128)
-    return c.kv8 ? launch_impl<128, true>(s, pos, c, window, sinks, q, out, status, st)
-                 : launch_impl<128, false>(s, pos, c, window, sinks, q, out, status, st);
-  return c.kv8 ? launch_impl<64, true>(s, pos, c, window, sinks, q, out, status, st)
-               : launch_impl<64, false>(s, pos, c, window, sinks, q, out, status, st);
+    return c.kv8 ? launch_impl<128, true>(s, pos, c, window, sinks, q, out, status, base, st)
+                 : launch_impl<128, false>(s, pos, c, window, sinks, q, out, status, base, st);
+  return c.kv8 ? launch_impl<64, true>(s, pos, c, window, sinks, q, out, status, base, st)
+               : launch_impl<64, false>(s, pos, c, window, sinks, q, out, status, base, st);
 }
 
 }  // namespace msa

@@ -9,7 +9,7 @@ from tests import serving_ref as sr
 
 pytestmark = pytest.mark.gpu
 
-KERNELS = ["streaming", "tensorcore"]
+KERNELS = ["streaming", "tensorcore", "auto"]
 
 
 @pytest.fixture(scope="module")

@@ -11,7 +11,7 @@ from tests.test_gpu_cache_q8 import Cache
 
 pytestmark = pytest.mark.gpu
 
-KERNELS = ["streaming", "tensorcore"]
+KERNELS = ["streaming", "tensorcore", "auto"]
 
 
 @pytest.fixture(scope="module")
@@ -97,6 +97,21 @@ def test_window(msa, lens, T, H, G, D, window, sinks, kernels, q8):
     k, v = c.values()
     want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, window, sinks, "cuda"),
                                  D ** -0.5, sr.U_BF16)
+    sr.check(out, want, bound)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("T", [1, 9, 50])
+def test_split_block_lists(msa, T, q8):
+    # few tiles, long lists: the tensor-core kernel splits every list over several
+    # items; the short sequence's list is shorter than the number of parts
+    lens = [9000, 60, 700]
+    c, q, q_start = make(lens, T, 12, 2, 64, seed=74)
+    nb = c.table.shape[1]
+    out = run(msa, c, q8, q, q_start, lens, nb, 1 << 22, 3, "tensorcore")
+    k, v = c.values()
+    want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, 1 << 22, 3, "cuda"),
+                                 0.125, sr.U_BF16)
     sr.check(out, want, bound)
 
 
