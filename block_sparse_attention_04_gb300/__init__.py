@@ -143,19 +143,26 @@ def _ptr(t):
     return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
-def _current_stream():
-    """The handle of torch's current stream: through the call that returns the
-    bare handle where torch has it (0.1 us; a Stream object costs 3 us, as much
-    as a launch)."""
+def _stream_getter():
+    """A function that returns the handle of torch's current stream: the call
+    that gives the bare handle where torch has it (0.1 us; a Stream object costs
+    3 us, as much as a launch)."""
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return raw(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    device = torch.cuda.current_device
+    return lambda: raw(device())
+
+
+_current_stream = None
 
 
 def _stream(stream):
+    global _current_stream
     if stream is None:
+        if _current_stream is None:
+            _current_stream = _stream_getter()
         return _current_stream()
     return getattr(stream, "cuda_stream", stream)
 
@@ -342,7 +349,7 @@ def _scratch(n, what, device):
 
 
 def _nbytes(ws):
-    return ws.numel() * ws.element_size()
+    return ws.nbytes
 
 
 def msa_q8_workspace_bytes(p):
