@@ -6,7 +6,6 @@
 
 #include "msa_pages.h"
 #include "msa_serve.h"
-#include "msa_tc.h"
 
 namespace msa {
 namespace {
@@ -34,7 +33,7 @@ int check_call(const msa_params* p, const int32_t* block_table, int num_pool_blo
 // Workspace of the attention calls: the status word, then their scratch.
 size_t stream_scratch(const msa_params* p) { return align_up(stream_plan(shape_of(p)).total); }
 size_t sparse_scratch(const msa_params* p) {
-  const size_t tc = tc_attn_workspace_bytes(shape_of(p)), stream = stream_scratch(p);
+  const size_t tc = tc_attn_q8_workspace_bytes(shape_of(p)), stream = stream_scratch(p);
   return align_up(tc > stream ? tc : stream);
 }
 

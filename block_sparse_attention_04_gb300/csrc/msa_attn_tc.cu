@@ -25,10 +25,13 @@
 // merge into the bf16 output.
 //
 // An 8-bit cache (kernels with Q8 set) has four more warps in place of warp 1:
-// they read a list's codes, convert them to bf16 (exact) and write them into
-// the same rings.  A tile has one KV block, so its exponents are two numbers:
-// 2^ek scales the scores, 2^ev the partial O; both travel in the tile's
-// descriptor.  Rows of V behind the call's last query are zeroed on the way.
+// they read a list's codes, convert them (K to bf16, V to f16, both exact) and
+// write them into the same rings.  A tile has one KV block, so its exponents
+// are two numbers, which travel in the tile's descriptor: 2^ek scales the
+// scores, 2^ev waits for the merge.  P is relative to the block's own maximum,
+// so f16 holds it (2^-11, and 2^-25 of the maximum at the small end, over 128
+// tokens), and O = sum p code is below 128 * 448 < 2^16: the partials are f16
+// too.  Rows of V behind the call's last query are zeroed on the way.
 #include <climits>
 
 #include "msa_q8.cuh"
@@ -61,8 +64,10 @@ struct AttnPass {
   int32_t* entries;      // packed (i - t0) * 16 + slot
   int4* tile_desc;       // per tile: list, first entry, entries (| (ek + 128) << 8 |
                          // (ev + 128) << 16 for an 8-bit cache), kb | g << 15 | b << 18
-  uint16_t* part_o;      // [B*Tp*H*16][D] bf16, O = sum 2^(s-m) v (unnormalised)
+  uint16_t* part_o;      // [B*Tp*H*16][D] bf16, O = sum 2^(s-m) v (unnormalised);
+                         // 8-bit cache: f16, O = sum 2^(s-m) code
   float2* part_ml;       // [B*Tp*H*16] (m in log2 units, l)
+  float4* part_mle;      // ... 8-bit cache, in its place: (m, l, ev)
   int* status;
   uint32_t wait_polls;   // poll cap of the pipeline waits (0: wall-clock bound only)
   const uint8_t* k8;     // an 8-bit cache's codes and exponents (null: bf16 cache)
@@ -477,7 +482,8 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
     // offset / 16 (measured: half the issue time of a loop run by lane 0).
     {
       constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
+      constexpr uint32_t idesc_o =
+          Q8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
       const uint64_t qdesc0 = smem_desc(smem_u32(sQ), 16, C::kQGroup, kSwizzle128B);
       const uint64_t kdesc0 = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
       const uint64_t vdesc0 = smem_desc(smem_u32(sV), C::kHalf, 1024, kSwizzle128B);
@@ -653,7 +659,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
                 pp.y = cc * 32 + hf * 16 + k + 1 <= lim ? pp.y : 0.f;
               }
               l2 = fadd2(l2, pp);
-              wv[uu] = pack_bf16(pp.x, pp.y);
+              wv[uu] = pack_f16(pp.x, pp.y);
               continue;
             }
             // 6 of 16 pairs on the FMA pipe, the rest on the MUFU unit
@@ -679,7 +685,11 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
       mbar_arrive(&p_full[c]);
       if (valid) {
         const size_t prow = (((size_t)b * a.Tp + il) * H + (size_t)g * hpg + hh) * kTopk + slot;
-        __stcs(a.part_ml + prow, make_float2(m, Q8 ? l2.x + l2.y : l0 + l1));
+        if constexpr (Q8)
+          __stcs(a.part_mle + prow,
+                 make_float4(m, l2.x + l2.y, (float)((d.z >> 16 & 0xFF) - 128), 0.f));
+        else
+          __stcs(a.part_ml + prow, make_float2(m, l0 + l1));
       }
     }
   } else if (!Q8 || warp < kConvWarp0) {
@@ -700,7 +710,6 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
       if (t + 2 < n) nd = desc[t + 2];
       const int g = (d.w >> 15) & 7, b = d.w >> 18;
       const bool valid = e < (d.z & 0xFF) && hh < hpg;
-      const float fo = Q8 ? pow2i((d.z >> 16 & 0xFF) - 128) : 1.f;
       const size_t prow =
           valid ? (((size_t)b * a.Tp + (en >> 4)) * H + (size_t)g * hpg + hh) * kTopk + (en & 15) : 0;
       if (!__all_sync(0xffffffffu, mbar_wait(&o_full[c], (uint32_t)(t >> 1) & 1, a.status, a.wait_polls))) {
@@ -715,23 +724,17 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
         uint32_t h[16];
         tmem_ld16(lane_base + cc * 16, h);
         tmem_ld_wait();
-        if constexpr (Q8) {
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const float2 o = fmul2(make_float2(__uint_as_float(h[k]), __uint_as_float(h[k + 1])),
-                                   make_float2(fo, fo));
-            h[k] = __float_as_uint(o.x);
-            h[k + 1] = __float_as_uint(o.y);
-          }
-        }
         if (valid) {
 #pragma unroll
           for (int e8 = 0; e8 < 2; ++e8) {
-            uint4 pk;
-            pk.x = pack_bf16(__uint_as_float(h[e8 * 8 + 0]), __uint_as_float(h[e8 * 8 + 1]));
-            pk.y = pack_bf16(__uint_as_float(h[e8 * 8 + 2]), __uint_as_float(h[e8 * 8 + 3]));
-            pk.z = pack_bf16(__uint_as_float(h[e8 * 8 + 4]), __uint_as_float(h[e8 * 8 + 5]));
-            pk.w = pack_bf16(__uint_as_float(h[e8 * 8 + 6]), __uint_as_float(h[e8 * 8 + 7]));
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float x = __uint_as_float(h[e8 * 8 + 2 * k]);
+              const float y = __uint_as_float(h[e8 * 8 + 2 * k + 1]);
+              w[k] = Q8 ? pack_f16(x, y) : pack_bf16(x, y);
+            }
+            const uint4 pk = make_uint4(w[0], w[1], w[2], w[3]);
             __stcs(reinterpret_cast<uint4*>(dst + cc * 16 + e8 * 8), pk);
           }
         }
@@ -756,7 +759,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
                          : __ldg(reinterpret_cast<const uint4*>(
                                base + off + (row0 + 32 * (u & 3)) * pitch + (4 * (u >> 2) + c4) * 16));
     };
-    auto store = [&](uint32_t tile, int last) {   // rows behind `last` as zeros
+    auto store = [&](const bool is_v, uint32_t tile, int last) {   // rows behind `last` as zeros
 #pragma unroll
       for (int u = 0; u < NL; ++u) {
         const int row = row0 + 32 * (u & 3), ch = 4 * (u >> 2) + c4;
@@ -764,7 +767,8 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
         uint32_t h[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          e4m3x4_to_bf16(row > last ? 0u : w[j], h[2 * j], h[2 * j + 1]);
+          if (is_v) e4m3x4_to_f16(row > last ? 0u : w[j], h[2 * j], h[2 * j + 1]);
+          else e4m3x4_to_bf16(w[j], h[2 * j], h[2 * j + 1]);
         }
         sts128(tile + tile_off(row, 2 * ch), make_uint4(h[0], h[1], h[2], h[3]));
         sts128(tile + tile_off(row, 2 * ch + 1), make_uint4(h[4], h[5], h[6], h[7]));
@@ -790,14 +794,14 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
         load(a.k8, off);
         ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[ks], par, a.status, a.wait_polls));
         if (!ok) break;
-        store(smem_u32(sK + ks * C::kSmemK), kBlock);
+        store(false, smem_u32(sK + ks * C::kSmemK), kBlock);
         fence_async();
         mbar_arrive(&k_full[ks]);
         load(a.v8, off);
         ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[ks], par, a.status, a.wait_polls));
         if (!ok) break;
         const int64_t last = (int64_t)a.pos.q_start[b] + a.s.T - 1 - (int64_t)kb * kBlock;
-        store(smem_u32(sV + ks * C::kSmemK), last < kBlock ? (int)last : kBlock);
+        store(true, smem_u32(sV + ks * C::kSmemK), last < kBlock ? (int)last : kBlock);
         fence_async();
         mbar_arrive(&v_full[ks]);
       }
@@ -814,7 +818,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
 }
 
 // ---- merge: one warp per (sequence, query, head) ----------------------------
-template <int D>
+template <int D, bool Q8>
 __global__ void __launch_bounds__(256) attn_tc_merge_kernel(AttnPass a, uint16_t* __restrict__ out) {
   constexpr int PER = D / 32;
   const int64_t gw = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -826,13 +830,20 @@ __global__ void __launch_bounds__(256) attn_tc_merge_kernel(AttnPass a, uint16_t
   const int b = (int)(r / a.Tp), il = (int)(r % a.Tp);
   const int i = a.t0 + il, g = h / hpg;
   const size_t prow0 = (((size_t)b * a.Tp + il) * H + h) * kTopk;
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f, ev = 0.f;
   if (lane < kTopk) {
     const int kb = a.sel[(((size_t)b * a.s.T + i) * a.s.G + g) * kTopk + lane];
     if (slot_valid(a, b, i, kb)) {
-      const float2 ml = __ldcs(a.part_ml + prow0 + lane);
-      m = ml.x;
-      l = ml.y;
+      if constexpr (Q8) {
+        const float4 mle = __ldcs(a.part_mle + prow0 + lane);
+        m = mle.x;
+        l = mle.y;
+        ev = mle.z;
+      } else {
+        const float2 ml = __ldcs(a.part_ml + prow0 + lane);
+        m = ml.x;
+        l = ml.y;
+      }
     }
   }
   float M = m;
@@ -840,8 +851,18 @@ __global__ void __launch_bounds__(256) attn_tc_merge_kernel(AttnPass a, uint16_t
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   // partial j holds O_j = sum p v with p = 2^(s - m_j): weight 2^(m_j - M),
   // normaliser sum_j 2^(m_j - M) l_j
-  const float w = (m == -INFINITY) ? 0.f : ex2(m - M);
+  float w = (m == -INFINITY) ? 0.f : ex2(m - M);
   float W = w * l;
+  float back = 1.f;
+  if constexpr (Q8) {
+    // O's terms also carry 2^ev: their weights relative to their own maximum
+    const float mo = m + ev;
+    float MO = mo;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
+    w = (m == -INFINITY) ? 0.f : ex2(mo - MO);
+    back = ex2(MO - M);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
   float acc[PER];
@@ -851,7 +872,22 @@ __global__ void __launch_bounds__(256) attn_tc_merge_kernel(AttnPass a, uint16_t
     const float wj = __shfl_sync(0xffffffffu, w, j);
     if (wj == 0.f) continue;
     const uint16_t* src = a.part_o + (prow0 + j) * D + lane * PER;
-    if constexpr (PER == 4) {
+    if constexpr (Q8) {
+      uint32_t u[PER / 2];
+      if constexpr (PER == 4) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src));
+        u[0] = v.x;
+        u[PER / 2 - 1] = v.y;
+      } else {
+        u[0] = __ldcs(reinterpret_cast<const unsigned int*>(src));
+      }
+#pragma unroll
+      for (int e = 0; e < PER / 2; ++e) {
+        const float2 v = unpack_f16(u[e]);
+        acc[2 * e] = fmaf(wj, v.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(wj, v.y, acc[2 * e + 1]);
+      }
+    } else if constexpr (PER == 4) {
       const uint2 u = __ldcs(reinterpret_cast<const uint2*>(src));
       acc[0] += wj * bf16lo(u.x);
       acc[1] += wj * bf16hi(u.x);
@@ -865,7 +901,7 @@ __global__ void __launch_bounds__(256) attn_tc_merge_kernel(AttnPass a, uint16_t
   }
   uint16_t* dst = out + (((size_t)b * a.s.T + i) * H + h) * D + lane * PER;
   // a selection without a visible token: zeros (8-bit calls)
-  const float inv = a.k_exp && W == 0.f ? 0.f : 1.f / W;
+  const float inv = Q8 && W == 0.f ? 0.f : back / W;
 #pragma unroll
   for (int e = 0; e < PER; e += 2)
     *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
@@ -875,7 +911,7 @@ struct AttnLayout {
   size_t lists, entries, count_off, off_off, toff_off, ent_off, tl_off, po_off, pml_off, total;
 };
 
-AttnLayout attn_layout(const Shape& s) {
+AttnLayout attn_layout(const Shape& s, bool q8) {
   AttnLayout L{};
   const int tp = pass_len(s);
   L.lists = (size_t)s.B * s.max_blocks * s.G;
@@ -889,7 +925,7 @@ AttnLayout attn_layout(const Shape& s) {
   L.tl_off = o;     o += al(L.entries * 16);
   const size_t prows = (size_t)s.B * tp * s.H * kTopk;
   L.po_off = o;     o += al(prows * s.D * 2);
-  L.pml_off = o;    o += al(prows * 8);
+  L.pml_off = o;    o += al(prows * (q8 ? sizeof(float4) : sizeof(float2)));
   L.total = o;
   return L;
 }
@@ -899,7 +935,7 @@ cudaError_t launch_attn_tc_impl(const Shape& s, const Positions& pos, const uint
                                 const CacheView& cv, const int32_t* sel, uint16_t* out,
                                 const Workspace& ws, cudaStream_t st) {
   using C = AttnCfg<D>;
-  const AttnLayout lay = attn_layout(s);
+  const AttnLayout lay = attn_layout(s, Q8);
   char* base = ws.tc_base;
   const int hpg = s.H / s.G;
   const int rpe = hpg <= 8 ? 8 : 16;
@@ -954,6 +990,7 @@ cudaError_t launch_attn_tc_impl(const Shape& s, const Positions& pos, const uint
     a.tile_desc = reinterpret_cast<int4*>(base + lay.tl_off);
     a.part_o = reinterpret_cast<uint16_t*>(base + lay.po_off);
     a.part_ml = reinterpret_cast<float2*>(base + lay.pml_off);
+    a.part_mle = reinterpret_cast<float4*>(base + lay.pml_off);
     a.status = ws.status;
     a.wait_polls = debug_wait_polls();
     a.k8 = Q8 ? static_cast<const uint8_t*>(cv.k) : nullptr;
@@ -970,7 +1007,7 @@ cudaError_t launch_attn_tc_impl(const Shape& s, const Positions& pos, const uint
     attn_tc_kernel<D, Q8><<<grid, attn_threads<Q8>(), C::kSmem, st>>>(tm_q, tm_k, tm_v, a);
     const int64_t warps = (int64_t)s.B * a.Tp * s.H;
     note_launches(1);
-    attn_tc_merge_kernel<D><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a, out);
+    attn_tc_merge_kernel<D, Q8><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a, out);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -984,7 +1021,8 @@ int pass_len(const Shape& s) {
   return tp < s.T ? tp : (s.T > 0 ? s.T : 1);
 }
 
-size_t tc_attn_workspace_bytes(const Shape& s) { return attn_layout(s).total; }
+size_t tc_attn_workspace_bytes(const Shape& s) { return attn_layout(s, false).total; }
+size_t tc_attn_q8_workspace_bytes(const Shape& s) { return attn_layout(s, true).total; }
 
 cudaError_t launch_attn_tc(const Shape& s, const Positions& pos, const uint16_t* q,
                            const uint16_t* k, const uint16_t* v, const int32_t* sel,

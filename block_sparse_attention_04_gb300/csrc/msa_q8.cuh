@@ -53,6 +53,11 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t h) {
   return f;
 }
 
+// Instruction descriptor of kind::f16 with f16 A and B (format 0), f32 D.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
+  return idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 // D = A(16x16 f16, row) * B(16x8 f16, col) + D, fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {

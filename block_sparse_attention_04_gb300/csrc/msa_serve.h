@@ -40,7 +40,8 @@ cudaError_t launch_stream_attn(const Shape& s, const Positions& pos, const Cache
                                bool join_status, char* base, cudaStream_t st);
 
 // Step 4 of an 8-bit call on tensor cores (prefill shapes).  base: scratch of
-// tc_attn_workspace_bytes(s) bytes; *status is cleared by the caller.
+// tc_attn_q8_workspace_bytes(s) bytes; *status is cleared by the caller.
+size_t tc_attn_q8_workspace_bytes(const Shape& s);
 cudaError_t launch_attn_tc_q8(const Shape& s, const Positions& pos, const uint16_t* q,
                               const CacheView& c, const int32_t* sel, uint16_t* out, int* status,
                               char* base, cudaStream_t st);

@@ -124,11 +124,6 @@ __device__ __forceinline__ int block_at(const Item& d, int p) {
   return p < d.nsink ? p : d.first + p;
 }
 
-// Instruction descriptor of kind::f16 with f16 A and B (format 0), f32 D.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
-  return idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
-}
-
 // Bits [0, n) of word w of a 128-bit mask.
 __device__ __forceinline__ uint32_t below(int n, int w) {
   const int k = n - 32 * w;
