@@ -445,6 +445,8 @@ def pages_workspace(num_pool_blocks, device="cuda"):
 
 def msa_pages_copy(pools, num_pool_blocks, src, dst, ws, stream=None):
     """Page dst[i] of every pool becomes a copy of page src[i] (device int32 lists)."""
+    if dst.numel() != src.numel():
+        raise ValueError("expected %d destination pages, got %d" % (src.numel(), dst.numel()))
     _call(load().msa_pages_copy(pools, len(pools), int(num_pool_blocks), _ptr(src), _ptr(dst),
                                 src.numel(), _ptr(ws), _nbytes(ws), _stream(stream)),
           "msa_pages_copy")
@@ -485,6 +487,8 @@ def msa_pages_alloc(num_pool_blocks, block_table, refs, rows, first, last, ws, s
 def msa_pages_compact(pools, num_pool_blocks, block_table, refs, table_out, refs_out, live, ws,
                       stream=None):
     """Move the pages in use to the front of the pools (see msa.h)."""
+    if table_out.shape != block_table.shape or refs_out.numel() != refs.numel():
+        raise ValueError("table_out and refs_out must have the shapes of block_table and refs")
     _call(load().msa_pages_compact(pools, len(pools), int(num_pool_blocks), _ptr(block_table),
                                    block_table.shape[0], block_table.shape[1], _ptr(refs),
                                    _ptr(table_out), _ptr(refs_out), _ptr(live), _ptr(ws),

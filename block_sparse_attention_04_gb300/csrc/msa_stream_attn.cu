@@ -15,8 +15,9 @@
 // The call's work is one sequence of (unit, block) steps, unit (b, t, g) after
 // unit, cut into equal runs, one per CTA and SM; a run's share of one unit is a
 // segment.  The last warp copies K and V of each block (128 tokens of one KV head)
-// into a ring of stages by TMA and runs ahead by its depth.  Warps 0-7 take 16
-// tokens of every block each and never wait for one another inside a segment:
+// into a ring of stages by TMA and runs ahead by its depth.  A team of eight warps
+// takes a block, 16 tokens each, and its warps never wait for one another inside
+// a segment:
 // S^T = K Q^T (tokens x heads) with mma.sync m16n8k16, softmax in registers,
 // P^T transposed inside the warp into the B operand of O^T += V^T P^T.  The
 // order of the contraction's terms is free, so dims are dealt to threads such
@@ -26,12 +27,20 @@
 // elements 2^-27 below the row's maximum, which round at 2^-38 of it).  Codes
 // of V become bf16 (exact), like P (2^-8): the largest p' may belong to values
 // that cancel or vanish, so the others need bf16's range.
-// At a segment's end the eight warps' (O, m, l) are joined in shared memory; a
+// At a segment's end all warps' (O, m, l) are joined in shared memory; a
 // whole unit is written out directly, a cut one leaves a partial per CTA (at
 // most two: the unit its run begins inside, the one it ends inside) that
 // stream_finish_kernel joins.  Small calls, where a launch counts, give every
 // unit a cluster of CTAs instead, which joins its parts through distributed
 // shared memory.
+//
+// Bound by HBM for decode: 64 sequences, a bf16 window of 4096 tokens and 4
+// sinks, G 8, D 128: 165 us against 155 for its bytes at the 6.78 TB/s of a plain copy; 4 sequences
+// of 64K tokens on an 8-bit cache: 80 us against 65 (a ring that only loads takes
+// nearly all of it); 64 selections of 16 8-bit blocks each: 63 us against 40,
+// because one head's codes of a block lie in pieces of 128 bytes, 1 KB apart,
+// and every group selects its own blocks (loads alone: 56 us).  L2 promotion of
+// the tensor maps is off: with 256 bytes HBM read 1.4 times the bytes.
 #include "msa_q8.cuh"
 #include "msa_tma.h"
 
@@ -41,7 +50,7 @@ namespace {
 constexpr int kTeam = 8;             // consumer warps that share a block, 16 tokens each
 // Teams: the blocks of an 8-bit cache take more instructions per byte, and two
 // teams on alternate blocks hide their latency (measured, 4 x 64K tokens: one
-// team 116 us, two TWOTEAM us); a bf16 cache keeps HBM busy with one.
+// team 116 us, two 108 us); a bf16 cache keeps HBM busy with one.
 template <bool Q8, int NTH>
 constexpr int teams() { return Q8 && NTH == 1 ? 2 : 1; }
 constexpr int kQBufs = 2;

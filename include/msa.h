@@ -341,7 +341,7 @@ int msa_forward_q8(const msa_params *p, const int32_t *block_table, int num_pool
  * pages that the window has left: msa_pages_free).  Rows of a block that no
  * query of the call sees may hold anything; a NaN or an infinity in V of a
  * token that one query of a prefill-sized call sees also reaches outputs of
- * the queries up to 127 positions from that one.  p->topk and p->Di are
+ * the queries up to 255 positions from that one.  p->topk and p->Di are
  * checked but not used.  out is bf16 (round to nearest even) from fp32
  * accumulation.  ws: at least msa_window_workspace_bytes(p) bytes, 256-byte
  * aligned. */
@@ -363,8 +363,8 @@ int msa_window_attn_q8(const msa_params *p, const int32_t *block_table, int num_
  * numbers, token counts and block ranges are HOST arrays of n entries, n <=
  * MSA_MAX_BATCH.  The calls only enqueue work and give the same result in any
  * order of execution.  Table entries outside [0, num_pool_blocks) other than
- * -1, and mappings of pages whose count is 0, are reported
- * (MSA_ERR_INVALID_ARG in ws); a call that runs out of free pages maps what it
+ * -1 that a call meets, and mappings of pages whose count is 0 that it shares,
+ * lets go of or compacts, are reported (MSA_ERR_INVALID_ARG in ws); a call that runs out of free pages maps what it
  * can, leaves the rest at -1 and reports MSA_ERR_PAGES (msa_workspace_status).
  * ws: at least msa_pages_workspace_bytes(num_pool_blocks), 256-byte aligned.
  *

@@ -193,4 +193,11 @@ def test_binding_helpers(lib):
     assert (d[1].page_bytes, d[1].per_token) == (2, 0)
     with pytest.raises(ValueError):
         msa.pools([x[:, ::2]])
+    lists = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        msa.msa_pages_copy(d, 6, lists, lists[:2], x)
+    table = torch.zeros(2, 4, dtype=torch.int32)
+    for table_out, refs_out in [(table[:1], lists), (table, lists[:2])]:
+        with pytest.raises(ValueError):
+            msa.msa_pages_compact(d, 6, table, lists, table_out, refs_out, lists, x)
     assert msa.msa_status_string(-6) == "no free page left"

@@ -237,6 +237,20 @@ def test_compact(msa, pages, rows, mb, fill, share, in_place):
     w.same(table, refs)
 
 
+def test_sharing_uncounted_pages_is_reported(msa):
+    w = contiguous_world(20, 4, 4, [500, 200], seed=19)
+    w.device(msa)
+    free = [int(i) for i in np.flatnonzero(w.refs == 0)[:2]]
+    w.d_table[3, 0], w.d_table[3, 1] = free        # pages whose count stayed 0
+    msa.msa_pages_fork(w.set, 20, w.d_table, w.d_refs, [0, 3], [2, 1], [256, 256], w.ws)
+    with pytest.raises(msa.MsaError) as e:
+        msa.msa_workspace_status(w.ws)
+    assert e.value.status == -1
+    assert (w.d_refs >= 0).all()
+    # the pair beside it is as it should be
+    assert np.array_equal(w.d_table[2].cpu().numpy(), list(w.table[0, :2]) + [-1, -1])
+
+
 def test_inconsistent_tables_are_reported(msa):
     w = contiguous_world(20, 4, 4, [500, 200], seed=9)
     w.device(msa)
