@@ -237,17 +237,17 @@ __global__ void __launch_bounds__(kBook) pages_fork_kernel(PageTable pt,
   for (int64_t x = (int64_t)blockIdx.x * kBook + threadIdx.x; x < entries; x += kBookCtas * kBook) {
     const int j = (int)(x / pt.max_blocks), kb = (int)(x % pt.max_blocks);
     int32_t* dst = pt.table + (int64_t)rl.b[j] * pt.max_blocks + kb;
-    int e = -1;
-    if (kb < rl.c[j] / kBlock) {
-      e = pt.table[(int64_t)rl.a[j] * pt.max_blocks + kb];
-      if (e < 0 || e >= pt.pages) {
-        code = worse(code, kDevInvalid);
-        e = -1;
-      } else if (atomicAdd(pt.refs + e, 1) <= 0) {   // the source's own mapping was not counted
-        code = worse(code, kDevInvalid);
-      }
+    // both reads, then both counts in flight at once
+    const bool share = kb < rl.c[j] / kBlock;
+    int e = share ? pt.table[(int64_t)rl.a[j] * pt.max_blocks + kb] : -1;
+    const int old = *dst;
+    if (e < 0 || e >= pt.pages) {
+      if (share) code = worse(code, kDevInvalid);
+      e = -1;
     }
-    code = worse(code, release(pt, *dst));
+    const int had = e >= 0 ? atomicAdd(pt.refs + e, 1) : 1;
+    code = worse(code, release(pt, old));
+    if (had <= 0) code = worse(code, kDevInvalid);   // the source's own mapping was not counted
     *dst = e;
   }
   // pair j of thread j: does its last page need a copy, and which free page is its
