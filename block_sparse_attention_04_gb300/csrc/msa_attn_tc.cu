@@ -29,9 +29,9 @@
 // write them into the same rings.  A tile has one KV block, so its exponents
 // are two numbers, which travel in the tile's descriptor: 2^ek scales the
 // scores, 2^ev waits for the merge.  P is relative to the block's own maximum,
-// so f16 holds it (2^-11, and 2^-25 of the maximum at the small end, over 128
-// tokens), and O = sum p code is below 128 * 448 < 2^16: the partials are f16
-// too.  Rows of V behind the call's last query are zeroed on the way.
+// so f16 holds it, as 2^15 p (2^-11, and 2^-40 of the maximum at the small
+// end: a weight that small counts for nothing beside codes that span 2^18), and
+// O = sum p code is below 128 * 448 < 2^16: the partials are f16 too.  Rows of V behind the call's last query are zeroed on the way.
 #include <climits>
 
 #include "msa_q8.cuh"
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
             if constexpr (Q8) {
               // every exponential on the MUFU unit, the rest two lanes at a time
               const float2 x = ffma2(make_float2(__uint_as_float(h[k]), __uint_as_float(h[k + 1])),
-                                     make_float2(sl, sl), make_float2(-m, -m));
+                                     make_float2(sl, sl), make_float2(kPUp - m, kPUp - m));
               float2 pp = make_float2(ex2(x.x), ex2(x.y));
               if (masked) {
                 pp.x = cc * 32 + hf * 16 + k <= lim ? pp.x : 0.f;
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
         const size_t prow = (((size_t)b * a.Tp + il) * H + (size_t)g * hpg + hh) * kTopk + slot;
         if constexpr (Q8)
           __stcs(a.part_mle + prow,
-                 make_float4(m, l2.x + l2.y, (float)((d.z >> 16 & 0xFF) - 128), 0.f));
+                 make_float4(m, (l2.x + l2.y) * kPDown, (float)((d.z >> 16 & 0xFF) - 128), 0.f));
         else
           __stcs(a.part_ml + prow, make_float2(m, l0 + l1));
       }
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
             for (int k = 0; k < 4; ++k) {
               const float x = __uint_as_float(h[e8 * 8 + 2 * k]);
               const float y = __uint_as_float(h[e8 * 8 + 2 * k + 1]);
-              w[k] = Q8 ? pack_f16(x, y) : pack_bf16(x, y);
+              w[k] = Q8 ? pack_f16(x * kPDown, y * kPDown) : pack_bf16(x, y);
             }
             const uint4 pk = make_uint4(w[0], w[1], w[2], w[3]);
             __stcs(reinterpret_cast<uint4*>(dst + cc * 16 + e8 * 8), pk);

@@ -8,6 +8,9 @@ namespace msa {
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
+// Weights in f16 are held as 2^15 p: p <= 1 then has f16's whole range.
+constexpr float kPUp = 15.f, kPDown = 1.f / 32768;
+
 // A stored exponent as the readers use it: any byte is defined.
 __device__ __forceinline__ int clamp_exp(int e) { return min(max(e, kMinExp), kMaxExp); }
 
