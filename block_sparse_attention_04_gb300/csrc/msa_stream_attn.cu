@@ -12,9 +12,9 @@
 // a block of zeros has the smallest ev, and p' of it would vanish beside other
 // blocks while its weights count.  The result is O / l * 2^(m' - n).
 //
-// The call's work is one sequence of (unit, block) steps, unit (b, t, g) after
-// unit, cut into equal runs, one per CTA and SM; a run's share of one unit is a
-// segment.  The last warp copies K and V of each block (128 tokens of one KV head)
+// The call's work is one sequence of (query, block) steps, query (b, t) after
+// query, cut into equal runs; G CTAs take a run, one KV head each, and a run's
+// share of one query is a segment.  The last warp copies K and V of each block (128 tokens of one KV head)
 // into a ring of stages by TMA and runs ahead by its depth.  A team of eight warps
 // takes a block, 16 tokens each, and its warps never wait for one another inside
 // a segment:
@@ -35,12 +35,15 @@
 // shared memory.
 //
 // Bound by HBM for decode: 64 sequences, a bf16 window of 4096 tokens and 4
-// sinks, G 8, D 128: 165 us against 155 for its bytes at the 6.78 TB/s of a plain copy; 4 sequences
-// of 64K tokens on an 8-bit cache: 80 us against 65 (a ring that only loads takes
-// nearly all of it); 64 selections of 16 8-bit blocks each: 63 us against 40,
-// because one head's codes of a block lie in pieces of 128 bytes, 1 KB apart,
-// and every group selects its own blocks (loads alone: 56 us).  L2 promotion of
-// the tensor maps is off: with 256 bytes HBM read 1.4 times the bytes.
+// sinks, G 8, D 128: 161 us against 155 for its bytes at the 6.78 TB/s of a plain
+// copy (the heads of a run at the same time: 167 us with one run per CTA, whose
+// rows of one head are 256 bytes apart by 2 KB).  An 8-bit cache needs as long
+// for its arithmetic as for its bytes: 4 sequences of 64K tokens 79 us (copies
+// alone 71, arithmetic alone 68, bytes 65); 64 selections of 16 blocks, of which
+// every group has its own, in pieces of 128 bytes 1 KB apart, 60 us (55, 56 and
+// 40).  f16 weights and values, whose conversion takes fewer instructions but
+// whose weights need a maximum per 16 tokens, took 83 and 66 us; three teams of
+// four warps with 32 tokens each 90 and 68 us.
 #include "msa_q8.cuh"
 #include "msa_tma.h"
 
@@ -49,8 +52,8 @@ namespace {
 
 constexpr int kTeam = 8;             // consumer warps that share a block, 16 tokens each
 // Teams: the blocks of an 8-bit cache take more instructions per byte, and two
-// teams on alternate blocks hide their latency (measured, 4 x 64K tokens: one
-// team 116 us, two 108 us); a bf16 cache keeps HBM busy with one.
+// teams on alternate blocks hide their latency (measured, 4 x 64K tokens, before
+// the heads of a run went together: one team 116 us, two 108 us); a bf16 cache keeps HBM busy with one.
 template <bool Q8, int NTH>
 constexpr int teams() { return Q8 && NTH == 1 ? 2 : 1; }
 constexpr int kQBufs = 2;
@@ -64,7 +67,7 @@ struct StreamArgs {
   Shape s;
   int32_t q_start[kMaxBatch];
   int32_t step0[kMaxBatch + 1];   // first step of each sequence; [B]: all steps
-  int t0, Tp, nctas, stages;
+  int t0, Tp, nruns, stages;
   int window, sinks;
   const int32_t* sel;
   const uint16_t* q;
@@ -80,21 +83,21 @@ struct StreamArgs {
   uint32_t wait_polls;
 };
 
-// CTA c's run of steps begins at floor(c * steps / nctas).
-__host__ __device__ __forceinline__ int run_begin(int steps, int nctas, int c) {
-  return (int)((int64_t)c * steps / nctas);
+// Run r begins at step floor(r * steps / nruns); CTA r * G + g takes its KV head g.
+__host__ __device__ __forceinline__ int run_begin(int steps, int nruns, int r) {
+  return (int)((int64_t)r * steps / nruns);
 }
-__device__ __forceinline__ int run_of(int steps, int nctas, int step) {
-  return (int)((((int64_t)step + 1) * nctas - 1) / steps);
+__device__ __forceinline__ int run_of(int steps, int nruns, int step) {
+  return (int)((((int64_t)step + 1) * nruns - 1) / steps);
 }
 
-// The unit that a step belongs to: its first step, its steps (the longest
-// list of its sequence in this pass) and its query.
+// A unit: a query and a KV head; the query's first step and its steps (the
+// longest list of its sequence in this pass).
 struct Unit {
   int b, i, g, t, first, len;
 };
 
-__device__ __forceinline__ Unit unit_of(const StreamArgs& a, int step) {
+__device__ __forceinline__ Unit unit_of(const StreamArgs& a, int step, int g) {
   int lo = 0, hi = a.s.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -102,11 +105,11 @@ __device__ __forceinline__ Unit unit_of(const StreamArgs& a, int step) {
   }
   Unit u;
   u.b = lo;
-  u.len = (a.step0[lo + 1] - a.step0[lo]) / (a.Tp * a.s.G);
-  const int ig = (step - a.step0[lo]) / u.len;
-  u.first = a.step0[lo] + ig * u.len;
-  u.g = ig % a.s.G;
-  u.i = a.t0 + ig / a.s.G;
+  u.len = (a.step0[lo + 1] - a.step0[lo]) / a.Tp;
+  const int i = (step - a.step0[lo]) / u.len;
+  u.first = a.step0[lo] + i * u.len;
+  u.g = g;
+  u.i = a.t0 + i;
   u.t = a.q_start[lo] + u.i;
   return u;
 }
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
   uint8_t* sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], q_full[kQBufs], q_empty[kQBufs];
-  __shared__ int meta_kb[kMaxStages], meta_ke[kMaxStages], meta_ve[kMaxStages];
+  __shared__ int2 meta[kMaxStages];       // block (-1: none), exponents ek and ev * 2^16
   __shared__ float sm_m[kWarps][NTH * 8], sm_n[kWarps][NTH * 8], sm_l[kWarps][NTH * 8];
   __shared__ int err;
   const Shape& s = a.s;
@@ -168,8 +171,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
   const uint32_t red = smem_u32(qbuf + kQBufs * hpg * D);                 // [kWarps][hpg][kRedRow] float
   const int steps = a.step0[s.B];
   // steps of this CTA; in cluster form one segment, numbered from 0
-  const int run0 = a.parts ? 0 : run_begin(steps, a.nctas, blockIdx.x);
-  const int run1 = a.parts ? 1 : run_begin(steps, a.nctas, blockIdx.x + 1);
+  const int run = (int)blockIdx.x / G;
+  const int run0 = a.parts ? 0 : run_begin(steps, a.nruns, run);
+  const int run1 = a.parts ? 1 : run_begin(steps, a.nruns, run + 1);
   // the segment that begins at `step`: its unit and list positions; the next step
   auto segment = [&](int step, Unit& u, BlockList& bl, int& p0, int& p1) -> int {
     if (a.parts) {
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
       p1 = (rank + 1) * bl.len / a.parts;
       return 1;
     }
-    u = unit_of(a, step);
+    u = unit_of(a, step, (int)blockIdx.x % G);
     bl = list_of(a, u.t);
     const int next = min(run1, u.first + u.len);
     p0 = step - u.first;
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
           a.sel ? a.sel + (((int64_t)u.b * s.T + u.i) * G + u.g) * kTopk : nullptr;
       for (int pc = p0; pc < p1 && ok; pc += 32) {
         // one list position per lane: its block, cache block and exponents
-        int kb = -1, ke = 0, ve = 0, row = 0;
+        int kb = -1, ex = 0, row = 0;
         const int p = pc + lane;
         if (p < p1) {
           kb = srow ? srow[p] : (p < bl.nsink ? p : bl.first + p);
@@ -246,8 +250,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
             } else {
               row = (int)(pb * kBlock);
               if (Q8) {
-                ke = clamp_exp(a.k_exp[pb * G + u.g]);
-                ve = clamp_exp(a.v_exp[pb * G + u.g]);
+                ex = (clamp_exp(a.k_exp[pb * G + u.g]) & 0xFFFF) |
+                     clamp_exp(a.v_exp[pb * G + u.g]) * 65536;
               }
             }
           }
@@ -255,13 +259,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
         const int n = min(32, p1 - pc);
         for (int j = 0; j < n; ++j) {
           const int kbj = __shfl_sync(0xffffffffu, kb, j), rowj = __shfl_sync(0xffffffffu, row, j);
-          const int kej = __shfl_sync(0xffffffffu, ke, j), vej = __shfl_sync(0xffffffffu, ve, j);
+          const int exj = __shfl_sync(0xffffffffu, ex, j);
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph, &err, a.wait_polls));
           if (!ok) break;
           if (lane == 0) {
-            meta_kb[st] = kbj;
-            meta_ke[st] = kej;
-            meta_ve[st] = vej;
+            meta[st] = make_int2(kbj, exj);
             if (kbj < 0) {
               mbar_arrive(&full[st]);
             } else {
@@ -302,7 +304,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
     const int g4 = lane >> 2, t4 = lane & 3;   // row group and column pair of a fragment
     const float qk = s.scale * kLog2e;
     const int wt = warp % kTeam;               // this warp's 16 tokens of a block
-    int st = 0, k = 0, turn = warp / kTeam;    // turn 0: the next block is this team's
+    int st = warp / kTeam, k = 0;              // the team's next stage
+    int turn = st;                             // blocks before its next one
     uint32_t ph = 0;
     bool ok = true;
     for (int step = run0, next; step < run1; step = next, ++k) {
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
       BlockList bl;
       int p0, p1;
       next = segment(step, u, bl, p0, p1);
-      const int nblk = p1 - p0;
+      const int nblk = max(0, p1 - p0);   // 0: a run past the end of a shorter list
       const int lo = a.sel ? 0 : max(0, u.t - a.window + 1);   // visible: j <= t and
       const int sinks = a.sel ? 0 : a.sinks;                   // (j >= lo or j < sinks)
       const int qs = k % kQBufs;
@@ -378,14 +381,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
           l[nt][e] = 0.f;
         }
 
-      for (int blk = 0; blk < nblk; ++blk) {
-        const bool mine = turn == 0;
-        turn = mine ? C::kTeams - 1 : turn - 1;
-        if (mine) {
-          ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[st], ph, &err, a.wait_polls));
-          if (!ok) break;
-        }
-        const int kb = mine ? meta_kb[st] : -1;
+      for (; turn < nblk; turn += C::kTeams) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[st], ph, &err, a.wait_polls));
+        if (!ok) break;
+        const int2 mt = meta[st];
+        const int kb = mt.x;
         if (kb >= 0) {
           const int tok0 = kb * kBlock;
           const int w0 = tok0 + wt * 16;              // this warp's first token
@@ -434,16 +434,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
             // ---- x = s log2(e), masked; the maxima move only when one grew
             float fk = 1.f, ev = 0.f;
             if constexpr (Q8) {
-              fk = pow2i(meta_ke[st]);
-              ev = (float)meta_ve[st];
-            }
-            bool vis[2] = {true, true};                   // tokens w0 + g4, w0 + g4 + 8
-            if (!whole) {
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int tok = w0 + g4 + 8 * j;
-                vis[j] = tok <= u.t && (tok >= lo || tok < sinks);
-              }
+              fk = pow2i((int16_t)mt.y);
+              ev = (float)(mt.y >> 16);
             }
             float mx[NTH][2];
             bool grow = false;
@@ -452,8 +444,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const float f = Q8 ? fminf(fmaxf(fq[nt][e] * fk, -3e38f), 3e38f) : fq[nt][e];
-                sc[nt][e] = vis[0] ? sc[nt][e] * f : -INFINITY;
-                sc[nt][2 + e] = vis[1] ? sc[nt][2 + e] * f : -INFINITY;
+                sc[nt][e] *= f;
+                sc[nt][2 + e] *= f;
+                if (!whole) {                             // tokens w0 + g4, w0 + g4 + 8
+                  const int tok = w0 + g4;
+                  if (!(tok <= u.t && (tok >= lo || tok < sinks))) sc[nt][e] = -INFINITY;
+                  if (!(tok + 8 <= u.t && (tok + 8 >= lo || tok + 8 < sinks)))
+                    sc[nt][2 + e] = -INFINITY;
+                }
                 mx[nt][e] = fmaxf(sc[nt][e], sc[nt][2 + e]);
                 grow |= mx[nt][e] + ev > m[nt][e] + kLazy || (Q8 && mx[nt][e] > n[nt][e] + kLazy);
               }
@@ -566,12 +564,13 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
           }
         }
         __syncwarp();
-        if (mine && lane == 0) mbar_arrive(&empty[st]);
-        if (++st == S) {
-          st = 0;
+        if (lane == 0) mbar_arrive(&empty[st]);
+        if ((st += C::kTeams) >= S) {
+          st -= S;
           ph ^= 1;
         }
       }
+      turn -= nblk;
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_empty[qs]);
 
@@ -691,7 +690,7 @@ __device__ __forceinline__ int worse(int x, int y) {
 }
 
 // Joins the partials of the units that a run's end cuts: one warp per (run,
-// head), for the first run that begins inside a unit.  The first CTA also
+// query head), for the first run that begins inside a unit.  The first CTA also
 // turns the CTAs' error words into the status.
 template <int D>
 __global__ void __launch_bounds__(256) stream_finish_kernel(const __grid_constant__ StreamArgs a) {
@@ -700,24 +699,24 @@ __global__ void __launch_bounds__(256) stream_finish_kernel(const __grid_constan
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x < 32) {
     int e = 0;
-    for (int c = lane; c < a.nctas; c += 32) e = worse(e, a.errs[c]);
+    for (int c = lane; c < a.nruns * s.G; c += 32) e = worse(e, a.errs[c]);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) e = worse(e, __shfl_xor_sync(0xffffffffu, e, x));
     if (lane == 0) *a.status = a.first_pass ? e : worse(e, *a.status);
   }
   const int hpg = s.H / s.G;
   const int gw = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int run = gw / hpg + 1, h = gw % hpg, steps = a.step0[s.B];
-  if (run >= a.nctas) return;
-  const int begin = run_begin(steps, a.nctas, run);
-  const Unit u = unit_of(a, begin);
-  const int r0 = run_of(steps, a.nctas, u.first);
+  const int run = gw / s.H + 1, g = gw % s.H / hpg, h = gw % hpg, steps = a.step0[s.B];
+  if (run >= a.nruns) return;
+  const int begin = run_begin(steps, a.nruns, run);
+  const Unit u = unit_of(a, begin, g);
+  const int r0 = run_of(steps, a.nruns, u.first);
   if (begin == u.first || run != r0 + 1) return;
-  const int r1 = run_of(steps, a.nctas, u.first + u.len - 1);
+  const int r1 = run_of(steps, a.nruns, u.first + u.len - 1);
   // run r0 ends inside the unit (its slot 1), runs r0 + 1 ... r1 begin inside it (slot 0)
   float M = -INFINITY, N = -INFINITY;
   for (int r = r0 + lane; r <= r1; r += 32) {
-    const float4 v = a.part_ml[(int64_t)(2 * r + (r == r0)) * hpg + h];
+    const float4 v = a.part_ml[(int64_t)(2 * (r * s.G + g) + (r == r0)) * hpg + h];
     M = fmaxf(M, v.x);
     N = fmaxf(N, v.y);
   }
@@ -731,7 +730,7 @@ __global__ void __launch_bounds__(256) stream_finish_kernel(const __grid_constan
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
 #pragma unroll 4
   for (int r = r0; r <= r1; ++r) {
-    const int64_t p = (int64_t)(2 * r + (r == r0)) * hpg + h;
+    const int64_t p = (int64_t)(2 * (r * s.G + g) + (r == r0)) * hpg + h;
     const float4 v = a.part_ml[p];
     const float w = v.x == -INFINITY ? 0.f : ex2(v.x - M);
     float x[PER];
@@ -828,8 +827,8 @@ cudaError_t launch_impl(const CacheView& c, StreamArgs& a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, stream_attn_kernel<D, Q8, NTH>, tm_k, tm_v, a);
   }
   note_launches(2);
-  stream_attn_kernel<D, Q8, NTH><<<a.nctas, C::kThreads, smem, st>>>(tm_k, tm_v, a);
-  const int warps = (a.nctas - 1) * hpg;
+  stream_attn_kernel<D, Q8, NTH><<<a.nruns * a.s.G, C::kThreads, smem, st>>>(tm_k, tm_v, a);
+  const int warps = (a.nruns - 1) * a.s.H;
   stream_finish_kernel<D><<<warps > 0 ? (warps + 7) / 8 : 1, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
@@ -893,14 +892,14 @@ cudaError_t launch_stream_attn(const Shape& s, const Positions& pos, const Cache
       }
     }
     a.step0[0] = 0;
-    for (int b = 0; b < s.B; ++b) a.step0[b + 1] = a.step0[b] + a.Tp * s.G * len[b];
+    for (int b = 0; b < s.B; ++b) a.step0[b + 1] = a.step0[b] + a.Tp * len[b];
     const int steps = a.step0[s.B];
-    a.nctas = steps < ctas ? steps : ctas;
+    a.nruns = steps < ctas / s.G ? steps : ctas / s.G;
     a.parts = 0;
     if (a.Tp == s.T && !join_status) {
       int longest = 1;
       for (int b = 0; b < s.B; ++b) longest = len[b] > longest ? len[b] : longest;
-      a.parts = cluster_parts(s.B * a.Tp * s.G, longest, steps, ctas);
+      a.parts = cluster_parts(s.B * a.Tp * s.G, longest, (int64_t)steps * s.G, ctas);
     }
     const bool wide = s.H / s.G > 8;    // heads of a group in one or two n-tiles of 8
     cudaError_t e;
