@@ -22,7 +22,9 @@
 //                 sees (they may hold anything) are zeroed before their first
 //                 use: a weight of 0 does not cancel a NaN.
 //   warps 3-10    one warpgroup per chain, a row per thread: mask, maximum,
-//                 P = 2^(x - m) over S, row sum; at the item's end O / l
+//                 P = 2^(x - m) over S, row sum; at the item's end O / l, written
+//                 64 bytes of a row at a time (16 bytes of 32 rows per store, as
+//                 the rows lie in tensor memory, cost 3 % of the call)
 //   warps 11-14   8-bit cache, in place of warp 1: codes of the next block to
 //                 registers, converted into the same rings: K to f16 and V to
 //                 bf16 (both exact); Q tiles to f16 in place, each row scaled by
@@ -41,6 +43,14 @@
 // latter by one factor per row and block, 2^(m - ev - n), unless that factor is
 // so large that p' may have vanished (blocks whose scale is 2^80 below the
 // others', such as blocks of zeros): then it is summed by exponentials of its own.
+//
+// Measured (us; the MMAs' time at cuBLAS' burst rate beside it): 16K queries, 48/8
+// heads, D 128, window 4096 and 64 sinks 1110 (764 for the visible tokens); 3 x
+// 1000 queries, 64/4, D 64, window 1000, 8-bit cache 114 (26), bf16 98.  A block
+// step of the two chains takes 1.5 us at D 64, 1.66 at D 128 (of which the MMAs
+// 1.34), with an 8-bit cache 1.76 and 2.13: the chain S, maximum, P, P.V has few
+// steps to overlap with, and power is at its limit.  An item costs 3-4 us beyond
+// its steps: masked blocks, output, the first S.
 #include "msa_q8.cuh"
 #include "msa_serve.h"
 #include "msa_tma.h"
@@ -89,7 +99,8 @@ struct WinCfg {
   static constexpr int kNHalf = D / 64;
   static constexpr int kHalf = 128 * 128;       // 128 rows x 64 dims of 16 bits (16 KiB)
   static constexpr int kTile = kNHalf * kHalf;  // a Q tile, a K or a V block
-  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + 2048 + 512 + 1024;
+  static constexpr int kStage = 32 * 64;        // a softmax warp's 32 output rows, 32 dims
+  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + 2048 + 8 * kStage + 512 + 1024;
   static constexpr uint32_t kTmemCols = 512;
 };
 
@@ -141,7 +152,8 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
   uint8_t* sK = sQ + 2 * C::kTile;            // [kStages] K blocks
   uint8_t* sV = sK + kStages * C::kTile;      // [kStages] V blocks
   float* q_scale = reinterpret_cast<float*>(sV + kStages * C::kTile);   // [2][chain][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(q_scale + 2 * 2 * 128);
+  uint8_t* sO = reinterpret_cast<uint8_t*>(q_scale + 2 * 2 * 128);        // [warp] output rows
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sO + 8 * C::kStage);
   uint64_t* q_full = bars;                    // per chain: the item's Q tile landed
   uint64_t* q_ready = q_full + 2;             // ... and is in f16 (8-bit cache)
   uint64_t* q_empty = q_ready + 2;            // per chain: the item's last S is done
@@ -355,11 +367,12 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         if (!Q8 && (phi < kBlock - 1 || (plo > 0 && psk < kBlock))) {
           // rows of V that no query of the item sees
           const uint32_t v = smem_u32(sV + pks * C::kTile);
-          for (int e = lane; e < kBlock * (D / 8); e += 32) {
-            const int r = e / (D / 8);
-            if (r > phi || (r < plo && r >= psk))
-              sts128(v + tile_off(r, e % (D / 8)), make_uint4(0, 0, 0, 0));
-          }
+          auto clear = [&](int r0, int r1) {
+            for (int e = lane + r0 * (D / 8); e < r1 * (D / 8); e += 32)
+              sts128(v + tile_off(e / (D / 8), e % (D / 8)), make_uint4(0, 0, 0, 0));
+          };
+          clear(max(psk, 0), min(plo, kBlock));
+          clear(phi + 1, kBlock);
           fence_async();
           __syncwarp();
         }
@@ -688,23 +701,36 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         continue;
       }
       const float inv = l == 0.f ? 0.f : (Q8 ? ex2(m_ref - n_ref) : 1.f) / l;
+      // rows go to memory 64 bytes at a time, by four lanes each, through shared
+      // memory: a lane's own row, 16 bytes at a time, touches 32 lines per store
       uint16_t* dst =
-          a.out + (((int64_t)d.b * T + (valid ? i : 0)) * H + d.g * hpg + rh) * D;
+          a.out + (((int64_t)d.b * T + d.i0 + c * nq) * H + (int64_t)d.g * hpg) * D;
+      const int rel = valid ? (rq * H + rh) * D : -1;
+      const uint32_t stage = smem_u32(sO) + (warp - kSoftWarp0) * C::kStage;
 #pragma unroll 1
-      for (int cc = 0; cc < D / 16; ++cc) {
-        uint32_t h[16];
-        tmem_ld16(o_base + cc * 16, h);
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t h[32];
+        tmem_ld16(o_base + cc * 32, *reinterpret_cast<uint32_t(*)[16]>(h));
+        tmem_ld16(o_base + cc * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(h + 16));
         tmem_ld_wait();
-        if (valid) {
+        __syncwarp();
 #pragma unroll
-          for (int e8 = 0; e8 < 2; ++e8) {
-            uint4 pk;
-            pk.x = pack_bf16(__uint_as_float(h[e8 * 8 + 0]) * inv, __uint_as_float(h[e8 * 8 + 1]) * inv);
-            pk.y = pack_bf16(__uint_as_float(h[e8 * 8 + 2]) * inv, __uint_as_float(h[e8 * 8 + 3]) * inv);
-            pk.z = pack_bf16(__uint_as_float(h[e8 * 8 + 4]) * inv, __uint_as_float(h[e8 * 8 + 5]) * inv);
-            pk.w = pack_bf16(__uint_as_float(h[e8 * 8 + 6]) * inv, __uint_as_float(h[e8 * 8 + 7]) * inv);
-            *reinterpret_cast<uint4*>(dst + cc * 16 + e8 * 8) = pk;
-          }
+        for (int e8 = 0; e8 < 4; ++e8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = pack_bf16(__uint_as_float(h[e8 * 8 + 2 * j]) * inv,
+                             __uint_as_float(h[e8 * 8 + 2 * j + 1]) * inv);
+          sts128(stage + lane * 64 + ((e8 ^ ((lane >> 1) & 3)) << 4),
+                 make_uint4(w[0], w[1], w[2], w[3]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = j * 8 + (lane >> 2), e8 = lane & 3;
+          const int at = __shfl_sync(0xffffffffu, rel, row);
+          const uint4 v = lds128(stage + row * 64 + ((e8 ^ ((row >> 1) & 3)) << 4));
+          if (at >= 0) *reinterpret_cast<uint4*>(dst + at + cc * 32 + e8 * 8) = v;
         }
       }
     }
