@@ -314,8 +314,8 @@ int msa_cache_append_q8(const msa_params *p, const int32_t *block_table, int num
 /* Step 4 (msa_sparse_attn) and steps 1-4 (msa_forward) on an 8-bit cache, per
  * sequence (block_table NULL) or paged.  The attention of the cached values is
  * computed as for a bf16 cache (fp32 accumulation, bf16 output); a row whose
- * selection holds no visible token is written as zeros.  Cache rows that no
- * query may see (behind the last query) may hold anything.  ws: at least
+ * selection holds no visible token is written as zeros, and an id that is
+ * listed twice counts twice.  Cache rows that no query may see (behind the last query) may hold anything.  ws: at least
  * msa_q8_workspace_bytes(p) bytes, 256-byte aligned. */
 size_t msa_q8_workspace_bytes(const msa_params *p);
 int msa_sparse_attn_q8(const msa_params *p, const int32_t *block_table, int num_pool_blocks,

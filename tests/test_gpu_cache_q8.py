@@ -387,3 +387,62 @@ def test_q8_bad_blocks_are_reported_and_skipped(msa, kernels):
         msa.msa_workspace_status(ws)
     assert e.value.status == -1
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("kernels", KERNELS)
+@pytest.mark.parametrize("T", [2, 200])
+def test_a_block_listed_twice_counts_twice(msa, kernels, T):
+    lens, H, G, D = [1500], 12, 4, 64
+    nb = 13
+    c = Cache(lens, G, D, nb, seed=61)
+    q = randq(1, T, H, D)
+    q_start = [1500 - T]
+    rng = np.random.default_rng(62)
+    sel = np.full((1, T, G, 16), -1, np.int32)
+    for i in range(T):
+        for g in range(G):
+            lb = (q_start[0] + i) // 128
+            ids = np.sort(np.append(rng.choice(lb, 6, replace=False), [lb]))
+            sel[0, i, g, :9] = np.sort(np.append(ids, ids[[1, 3]]))
+    sel = torch.from_numpy(sel).cuda()
+    out = run_sparse(msa, c, q, sel, q_start, lens, nb, 32, kernels)
+    k, v = c.values()
+    # the reference holds every row twice; the second copy is visible where its
+    # block is listed twice
+    N = nb * 128
+    block = torch.arange(N, device="cuda") // 128
+
+    def seen(b, g, t):
+        count = (sel[b, :, g, :, None] == torch.arange(nb, device="cuda")).sum(1)[:, block]
+        causal = torch.arange(N, device="cuda") <= t[:, None]
+        return torch.cat([(count > 0) & causal, (count > 1) & causal], 1)
+
+    twice = [[torch.cat([x, x]) for x in y] for y in (k, v)]
+    u = sr.U_BF16 if kernels == "streaming" else 2 * sr.U_BF16
+    want, bound = sr.attend_call(q, *twice, q_start, seen, D ** -0.5, u)
+    sr.check(out, want, bound)
+
+
+def test_append_of_the_largest_batch(msa):
+    # 256 sequences, one of them without room left behind it
+    G, D, Di, nb = 2, 64, 32, 2
+    c = Cache([0] * 256, G, D, nb, seed=63)
+    g = torch.Generator(device="cuda").manual_seed(64)
+    new = [torch.randn(256, 3, G, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    ki_new = torch.randn(256, 3, Di, generator=g, device="cuda").to(torch.bfloat16)
+    ki = torch.zeros(c.pages, 128, Di, dtype=torch.bfloat16, device="cuda")
+    q_start = [(i * 5) % 254 for i in range(255)] + [253]
+    p = msa.params(256, 3, G, G, D, Di, nb)
+    ws = msa.q8_workspace(p)
+    msa.msa_cache_append_q8(p, *new, ki_new, q_start, *c.codes, *c.exps, ki, ws,
+                            block_table=c.table, num_pool_blocks=c.pages)
+    msa.msa_workspace_status(ws)
+    for b, a in enumerate(q_start):
+        for i in range(3):
+            page, r = int(c.table[b, (a + i) // 128]), (a + i) % 128
+            assert torch.equal(ki[page, r], ki_new[b, i])
+            for x, codes, e in zip(new, c.codes, c.exps):
+                got = sr.dequant(codes[page:page + 1], e[page:page + 1])[0, r]
+                scale = torch.exp2(e[page].double())[:, None]
+                bound = (x[b, i].double().abs() * 2.0 ** -4).maximum(scale * 2.0 ** -10)
+                assert ((got.double() - x[b, i].double()).abs() <= bound).all()

@@ -293,3 +293,81 @@ def test_window_all_scores_minus_infinity_then_finite(msa, kernels):
         return s
     want, bound = sr.attend_call(q, k, v, q_start, seen, 64 ** -0.5, sr.U_BF16)
     sr.check(out, want, bound)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("H,G", [(12, 3), (5, 5), (18, 6), (14, 7)])
+def test_window_any_number_of_kv_heads(msa, H, G, q8):
+    # runs of blocks are shared by G CTAs each, whatever G leaves of the SMs
+    lens = [6000, 4100, 130]
+    c, q, q_start = make(lens, 2, H, G, 64, seed=H)
+    nb = c.table.shape[1]
+    out = run(msa, c, q8, q, q_start, lens, nb, 5000, 70, "streaming")
+    k, v = c.values()
+    want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, 5000, 70, "cuda"),
+                                 0.125, sr.U_BF16)
+    sr.check(out, want, bound)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_streaming_in_several_passes_joins_their_status(msa, q8):
+    # 2 x 1300 queries: more than one pass of the streaming kernels.  A bad entry
+    # that only queries of the first pass read is still reported at the end.
+    lens, T, window = [1300, 1500], 1300, 100
+    c, q, q_start = make(lens, T, 4, 2, 64, seed=41)
+    nb = c.table.shape[1]
+    out = run(msa, c, q8, q, q_start, lens, nb, window, 0, "streaming")
+    k, v = c.values()
+    want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, window, 0, "cuda"),
+                                 0.125, sr.U_BF16)
+    sr.check(out, want, bound)
+    p = msa.params(2, T, 4, 2, 64, 32, nb, kernels="streaming")
+    ws = msa.window_workspace(p)
+    kv = (*c.codes, *c.exps) if q8 else bf16_cache(c)
+    fn = msa.msa_window_attn_q8 if q8 else msa.msa_window_attn
+    table = c.table.clone()
+    table[0, 1] = c.pages
+    got = torch.empty_like(out)
+    fn(p, window, 0, q, *kv, q_start, lens, got, ws, block_table=table, num_pool_blocks=c.pages)
+    with pytest.raises(msa.MsaError) as e:
+        msa.msa_workspace_status(ws)
+    assert e.value.status == -1
+    assert torch.equal(got[1], out[1]) and torch.equal(got[0, 400:], out[0, 400:])
+
+
+@pytest.mark.parametrize("kernels", KERNELS)
+def test_window_of_the_largest_batch(msa, kernels):
+    # 256 sequences, nine tokens each: two streaming passes of eight queries
+    lens = [9 + (37 * i) % 400 for i in range(256)]
+    c, q, q_start = make(lens, 9, 2, 1, 64, seed=43)
+    nb = c.table.shape[1]
+    for q8 in (False, True):
+        out = run(msa, c, q8, q, q_start, lens, nb, 150, 3, kernels)
+        k, v = c.values()
+        want, bound = sr.attend_call(q, k, v, q_start, sr.window_seen(nb * 128, 150, 3, "cuda"),
+                                     0.125, sr.U_BF16)
+        sr.check(out, want, bound)
+
+
+def test_two_calls_at_once_on_two_streams(msa):
+    # the same inputs on two side streams, with a workspace each
+    lens = [5000, 3000, 700]
+    c, q, q_start = make(lens, 40, 12, 4, 128, seed=47)
+    nb = c.table.shape[1]
+    calls = []
+    for kernels in ("streaming", "tensorcore"):
+        p = msa.params(3, 40, 12, 4, 128, 32, nb, kernels=kernels)
+        calls.append((p, msa.window_workspace(p), torch.empty_like(q), torch.cuda.Stream()))
+    args = ((*c.codes, *c.exps), q_start, lens)
+    kw = dict(block_table=c.table, num_pool_blocks=c.pages)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for p, ws, out, st in calls:
+            with torch.cuda.stream(st):
+                msa.msa_window_attn_q8(p, 900, 5, q, *args[0], *args[1:], out, ws, **kw)
+    for p, ws, out, st in calls:
+        msa.msa_workspace_status(ws, st)
+        alone = torch.empty_like(out)
+        msa.msa_window_attn_q8(p, 900, 5, q, *args[0], *args[1:], alone, ws, **kw)
+        msa.msa_workspace_status(ws)
+        assert torch.equal(out, alone)
