@@ -371,3 +371,66 @@ def test_two_calls_at_once_on_two_streams(msa):
         msa.msa_window_attn_q8(p, 900, 5, q, *args[0], *args[1:], alone, ws, **kw)
         msa.msa_workspace_status(ws)
         assert torch.equal(out, alone)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("kernels", ["streaming", "tensorcore"])
+def test_pools_past_32_bits_of_offset(msa, kernels, q8):
+    # the same few pages at the front of a small pool and at the end of one of
+    # 4.6 GB: the same outputs, and the same bytes from the writer and the copy
+    G, D, nb, T = 8, 128, 6, 33
+    lens = [700, 333]
+    c, q, q_start = make(lens, T, 16, G, D, seed=51, nb=nb)
+    kv = list((*c.codes, *c.exps) if q8 else bf16_cache(c))
+    page = kv[0][0].numel() * kv[0].element_size()
+    pages = (4600 << 20) // page
+    shift = pages - c.pages
+    assert shift * page > 1 << 32
+    big = []
+    for x in kv:
+        y = torch.empty((pages, *x.shape[1:]), dtype=x.dtype, device="cuda")
+        y[shift:] = x
+        big.append(y)
+    p = msa.params(2, T, 16, G, D, 32, nb, kernels=kernels)
+    ws = msa.window_workspace(p)
+    fn = msa.msa_window_attn_q8 if q8 else msa.msa_window_attn
+    outs = []
+    for pool, table, n in [(kv, c.table, c.pages), (big, c.table + shift, pages)]:
+        out = torch.empty_like(q)
+        fn(p, 500, 9, q, *pool, q_start, lens, out, ws, block_table=table, num_pool_blocks=n)
+        msa.msa_workspace_status(ws)
+        outs.append(out)
+    assert torch.equal(*outs)
+    pw = msa.pages_workspace(pages)
+    lists = [torch.tensor(x, dtype=torch.int32, device="cuda")
+             for x in ([shift, shift + 1], [shift + 3, 5])]
+    want = [y[[shift, shift + 1]].clone() for y in big]
+    msa.msa_pages_copy(msa.pools(big), pages, *lists, pw)
+    msa.msa_workspace_status(pw)
+    for y, w in zip(big, want):
+        assert torch.equal(y[[shift + 3, 5]].view(torch.uint8), w.view(torch.uint8))
+    if not q8:
+        return
+    # the sparse call and the writer on the same pools (copied pages put back)
+    for x, y in zip(kv, big):
+        y[shift:] = x
+    sel = torch.full((2, T, G, 16), -1, dtype=torch.int32, device="cuda")
+    sel[..., 0], sel[..., 1] = 0, 2
+    w8 = msa.q8_workspace(p)
+    new = [torch.randn(2, T, G, D, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    ki_new = torch.randn(2, T, 32, device="cuda").to(torch.bfloat16)
+    outs, kis = [], []
+    for pool, table, n in [(kv, c.table, c.pages), (big, c.table + shift, pages)]:
+        kw = dict(block_table=table, num_pool_blocks=n)
+        out = torch.empty_like(q)
+        msa.msa_sparse_attn_q8(p, q, *pool, sel, q_start, lens, out, w8, **kw)
+        msa.msa_workspace_status(w8)
+        ki = torch.zeros(n, 128, 32, dtype=torch.bfloat16, device="cuda")
+        msa.msa_cache_append_q8(p, *new, ki_new, q_start, *pool, ki, w8, **kw)
+        msa.msa_workspace_status(w8)
+        outs.append(out)
+        kis.append(ki)
+    assert torch.equal(*outs)
+    assert torch.equal(kis[0], kis[1][shift:])
+    for x, y in zip(kv, big):
+        assert torch.equal(x, y[shift:])
