@@ -598,16 +598,17 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
       }
       tc_fence_after();
       if (t + 2 < n && e < (nd.z & 0xFF)) nen = a.entries[nd.y + e];
-      // TMEM is read in 16-column loads, each waited before the next: small
-      // loads leave the MMAs of the other chain more of tensor memory than
-      // larger ones (measured).
+      // TMEM is read in 16-column loads: small loads leave the MMAs of the other
+      // chain more of tensor memory than larger ones (measured).  Pass 1 waits for
+      // two of them at a time (128K prefill attention 16.40 ms with one, 15.44
+      // with two, 15.63 with four), pass 2 for each (15.49 with two).
       // pass 1: row maximum of the scaled scores: the maximum of the raw
       // scores, or their minimum when the scale is negative
       const bool neg = sl < 0.f;
       float mx = neg ? INFINITY : -INFINITY;
+      if (masked) {
 #pragma unroll 1
-      for (int cc = 0; cc < 8; ++cc) {
-        if (masked) {
+        for (int cc = 0; cc < 8; ++cc) {
           uint32_t h[16];
           tmem_ld16(lane_base + cc * 16, h);
           tmem_ld_wait();
@@ -617,17 +618,22 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
             const bool in = cc * 16 + k <= lim;
             mx = neg ? fminf(mx, in ? x : INFINITY) : fmaxf(mx, in ? x : -INFINITY);
           }
-        } else {
-          // the load reduces the 16 scores itself
-          if (neg) {
-            const float r = tmem_ld16_red<false>(lane_base + cc * 16);
-            tmem_ld_wait();
-            mx = fminf(mx, r);
-          } else {
-            const float r = tmem_ld16_red<true>(lane_base + cc * 16);
-            tmem_ld_wait();
-            mx = fmaxf(mx, r);
-          }
+        }
+      } else if (neg) {
+#pragma unroll 1
+        for (int cc = 0; cc < 8; cc += 2) {
+          const float r0 = tmem_ld16_red<false>(lane_base + (cc + 0) * 16);
+          const float r1 = tmem_ld16_red<false>(lane_base + (cc + 1) * 16);
+          tmem_ld_wait();
+          mx = fminf(mx, fminf(r0, r1));
+        }
+      } else {   // the loads reduce 16 scores each
+#pragma unroll 1
+        for (int cc = 0; cc < 8; cc += 2) {
+          const float r0 = tmem_ld16_red<true>(lane_base + (cc + 0) * 16);
+          const float r1 = tmem_ld16_red<true>(lane_base + (cc + 1) * 16);
+          tmem_ld_wait();
+          mx = fmaxf(mx, fmaxf(r0, r1));
         }
       }
       const float m = mx * sl;
@@ -635,7 +641,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
       // over S in TMEM: the 32 scores of columns [32cc, 32cc+32) are read (two
       // loads) before columns [16cc, 16cc+16) are written, and those belong to
       // chunks already read; row sum
-      float l0 = 0.f, l1 = 0.f;
+      const float nm = Q8 ? kPUp - m : -m;
       float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
@@ -649,33 +655,19 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
           for (int u = 0; u < 8; ++u) {
             const int k = 2 * u;
             const int uu = hf * 8 + u;
-            if constexpr (Q8) {
-              // every exponential on the MUFU unit, the rest two lanes at a time
-              const float2 x = ffma2(make_float2(__uint_as_float(h[k]), __uint_as_float(h[k + 1])),
-                                     make_float2(sl, sl), make_float2(kPUp - m, kPUp - m));
-              float2 pp = make_float2(ex2(x.x), ex2(x.y));
-              if (masked) {
-                pp.x = cc * 32 + hf * 16 + k <= lim ? pp.x : 0.f;
-                pp.y = cc * 32 + hf * 16 + k + 1 <= lim ? pp.y : 0.f;
-              }
-              l2 = fadd2(l2, pp);
-              wv[uu] = pack_f16(pp.x, pp.y);
-              continue;
-            }
-            // 6 of 16 pairs on the FMA pipe, the rest on the MUFU unit
-            constexpr unsigned kPolyPairs = 0x4925u;  // uu = 0, 2, 5, 8, 11, 14
+            const float2 x =
+                ffma2(make_float2(__uint_as_float(h[k]), __uint_as_float(h[k + 1])),
+                      make_float2(sl, sl), make_float2(nm, nm));
+            // bf16 cache: 6 of 16 pairs on the FMA pipe, the rest on the MUFU unit
+            constexpr unsigned kPolyPairs = Q8 ? 0u : 0x4925u;  // uu = 0, 2, 5, 8, 11, 14
             const bool poly = (kPolyPairs >> uu) & 1u;
-            const float x0 = fmaf(__uint_as_float(h[k]), sl, -m);
-            const float x1 = fmaf(__uint_as_float(h[k + 1]), sl, -m);
-            float p0 = poly ? exp2_poly(x0) : ex2(x0);
-            float p1 = poly ? exp2_poly(x1) : ex2(x1);
+            float2 pp = make_float2(poly ? exp2_poly(x.x) : ex2(x.x), poly ? exp2_poly(x.y) : ex2(x.y));
             if (masked) {
-              p0 = cc * 32 + hf * 16 + k <= lim ? p0 : 0.f;
-              p1 = cc * 32 + hf * 16 + k + 1 <= lim ? p1 : 0.f;
+              pp.x = cc * 32 + hf * 16 + k <= lim ? pp.x : 0.f;
+              pp.y = cc * 32 + hf * 16 + k + 1 <= lim ? pp.y : 0.f;
             }
-            l0 += p0;
-            l1 += p1;
-            wv[uu] = pack_bf16(p0, p1);
+            l2 = fadd2(l2, pp);
+            wv[uu] = Q8 ? pack_f16(pp.x, pp.y) : pack_bf16(pp.x, pp.y);
           }
         }
         tmem_st16(lane_base + cc * 16, wv);
@@ -689,7 +681,7 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
           __stcs(a.part_mle + prow,
                  make_float4(m, (l2.x + l2.y) * kPDown, (float)((d.z >> 16 & 0xFF) - 128), 0.f));
         else
-          __stcs(a.part_ml + prow, make_float2(m, l0 + l1));
+          __stcs(a.part_ml + prow, make_float2(m, l2.x + l2.y));
       }
     }
   } else if (!Q8 || warp < kConvWarp0) {
