@@ -44,11 +44,12 @@ size_t sparse_scratch(const msa_params* p) {
 // measurements behind them).
 constexpr double kSms = 152;
 
-// Streaming: 0.8 us per (unit, block) step and CTA and 1.6 us per unit (the
+// Streaming: a time per (unit, block) step and CTA and 1.6 us per unit (the
 // join of its warps), or the blocks' bytes where they do not stay in L2 between
 // the queries that read them.
-double stream_us(double units, double steps, double step_bytes, double distinct_bytes) {
-  const double compute = steps / kSms * 0.8 + units / kSms * 1.6;
+double stream_us(double units, double steps, double step_bytes, double distinct_bytes,
+                 double step = 0.8) {
+  const double compute = steps / kSms * step + units / kSms * 1.6;
   const double memory = distinct_bytes > 64e6 ? steps * step_bytes / 6.6e6 : 0.0;
   return 6.0 + (compute > memory ? compute : memory);
 }
@@ -81,9 +82,9 @@ bool window_on_tc(const msa_params* p, const Shape& s, const Positions& pos, con
 
 // Selected blocks of an 8-bit cache: the streaming kernel reads 16 blocks per
 // (query, group); the KV-outer kernels read a block once per list and work in
-// tiles of 128 query-head rows, of which a list has at least one: 256 queries
-// of one sequence at 16K, 48/8 heads, 203 us streaming, 74 us KV-outer; 16 x 8
-// queries 111 and 203 us.
+// tiles of 128 query-head rows, of which a list has at least one: 96 queries of
+// one sequence at 16K, 48/8 heads, 77 us streaming, 47 us KV-outer; 16 x 16
+// queries 193 and 259 us.
 bool sparse_on_tc(const msa_params* p, const Shape& s, const Positions& pos) {
   if (p->kernels != MSA_KERNELS_AUTO) return p->kernels == MSA_KERNELS_TENSORCORE;
   const double entries = (double)s.B * s.T * s.G * MSA_TOPK;
@@ -91,11 +92,12 @@ bool sparse_on_tc(const msa_params* p, const Shape& s, const Positions& pos) {
   for (int b = 0; b < s.B; ++b) lists += (pos.q_start[b] + s.T - 1) / kBlock + 1;
   lists *= s.G;
   const double block_bytes = 2.0 * kBlock * s.D;
-  const double stream = stream_us(entries / MSA_TOPK, entries, block_bytes, lists * block_bytes);
   const int rows = s.H / s.G <= 8 ? 8 : 16;
+  const double stream = stream_us(entries / MSA_TOPK, entries, block_bytes, lists * block_bytes,
+                                  s.D == 128 && rows > 8 ? 1.25 : 0.8);
   // lists that at least one of `entries` random choices meets, and full tiles
   const double tiles = lists * (1.0 - std::exp(-entries / lists)) + entries / (128 / rows);
-  const double tc = 27.0 + tiles / kSms * (s.D == 128 ? 2.3 : 1.6);
+  const double tc = 27.0 + tiles / kSms * (s.D == 128 ? 2.1 : 1.45);
   return tc < stream;
 }
 
