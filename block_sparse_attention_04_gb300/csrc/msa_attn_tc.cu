@@ -710,18 +710,21 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
       }
       tc_fence_after();
       if (t + 2 < n && e < (nd.z & 0xFF)) nen = a.entries[nd.y + e];
-      // 16 bytes of four rows per lane become 64 bytes of a row over four lanes
-      // (a 4 x 4 transposition of 16-byte pieces), so that a store touches 8
-      // lines instead of 32: with one row per lane the stores of a tile took 2048
-      // line accesses (128K prefill attention 17.46 -> 16.46 ms; 2048 queries of
-      // 32K, 8-bit cache 300 -> 274 us; 64/4 heads, bf16 508 -> 389 us)
-      const int own = valid ? (int)prow : -1, j4 = lane & 3;
-      int at[4];
+      // 32 bytes of two rows per lane become 64 bytes of a row over two lanes, so
+      // that a store touches 16 lines and eight stores do for a lane: with one row
+      // per lane and 16-byte stores a tile took 2048 line accesses, which paced it
+      // (128K prefill attention 17.46 ms, now 14.89; 2048 queries of 32K on an
+      // 8-bit cache 300 and 252 us with the softmax's changes; 64-byte rows over
+      // four lanes with 16-byte stores 15.29 ms, over two 15.01; 32-byte stores
+      // of a lane's own row 14.84, but 4096 queries at 64/8 heads 815 us for 787)
+      const int own = valid ? (int)prow : -1;
+      const bool up = lane & 1;
+      int at[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) at[j] = __shfl_sync(0xffffffffu, own, (lane & ~3) + j);
+      for (int j = 0; j < 2; ++j) at[j] = __shfl_sync(0xffffffffu, own, (lane & ~1) + j);
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t w[4][4];
+        uint32_t w[2][8];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t h[16];
@@ -730,29 +733,18 @@ __global__ void __launch_bounds__(attn_threads<Q8>(), 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float x = __uint_as_float(h[2 * k]), y = __uint_as_float(h[2 * k + 1]);
-            w[hf * 2 + k / 4][k % 4] = Q8 ? pack_f16(x * kPDown, y * kPDown) : pack_bf16(x, y);
+            w[hf][k] = Q8 ? pack_f16(x * kPDown, y * kPDown) : pack_bf16(x, y);
           }
         }
 #pragma unroll
-        for (int bit = 1; bit < 4; bit <<= 1) {
-          const bool up = j4 & bit;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (x & bit) continue;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t got =
-                  __shfl_xor_sync(0xffffffffu, up ? w[x][k] : w[x | bit][k], bit);
-              w[x][k] = up ? got : w[x][k];
-              w[x | bit][k] = up ? w[x | bit][k] : got;
-            }
-          }
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[0][k] : w[1][k], 1);
+          w[0][k] = up ? got : w[0][k];
+          w[1][k] = up ? w[1][k] : got;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (at[j] >= 0)
-            __stcs(reinterpret_cast<uint4*>(a.part_o + (size_t)at[j] * D + cc * 32 + j4 * 8),
-                   make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]));
+        for (int j = 0; j < 2; ++j)
+          if (at[j] >= 0) stg256(a.part_o + (size_t)at[j] * D + cc * 32 + up * 16, w[j]);
       }
       tc_fence_before();
       mbar_arrive(&o_empty[c]);
