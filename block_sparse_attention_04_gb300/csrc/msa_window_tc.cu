@@ -23,8 +23,9 @@
 //                 use: a weight of 0 does not cancel a NaN.
 //   warps 3-10    one warpgroup per chain, a row per thread: mask, maximum,
 //                 P = 2^(x - m) over S, row sum; at the item's end O / l, written
-//                 64 bytes of a row at a time (16 bytes of 32 rows per store, as
-//                 the rows lie in tensor memory, cost 3 % of the call)
+//                 64 bytes of a row at a time by two lanes (16 bytes of 32 rows per
+//                 store, as the rows lie in tensor memory, cost 4 % of the call;
+//                 through shared memory the rows took 1 % more)
 //   warps 11-14   8-bit cache, in place of warp 1: codes of the next block to
 //                 registers, converted into the same rings: K to f16 and V to
 //                 bf16 (both exact); Q tiles to f16 in place, each row scaled by
@@ -45,7 +46,7 @@
 // others', such as blocks of zeros): then it is summed by exponentials of its own.
 //
 // Measured (us; the MMAs' time at cuBLAS' burst rate beside it): 16K queries, 48/8
-// heads, D 128, window 4096 and 64 sinks 1110 (764 for the visible tokens); 3 x
+// heads, D 128, window 4096 and 64 sinks 1094 (764 for the visible tokens); 3 x
 // 1000 queries, 64/4, D 64, window 1000, 8-bit cache 114 (26), bf16 98.  A block
 // step of the two chains takes 1.5 us at D 64, 1.66 at D 128 (of which the MMAs
 // 1.34), with an 8-bit cache 1.76 and 2.13: the chain S, maximum, P, P.V has few
@@ -99,8 +100,7 @@ struct WinCfg {
   static constexpr int kNHalf = D / 64;
   static constexpr int kHalf = 128 * 128;       // 128 rows x 64 dims of 16 bits (16 KiB)
   static constexpr int kTile = kNHalf * kHalf;  // a Q tile, a K or a V block
-  static constexpr int kStage = 32 * 64;        // a softmax warp's 32 output rows, 32 dims
-  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + 2048 + 8 * kStage + 512 + 1024;
+  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + 2048 + 512 + 1024;
   static constexpr uint32_t kTmemCols = 512;
 };
 
@@ -152,8 +152,7 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
   uint8_t* sK = sQ + 2 * C::kTile;            // [kStages] K blocks
   uint8_t* sV = sK + kStages * C::kTile;      // [kStages] V blocks
   float* q_scale = reinterpret_cast<float*>(sV + kStages * C::kTile);   // [2][chain][128]
-  uint8_t* sO = reinterpret_cast<uint8_t*>(q_scale + 2 * 2 * 128);        // [warp] output rows
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sO + 8 * C::kStage);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(q_scale + 2 * 2 * 128);
   uint64_t* q_full = bars;                    // per chain: the item's Q tile landed
   uint64_t* q_ready = q_full + 2;             // ... and is in f16 (8-bit cache)
   uint64_t* q_empty = q_ready + 2;            // per chain: the item's last S is done
@@ -701,37 +700,43 @@ __global__ void __launch_bounds__(threads<Q8>(), 1)
         continue;
       }
       const float inv = l == 0.f ? 0.f : (Q8 ? ex2(m_ref - n_ref) : 1.f) / l;
-      // rows go to memory 64 bytes at a time, by four lanes each, through shared
-      // memory: a lane's own row, 16 bytes at a time, touches 32 lines per store
+      // two lanes' rows, 32 bytes each, become 64 bytes of a row over both lanes
       uint16_t* dst =
           a.out + (((int64_t)d.b * T + d.i0 + c * nq) * H + (int64_t)d.g * hpg) * D;
       const int rel = valid ? (rq * H + rh) * D : -1;
-      const uint32_t stage = smem_u32(sO) + (warp - kSoftWarp0) * C::kStage;
+      const bool up = lane & 1, wide = ((uintptr_t)a.out & 31) == 0;
+      int at[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) at[j] = __shfl_sync(0xffffffffu, rel, (lane & ~1) + j);
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t h[32];
-        tmem_ld16(o_base + cc * 32, *reinterpret_cast<uint32_t(*)[16]>(h));
-        tmem_ld16(o_base + cc * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(h + 16));
-        tmem_ld_wait();
-        __syncwarp();
+        uint32_t w[2][8];
 #pragma unroll
-        for (int e8 = 0; e8 < 4; ++e8) {
-          uint32_t w[4];
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t h[16];
+          tmem_ld16(o_base + cc * 32 + hf * 16, h);
+          tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[j] = pack_bf16(__uint_as_float(h[e8 * 8 + 2 * j]) * inv,
-                             __uint_as_float(h[e8 * 8 + 2 * j + 1]) * inv);
-          sts128(stage + lane * 64 + ((e8 ^ ((lane >> 1) & 3)) << 4),
-                 make_uint4(w[0], w[1], w[2], w[3]));
+          for (int j = 0; j < 8; ++j)
+            w[hf][j] = pack_bf16(__uint_as_float(h[2 * j]) * inv, __uint_as_float(h[2 * j + 1]) * inv);
         }
-        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int row = j * 8 + (lane >> 2), e8 = lane & 3;
-          const int at = __shfl_sync(0xffffffffu, rel, row);
-          const uint4 v = lds128(stage + row * 64 + ((e8 ^ ((row >> 1) & 3)) << 4));
-          if (at >= 0) *reinterpret_cast<uint4*>(dst + at + cc * 32 + e8 * 8) = v;
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[0][j] : w[1][j], 1);
+          w[0][j] = up ? got : w[0][j];
+          w[1][j] = up ? w[1][j] : got;
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (at[j] >= 0) {
+            uint16_t* p = dst + at[j] + cc * 32 + up * 16;
+            if (wide) {
+              stg256(p, w[j]);
+            } else {                     // an output aligned to 16 bytes only
+              *reinterpret_cast<uint4*>(p) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+              *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[j][4], w[j][5], w[j][6], w[j][7]);
+            }
+          }
       }
     }
     if (!ok) *abort_flag = 1;

@@ -434,3 +434,22 @@ def test_pools_past_32_bits_of_offset(msa, kernels, q8):
     assert torch.equal(kis[0], kis[1][shift:])
     for x, y in zip(kv, big):
         assert torch.equal(x, y[shift:])
+
+
+@pytest.mark.parametrize("kernels", KERNELS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_output_aligned_to_16_bytes_only(msa, kernels, D):
+    lens, T = [700, 400], 130
+    c, q, q_start = make(lens, T, 6, 2, D, seed=57)
+    nb = c.table.shape[1]
+    want = run(msa, c, True, q, q_start, lens, nb, 300, 4, kernels)
+    p = msa.params(2, T, 6, 2, D, 32, nb, kernels=kernels)
+    ws = msa.window_workspace(p)
+    raw = torch.full((q.numel() + 24,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = raw[8:8 + q.numel()].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    msa.msa_window_attn_q8(p, 300, 4, q, *c.codes, *c.exps, q_start, lens, out, ws,
+                           block_table=c.table, num_pool_blocks=c.pages)
+    msa.msa_workspace_status(ws)
+    assert torch.equal(out, want)
+    assert (raw[:8] == 7).all() and (raw[8 + q.numel():] == 7).all()
