@@ -14,8 +14,8 @@
 //
 // The call's work is one sequence of (query, block) steps, query (b, t) after
 // query, cut into equal runs; G CTAs take a run, one KV head each, and a run's
-// share of one query is a segment.  The last warp copies K and V of each block (128 tokens of one KV head)
-// into a ring of stages by TMA and runs ahead by its depth.  A team of eight warps
+// share of one query is a segment.  The last warp copies K and V of each block
+// (128 tokens of one KV head) into a ring of stages by TMA and runs ahead by its depth.  A team of eight warps
 // takes a block, 16 tokens each, and its warps never wait for one another inside
 // a segment:
 // S^T = K Q^T (tokens x heads) with mma.sync m16n8k16, softmax in registers,
@@ -36,8 +36,8 @@
 //
 // Bound by HBM for decode: 64 sequences, a bf16 window of 4096 tokens and 4
 // sinks, G 8, D 128: 161 us against 155 for its bytes at the 6.78 TB/s of a plain
-// copy (the heads of a run at the same time: 167 us with one run per CTA, whose
-// rows of one head are 256 bytes apart by 2 KB).  An 8-bit cache needs as long
+// copy (167 us when the heads of a block, whose rows lie side by side, were read
+// by CTAs at different times).  An 8-bit cache needs as long
 // for its arithmetic as for its bytes: 4 sequences of 64K tokens 79 us (copies
 // alone 71, arithmetic alone 68, bytes 65); 64 selections of 16 blocks, of which
 // every group has its own, in pieces of 128 bytes 1 KB apart, 60 us (55, 56 and
