@@ -432,8 +432,7 @@ def _compact(s):
     ok = (table >= 0) & (table < pages)
     out = torch.where(ok, to[torch.where(ok, table, 0).long()].int(), table)
     refs_out = torch.zeros_like(refs)
-    refs_out[to] = torch.where(live, refs, 0)
-    refs_out[src] = 0
+    refs_out[to[live]] = refs[live]              # live pages only: their places are distinct
     return _page_state(s, out, refs_out, live=n.int().reshape(1))
 
 
