@@ -61,7 +61,9 @@ constexpr int kMaxStages = 8;
 constexpr int kMaxCtas = kMaxStatusWords;        // partials and error words in the workspace
 constexpr int kPassRows = 2048;      // (sequence, query) rows per pass
 constexpr float kLazy = 8.f;         // log2 growth of p tolerated before O is rescaled
-constexpr int kSmemMax = 227 * 1024;
+// Most dynamic shared memory of a CTA: 227 KiB but for the static part (barriers,
+// row statistics: under 2 KiB).
+constexpr int kSmemMax = 227 * 1024 - 2048;
 
 struct StreamArgs {
   Shape s;
@@ -800,16 +802,18 @@ cudaError_t launch_impl(const CacheView& c, StreamArgs& a, cudaStream_t st) {
       return cudaErrorInvalidValue;
   }
   const int fixed = 1024 + kQBufs * hpg * D * 2 + C::kWarps * hpg * C::kRedRow * 4;
-  // static shared memory (barriers, row statistics) takes under 2 KiB
-  a.stages = (kSmemMax - 2048 - fixed) / C::kStage;
+  a.stages = (kSmemMax - fixed) / C::kStage;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   // a stage always serves the same team, whose waits on it then alternate in
   // parity (a team that met a stage every other lap would take the phase
   // before last for its own)
   a.stages -= a.stages % C::kTeams;
   const int smem = fixed + a.stages * C::kStage;
+  // The limit belongs to the kernel, which calls of all threads share: always the
+  // same value.  This call's own size, which depends on H/G, would let another
+  // thread lower the limit between this thread's setting and its launch.
   cudaError_t e = cudaFuncSetAttribute(stream_attn_kernel<D, Q8, NTH>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (e != cudaSuccess) return e;
   if (a.parts) {
     cudaLaunchConfig_t cfg{};
