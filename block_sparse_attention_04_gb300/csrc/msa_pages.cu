@@ -256,24 +256,32 @@ __global__ void __launch_bounds__(kBook) pages_fork_kernel(PageTable pt,
   int need;
   const int f = cta_rank(part, sm, &need);
   const int got = need ? list_free(pt, need, w.x, sm) : 0;
-  if (blockIdx.x == 0 && j < rl.n) {
+  if (blockIdx.x == 0) {
     int from = -1, to = -1;
+    const int kb = part ? rl.c[j] / kBlock : 0;
     if (part) {
-      const int kb = rl.c[j] / kBlock;
-      const int e = pt.table[(int64_t)rl.a[j] * pt.max_blocks + kb];
-      if (e < 0 || e >= pt.pages) {
+      // a page that nobody counts is on the free list: another pair may write it
+      from = pt.table[(int64_t)rl.a[j] * pt.max_blocks + kb];
+      if (from < 0 || from >= pt.pages || __ldcg(pt.refs + from) <= 0) {
         code = worse(code, kDevInvalid);
-      } else if (f >= got) {
+        from = -1;
+      }
+    }
+    __syncthreads();                 // every count is read before a page is handed out
+    if (from >= 0) {
+      if (f >= got) {
         code = worse(code, kDevNoPages);
+        from = -1;
       } else {
-        from = e;
         to = __ldcg(w.x + f);
         pt.table[(int64_t)rl.b[j] * pt.max_blocks + kb] = to;
         pt.refs[to] = 1;
       }
     }
-    w.y[j] = from;
-    w.z[j] = to;
+    if (j < rl.n) {
+      w.y[j] = from;
+      w.z[j] = to;
+    }
   }
   write_status(code, w.status);
 }

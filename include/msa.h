@@ -364,8 +364,9 @@ int msa_window_attn_q8(const msa_params *p, const int32_t *block_table, int num_
  * MSA_MAX_BATCH.  The calls only enqueue work and give the same result in any
  * order of execution.  Table entries outside [0, num_pool_blocks) other than
  * -1 that a call meets, and mappings of pages whose count is 0 that it shares,
- * lets go of or compacts, are reported (MSA_ERR_INVALID_ARG in ws); a call that runs out of free pages maps what it
- * can, leaves the rest at -1 and reports MSA_ERR_PAGES (msa_workspace_status).
+ * copies, lets go of or compacts, are reported (MSA_ERR_INVALID_ARG in ws); a
+ * call that runs out of free pages maps what it can, leaves the rest at -1 and
+ * reports MSA_ERR_PAGES (msa_workspace_status).
  * ws: at least msa_pages_workspace_bytes(num_pool_blocks), 256-byte aligned.
  *
  * The pools that move together are described by up to MSA_MAX_POOLS entries:
@@ -391,7 +392,8 @@ int msa_pages_copy(const msa_pool *pools, int npools, int num_pool_blocks, const
  * maps the first len[j] tokens of row src_rows[j]: the pages that they fill
  * completely are shared (their counts rise), a partly filled last one is
  * copied to the lowest free page (its used rows), and the row's other entries
- * become -1.  dst_rows are distinct and none is in src_rows. */
+ * become -1.  A partly filled page whose count is 0 is not copied (its entry
+ * becomes -1).  dst_rows are distinct and none is in src_rows. */
 int msa_pages_fork(const msa_pool *pools, int npools, int num_pool_blocks, int32_t *block_table,
                    int rows, int max_blocks, int32_t *refs, const int32_t *src_rows,
                    const int32_t *dst_rows, const int32_t *len, int n, void *ws, size_t ws_bytes,

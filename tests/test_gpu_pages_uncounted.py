@@ -1,0 +1,63 @@
+"""Page operations on tables that map pages which no count owns (count 0, so
+free): such mappings are reported and never make two rows share a page unnoticed."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_pages import contiguous_world
+
+pytestmark = pytest.mark.gpu
+
+INVALID = -1
+
+
+@pytest.fixture(scope="module")
+def msa():
+    assert torch.cuda.is_available()
+    import block_sparse_attention_04_gb300 as m
+    m.load()
+    return m
+
+
+def reported(msa, ws):
+    with pytest.raises(msa.MsaError) as e:
+        msa.msa_workspace_status(ws)
+    assert e.value.status == INVALID
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_fork_does_not_copy_an_uncounted_last_page(msa, which):
+    # row 1's last page has count 0 and is the first, second or third free page,
+    # i.e. the destination that this pair or another one would get
+    w = contiguous_world(30, 8, 4, [300, 290, 257, 0, 500], seed=which + 1)
+    free = np.flatnonzero(w.refs == 0)
+    w.refs[w.table[1, 2]] = 0
+    e = w.table[1, 2] = free[which]
+    free = np.flatnonzero(w.refs == 0)
+    w.device(msa)
+    src, dst, lens = [0, 1, 2], [5, 6, 7], [300, 290, 257]
+    msa.msa_pages_fork(w.set, 30, w.d_table, w.d_refs, src, dst, lens, w.ws)
+    reported(msa, w.ws)
+    for j in (0, 2):                          # the pairs beside it are as they should be
+        pg, old, n = free[j], w.table[src[j], 2], lens[j] % 128
+        w.table[dst[j], :3] = [*w.table[src[j], :2], pg]
+        w.refs[w.table[dst[j], :3]] += 1
+        for x in w.pools:
+            if x.ndim > 2:
+                x[pg, :n] = x[old, :n]
+            else:
+                x[pg] = x[old]
+    w.table[6, :2] = w.table[1, :2]           # complete pages shared, nothing in the last one's place
+    w.refs[w.table[6, :2]] += 1
+    w.same()
+    assert w.table[1, 2] == e and w.refs[e] == int(e in (free[0], free[2]))
+
+
+def test_fork_copies_a_last_page_that_the_call_itself_shares(msa):
+    # the page's own count is there: one pair shares it whole, another copies rows of it
+    w = contiguous_world(20, 6, 4, [384, 0, 0], seed=4)
+    w.device(msa)
+    msa.msa_pages_fork(w.set, 20, w.d_table, w.d_refs, [0, 0], [1, 2], [384, 300], w.ws)
+    msa.msa_workspace_status(w.ws)
+    w.fork([0, 0], [1, 2], [384, 300])
+    w.same()
