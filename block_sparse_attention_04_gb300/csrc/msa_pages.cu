@@ -390,10 +390,17 @@ __global__ void __launch_bounds__(kThreads) pages_move_kernel(const __grid_const
     int e = pt.table[i];
     if (e >= 0 && e < pt.pages) {
       const int fate = w.z[e];
-      if (fate >= 0) e = w.x[fate];
-      else if (fate != kStays) atomicMax(w.status, kDevInvalid);   // maps a page nobody counts
+      if (fate >= 0) {
+        e = w.x[fate];
+      } else if (fate != kStays) {
+        // a page nobody counts: another row's page may move there, and the
+        // entry would pass for a counted mapping of it
+        atomicMax(w.status, kDevInvalid);
+        e = -1;
+      }
     } else if (e != -1) {
       atomicMax(w.status, kDevInvalid);
+      e = -1;
     }
     table_out[i] = e;
   }

@@ -415,8 +415,9 @@ int msa_pages_alloc(int num_pool_blocks, int32_t *block_table, int rows, int max
 /* Moves the pages in use to the front of the pools: with live[0] (device,
  * written) pages in use, the i-th one at or behind that index goes to the i-th
  * free page before it.  table_out and refs_out receive the table and counts
- * after the move (they may be block_table and refs themselves).  The bytes of
- * the pages that were moved away stay behind. */
+ * after the move (they may be block_table and refs themselves); an entry that
+ * maps a page whose count is 0 or lies outside the pool becomes -1.  The bytes
+ * of the pages that were moved away stay behind. */
 int msa_pages_compact(const msa_pool *pools, int npools, int num_pool_blocks,
                       const int32_t *block_table, int rows, int max_blocks, const int32_t *refs,
                       int32_t *table_out, int32_t *refs_out, int32_t *live, void *ws,

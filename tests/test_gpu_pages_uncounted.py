@@ -61,3 +61,28 @@ def test_fork_copies_a_last_page_that_the_call_itself_shares(msa):
     msa.msa_workspace_status(w.ws)
     w.fork([0, 0], [1, 2], [384, 300])
     w.same()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compact_unmaps_uncounted_pages(msa, in_place):
+    # entries of a hole that another row's page fills, of a free page behind the
+    # live ones, and of no page at all: unmapped, so that every count is the
+    # number of entries that map its page
+    w = contiguous_world(40, 6, 5, [500, 640, 257], seed=8)
+    live = int((w.refs > 0).sum())
+    free = np.flatnonzero(w.refs == 0)
+    hole, dead = int(free[0]), int(free[-1])
+    assert hole < live <= dead
+    bad = {(3, 1): hole, (4, 4): dead, (5, 0): 40, (5, 1): -9}
+    w.device(msa)
+    for at, e in bad.items():
+        w.d_table[at] = e
+    table = w.d_table if in_place else torch.full_like(w.d_table, 77)
+    refs = w.d_refs if in_place else torch.full_like(w.d_refs, 77)
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    msa.msa_pages_compact(w.set, 40, w.d_table, w.d_refs, table, refs, n, w.ws)
+    reported(msa, w.ws)
+    assert n.item() == w.compact() == live
+    w.same(table, refs)                       # the bad entries at -1, the rest as without them
+    mapped = table[table >= 0].long()
+    assert torch.equal(refs, torch.bincount(mapped, minlength=40).int())
