@@ -241,13 +241,15 @@ __global__ void __launch_bounds__(kBook) pages_fork_kernel(PageTable pt,
     const bool share = kb < rl.c[j] / kBlock;
     int e = share ? pt.table[(int64_t)rl.a[j] * pt.max_blocks + kb] : -1;
     const int old = *dst;
-    if (e < 0 || e >= pt.pages) {
-      if (share) code = worse(code, kDevInvalid);
-      e = -1;
-    }
-    const int had = e >= 0 ? atomicAdd(pt.refs + e, 1) : 1;
+    // A page that nobody counts is not shared: its count would then miss the
+    // source's mapping for good.  So no thread adds to such a count, and the
+    // source's own mapping keeps a counted page's above 0: what is read here does
+    // not depend on the order of the threads.
+    const bool counted = e >= 0 && e < pt.pages && __ldcg(pt.refs + e) > 0;
+    if (share && !counted) code = worse(code, kDevInvalid);
+    if (!counted) e = -1;
+    if (counted) atomicAdd(pt.refs + e, 1);
     code = worse(code, release(pt, old));
-    if (had <= 0) code = worse(code, kDevInvalid);   // the source's own mapping was not counted
     *dst = e;
   }
   // pair j of thread j: does its last page need a copy, and which free page is its

@@ -392,7 +392,7 @@ int msa_pages_copy(const msa_pool *pools, int npools, int num_pool_blocks, const
  * maps the first len[j] tokens of row src_rows[j]: the pages that they fill
  * completely are shared (their counts rise), a partly filled last one is
  * copied to the lowest free page (its used rows), and the row's other entries
- * become -1.  A partly filled page whose count is 0 is not copied (its entry
+ * become -1.  A page whose count is 0 is neither shared nor copied (its entry
  * becomes -1).  dst_rows are distinct and none is in src_rows. */
 int msa_pages_fork(const msa_pool *pools, int npools, int num_pool_blocks, int32_t *block_table,
                    int rows, int max_blocks, int32_t *refs, const int32_t *src_rows,

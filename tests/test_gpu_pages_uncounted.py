@@ -86,3 +86,26 @@ def test_compact_unmaps_uncounted_pages(msa, in_place):
     w.same(table, refs)                       # the bad entries at -1, the rest as without them
     mapped = table[table >= 0].long()
     assert torch.equal(refs, torch.bincount(mapped, minlength=40).int())
+
+
+def test_fork_does_not_share_uncounted_pages(msa):
+    # two pairs meet the same uncounted page, a third a page of its own kind; the
+    # destination rows were mapped before
+    w = contiguous_world(40, 9, 4, [500, 384, 130, 300, 200], seed=12)
+    a, b = (int(i) for i in np.flatnonzero(w.refs == 0)[:2])
+    w.table[0, 1], w.table[2, 0] = a, b       # row 0's block 1 and row 2's block 0: count 0
+    w.refs[:] = 0
+    np.add.at(w.refs, w.table[w.table >= 0], 1)
+    w.refs[[a, b]] = 0
+    w.device(msa)
+    src, dst, lens = [0, 0, 2, 1], [5, 6, 3, 4], [384, 256, 128, 384]
+    msa.msa_pages_fork(w.set, 40, w.d_table, w.d_refs, src, dst, lens, w.ws)
+    reported(msa, w.ws)
+    w.fork(src, dst, lens)
+    w.table[[5, 6, 3], [1, 1, 0]] = -1
+    w.refs[[a, b]] = 0
+    w.same()
+    # every other page is counted once per mapping
+    t = w.d_table.clone()
+    t[0, 1] = t[2, 0] = -1
+    assert torch.equal(w.d_refs, torch.bincount(t[t >= 0].long(), minlength=40).int())
