@@ -388,12 +388,15 @@ size_t msa_pages_workspace_bytes(int num_pool_blocks);
 int msa_pages_copy(const msa_pool *pools, int npools, int num_pool_blocks, const int32_t *src,
                    const int32_t *dst, int n, void *ws, size_t ws_bytes, cudaStream_t stream);
 
-/* For each pair j in order: row dst_rows[j] lets go of the pages it maps, then
- * maps the first len[j] tokens of row src_rows[j]: the pages that they fill
- * completely are shared (their counts rise), a partly filled last one is
- * copied to the lowest free page (its used rows), and the row's other entries
- * become -1.  A page whose count is 0 is neither shared nor copied (its entry
- * becomes -1).  dst_rows are distinct and none is in src_rows. */
+/* Every row dst_rows[j] lets go of the pages it maps; then maps the first len[j]
+ * tokens of row src_rows[j]: the pages that they fill completely are shared
+ * (their counts rise), and a partly filled last one is copied (its used rows) to
+ * a free page; the row's other entries become -1.  All rows have let go and all
+ * complete pages are shared before the free pages are handed out, the lowest
+ * first, to the pairs with a partly filled page in order of j.  A page whose
+ * count is 0 is neither shared nor copied (its entry becomes -1; the free page
+ * of a pair that does not copy stays free).  dst_rows are distinct and none is
+ * in src_rows. */
 int msa_pages_fork(const msa_pool *pools, int npools, int num_pool_blocks, int32_t *block_table,
                    int rows, int max_blocks, int32_t *refs, const int32_t *src_rows,
                    const int32_t *dst_rows, const int32_t *len, int n, void *ws, size_t ws_bytes,
