@@ -247,14 +247,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8, NTH>::kThreads, 1) stream_attn_kern
           }
           if (kb >= 0) {
             const int64_t pb = cache_block(s, u.b, kb, &err);
-            if (pb < 0) {
-              kb = -1;
-            } else {
-              row = (int)(pb * kBlock);
-              if (Q8) {
-                ex = (clamp_exp(a.k_exp[pb * G + u.g]) & 0xFFFF) |
-                     clamp_exp(a.v_exp[pb * G + u.g]) * 65536;
-              }
+            // an entry outside the pool (flagged) reads zeros from past its end
+            row = (int)((pb < 0 ? s.cache_blocks() : pb) * kBlock);
+            if (Q8 && pb >= 0) {
+              ex = (clamp_exp(a.k_exp[pb * G + u.g]) & 0xFFFF) |
+                   clamp_exp(a.v_exp[pb * G + u.g]) * 65536;
             }
           }
         }

@@ -315,8 +315,11 @@ int msa_cache_append_q8(const msa_params *p, const int32_t *block_table, int num
  * sequence (block_table NULL) or paged.  The attention of the cached values is
  * computed as for a bf16 cache (fp32 accumulation, bf16 output); a row whose
  * selection holds no visible token is written as zeros, and an id that is
- * listed twice counts twice.  Cache rows that no query may see (behind the last query) may hold anything.  ws: at least
- * msa_q8_workspace_bytes(p) bytes, 256-byte aligned. */
+ * listed twice counts twice.  An id outside [0, lb] is reported and skipped; a
+ * block behind a table entry outside the pool is reported and attended to as 128
+ * tokens whose K and V are zero.  Cache rows that no query may see (behind the
+ * last query) may hold anything.  ws: at least msa_q8_workspace_bytes(p) bytes,
+ * 256-byte aligned. */
 size_t msa_q8_workspace_bytes(const msa_params *p);
 int msa_sparse_attn_q8(const msa_params *p, const int32_t *block_table, int num_pool_blocks,
                        const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache,
@@ -342,9 +345,10 @@ int msa_forward_q8(const msa_params *p, const int32_t *block_table, int num_pool
  * query of the call sees may hold anything; a NaN or an infinity in V of a
  * token that one query of a prefill-sized call sees also reaches outputs of
  * the queries up to 255 positions from that one.  p->topk and p->Di are
- * checked but not used.  out is bf16 (round to nearest even) from fp32
- * accumulation.  ws: at least msa_window_workspace_bytes(p) bytes, 256-byte
- * aligned. */
+ * checked but not used.  A block behind a table entry outside the pool is
+ * reported and attended to as tokens whose K and V are zero.  out is bf16 (round
+ * to nearest even) from fp32 accumulation.  ws: at least
+ * msa_window_workspace_bytes(p) bytes, 256-byte aligned. */
 size_t msa_window_workspace_bytes(const msa_params *p);
 int msa_window_attn(const msa_params *p, const int32_t *block_table, int num_pool_blocks,
                     int window, int sinks, const uint16_t *q, const uint16_t *k_cache,
