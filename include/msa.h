@@ -318,7 +318,10 @@ int msa_cache_append_q8(const msa_params *p, const int32_t *block_table, int num
  * listed twice counts twice.  An id outside [0, lb] is reported and skipped; a
  * block behind a table entry outside the pool is reported and attended to as 128
  * tokens whose K and V are zero.  Cache rows that no query may see (behind the
- * last query) may hold anything.  ws: at least msa_q8_workspace_bytes(p) bytes,
+ * last query) may hold anything; a NaN in V of a token that one query of the
+ * call sees may also reach, in the same dim and heads, outputs of earlier queries
+ * of the call in the same block that select it (up to 127 positions before the
+ * token; on the prefill kernels).  ws: at least msa_q8_workspace_bytes(p) bytes,
  * 256-byte aligned. */
 size_t msa_q8_workspace_bytes(const msa_params *p);
 int msa_sparse_attn_q8(const msa_params *p, const int32_t *block_table, int num_pool_blocks,
