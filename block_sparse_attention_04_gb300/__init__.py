@@ -168,13 +168,23 @@ def _stream(stream):
 
 
 def _int32s(x):
-    if type(x) in (list, tuple) and x:
-        try:
-            a = array.array("i", x)         # a third of the time of the general form
-            return (ctypes.c_int32 * len(a)).from_buffer(a)
-        except (TypeError, OverflowError):
-            pass                            # floats, tensors; values past 32 bits wrap
-    return (ctypes.c_int32 * len(x))(*[int(v) for v in x])
+    try:
+        if type(x) in (list, tuple) and x:
+            try:
+                a = array.array("i", x)         # a third of the time of the general form
+                return (ctypes.c_int32 * len(a)).from_buffer(a)
+            except TypeError:
+                pass                            # floats
+        x = [int(v) for v in x]
+        return (ctypes.c_int32 * len(x))(*array.array("i", x))
+    except OverflowError:                       # ctypes alone would wrap it
+        raise ValueError("a position, length or row number does not fit 32 bits") from None
+
+
+def _tokens(n):
+    """A count of tokens as the C ABI takes it: past its ends, the end (a window
+    longer than any context, or one that the library refuses)."""
+    return max(-1, min(int(n), 0x7FFFFFFF))
 
 
 def positions(x):
@@ -405,16 +415,17 @@ def msa_window_attn(p, window, sinks, q, k_cache, v_cache, q_start, kv_len, out,
                     block_table=None, num_pool_blocks=0, stream=None):
     """GQA attention over the last `window` and the first `sinks` tokens (see msa.h)."""
     _call(load().msa_window_attn(ctypes.byref(p), _ptr(block_table), int(num_pool_blocks),
-                                 int(window), int(sinks), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                 _host_i32(q_start, p.B), _host_i32(kv_len, p.B), _ptr(out),
-                                 _ptr(ws), _nbytes(ws), _stream(stream)), "msa_window_attn")
+                                 _tokens(window), _tokens(sinks), _ptr(q), _ptr(k_cache),
+                                 _ptr(v_cache), _host_i32(q_start, p.B), _host_i32(kv_len, p.B),
+                                 _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream)),
+          "msa_window_attn")
 
 
 def msa_window_attn_q8(p, window, sinks, q, k_cache, v_cache, k_exp, v_exp, q_start, kv_len, out,
                        ws, block_table=None, num_pool_blocks=0, stream=None):
     """msa_window_attn on an 8-bit cache (see msa.h)."""
     _call(load().msa_window_attn_q8(ctypes.byref(p), _ptr(block_table), int(num_pool_blocks),
-                                    int(window), int(sinks), _ptr(q), _ptr(k_cache),
+                                    _tokens(window), _tokens(sinks), _ptr(q), _ptr(k_cache),
                                     _ptr(v_cache), _ptr(k_exp), _ptr(v_exp),
                                     _host_i32(q_start, p.B), _host_i32(kv_len, p.B), _ptr(out),
                                     _ptr(ws), _nbytes(ws), _stream(stream)), "msa_window_attn_q8")
