@@ -256,18 +256,16 @@ __global__ void __launch_bounds__(kBook) pages_fork_kernel(PageTable pt,
   const int j = threadIdx.x;
   const bool part = j < rl.n && rl.c[j] % kBlock != 0;
   int need;
+  const int kb = part ? rl.c[j] / kBlock : 0;
+  int from = part ? pt.table[(int64_t)rl.a[j] * pt.max_blocks + kb] : -1;   // no row of dst_rows
   const int f = cta_rank(part, sm, &need);
   const int got = need ? list_free(pt, need, w.x, sm) : 0;
   if (blockIdx.x == 0) {
-    int from = -1, to = -1;
-    const int kb = part ? rl.c[j] / kBlock : 0;
-    if (part) {
-      // a page that nobody counts is on the free list: another pair may write it
-      from = pt.table[(int64_t)rl.a[j] * pt.max_blocks + kb];
-      if (from < 0 || from >= pt.pages || __ldcg(pt.refs + from) <= 0) {
-        code = worse(code, kDevInvalid);
-        from = -1;
-      }
+    int to = -1;
+    // a page that nobody counts is on the free list: another pair may write it
+    if (part && (from < 0 || from >= pt.pages || __ldcg(pt.refs + from) <= 0)) {
+      code = worse(code, kDevInvalid);
+      from = -1;
     }
     __syncthreads();                 // every count is read before a page is handed out
     if (from >= 0) {
