@@ -9,7 +9,7 @@
 // bound by launch latency, so each operation does all of it in one launch: one
 // cluster of CTAs whose steps are separated by cluster barriers, and whose
 // error words are joined at the end into the status (no clearing launch).
-// Fork of 32 sequences of up to 4000 tokens, 16 MB of last pages moved: 14.3 us.
+// Fork of 32 sequences of up to 4000 tokens, 16 MB of last pages moved: 14.4 us.
 // Page contents move in 16-byte chunks, four per thread in flight, by a grid of
 // their own; copying is bound by HBM, 2 bytes per byte moved (a
 // compaction that moves 440 MB both ways counted: 77 us, 5.7 TB/s).
@@ -212,7 +212,8 @@ __device__ __forceinline__ int list_free(const PageTable& pt, int most, int32_t*
   return min(all, most);
 }
 
-// Unmaps ranges of blocks.
+// Unmaps ranges of blocks, range after range: one block of 64 rows 38 us, of 256
+// rows 155 us, 4096 blocks of one row 3.3 us.
 __global__ void __launch_bounds__(kBook) pages_free_kernel(PageTable pt,
                                                            const __grid_constant__ RowList rl,
                                                            PageWs w) {
@@ -295,7 +296,9 @@ __global__ void __launch_bounds__(kThreads) pages_fork_copy_kernel(
     copy_segment(c, seg, w.y[j], to, rows);
 }
 
-// Maps the unmapped blocks of the ranges, in order, to the lowest free pages.
+// Maps the unmapped blocks of the ranges, in order, to the lowest free pages.  One
+// CTA takes range after range: one block of 64 rows 108 us, of 256 rows 414 us (1.6
+// us a row: a table read and the rank of its result), 4096 blocks of one row 13.6 us.
 __global__ void __launch_bounds__(kBook) pages_alloc_kernel(PageTable pt,
                                                             const __grid_constant__ RowList rl,
                                                             PageWs w) {

@@ -46,8 +46,9 @@
 // others', such as blocks of zeros): then it is summed by exponentials of its own.
 //
 // Measured (us; the MMAs' time at cuBLAS' burst rate beside it): 16K queries, 48/8
-// heads, D 128, window 4096 and 64 sinks 1094 (764 for the visible tokens); 3 x
-// 1000 queries, 64/4, D 64, window 1000, 8-bit cache 114 (26), bf16 98.  A block
+// heads, D 128, window 4096 and 64 sinks 1094 to 1141 on different machines (764 for
+// the visible tokens), 8-bit cache 1449; 3 x 1000 queries, 64/4, D 64, window 1000,
+// 8-bit cache 114 to 117 (26), bf16 98 to 100.  A block
 // step of the two chains takes 1.5 us at D 64, 1.66 at D 128 (of which the MMAs
 // 1.34), with an 8-bit cache 1.76 and 2.13: the chain S, maximum, P, P.V has few
 // steps to overlap with, and power is at its limit.  An item costs 3-4 us beyond

@@ -373,7 +373,8 @@ int msa_window_attn_q8(const msa_params *p, const int32_t *block_table, int num_
  * -1 that a call meets, and mappings of pages whose count is 0 that it shares,
  * copies, lets go of or compacts, are reported (MSA_ERR_INVALID_ARG in ws); a
  * call that runs out of free pages maps what it can, leaves the rest at -1 and
- * reports MSA_ERR_PAGES (msa_workspace_status).
+ * reports MSA_ERR_PAGES (msa_workspace_status).  A call with n == 0 does nothing
+ * and leaves ws as it was.
  * ws: at least msa_pages_workspace_bytes(num_pool_blocks), 256-byte aligned.
  *
  * The pools that move together are described by up to MSA_MAX_POOLS entries:
