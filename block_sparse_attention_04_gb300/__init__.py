@@ -25,11 +25,16 @@ __all__ = ["MsaParams", "MsaError", "params", "load", "msa_workspace_bytes", "ms
            "msa_sparse_attn_q8", "msa_forward_q8", "msa_window_workspace_bytes",
            "window_workspace", "msa_window_attn", "msa_window_attn_q8", "MsaPool", "pools",
            "msa_pages_workspace_bytes", "pages_workspace", "msa_pages_copy", "msa_pages_fork",
-           "msa_pages_free", "msa_pages_alloc", "msa_pages_compact", "positions",
-           "workspace", "BLOCK", "TOPK"]
+           "msa_pages_free", "msa_pages_alloc", "msa_pages_compact", "positions", "MsaRope",
+           "rope", "yarn_mscale", "msa_rope_append", "msa_rope_append_bwd_workspace_bytes",
+           "rope_append_bwd_workspace", "msa_rope_append_bwd", "msa_sparse_attn_lse",
+           "msa_dense_attn_lse", "msa_sparse_bwd_workspace_bytes", "sparse_bwd_workspace",
+           "msa_sparse_attn_bwd", "msa_dense_bwd_workspace_bytes", "dense_bwd_workspace",
+           "msa_dense_attn_bwd", "workspace", "BLOCK", "TOPK", "MAX_ROT"]
 
 BLOCK = 128
 TOPK = 16
+MAX_ROT = 128
 KERNELS = {"auto": 0, "streaming": 1, "tensorcore": 2}
 EXPORTS = ("msa_workspace_bytes", "msa_index_topk", "msa_sparse_attn", "msa_forward",
            "msa_workspace_status", "msa_status_string", "msa_kernel_launch_count",
@@ -40,7 +45,10 @@ EXPORTS = ("msa_workspace_bytes", "msa_index_topk", "msa_sparse_attn", "msa_forw
            "msa_sparse_attn_q8", "msa_forward_q8", "msa_window_workspace_bytes",
            "msa_window_attn", "msa_window_attn_q8", "msa_pages_workspace_bytes",
            "msa_pages_copy", "msa_pages_fork", "msa_pages_free", "msa_pages_alloc",
-           "msa_pages_compact")
+           "msa_pages_compact", "msa_rope_append", "msa_rope_append_bwd_workspace_bytes",
+           "msa_rope_append_bwd", "msa_sparse_attn_lse", "msa_dense_attn_lse",
+           "msa_sparse_bwd_workspace_bytes", "msa_sparse_attn_bwd",
+           "msa_dense_bwd_workspace_bytes", "msa_dense_attn_bwd")
 
 
 class MsaError(RuntimeError):
@@ -59,6 +67,11 @@ class MsaParams(ctypes.Structure):
 class MsaPool(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t),
                 ("per_token", ctypes.c_int)]
+
+
+class MsaRope(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("eps", ctypes.c_float),
+                ("mscale", ctypes.c_float), ("inv_freq", ctypes.c_double * (MAX_ROT // 2))]
 
 
 def params(B, T, H, G, D, Di, max_blocks, scale=None, kernels="auto"):
@@ -116,6 +129,18 @@ def load(path=None):
     for name in ("msa_q8_workspace_bytes", "msa_window_workspace_bytes",
                  "msa_pages_workspace_bytes"):
         getattr(L, name).restype = sz
+    RP, i64 = ctypes.POINTER(MsaRope), ctypes.c_int64
+    L.msa_rope_append.argtypes = [PP, RP, P, ci, P, P, P, i64, i64, i64] + [P] * 9 + [sz, P]
+    L.msa_rope_append_bwd.argtypes = ([PP, RP, P, P, i64, i64] + [P] * 9 + [i64, i64, i64] +
+                                      [P] * 3 + [sz, P])
+    L.msa_sparse_attn_lse.argtypes = [PP] + [P] * 9 + [sz, P]
+    L.msa_dense_attn_lse.argtypes = [PP] + [P] * 8 + [sz, P]
+    L.msa_sparse_attn_bwd.argtypes = [PP] + [P] * 13 + [sz, P]
+    L.msa_dense_attn_bwd.argtypes = [PP] + [P] * 12 + [sz, P]
+    for name in ("msa_rope_append_bwd_workspace_bytes", "msa_sparse_bwd_workspace_bytes",
+                 "msa_dense_bwd_workspace_bytes"):
+        getattr(L, name).argtypes = [PP]
+        getattr(L, name).restype = sz
     L.msa_debug_set_wait_polls.argtypes = [ctypes.c_uint32]
     L.msa_debug_set_wait_polls.restype = None
     L.msa_kernel_launch_count.argtypes = []
@@ -127,7 +152,8 @@ def load(path=None):
               "msa_forward_paged", "msa_dense_attn", "msa_index_kl", "msa_cache_append_q8",
               "msa_sparse_attn_q8", "msa_forward_q8", "msa_window_attn", "msa_window_attn_q8",
               "msa_pages_copy", "msa_pages_fork", "msa_pages_free", "msa_pages_alloc",
-              "msa_pages_compact"):
+              "msa_pages_compact", "msa_rope_append", "msa_rope_append_bwd", "msa_sparse_attn_lse",
+              "msa_dense_attn_lse", "msa_sparse_attn_bwd", "msa_dense_attn_bwd"):
         getattr(L, f).restype = ci
     if path == _build.LIBMSA:
         _lib = L
@@ -504,6 +530,146 @@ def msa_pages_compact(pools, num_pool_blocks, block_table, refs, table_out, refs
                                    block_table.shape[0], block_table.shape[1], _ptr(refs),
                                    _ptr(table_out), _ptr(refs_out), _ptr(live), _ptr(ws),
                                    _nbytes(ws), _stream(stream)), "msa_pages_compact")
+
+
+def rope(rot, base=10000.0, interleaved=False, eps=1e-6, linear=1.0, yarn=None, mscale=1.0):
+    """How positions rotate the first `rot` dims of every head, and the norm's eps
+    (see msa.h).  Frequencies base^(-2i/rot) / linear, the position divided by
+    `linear`.  yarn=(factor, trained_length[, beta_fast, beta_slow]): each frequency
+    between itself and its `factor`-th part by how often it turns within the trained
+    length (all of itself from beta_fast turns on, 32; the part below beta_slow, 1);
+    the usual factor of cos and sin goes with it as mscale=yarn_mscale(factor)."""
+    if not 0 <= rot <= MAX_ROT or rot % 2:
+        raise ValueError("rot must be even and in 0 .. %d" % MAX_ROT)
+    f = [base ** (-2.0 * i / rot) / linear for i in range(rot // 2)]
+    if yarn is not None:
+        factor, trained, fast, slow = (tuple(yarn) + (32.0, 1.0)[len(yarn) - 2:])
+
+        def dim(turns):        # the pair (a fraction) that turns so often in `trained`
+            return rot * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        lo, hi = max(math.floor(dim(fast)), 0), min(math.ceil(dim(slow)), rot - 1)
+        for i, x in enumerate(f):
+            part = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)
+            f[i] = x * (1 - part) + x / factor * part
+    r = MsaRope(rot, int(bool(interleaved)), eps, mscale)
+    r.inv_freq[:len(f)] = f
+    return r
+
+
+def yarn_mscale(factor):
+    return 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+
+
+def _row_stride(t, p, heads, what):
+    """Elements between consecutive tokens of [B][T][heads][D] (a plain address: the
+    row itself)."""
+    row = heads * p.D
+    if t is None or isinstance(t, int) or not hasattr(t, "stride"):
+        return row
+    if tuple(t.shape) not in ((p.B, p.T, heads, p.D), (p.B, p.T, row)):
+        raise ValueError("%s must be [B][T][%d][%d], got %s" % (what, heads, p.D, tuple(t.shape)))
+    st = t.stride()
+    step = st[1] if p.T > 1 else st[0]
+    ok = st[-1] == 1 and (t.dim() == 3 or heads == 1 or st[2] == p.D)
+    ok = ok and (p.B == 1 or st[0] == p.T * step)
+    if p.B == 1 and p.T == 1:
+        step = row
+    if not ok:
+        raise ValueError("%s: the rows of a token must be contiguous and the tokens evenly "
+                         "spaced" % what)
+    return step
+
+
+def msa_rope_append(p, r, q, k, v, k_idx_new, q_weight, k_weight, q_start, q_out, k_cache, v_cache,
+                    k_idx_cache, ws, block_table=None, num_pool_blocks=0, stream=None):
+    """Norm and rotation of q and k, and the rows of K, V and K_idx into the caches
+    (see msa.h).  q, k and v may be parts of one tensor; the weights and k_idx_new
+    (with k_idx_cache) may be None."""
+    _call(load().msa_rope_append(ctypes.byref(p), ctypes.byref(r), _ptr(block_table),
+                                 int(num_pool_blocks), _ptr(q), _ptr(k), _ptr(v),
+                                 _row_stride(q, p, p.H, "q"), _row_stride(k, p, p.G, "k"),
+                                 _row_stride(v, p, p.G, "v"), _ptr(q_weight), _ptr(k_weight),
+                                 _ptr(k_idx_new), _host_i32(q_start, p.B), _ptr(q_out),
+                                 _ptr(k_cache), _ptr(v_cache), _ptr(k_idx_cache), _ptr(ws),
+                                 _nbytes(ws), _stream(stream)), "msa_rope_append")
+
+
+def msa_rope_append_bwd_workspace_bytes(p):
+    return int(load().msa_rope_append_bwd_workspace_bytes(ctypes.byref(p)))
+
+
+def rope_append_bwd_workspace(p, device="cuda"):
+    """A device scratch buffer of msa_rope_append_bwd_workspace_bytes(p) bytes."""
+    return _scratch(msa_rope_append_bwd_workspace_bytes(p), "msa_rope_append_bwd_workspace_bytes",
+                    device)
+
+
+def msa_rope_append_bwd(p, r, q, k, q_weight, k_weight, q_start, dq_out, dk_cache, dv_cache, dq, dk,
+                        dv, dq_weight, dk_weight, ws, stream=None):
+    """From the gradients of q_out and of the caches to those of the projections and of
+    the norms' weights (see msa.h)."""
+    _call(load().msa_rope_append_bwd(ctypes.byref(p), ctypes.byref(r), _ptr(q), _ptr(k),
+                                     _row_stride(q, p, p.H, "q"), _row_stride(k, p, p.G, "k"),
+                                     _ptr(q_weight), _ptr(k_weight), _host_i32(q_start, p.B),
+                                     _ptr(dq_out), _ptr(dk_cache), _ptr(dv_cache), _ptr(dq), _ptr(dk),
+                                     _ptr(dv), _row_stride(dq, p, p.H, "dq"),
+                                     _row_stride(dk, p, p.G, "dk"), _row_stride(dv, p, p.G, "dv"),
+                                     _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), _nbytes(ws),
+                                     _stream(stream)), "msa_rope_append_bwd")
+
+
+def msa_sparse_attn_lse(p, q, k_cache, v_cache, sel, q_start, kv_len, out, lse, ws, stream=None):
+    """msa_sparse_attn that also writes lse [B][T][H] (see msa.h)."""
+    _call(load().msa_sparse_attn_lse(ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                     _ptr(sel), _host_i32(q_start, p.B), _host_i32(kv_len, p.B),
+                                     _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)),
+          "msa_sparse_attn_lse")
+
+
+def msa_dense_attn_lse(p, q, k_cache, v_cache, q_start, kv_len, out, lse, ws, stream=None):
+    """msa_dense_attn that also writes lse [B][T][H] (see msa.h)."""
+    _call(load().msa_dense_attn_lse(ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                    _host_i32(q_start, p.B), _host_i32(kv_len, p.B), _ptr(out),
+                                    _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)),
+          "msa_dense_attn_lse")
+
+
+def msa_sparse_bwd_workspace_bytes(p):
+    return int(load().msa_sparse_bwd_workspace_bytes(ctypes.byref(p)))
+
+
+def sparse_bwd_workspace(p, device="cuda"):
+    """A device scratch buffer of msa_sparse_bwd_workspace_bytes(p) bytes."""
+    return _scratch(msa_sparse_bwd_workspace_bytes(p), "msa_sparse_bwd_workspace_bytes", device)
+
+
+def msa_sparse_attn_bwd(p, q, k_cache, v_cache, sel, out, lse, dout, q_start, kv_len, dq, dk, dv, ws,
+                        stream=None):
+    """dq, and the rows of dk and dv in the caches' layout, of msa_sparse_attn (see msa.h)."""
+    _call(load().msa_sparse_attn_bwd(ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                     _ptr(sel), _ptr(out), _ptr(lse), _ptr(dout),
+                                     _host_i32(q_start, p.B), _host_i32(kv_len, p.B), _ptr(dq),
+                                     _ptr(dk), _ptr(dv), _ptr(ws), _nbytes(ws), _stream(stream)),
+          "msa_sparse_attn_bwd")
+
+
+def msa_dense_bwd_workspace_bytes(p):
+    return int(load().msa_dense_bwd_workspace_bytes(ctypes.byref(p)))
+
+
+def dense_bwd_workspace(p, device="cuda"):
+    """A device scratch buffer of msa_dense_bwd_workspace_bytes(p) bytes."""
+    return _scratch(msa_dense_bwd_workspace_bytes(p), "msa_dense_bwd_workspace_bytes", device)
+
+
+def msa_dense_attn_bwd(p, q, k_cache, v_cache, out, lse, dout, q_start, kv_len, dq, dk, dv, ws,
+                       stream=None):
+    """dq, and the rows of dk and dv in the caches' layout, of msa_dense_attn (see msa.h)."""
+    _call(load().msa_dense_attn_bwd(ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out),
+                                    _ptr(lse), _ptr(dout), _host_i32(q_start, p.B),
+                                    _host_i32(kv_len, p.B), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
+                                    _nbytes(ws), _stream(stream)), "msa_dense_attn_bwd")
 
 
 def msa_workspace_status(ws, stream=None):

@@ -171,12 +171,12 @@ int run_index(const msa_params* p, const Shape& s, const Positions& pos, const u
 
 int run_attn(const msa_params* p, const Shape& s, const Positions& pos, const uint16_t* q,
              const uint16_t* k, const uint16_t* v, const int32_t* sel, uint16_t* out,
-             const Workspace& w, cudaStream_t st) {
-  if (use_tc_attn(p)) return cuda_status(launch_attn_tc(s, pos, q, k, v, sel, out, w, st));
+             const Workspace& w, cudaStream_t st, float* lse = nullptr) {
+  if (use_tc_attn(p)) return cuda_status(launch_attn_tc(s, pos, q, k, v, sel, out, w, st, lse));
   const int tc = stream_pass_len(p);
   for (int t0 = 0; t0 < p->T; t0 += tc) {
     const int t1 = t0 + tc < p->T ? t0 + tc : p->T;
-    cudaError_t e = launch_attn_stream(s, pos, t0, t1, q, k, v, sel, out, w, st);
+    cudaError_t e = launch_attn_stream(s, pos, t0, t1, q, k, v, sel, out, w, st, nullptr, lse);
     if (e != cudaSuccess) return MSA_ERR_CUDA;
   }
   return MSA_OK;
@@ -232,6 +232,73 @@ int forward(const msa_params* p, const Shape& s, const uint16_t* q_idx, const ui
   return run_attn(p, s, pos, q, k_cache, v_cache, sel, out, w, stream);
 }
 
+// msa_sparse_attn and msa_dense_attn, with the softmax's lse or without (null).
+int sparse_attn(const msa_params* p, const uint16_t* q, const uint16_t* k_cache,
+                const uint16_t* v_cache, const int32_t* sel, const int32_t* q_start,
+                const int32_t* kv_len, uint16_t* out, float* lse, void* ws,
+                size_t ws_bytes, cudaStream_t stream) {
+  int rc = validate_params(p);
+  if (rc) return rc;
+  Positions pos;
+  if ((rc = validate_positions(p, q_start, kv_len, &pos))) return rc;
+  if (!q || !k_cache || !v_cache || !sel || !out) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(sel) ||
+      !aligned16(out))
+    return MSA_ERR_INVALID_ARG;
+  Plan pl;
+  if ((rc = check_ws(p, ws, ws_bytes, &pl))) return rc;
+  if (p->T == 0) return MSA_OK;
+  Workspace w = carve(p, pl, ws);
+  if (cudaMemsetAsync(w.status, 0, sizeof(int), stream) != cudaSuccess) return MSA_ERR_CUDA;
+  return run_attn(p, shape_of(p), pos, q, k_cache, v_cache, sel, out, w, stream, lse);
+}
+
+int dense_attn(const msa_params* p, const uint16_t* q, const uint16_t* k_cache,
+               const uint16_t* v_cache, const int32_t* q_start, const int32_t* kv_len,
+               uint16_t* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  int rc = validate_params(p);
+  if (rc) return rc;
+  Positions pos;
+  if ((rc = validate_positions(p, q_start, kv_len, &pos))) return rc;
+  if (!q || !k_cache || !v_cache || !out) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return MSA_ERR_INVALID_ARG;
+  if (!ws || ((uintptr_t)ws & (kAlign - 1)) != 0) return MSA_ERR_INVALID_ARG;
+  const DensePlan d = dense_plan_for(p);
+  if (ws_bytes < d.total) return MSA_ERR_WORKSPACE;
+  if (p->T == 0) return MSA_OK;
+  char* base = static_cast<char*>(ws);
+  Workspace w{};
+  w.status = reinterpret_cast<int*>(base);
+  int32_t* sel = reinterpret_cast<int32_t*>(base + d.sel_off);
+  char* scr = base + d.scratch_off;
+  w.part_o = reinterpret_cast<float*>(scr);
+  w.part_rows = d.part_rows;
+  w.part_ml = reinterpret_cast<float*>(scr + align_up(d.part_rows * p->D * sizeof(float)));
+  w.tc_base = scr;
+  w.tc_bytes = d.total - d.scratch_off;
+  if (cudaMemsetAsync(w.status, 0, sizeof(int), stream) != cudaSuccess) return MSA_ERR_CUDA;
+  const Shape s = shape_of(p);
+  if (use_tc_attn(p))
+    return cuda_status(launch_dense_tc(s, pos, q, k_cache, v_cache, out, w.status, stream, lse));
+  // streaming shapes: chunks of 16 consecutive blocks, up to the last query's
+  // local block, each folded into fp32 running accumulators
+  const int nchunks = (max_local_block(s, pos, 0, p->T) + MSA_TOPK) / MSA_TOPK;
+  for (int c = 0; c < nchunks; ++c) {
+    if (launch_dense_sel(s, pos, c, sel, stream) != cudaSuccess) return MSA_ERR_CUDA;
+    DenseStep ds{reinterpret_cast<float*>(base + d.acc_o_off),
+                 reinterpret_cast<float2*>(base + d.acc_ml_off), c == 0, c == nchunks - 1};
+    const int tc = stream_pass_len(p);
+    for (int t0 = 0; t0 < p->T; t0 += tc) {
+      const int t1 = t0 + tc < p->T ? t0 + tc : p->T;
+      if (launch_attn_stream(s, pos, t0, t1, q, k_cache, v_cache, sel, out, w, stream, &ds,
+                             lse) != cudaSuccess)
+        return MSA_ERR_CUDA;
+    }
+  }
+  return MSA_OK;
+}
+
 }  // namespace
 
 int run_index_in(const msa_params* p, const Shape& s, const Positions& pos, const uint16_t* q_idx,
@@ -273,20 +340,16 @@ int msa_sparse_attn(const msa_params* p, const uint16_t* q, const uint16_t* k_ca
                     const uint16_t* v_cache, const int32_t* sel, const int32_t* q_start,
                     const int32_t* kv_len, uint16_t* out, void* ws, size_t ws_bytes,
                     cudaStream_t stream) {
-  int rc = validate_params(p);
-  if (rc) return rc;
-  Positions pos;
-  if ((rc = validate_positions(p, q_start, kv_len, &pos))) return rc;
-  if (!q || !k_cache || !v_cache || !sel || !out) return MSA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(sel) ||
-      !aligned16(out))
-    return MSA_ERR_INVALID_ARG;
-  Plan pl;
-  if ((rc = check_ws(p, ws, ws_bytes, &pl))) return rc;
-  if (p->T == 0) return MSA_OK;
-  Workspace w = carve(p, pl, ws);
-  if (cudaMemsetAsync(w.status, 0, sizeof(int), stream) != cudaSuccess) return MSA_ERR_CUDA;
-  return run_attn(p, shape_of(p), pos, q, k_cache, v_cache, sel, out, w, stream);
+  return sparse_attn(p, q, k_cache, v_cache, sel, q_start, kv_len, out, nullptr, ws, ws_bytes,
+                     stream);
+}
+
+int msa_sparse_attn_lse(const msa_params* p, const uint16_t* q, const uint16_t* k_cache,
+                        const uint16_t* v_cache, const int32_t* sel, const int32_t* q_start,
+                        const int32_t* kv_len, uint16_t* out, float* lse, void* ws,
+                        size_t ws_bytes, cudaStream_t stream) {
+  if (!lse || !aligned16(lse)) return MSA_ERR_INVALID_ARG;
+  return sparse_attn(p, q, k_cache, v_cache, sel, q_start, kv_len, out, lse, ws, ws_bytes, stream);
 }
 
 int msa_forward(const msa_params* p, const uint16_t* q_idx, const uint16_t* k_idx,
@@ -350,47 +413,14 @@ size_t msa_dense_workspace_bytes(const msa_params* p) {
 int msa_dense_attn(const msa_params* p, const uint16_t* q, const uint16_t* k_cache,
                    const uint16_t* v_cache, const int32_t* q_start, const int32_t* kv_len,
                    uint16_t* out, void* ws, size_t ws_bytes, cudaStream_t stream) {
-  int rc = validate_params(p);
-  if (rc) return rc;
-  Positions pos;
-  if ((rc = validate_positions(p, q_start, kv_len, &pos))) return rc;
-  if (!q || !k_cache || !v_cache || !out) return MSA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
-    return MSA_ERR_INVALID_ARG;
-  if (!ws || ((uintptr_t)ws & (kAlign - 1)) != 0) return MSA_ERR_INVALID_ARG;
-  const DensePlan d = dense_plan_for(p);
-  if (ws_bytes < d.total) return MSA_ERR_WORKSPACE;
-  if (p->T == 0) return MSA_OK;
-  char* base = static_cast<char*>(ws);
-  Workspace w{};
-  w.status = reinterpret_cast<int*>(base);
-  int32_t* sel = reinterpret_cast<int32_t*>(base + d.sel_off);
-  char* scr = base + d.scratch_off;
-  w.part_o = reinterpret_cast<float*>(scr);
-  w.part_rows = d.part_rows;
-  w.part_ml = reinterpret_cast<float*>(scr + align_up(d.part_rows * p->D * sizeof(float)));
-  w.tc_base = scr;
-  w.tc_bytes = d.total - d.scratch_off;
-  if (cudaMemsetAsync(w.status, 0, sizeof(int), stream) != cudaSuccess) return MSA_ERR_CUDA;
-  const Shape s = shape_of(p);
-  if (use_tc_attn(p))
-    return cuda_status(launch_dense_tc(s, pos, q, k_cache, v_cache, out, w.status, stream));
-  // streaming shapes: chunks of 16 consecutive blocks, up to the last query's
-  // local block, each folded into fp32 running accumulators
-  const int nchunks = (max_local_block(s, pos, 0, p->T) + MSA_TOPK) / MSA_TOPK;
-  for (int c = 0; c < nchunks; ++c) {
-    if (launch_dense_sel(s, pos, c, sel, stream) != cudaSuccess) return MSA_ERR_CUDA;
-    DenseStep ds{reinterpret_cast<float*>(base + d.acc_o_off),
-                 reinterpret_cast<float2*>(base + d.acc_ml_off), c == 0, c == nchunks - 1};
-    const int tc = stream_pass_len(p);
-    for (int t0 = 0; t0 < p->T; t0 += tc) {
-      const int t1 = t0 + tc < p->T ? t0 + tc : p->T;
-      if (launch_attn_stream(s, pos, t0, t1, q, k_cache, v_cache, sel, out, w, stream, &ds) !=
-          cudaSuccess)
-        return MSA_ERR_CUDA;
-    }
-  }
-  return MSA_OK;
+  return dense_attn(p, q, k_cache, v_cache, q_start, kv_len, out, nullptr, ws, ws_bytes, stream);
+}
+
+int msa_dense_attn_lse(const msa_params* p, const uint16_t* q, const uint16_t* k_cache,
+                       const uint16_t* v_cache, const int32_t* q_start, const int32_t* kv_len,
+                       uint16_t* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!lse || !aligned16(lse)) return MSA_ERR_INVALID_ARG;
+  return dense_attn(p, q, k_cache, v_cache, q_start, kv_len, out, lse, ws, ws_bytes, stream);
 }
 
 size_t msa_index_kl_workspace_bytes(const msa_params* p) {

@@ -78,6 +78,7 @@ struct AttnPass {
   const uint8_t* v8;
   const int8_t* k_exp;
   const int8_t* v_exp;
+  float* lse;            // [B][T][H], or null
 };
 
 // Lists are ordered group-major, list (b, kb, g) at index (g*B + b)*nbl + kb:
@@ -916,6 +917,7 @@ __global__ void __launch_bounds__(256) attn_tc_merge_kernel(AttnPass a, uint16_t
 #pragma unroll
   for (int e = 0; e < PER; e += 2)
     *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (a.lse && lane == 0) a.lse[((size_t)b * a.s.T + i) * H + h] = lse_of(M, W);
 }
 
 struct AttnLayout {
@@ -944,7 +946,7 @@ AttnLayout attn_layout(const Shape& s, bool q8) {
 template <int D, bool Q8>
 cudaError_t launch_attn_tc_impl(const Shape& s, const Positions& pos, const uint16_t* q,
                                 const CacheView& cv, const int32_t* sel, uint16_t* out,
-                                const Workspace& ws, cudaStream_t st) {
+                                const Workspace& ws, cudaStream_t st, float* lse = nullptr) {
   using C = AttnCfg<D>;
   const AttnLayout lay = attn_layout(s, Q8);
   char* base = ws.tc_base;
@@ -1008,6 +1010,7 @@ cudaError_t launch_attn_tc_impl(const Shape& s, const Positions& pos, const uint
     a.v8 = Q8 ? static_cast<const uint8_t*>(cv.v) : nullptr;
     a.k_exp = cv.k_exp;
     a.v_exp = cv.v_exp;
+    a.lse = lse;
     const CsrGrid cg = csr_grid(s, a.nbl);
     const unsigned csr_ctas = (unsigned)(s.G * cg.per_group);
     const size_t csr_smem = (size_t)cg.span * 4;
@@ -1037,10 +1040,10 @@ size_t tc_attn_q8_workspace_bytes(const Shape& s) { return attn_layout(s, true).
 
 cudaError_t launch_attn_tc(const Shape& s, const Positions& pos, const uint16_t* q,
                            const uint16_t* k, const uint16_t* v, const int32_t* sel,
-                           uint16_t* out, const Workspace& ws, cudaStream_t st) {
+                           uint16_t* out, const Workspace& ws, cudaStream_t st, float* lse) {
   const CacheView cv{k, v, nullptr, nullptr, false};
-  if (s.D == 128) return launch_attn_tc_impl<128, false>(s, pos, q, cv, sel, out, ws, st);
-  return launch_attn_tc_impl<64, false>(s, pos, q, cv, sel, out, ws, st);
+  if (s.D == 128) return launch_attn_tc_impl<128, false>(s, pos, q, cv, sel, out, ws, st, lse);
+  return launch_attn_tc_impl<64, false>(s, pos, q, cv, sel, out, ws, st, lse);
 }
 
 cudaError_t launch_attn_tc_q8(const Shape& s, const Positions& pos, const uint16_t* q,

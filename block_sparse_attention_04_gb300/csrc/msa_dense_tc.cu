@@ -41,6 +41,7 @@ struct DenseArgs {
   int nitems;   // nqt * B * G * npair
   int* next_item;  // shared counter of taken items (zeroed with the status word)
   uint16_t* out;
+  float* lse;      // [B][T][H], or null
   int* status;
   uint32_t wait_polls;  // poll cap of the pipeline waits (0: wall-clock bound only)
 };
@@ -459,6 +460,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       }
       tc_fence_after();
       const float inv = 1.f / l;
+      if (a.lse && valid)
+        a.lse[((size_t)d.b * T + i) * a.s.H + (c == 0 ? d.ha : d.hb)] = lse_of(m_ref, l);
       uint16_t* dst =
           a.out + (((size_t)d.b * T + (valid ? i : 0)) * a.s.H + (c == 0 ? d.ha : d.hb)) * D;
 #pragma unroll 1
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
 template <int D>
 cudaError_t launch_dense_tc_impl(const Shape& s, const Positions& pos, const uint16_t* q,
                                  const uint16_t* k, const uint16_t* v, uint16_t* out, int* status,
-                                 cudaStream_t st) {
+                                 cudaStream_t st, float* lse) {
   using C = DenseCfg<D>;
   // the item counter sits in the word after the status word; both are zeroed
   if (cudaMemsetAsync(status, 0, 2 * sizeof(int), st) != cudaSuccess) return cudaErrorUnknown;
@@ -523,6 +526,7 @@ cudaError_t launch_dense_tc_impl(const Shape& s, const Positions& pos, const uin
   a.nitems = a.nqt * s.B * s.G * a.npair;
   a.next_item = status + 1;
   a.out = out;
+  a.lse = lse;
   a.status = status;
   a.wait_polls = debug_wait_polls();
   cudaError_t e = cudaFuncSetAttribute(dense_tc_kernel<D>,
@@ -539,10 +543,10 @@ cudaError_t launch_dense_tc_impl(const Shape& s, const Positions& pos, const uin
 
 cudaError_t launch_dense_tc(const Shape& s, const Positions& pos, const uint16_t* q,
                             const uint16_t* k, const uint16_t* v, uint16_t* out, int* status,
-                            cudaStream_t st) {
+                            cudaStream_t st, float* lse) {
   if (s.B == 0 || s.T == 0) return cudaSuccess;
-  return s.D == 128 ? launch_dense_tc_impl<128>(s, pos, q, k, v, out, status, st)
-                    : launch_dense_tc_impl<64>(s, pos, q, k, v, out, status, st);
+  return s.D == 128 ? launch_dense_tc_impl<128>(s, pos, q, k, v, out, status, st, lse)
+                    : launch_dense_tc_impl<64>(s, pos, q, k, v, out, status, st, lse);
 }
 
 }  // namespace msa

@@ -452,11 +452,17 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
          | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
 
+// The natural logarithm of a softmax's sum: l relative to 2^m.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return (m + __log2f(l)) * 0.6931471805599453f;
+}
+
 // Dense attention: folds one chunk into the running accumulator (see
 // DenseStep).  Mc = -inf means the chunk held no causal block for this query.
 template <int PER>
 __device__ __forceinline__ void dense_fold(const DenseStep& ds, size_t acc_row, float Mc, float Wc,
-                                           float (&oc)[PER], int lane, uint16_t* dst) {
+                                           float (&oc)[PER], int lane, uint16_t* dst,
+                                           float* lse) {
   float* ao = ds.acc_o + acc_row * (32 * PER) + lane * PER;
   float am = -INFINITY, al = 0.f;
   if (!ds.first) {
@@ -476,6 +482,7 @@ __device__ __forceinline__ void dense_fold(const DenseStep& ds, size_t acc_row, 
 #pragma unroll
     for (int e = 0; e < PER; e += 2)
       *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
+    if (lse && lane == 0) lse[acc_row] = lse_of(M, L);
   } else {
 #pragma unroll
     for (int e = 0; e < PER; ++e) ao[e] = o[e];

@@ -97,7 +97,8 @@ cudaError_t launch_topk_merge(const Shape& s, const Positions& pos, int t0, int 
 cudaError_t launch_attn_stream(const Shape& s, const Positions& pos, int t0, int t1,
                                const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                const int32_t* sel, uint16_t* out, const Workspace& ws,
-                               cudaStream_t st, const DenseStep* dense = nullptr);
+                               cudaStream_t st, const DenseStep* dense = nullptr,
+                               float* lse = nullptr);   // lse [B][T][H]: written if given
 
 // Dense attention: the selection of chunk j (blocks 16j .. 16j+15 that are
 // causal for each query, -1 elsewhere) for every query of the call.

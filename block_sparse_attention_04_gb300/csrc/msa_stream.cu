@@ -644,7 +644,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_dec_kernel(
 template <int D, bool DENSE>
 __global__ void __launch_bounds__(256) attn_merge_kernel(
     Shape s, int T, int t0, int Tp, int nrows, int nparts, const float* __restrict__ part_o,
-    const float* __restrict__ part_ml, uint16_t* __restrict__ out, DenseStep ds) {
+    const float* __restrict__ part_ml, uint16_t* __restrict__ out, DenseStep ds,
+    float* __restrict__ lse) {
   constexpr int PER = D / 32;
   const int gw = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -676,13 +677,14 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(
   }
   uint16_t* dst = out + ((size_t)(b * T + i) * s.H + h) * D + lane * PER;
   if constexpr (DENSE) {
-    dense_fold<PER>(ds, (size_t)(b * T + i) * s.H + h, M, L, acc, lane, dst);
+    dense_fold<PER>(ds, (size_t)(b * T + i) * s.H + h, M, L, acc, lane, dst, lse);
   } else {
     const float inv = 1.f / L;
 #pragma unroll
     for (int e = 0; e < PER; e += 2) {
       *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
     }
+    if (lse && lane == 0) lse[(size_t)(b * T + i) * s.H + h] = lse_of(M, L);
   }
 }
 
@@ -885,7 +887,7 @@ cudaError_t launch_attn_dec(const CUtensorMap& tm_k, const CUtensorMap& tm_v, co
 cudaError_t launch_attn_stream(const Shape& s, const Positions& pos, int t0, int t1,
                                const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                const int32_t* sel, uint16_t* out, const Workspace& ws,
-                               cudaStream_t st, const DenseStep* dense) {
+                               cudaStream_t st, const DenseStep* dense, float* lse) {
   const int Tp = t1 - t0;
   const int rows = s.B * Tp;
   if (rows <= 0) return cudaSuccess;
@@ -934,11 +936,11 @@ cudaError_t launch_attn_stream(const Shape& s, const Positions& pos, int t0, int
   if (dense)                                                                                    \
     attn_merge_kernel<DD, true><<<(warps + 7) / 8, 256, 0, st>>>(s, s.T, t0, Tp, rows,          \
                                                                  a.nparts, ws.part_o,           \
-                                                                 ws.part_ml, out, ds);          \
+                                                                 ws.part_ml, out, ds, lse);     \
   else                                                                                          \
     attn_merge_kernel<DD, false><<<(warps + 7) / 8, 256, 0, st>>>(s, s.T, t0, Tp, rows,         \
                                                                   a.nparts, ws.part_o,          \
-                                                                  ws.part_ml, out, ds)
+                                                                  ws.part_ml, out, ds, lse)
   if (s.D == 128) {
     MSA_ATTN_MERGE(128);
   } else {

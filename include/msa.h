@@ -72,6 +72,7 @@ extern "C" {
 #define MSA_Q8_MIN_EXP (-126) /* exponents of an 8-bit cache's block scales */
 #define MSA_Q8_MAX_EXP 119
 #define MSA_MAX_POOLS 8       /* pools that move together in a page operation */
+#define MSA_MAX_ROT 128       /* rotated dims of a head */
 
 typedef enum {
   MSA_OK = 0,
@@ -433,6 +434,114 @@ int msa_pages_compact(const msa_pool *pools, int npools, int num_pool_blocks,
                       const int32_t *block_table, int rows, int max_blocks, const int32_t *refs,
                       int32_t *table_out, int32_t *refs_out, int32_t *live, void *ws,
                       size_t ws_bytes, cudaStream_t stream);
+
+/* ---- The step in front of the attention: norm, rotation, cache write --------
+ * Queries and keys as the projections leave them become the attention's inputs in
+ * one pass over the data: for each head of a token,
+ *     n = x * w / sqrt(mean(x^2) + eps)     (w: one weight per dim, shared by the
+ *                                            heads; no weights: n = x)
+ *     (a, b) -> (a c - b s, b c + a s)      for each rotated pair of n, with
+ *     c, s = mscale * cos, sin(t * inv_freq[i]) at the token's position t
+ * in fp32, rounded to bf16 once (nearest even).  The pairs are dims (i, i + rot/2)
+ * or, interleaved, dims (2i, 2i + 1) of the first rot dims, i < rot/2; the dims
+ * behind them are normed only.  Angles are reduced in fp64: they keep their
+ * precision at any position.  Scalings for long contexts are frequencies (and
+ * mscale) like any others. */
+typedef struct {
+  int rot;          /* rotated dims: a multiple of 16, 0 .. D                     */
+  int interleaved;  /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1)             */
+  float eps;        /* of the norm, >= 0                                          */
+  float mscale;     /* factor of cos and sin, normally 1                          */
+  double inv_freq[MSA_MAX_ROT / 2]; /* radians per position of pair i < rot/2      */
+} msa_rope;
+
+/* Appends p->T new tokens to every sequence's caches as msa_cache_append does
+ * (block_table, num_pool_blocks, positions and ws as there), from the projections:
+ *   q [B][T] rows of H*D, k and v [B][T] rows of G*D (bf16), consecutive tokens
+ *     q_stride, k_stride and v_stride elements apart (multiples of 8, at least the
+ *     row: the three may be parts of one tensor)
+ *   q_weight, k_weight [D] bf16, or NULL: no norm of the queries, of the keys
+ *   k_idx_new [B][T][Di] or NULL (then k_idx_cache is not used)
+ * Writes q_out[B][T][H][D] (normed and rotated), the K rows (the same), the V rows
+ * and the K_idx rows (copied) of the caches.  Outputs must not overlap inputs.
+ * Where a table entry lies outside the pool, only q_out is written for the token
+ * (reported in ws). */
+int msa_rope_append(const msa_params *p, const msa_rope *r, const int32_t *block_table,
+                    int num_pool_blocks, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                    int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                    const uint16_t *q_weight, const uint16_t *k_weight, const uint16_t *k_idx_new,
+                    const int32_t *q_start, uint16_t *q_out, uint16_t *k_cache, uint16_t *v_cache,
+                    uint16_t *k_idx_cache, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Its backward pass on per-sequence caches: from the gradients of q_out and of the
+ * caches' rows q_start[b] .. q_start[b] + T - 1 (dq_out [B][T][H][D]; dk_cache and
+ * dv_cache [B][max_blocks][128][G][D], bf16, as the backward passes below write
+ * them) to those of the projections,
+ *   dq, dk, dv   bf16, rows as q, k and v above (their own strides)
+ *   dq_weight, dk_weight [D] fp32, written: the sums over all tokens and heads
+ * q, k, q_weight and k_weight are the forward call's; q (k) is not read where
+ * q_weight (k_weight) is NULL, and dq_weight (dk_weight) is then not written.
+ * Sums are in fp32 in an order that the shape alone decides (calls with the same
+ * inputs on the same device give the same bits).  ws: at least
+ * msa_rope_append_bwd_workspace_bytes(p) bytes, 256-byte aligned. */
+size_t msa_rope_append_bwd_workspace_bytes(const msa_params *p);
+int msa_rope_append_bwd(const msa_params *p, const msa_rope *r, const uint16_t *q,
+                        const uint16_t *k, int64_t q_stride, int64_t k_stride,
+                        const uint16_t *q_weight, const uint16_t *k_weight,
+                        const int32_t *q_start, const uint16_t *dq_out, const uint16_t *dk_cache,
+                        const uint16_t *dv_cache, uint16_t *dq, uint16_t *dk, uint16_t *dv,
+                        int64_t dq_stride, int64_t dk_stride, int64_t dv_stride, float *dq_weight,
+                        float *dk_weight, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ---- The main branch's backward pass ------------------------------------------
+ * msa_sparse_attn and msa_dense_attn that also return what the backward pass needs
+ * of the softmax: lse[B][T][H] (fp32), the natural logarithm of the sum of
+ * exp(scale * s) over the tokens that the (query, head) attends to (-inf where
+ * there is none).  out and ws are as without it. */
+int msa_sparse_attn_lse(const msa_params *p, const uint16_t *q, const uint16_t *k_cache,
+                        const uint16_t *v_cache, const int32_t *sel, const int32_t *q_start,
+                        const int32_t *kv_len, uint16_t *out, float *lse, void *ws,
+                        size_t ws_bytes, cudaStream_t stream);
+int msa_dense_attn_lse(const msa_params *p, const uint16_t *q, const uint16_t *k_cache,
+                       const uint16_t *v_cache, const int32_t *q_start, const int32_t *kv_len,
+                       uint16_t *out, float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Gradients of the attention for dout[B][T][H][D] (bf16), the gradient of out, by
+ * recomputing the probabilities from q, the caches and lse.  Over the tokens j
+ * that query i's head attends to (all j <= t; those of its selected blocks):
+ *   P_ij  = exp(scale q_i.k_j - lse_i)       dP_ij = dout_i . v_j
+ *   dS_ij = P_ij (dP_ij - delta_i)           delta_i = dout_i . out_i
+ *   dv_j = sum_i P_ij dout_i                 (over the queries and the heads of the
+ *   dk_j = scale sum_i dS_ij q_i              group that attend to j)
+ *   dq_i = scale sum_j dS_ij k_j
+ * dq [B][T][H][D]; dk, dv [B][max_blocks][128][G][D] bf16: the rows of tokens
+ * below kv_len[b] are written (zeros where no query attends), those behind are left
+ * as they were.  Products are of bf16 operands (P and dS rounded to nearest) and
+ * sums in fp32, in an order that inputs and shape decide (no atomics: calls with
+ * the same inputs on the same device give the same bits).  Where a query's whole
+ * context lies in one block, delta is taken from P and dP, which keeps the
+ * difference exact where few tokens are seen.  out and lse are the forward call's;
+ * sel and an id's meaning are as in msa_sparse_attn (an id listed twice counts
+ * twice; ids outside [0, lb] are reported and skipped; a query without a visible
+ * token gets dq = 0).  Cache rows behind the last query of a sequence may hold
+ * anything; a NaN or an infinity in q, dout or lse of one query may also reach, in
+ * the gradients of the heads of its group, dk and dv of tokens of the blocks that it
+ * attends to which it does not see itself, and one in k or v of a token dq of
+ * queries that share that block with it.  ws: at least
+ * msa_sparse_bwd_workspace_bytes(p), msa_dense_bwd_workspace_bytes(p) bytes, 256-byte
+ * aligned. */
+size_t msa_sparse_bwd_workspace_bytes(const msa_params *p);
+int msa_sparse_attn_bwd(const msa_params *p, const uint16_t *q, const uint16_t *k_cache,
+                        const uint16_t *v_cache, const int32_t *sel, const uint16_t *out,
+                        const float *lse, const uint16_t *dout, const int32_t *q_start,
+                        const int32_t *kv_len, uint16_t *dq, uint16_t *dk, uint16_t *dv, void *ws,
+                        size_t ws_bytes, cudaStream_t stream);
+size_t msa_dense_bwd_workspace_bytes(const msa_params *p);
+int msa_dense_attn_bwd(const msa_params *p, const uint16_t *q, const uint16_t *k_cache,
+                       const uint16_t *v_cache, const uint16_t *out, const float *lse,
+                       const uint16_t *dout, const int32_t *q_start, const int32_t *kv_len,
+                       uint16_t *dq, uint16_t *dk, uint16_t *dv, void *ws, size_t ws_bytes,
+                       cudaStream_t stream);
 
 /* Waits for `stream`, then returns the status the last call on ws left in
  * it: MSA_OK; MSA_ERR_TIMEOUT if a kernel's bounded wait ran out (its
