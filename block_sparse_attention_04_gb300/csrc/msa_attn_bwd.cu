@@ -1,148 +1,177 @@
-// The attention's backward pass (msa_sparse_attn_bwd, msa_dense_attn_bwd).
-#include "msa_device.cuh"
-#include "msa_train.h"
+// The attention's backward pass (msa_sparse_attn_bwd, msa_dense_attn_bwd): its scratch
+// and the sequence of its kernels.
+//   dense    statistics; units; dK and dV (KV-outer); dQ (query-outer)
+//   sparse   statistics; per pass of at most 8192 query rows: lists, units; dK, dV and
+//            dQ's parts (KV-outer); the parts' sums.  Several passes add dK and dV up
+//            in fp32.
+// Dense takes two kernels of four and three products where one of five would do: dQ
+// would then need one sum per (query, head) over all key blocks, i.e. atomic adds (whose
+// order changes the bits) of 128 x D fp32 per tile.
+#include "msa_bwd.h"
+#include "msa_tc.h"
+#include "msa_tma.h"
 
 namespace msa {
 namespace {
 
-// How often query row r (of [B*T]) attends to block kb of group g.
-__device__ __forceinline__ int listed(const Shape& s, const int32_t* sel, int64_t r, int g, int kb) {
-  if (!sel) return 1;
-  int n = 0;
-  for (int j = 0; j < kTopk; ++j) n += sel[(r * s.G + g) * kTopk + j] == kb;
-  return n;
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Tiles per unit: a block's work is divided where it would hold up the others, i.e. is
+// more than a quarter of a CTA's share of all `tiles`, but not below 16 tiles (a piece
+// costs about three tiles' time: K and V, the sums' way out and back).  A divided block
+// of n > piece tiles has ceil(n / piece) <= 2 n / piece slots, so a call has at most 2
+// tiles / piece, and no call of up to `tiles` tiles more than the second bound.
+constexpr int kMinPiece = 16;
+int piece_tiles(int64_t tiles) {
+  const int64_t p = tiles / (4 * kBwdSms) + 1;
+  return (int)(p < kMinPiece ? kMinPiece : (p > (1 << 28) ? 1 << 28 : p));
+}
+int slots_of(int64_t tiles) { return (int)(2 * tiles / piece_tiles(tiles)); }
+int most_slots(int64_t tiles) {
+  const int64_t n = 2 * tiles / kMinPiece;
+  return (int)(n < 8 * kBwdSms ? n : 8 * kBwdSms);
 }
 
-template <int PER>
-__device__ __forceinline__ void load(const uint16_t* p, float (&x)[PER]) {
-#pragma unroll
-  for (int e = 0; e < PER; ++e) x[e] = bf16lo(p[e]);
-}
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-template <int PER>
-__device__ __forceinline__ float dot(const float (&x)[PER], const float (&y)[PER]) {
-  float r = 0.f;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) r = fmaf(x[e], y[e], r);
-  return warp_sum(r);
-}
+int rows_per_entry(const Shape& s) { return s.H / s.G <= 8 ? 8 : 16; }
 
-// One warp per (query, head): delta = sum P dP / sum P, then dq.
-template <int D>
-__global__ void __launch_bounds__(256) bwd_dq_kernel(Shape s, const __grid_constant__ Positions pos,
-                                                     AttnBwd a, float* delta, int* status) {
-  constexpr int PER = D / 32;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (w >= (int64_t)s.B * s.T * s.H) return;
-  const int h = (int)(w % s.H), g = h / (s.H / s.G);
-  const int64_t r = w / s.H;
-  const int b = (int)(r / s.T);
-  const int t = pos.q_start[b] + (int)(r % s.T);
-  float q[PER], go[PER], x[PER], acc[PER];
-  load(a.q + w * D + lane * PER, q);
-  load(a.dout + w * D + lane * PER, go);
-#pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  const float lse = a.lse[w];
-  float sp = 0.f, spd = 0.f, dl = 0.f;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int kb = 0; kb <= t / kBlock; ++kb) {
-      const int mult = listed(s, a.sel, r, g, kb);
-      if (mult == 0) continue;
-      const int last = min(t, kb * kBlock + kBlock - 1);
-      for (int j = kb * kBlock; j <= last; ++j) {
-        const int64_t row = (((int64_t)b * s.max_blocks * kBlock + j) * s.G + g) * D + lane * PER;
-        float k[PER];
-        load(a.k + row, k);
-        load(a.v + row, x);
-        const float p = __expf(dot(q, k) * s.scale - lse) * mult, dp = dot(go, x);
-        if (pass == 0) {
-          sp += p;
-          spd = fmaf(p, dp, spd);
-        } else {
-          const float ds = p * (dp - dl);
-#pragma unroll
-          for (int e = 0; e < PER; ++e) acc[e] = fmaf(ds, k[e], acc[e]);
-        }
-      }
-    }
-    if (pass == 0) dl = sp > 0.f ? spd / sp : 0.f;
+// Tiles of a call or a pass, at most.
+int64_t max_tiles(const Shape& s, bool sparse, int tp, int nbl) {
+  const int64_t lists = (int64_t)s.B * nbl * s.G;
+  if (sparse) {
+    const int64_t entries = (int64_t)s.B * tp * s.G * kTopk, r = 128 / rows_per_entry(s);
+    return entries / r + (lists < entries ? lists : entries);
   }
-  if (lane == 0) delta[w] = dl;
-  if (a.sel && h % (s.H / s.G) == 0 && lane < kTopk)
-    if (a.sel[(r * s.G + g) * kTopk + lane] > t / kBlock) flag_invalid(status);
-#pragma unroll
-  for (int e = 0; e < PER; ++e)
-    a.dq[w * D + lane * PER + e] = (uint16_t)pack_bf16(acc[e] * s.scale, 0.f);
+  return lists * (s.H / s.G) * ((s.T + 127) / 128);
 }
 
-// One warp per (token, group): dk and dv.
-template <int D>
-__global__ void __launch_bounds__(256) bwd_dkv_kernel(Shape s, const __grid_constant__ Positions pos,
-                                                      AttnBwd a, const float* delta) {
-  constexpr int PER = D / 32;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int rows = s.max_blocks * kBlock, hpg = s.H / s.G;
-  if (w >= (int64_t)s.B * rows * s.G) return;
-  const int g = (int)(w % s.G);
-  const int b = (int)(w / s.G / rows), j = (int)(w / s.G % rows);
-  if (j >= pos.kv_len[b]) return;
-  float k[PER], v[PER], q[PER], go[PER], dk[PER], dv[PER];
-  load(a.k + w * D + lane * PER, k);
-  load(a.v + w * D + lane * PER, v);
-#pragma unroll
-  for (int e = 0; e < PER; ++e) dk[e] = dv[e] = 0.f;
-  for (int i = max(0, j - pos.q_start[b]); i < s.T; ++i) {
-    const int64_t r = (int64_t)b * s.T + i;
-    const int mult = listed(s, a.sel, r, g, j / kBlock);
-    if (mult == 0) continue;
-    for (int h = g * hpg; h < (g + 1) * hpg; ++h) {
-      const int64_t at = r * s.H + h;
-      load(a.q + at * D + lane * PER, q);
-      load(a.dout + at * D + lane * PER, go);
-      const float p = __expf(dot(q, k) * s.scale - a.lse[at]) * mult;
-      const float ds = p * (dot(go, v) - delta[at]);
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        dv[e] = fmaf(p, go[e], dv[e]);
-        dk[e] = fmaf(ds, q[e], dk[e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    a.dk[w * D + lane * PER + e] = (uint16_t)pack_bf16(dk[e] * s.scale, 0.f);
-    a.dv[w * D + lane * PER + e] = (uint16_t)pack_bf16(dv[e], 0.f);
-  }
-}
+// Dense: at most this many (item, split) partials.
+constexpr int kMaxQParts = 4 * kBwdSms;
+int q_items(const Shape& s) { return (s.T + 127) / 128 * s.B * s.H; }
 
-template <int D>
-void launch(const Shape& s, const Positions& pos, const AttnBwd& a, int* status, float* delta,
-            cudaStream_t st) {
-  const int64_t rows = (int64_t)s.B * s.T * s.H;
-  const int64_t toks = (int64_t)s.B * s.max_blocks * kBlock * s.G;
-  note_launches(2);
-  bwd_dq_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(s, pos, a, delta, status);
-  bwd_dkv_kernel<D><<<(unsigned)((toks + 7) / 8), 256, 0, st>>>(s, pos, a, delta);
+struct Layout {
+  size_t stat, cnt, count, off, entries, units, slots, part_dq, part_kv, acc, part_q, total;
+  uint32_t stat_groups;
+  int chunks;
+};
+
+Layout layout(const Shape& s, bool sparse) {
+  Layout L{};
+  const int tp = pass_len(s), nbl = s.max_blocks;
+  const int64_t lists = (int64_t)s.B * nbl * s.G;
+  const int rpe = rows_per_entry(s);
+  size_t o = 256;                        // the counters
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes);
+    return at;
+  };
+  const int slots = most_slots(max_tiles(s, sparse, tp, nbl));
+  if (sparse) {
+    L.stat_groups = (uint32_t)((size_t)s.B * s.T * s.G * (rpe / 8));
+    L.stat = take(((size_t)L.stat_groups + 1) * kStatBytes);
+    L.chunks = (tp + kChunkRows - 1) / kChunkRows;
+    L.cnt = take((size_t)s.B * L.chunks * s.G * nbl * sizeof(int32_t));
+    L.count = take(lists * sizeof(int32_t));
+    L.off = take(lists * sizeof(int32_t));
+    L.entries = take((size_t)s.B * tp * s.G * kTopk * sizeof(int32_t));
+    L.part_dq = take((size_t)s.B * tp * s.H * kTopk * s.D * 2);
+    if (tp < s.T) L.acc = take((size_t)lists * kBlock * s.D * 2 * sizeof(float));
+  } else {
+    L.stat_groups = (uint32_t)((s.T + 127) / 128 * 16);
+    L.stat = take((size_t)s.B * s.H * L.stat_groups * kStatBytes);
+    const int items = q_items(s);
+    if (items < kMaxQParts) L.part_q = take((size_t)kMaxQParts * 128 * s.D * sizeof(float));
+  }
+  L.units = take((lists + slots) * sizeof(int4));
+  L.slots = take((size_t)slots * sizeof(int4));
+  L.part_kv = take((size_t)slots * 2 * kBlock * s.D * sizeof(float));
+  L.total = o;
+  return L;
 }
 
 }  // namespace
 
-size_t attn_bwd_scratch_bytes(const Shape& s, bool) {
-  return (size_t)s.B * s.T * s.H * sizeof(float);
-}
+size_t attn_bwd_scratch_bytes(const Shape& s, bool sparse) { return layout(s, sparse).total; }
 
-cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd& a, int* status,
+cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd& t, int* status,
                             char* base, cudaStream_t st) {
-  if (s.D == 128) launch<128>(s, pos, a, status, reinterpret_cast<float*>(base), st);
-  else launch<64>(s, pos, a, status, reinterpret_cast<float*>(base), st);
-  return cudaGetLastError();
+  const bool sparse = t.sel != nullptr;
+  const Layout L = layout(s, sparse);
+  BwdArgs a{};
+  a.s = s;
+  a.pos = pos;
+  a.hpg = s.H / s.G;
+  a.rpe = rows_per_entry(s);
+  a.R = 128 / a.rpe;
+  a.nqt = (s.T + 127) / 128;
+  a.sel = t.sel;
+  a.n_units = reinterpret_cast<int*>(base);
+  a.next_unit = a.n_units + 2;
+  a.stat = reinterpret_cast<uint8_t*>(base + L.stat);
+  a.stat_groups = L.stat_groups;
+  a.chunks = L.chunks;
+  a.cnt = reinterpret_cast<int32_t*>(base + L.cnt);
+  a.count = reinterpret_cast<int32_t*>(base + L.count);
+  a.off = reinterpret_cast<int32_t*>(base + L.off);
+  a.entries = reinterpret_cast<int32_t*>(base + L.entries);
+  a.units = reinterpret_cast<int4*>(base + L.units);
+  a.slots = reinterpret_cast<int4*>(base + L.slots);
+  a.part_dq = reinterpret_cast<uint16_t*>(base + L.part_dq);
+  a.part_kv = reinterpret_cast<float*>(base + L.part_kv);
+  a.acc = reinterpret_cast<float*>(base + L.acc);
+  a.dq = t.dq;
+  a.dk = t.dk;
+  a.dv = t.dv;
+  a.status = status;
+  a.wait_polls = debug_wait_polls();
+  int max_len = 1;
+  for (int b = 0; b < s.B; ++b) max_len = pos.kv_len[b] > max_len ? pos.kv_len[b] : max_len;
+  a.nbl = (max_len + kBlock - 1) / kBlock;
+  cudaError_t e;
+  if ((e = launch_bwd_stats(s, pos, t, sparse ? a.rpe : 0, reinterpret_cast<uint8_t*>(base + L.stat),
+                            L.stat_groups, st)) != cudaSuccess)
+    return e;
+  const int tp = sparse ? pass_len(s) : s.T;
+  for (int t0 = 0; t0 < s.T; t0 += tp) {
+    a.t0 = t0;
+    a.Tp = tp < s.T - t0 ? tp : s.T - t0;
+    a.first = t0 == 0;
+    a.last = t0 + tp >= s.T;
+    const int64_t tiles = max_tiles(s, sparse, a.Tp, a.nbl);
+    a.piece = piece_tiles(tiles);
+    a.max_slots = slots_of(tiles);
+    if ((e = cudaMemsetAsync(a.n_units, 0, 256, st)) != cudaSuccess) return e;
+    if ((e = sparse ? launch_bwd_lists(a, st) : launch_bwd_units(a, st)) != cudaSuccess) return e;
+    if ((e = launch_bwd_kv(a, t, st)) != cudaSuccess) return e;
+    if ((e = launch_bwd_join_kv(a, st)) != cudaSuccess) return e;
+    if (sparse && (e = launch_bwd_join_q(a, st)) != cudaSuccess) return e;
+  }
+  if (sparse) return cudaSuccess;
+  BwdQArgs q{};
+  q.s = s;
+  q.pos = pos;
+  q.nqt = a.nqt;
+  q.nitems = q_items(s);
+  // few items: the key blocks of each over several CTAs, at least 4 blocks a split
+  q.splits = 1;
+  if (q.nitems < kMaxQParts) {
+    int blocks = 1;
+    for (int b = 0; b < s.B; ++b) {
+      const int n = (int)(((int64_t)pos.q_start[b] + s.T - 1) / kBlock) + 1;
+      blocks = n > blocks ? n : blocks;
+    }
+    const int by_parts = kMaxQParts / q.nitems, by_blocks = blocks / 4;
+    q.splits = by_parts < by_blocks ? by_parts : by_blocks;
+    if (q.splits < 1) q.splits = 1;
+  }
+  q.next_item = a.n_units + 3;
+  q.stat = a.stat;
+  q.stat_groups = L.stat_groups;
+  q.part = reinterpret_cast<float*>(base + L.part_q);
+  q.dq = t.dq;
+  q.status = status;
+  q.wait_polls = a.wait_polls;
+  return launch_bwd_q(q, t, st);
 }
 
 }  // namespace msa

@@ -1,0 +1,86 @@
+// The attention's backward pass: what its kernels share (internal interface).
+//
+// Row statistics.  The kernels recompute P = 2^(s scale log2e - lse log2e) and
+// dS = P (dP - delta); the two numbers of a (query, head) row are kept in groups of
+// 8 rows, 64 bytes: eight -lse log2e, then eight -delta.
+//   dense    group ((b H + h) ngroups + i/8), a tile's 16 groups in a row; rows past
+//            the last query hold (-inf, 0): their P and dS vanish
+//   sparse   group (((b T + i) G + g) rpe/8 + head/8): an entry's rows; heads past
+//            the group's last as above, and one such group behind all others
+#pragma once
+#include "msa_train.h"
+
+namespace msa {
+
+constexpr int kStatBytes = 64;          // a group of 8 rows
+constexpr int kBwdSms = 152;            // what sizes of scratch are made for
+constexpr int kChunkRows = 64;          // query rows whose list entries keep their order
+
+// A piece of the work of one KV block: x = kb | g << 15 | b << 18; dense: y = first
+// tile, z = tiles (a head's query tiles are consecutive); sparse: y = first entry, z =
+// entries; w = slot of the piece's partial sums, or -1 where it is the block's only one.
+struct BwdArgs {
+  Shape s;
+  Positions pos;
+  int t0, Tp;                // queries of the pass: [t0, t0 + Tp) of every sequence
+  int nbl;                   // KV blocks per sequence in the item space
+  int hpg, rpe, R;           // heads per group; sparse: rows per entry, entries per tile
+  int nqt;                   // dense: 128-query tiles per sequence
+  int piece;                 // tiles per unit (at most)
+  const int32_t* sel;        // sparse: the selection
+  int32_t* cnt;              // [B][chunks][G][nbl]: entries per chunk, then those before
+  int chunks;
+  int32_t* count;            // [G][B][nbl] entries of a list
+  int32_t* off;              // [G][B][nbl] its first entry
+  int32_t* entries;          // (i - t0) * 16 + slot
+  int4* units;
+  int* n_units;              // [2]: units, partial slots
+  int4* slots;               // per slot: (b, g, kb packed as x; its unit's slots, 0 but for the first)
+  int max_slots;
+  int* next_unit;
+  const uint8_t* stat;
+  uint32_t stat_groups;      // dense: groups per (b, h); sparse: index of the neutral group
+  uint16_t* part_dq;         // sparse: [B*Tp*H*16][D] bf16 partial dq, without the scale
+  float* part_kv;            // [max_slots][2][128][D]: dv, dk (dk without the scale)
+  float* acc;                // several passes: running dv, dk [2][B][max_blocks][128][G][D]
+  bool first, last;          // pass
+  uint16_t *dq, *dk, *dv;
+  int* status;
+  uint32_t wait_polls;       // poll cap of the pipeline waits (0: wall-clock bound only)
+};
+
+// Dense: the first query tile that sees block kb of sequence b (nqt: none does).
+__host__ __device__ inline int bwd_first_tile(const BwdArgs& a, int b, int kb) {
+  const int64_t i0 = (int64_t)kb * kBlock - a.pos.q_start[b];
+  if (i0 >= a.s.T) return a.nqt;
+  return i0 > 0 ? (int)(i0 / 128) : 0;
+}
+
+// Units of the dense call: (query tile, head) items x splits of the key blocks.
+struct BwdQArgs {
+  Shape s;
+  Positions pos;
+  int nqt, nitems, splits;
+  int* next_item;
+  const uint8_t* stat;
+  uint32_t stat_groups;
+  float* part;               // splits > 1: [nitems][splits][128][D] partial dq
+  uint16_t* dq;
+  int* status;
+  uint32_t wait_polls;
+};
+
+// Preparation: row statistics, lists (sparse), units.
+cudaError_t launch_bwd_stats(const Shape& s, const Positions& pos, const AttnBwd& a, int rpe,
+                             uint8_t* stat, uint32_t stat_groups, cudaStream_t st);
+cudaError_t launch_bwd_lists(const BwdArgs& a, cudaStream_t st);
+cudaError_t launch_bwd_units(const BwdArgs& a, cudaStream_t st);
+// dK and dV (and, sparse, dQ's parts), one owner per KV block.
+cudaError_t launch_bwd_kv(const BwdArgs& a, const AttnBwd& t, cudaStream_t st);
+// Dense dQ.
+cudaError_t launch_bwd_q(const BwdQArgs& a, const AttnBwd& t, cudaStream_t st);
+// Joins: dQ from the selected blocks' parts; dK and dV of blocks in several pieces.
+cudaError_t launch_bwd_join_q(const BwdArgs& a, cudaStream_t st);
+cudaError_t launch_bwd_join_kv(const BwdArgs& a, cudaStream_t st);
+
+}  // namespace msa
