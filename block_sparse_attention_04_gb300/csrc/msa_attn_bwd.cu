@@ -34,6 +34,19 @@ int most_slots(int64_t tiles) {
 
 int rows_per_entry(const Shape& s) { return s.H / s.G <= 8 ? 8 : 16; }
 
+// Tiles of a dense call.
+int64_t dense_tiles(const BwdArgs& a) {
+  int64_t n = 0;
+  for (int b = 0; b < a.s.B; ++b) {
+    // blocks up to the first query's see every tile, each later one a tile less or the same
+    const int first = a.pos.q_start[b] / kBlock;
+    const int last = (int)(((int64_t)a.pos.q_start[b] + a.s.T - 1) / kBlock);
+    n += (int64_t)(first + 1) * a.nqt;
+    for (int kb = first + 1; kb <= last; ++kb) n += a.nqt - bwd_first_tile(a, b, kb);
+  }
+  return n * a.s.G * a.hpg;
+}
+
 // Tiles of a call or a pass, at most.
 int64_t max_tiles(const Shape& s, bool sparse, int tp, int nbl) {
   const int64_t lists = (int64_t)s.B * nbl * s.G;
@@ -49,7 +62,7 @@ constexpr int kMaxQParts = 4 * kBwdSms;
 int q_items(const Shape& s) { return (s.T + 127) / 128 * s.B * s.H; }
 
 struct Layout {
-  size_t stat, cnt, count, off, entries, units, slots, part_dq, part_kv, acc, part_q, total;
+  size_t stat, cnt, count, off, entries, where, units, slots, part_dq, part_kv, acc, part_q, total;
   uint32_t stat_groups;
   int chunks;
 };
@@ -65,7 +78,8 @@ Layout layout(const Shape& s, bool sparse) {
     o += align_up(bytes);
     return at;
   };
-  const int slots = most_slots(max_tiles(s, sparse, tp, nbl));
+  const int64_t tiles = max_tiles(s, sparse, tp, nbl);
+  const int slots = most_slots(tiles);
   if (sparse) {
     L.stat_groups = (uint32_t)((size_t)s.B * s.T * s.G * (rpe / 8));
     L.stat = take(((size_t)L.stat_groups + 1) * kStatBytes);
@@ -73,8 +87,9 @@ Layout layout(const Shape& s, bool sparse) {
     L.cnt = take((size_t)s.B * L.chunks * s.G * nbl * sizeof(int32_t));
     L.count = take(lists * sizeof(int32_t));
     L.off = take(lists * sizeof(int32_t));
-    L.entries = take((size_t)s.B * tp * s.G * kTopk * sizeof(int32_t));
-    L.part_dq = take((size_t)s.B * tp * s.H * kTopk * s.D * 2);
+    L.entries = take((size_t)tiles * (128 / rpe) * sizeof(int32_t));
+    L.where = take((size_t)s.B * tp * s.G * kTopk * sizeof(int32_t));
+    L.part_dq = take((size_t)tiles * 128 * s.D * 2);
     if (tp < s.T) L.acc = take((size_t)lists * kBlock * s.D * 2 * sizeof(float));
   } else {
     L.stat_groups = (uint32_t)((s.T + 127) / 128 * 16);
@@ -114,6 +129,7 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
   a.count = reinterpret_cast<int32_t*>(base + L.count);
   a.off = reinterpret_cast<int32_t*>(base + L.off);
   a.entries = reinterpret_cast<int32_t*>(base + L.entries);
+  a.where = reinterpret_cast<int32_t*>(base + L.where);
   a.units = reinterpret_cast<int4*>(base + L.units);
   a.slots = reinterpret_cast<int4*>(base + L.slots);
   a.part_dq = reinterpret_cast<uint16_t*>(base + L.part_dq);
@@ -137,10 +153,11 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
     a.Tp = tp < s.T - t0 ? tp : s.T - t0;
     a.first = t0 == 0;
     a.last = t0 + tp >= s.T;
-    const int64_t tiles = max_tiles(s, sparse, a.Tp, a.nbl);
+    const int64_t tiles = sparse ? max_tiles(s, true, a.Tp, a.nbl) : dense_tiles(a);
     a.piece = piece_tiles(tiles);
     a.max_slots = slots_of(tiles);
-    if ((e = cudaMemsetAsync(a.n_units, 0, 256, st)) != cudaSuccess) return e;
+    // a group's work for each CTA is less than a few of its largest units
+    a.mixed = tiles / s.G / kBwdSms < 4 * (int64_t)a.piece;
     if ((e = sparse ? launch_bwd_lists(a, st) : launch_bwd_units(a, st)) != cudaSuccess) return e;
     if ((e = launch_bwd_kv(a, t, st)) != cudaSuccess) return e;
     if ((e = launch_bwd_join_kv(a, st)) != cudaSuccess) return e;

@@ -16,9 +16,15 @@ constexpr int kStatBytes = 64;          // a group of 8 rows
 constexpr int kBwdSms = 152;            // what sizes of scratch are made for
 constexpr int kChunkRows = 64;          // query rows whose list entries keep their order
 
-// A piece of the work of one KV block: x = kb | g << 15 | b << 18; dense: y = first
-// tile, z = tiles (a head's query tiles are consecutive); sparse: y = first entry, z =
-// entries; w = slot of the piece's partial sums, or -1 where it is the block's only one.
+// A unit is a piece of the work of one KV block: x = kb | g << 15 | b << 18; dense: y =
+// first tile, z = tiles (a head's query tiles are consecutive); sparse: y = first entry (a
+// multiple of R), z = entries; w = slot of the piece's partial sums, or -1 where it is the
+// block's only one.  A list's entries start at a multiple of R, so that entry e is in tile
+// e / R of the pass.
+//
+// Layouts of partial sums, in which a warp's 32-byte stores are contiguous:
+//   part_dq  [tile][D/16][128 rows][16 dims] bf16     row (e % R) rpe + head of the group
+//   part_kv  [slot][dv, dk][D/8][128 tokens][8 dims] fp32
 struct BwdArgs {
   Shape s;
   Positions pos;
@@ -27,21 +33,23 @@ struct BwdArgs {
   int hpg, rpe, R;           // heads per group; sparse: rows per entry, entries per tile
   int nqt;                   // dense: 128-query tiles per sequence
   int piece;                 // tiles per unit (at most)
+  bool mixed;                // units of all groups by size (else group by group)
   const int32_t* sel;        // sparse: the selection
   int32_t* cnt;              // [B][chunks][G][nbl]: entries per chunk, then those before
   int chunks;
   int32_t* count;            // [G][B][nbl] entries of a list
   int32_t* off;              // [G][B][nbl] its first entry
   int32_t* entries;          // (i - t0) * 16 + slot
+  int32_t* where;            // [B*Tp][G][16]: the entry of each selected id, -1: none
   int4* units;
   int* n_units;              // [2]: units, partial slots
   int4* slots;               // per slot: (b, g, kb packed as x; its unit's slots, 0 but for the first)
   int max_slots;
-  int* next_unit;
+  int* next_unit;            // [2] counters of taken units and of taken dQ items
   const uint8_t* stat;
   uint32_t stat_groups;      // dense: groups per (b, h); sparse: index of the neutral group
-  uint16_t* part_dq;         // sparse: [B*Tp*H*16][D] bf16 partial dq, without the scale
-  float* part_kv;            // [max_slots][2][128][D]: dv, dk (dk without the scale)
+  uint16_t* part_dq;         // sparse: dq of each tile, without the scale
+  float* part_kv;            // dv, dk of each slot (dk without the scale)
   float* acc;                // several passes: running dv, dk [2][B][max_blocks][128][G][D]
   bool first, last;          // pass
   uint16_t *dq, *dk, *dv;

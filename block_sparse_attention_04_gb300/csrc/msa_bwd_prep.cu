@@ -109,6 +109,9 @@ __device__ __forceinline__ void stat_first(const StatArgs& a, int64_t task) {
   }
 }
 
+// A group of 8 rows per D/8 lanes: its 16 row reads are in flight together, and it is
+// written whole.  (One row at a time, with its two numbers stored singly: 438 us for 16K
+// queries of 48 heads, 403 MB.)
 template <int D>
 __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_constant__ StatArgs a) {
   constexpr int LPR = D / 8;
@@ -118,48 +121,67 @@ __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_con
     return;
   }
   const int l = threadIdx.x % LPR;
-  const int per_row = a.rpe ? G * a.rpe : H;              // rows of a query
-  const int Tn = a.rpe ? a.s.T : (int)a.groups * 8;
-  const int64_t n = (int64_t)a.s.B * Tn * per_row;
-  const int64_t step = (int64_t)a.row_ctas * (kStatThreads / LPR);
-  for (int64_t e0 = (int64_t)blockIdx.x * (kStatThreads / LPR); e0 < n; e0 += step) {
-    const int64_t e = e0 + threadIdx.x / LPR;
-    const bool in = e < n;
-    const int64_t r = (in ? e : n - 1) / per_row;
-    const int hr = (int)((in ? e : n - 1) - r * per_row);
-    const int b = (int)(r / Tn), i = (int)(r - (int64_t)b * Tn);
-    const int hh = a.rpe ? hr % a.rpe : 0;
-    const int h = a.rpe ? hr / a.rpe * hpg + hh : hr;
-    const bool real = in && i < a.s.T && hh < hpg;
+  const int64_t grp = (int64_t)blockIdx.x * (kStatThreads / LPR) + threadIdx.x / LPR;
+  // dense: groups in order (b, 8 queries, h); sparse: (b, query, g, 8 heads)
+  int b, i0, h0, n;
+  int64_t row;                       // the first row, of rows [B][T][H]
+  const int step = a.rpe ? 1 : H;    // to the next
+  bool in;
+  uint8_t* dst;
+  if (a.rpe) {
+    const int sub = a.rpe >> 3;
+    in = grp < (int64_t)a.s.B * a.s.T * G * sub;
+    const int64_t q = grp / (G * sub);
+    const int x = (int)(grp - q * (G * sub));
+    b = (int)(q / a.s.T);
+    i0 = (int)(q - (int64_t)b * a.s.T);
+    h0 = x / sub * hpg + x % sub * 8;
+    n = min(8, hpg - x % sub * 8);
+    row = q * H + h0;
+    dst = a.stat + grp * kStatBytes;
+  } else {
+    const int64_t q = grp / H;
+    h0 = (int)(grp - q * H);
+    in = q < (int64_t)a.s.B * a.groups;
+    b = (int)(q / a.groups);
+    i0 = (int)(q - (int64_t)b * a.groups) * 8;
+    n = min(8, a.s.T - i0);
+    row = ((int64_t)b * a.s.T + i0) * H + h0;
+    dst = a.stat + ((size_t)(b * H + h0) * a.groups + (i0 >> 3)) * kStatBytes;
+  }
+  if (!in) n = 0;
+  uint4 o[8], g[8];
+  const size_t at = row * D + 8 * l, next = (size_t)step * D;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    o[k] = g[k] = make_uint4(0, 0, 0, 0);
+    if (k < n) {
+      o[k] = __ldcs(reinterpret_cast<const uint4*>(a.out + at + k * next));
+      g[k] = *reinterpret_cast<const uint4*>(a.dout + at + k * next);
+    }
+  }
+  float lse = INFINITY;
+  if ((l & 7) < n) lse = a.lse[row + (l & 7) * step];
+  float mine = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t ow[4] = {o[k].x, o[k].y, o[k].z, o[k].w}, gw[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
     float d = 0.f;
-    if (real) {
-      const size_t at = (((size_t)b * a.s.T + i) * H + h) * D + 8 * l;
-      const uint4 o = *reinterpret_cast<const uint4*>(a.out + at);
-      const uint4 g = *reinterpret_cast<const uint4*>(a.dout + at);
-      const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        d = fmaf(bf16lo(ow[k]), bf16lo(gw[k]), d);
-        d = fmaf(bf16hi(ow[k]), bf16hi(gw[k]), d);
-      }
+    for (int e = 0; e < 4; ++e) {
+      d = fmaf(bf16lo(ow[e]), bf16lo(gw[e]), d);
+      d = fmaf(bf16hi(ow[e]), bf16hi(gw[e]), d);
     }
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (!in || l != 0) continue;
-    if (real) {
-      float* st = stat_row(a, b, i, h);
-      st[0] = -kLog2e * a.lse[((size_t)b * a.s.T + i) * H + h];
-      if (a.pos.q_start[b] + (int64_t)i >= kBlock) st[8] = -d;
-    } else if (a.rpe) {
-      float* st = reinterpret_cast<float*>(
-          a.stat + (((r * G + hr / a.rpe) * (a.rpe >> 3)) + (hh >> 3)) * kStatBytes) + (hh & 7);
-      st[0] = -INFINITY;
-      st[8] = 0.f;
-    } else {
-      float* st = stat_row(a, b, i, h);
-      st[0] = -INFINITY;
-      st[8] = 0.f;
-    }
+    for (int e = LPR / 2; e > 0; e >>= 1) d += __shfl_xor_sync(0xffffffffu, d, e);
+    if ((l & 7) == k) mine = d;
+  }
+  if (in) {
+    float* st = reinterpret_cast<float*>(dst) + (l & 7);
+    // rows of the second kind leave delta alone
+    const int64_t t = (int64_t)a.pos.q_start[b] + i0 + (a.rpe ? 0 : l & 7);
+    if (l < 8) st[0] = -kLog2e * lse;
+    if ((LPR == 8 || l >= 8) && ((l & 7) >= n || t >= kBlock)) st[8] = -mine;
   }
   if (a.rpe && blockIdx.x == 0 && threadIdx.x < 16)
     reinterpret_cast<float*>(a.stat + (size_t)a.groups * kStatBytes)[threadIdx.x] =
@@ -210,6 +232,7 @@ __global__ void __launch_bounds__(32) bwd_lists_kernel(const __grid_constant__ B
     const int il = r0 + lane;
     int id[kTopk];
     chunk_ids(a, b, il, g, !FILL, id);
+    int place[kTopk];
 #pragma unroll
     for (int j = 0; j < kTopk; ++j) {
       if (!FILL) {
@@ -219,12 +242,19 @@ __global__ void __launch_bounds__(32) bwd_lists_kernel(const __grid_constant__ B
         int at = 0;
         if (id[j] >= 0) at = s_cnt[id[j]] + __popc(same & ((1u << lane) - 1));
         __syncwarp();
+        place[j] = id[j] >= 0 ? at : -1;
         if (id[j] >= 0) {
           a.entries[at] = il * kTopk + j;
           if ((same >> lane) == 1) s_cnt[id[j]] = at + 1;   // the last lane of the list
         }
         __syncwarp();
       }
+    }
+    if (FILL && il < a.Tp) {
+      int4* w = reinterpret_cast<int4*>(a.where + (((size_t)b * a.Tp + il) * a.s.G + g) * kTopk);
+#pragma unroll
+      for (int v = 0; v < kTopk / 4; ++v)
+        w[v] = make_int4(place[4 * v], place[4 * v + 1], place[4 * v + 2], place[4 * v + 3]);
     }
   }
   __syncwarp();
@@ -261,7 +291,10 @@ __global__ void __launch_bounds__(128) bwd_prefix_kernel(const __grid_constant__
 
 // ---- units ------------------------------------------------------------------
 // One CTA: every item (g, b, kb) below kv_len as one unit, or as several of at most
-// `piece` tiles, whose sums are joined in their order afterwards.
+// `piece` tiles, whose sums are joined in their order afterwards.  The units are handed
+// out as CTAs become free, so the large ones come first: in each group (its queries'
+// rows stay in L2 meanwhile), or, where a group has little work for each CTA, of all.
+constexpr int kClasses = 64;               // of sizes, the largest first
 __device__ __forceinline__ int item_tiles(const BwdArgs& a, int64_t L, int* n) {
   const int kb = (int)(L % a.nbl), b = (int)(L / a.nbl % a.s.B);
   if ((int64_t)kb * kBlock >= a.pos.kv_len[b]) return -1;
@@ -271,54 +304,81 @@ __device__ __forceinline__ int item_tiles(const BwdArgs& a, int64_t L, int* n) {
   }
   return *n = (a.nqt - bwd_first_tile(a, b, kb)) * a.hpg;
 }
+__device__ __forceinline__ int item_class(const BwdArgs& a, int64_t L, int tiles) {
+  const int g = a.mixed ? 0 : (int)(L / a.nbl / a.s.B);
+  const int size = (int)((int64_t)min(tiles, a.piece) * (kClasses - 1) / a.piece);
+  return g * kClasses + kClasses - 1 - size;
+}
 
 __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__ BwdArgs a) {
-  __shared__ int s_u[1024], s_s[1024], s_e[1024];
+  __shared__ int s_s[1024], s_e[1024];
+  __shared__ int s_class[8 * kClasses];    // units of a class, then the next one's place
   const int64_t n = (int64_t)a.s.G * a.s.B * a.nbl;
   const int64_t per = (n + 1023) / 1024;
   const int64_t lo = min(n, (int64_t)threadIdx.x * per), hi = min(n, lo + per);
-  int u = 0, sl = 0, en = 0;
+  for (int k = threadIdx.x; k < 8 * kClasses; k += 1024) s_class[k] = 0;
+  __syncthreads();
+  int sl = 0, en = 0;
   for (int64_t L = lo; L < hi; ++L) {
     int cnt = 0;
     const int t = item_tiles(a, L, &cnt);
-    if (a.sel) en += a.count[L];
     if (t < 0) continue;
+    en += t * a.R;
     const int pieces = t > a.piece ? (t + a.piece - 1) / a.piece : 1;
-    u += pieces;
+    atomicAdd(&s_class[item_class(a, L, t)], pieces);
     if (pieces > 1) sl += pieces;
   }
-  s_u[threadIdx.x] = u;
   s_s[threadIdx.x] = sl;
   s_e[threadIdx.x] = en;
   __syncthreads();
   for (int d = 1; d < 1024; d <<= 1) {
-    int x = 0, y = 0, z = 0;
+    int y = 0, z = 0;
     if ((int)threadIdx.x >= d) {
-      x = s_u[threadIdx.x - d];
       y = s_s[threadIdx.x - d];
       z = s_e[threadIdx.x - d];
     }
     __syncthreads();
-    s_u[threadIdx.x] += x;
     s_s[threadIdx.x] += y;
     s_e[threadIdx.x] += z;
     __syncthreads();
   }
-  u = s_u[threadIdx.x] - u;
   sl = s_s[threadIdx.x] - sl;
   en = s_e[threadIdx.x] - en;
+  if (threadIdx.x < 32) {                  // exclusive scan of the classes, 16 a lane
+    int v[8 * kClasses / 32], sum = 0;
+    for (int k = 0; k < 8 * kClasses / 32; ++k) {
+      v[k] = s_class[threadIdx.x * (8 * kClasses / 32) + k];
+      sum += v[k];
+    }
+    int x = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if ((int)threadIdx.x >= o) x += y;
+    }
+    if (threadIdx.x == 31) a.n_units[0] = x;
+    x -= sum;
+    for (int k = 0; k < 8 * kClasses / 32; ++k) {
+      s_class[threadIdx.x * (8 * kClasses / 32) + k] = x;
+      x += v[k];
+    }
+  }
+  if (threadIdx.x == 1023) {
+    a.n_units[1] = s_s[1023];
+    a.next_unit[0] = a.next_unit[1] = 0;   // taken units; dense: taken items of dQ
+  }
+  __syncthreads();
   for (int64_t L = lo; L < hi; ++L) {
     int cnt = 0;
     const int t = item_tiles(a, L, &cnt);
-    const int e0 = en;
-    if (a.sel) {
-      a.off[L] = e0;
-      en += a.count[L];
-    }
+    if (a.sel) a.off[L] = en;
     if (t < 0) continue;
+    const int e0 = en;
+    en += t * a.R;
     const int kb = (int)(L % a.nbl), b = (int)(L / a.nbl % a.s.B), g = (int)(L / a.nbl / a.s.B);
     const int x = kb | g << 15 | b << 18;
     const int pieces = t > a.piece ? (t + a.piece - 1) / a.piece : 1;
+    // (the order within a class is the run's own: the units do not depend on one another)
+    int at = atomicAdd(&s_class[item_class(a, L, t)], pieces);
     for (int k = 0; k < pieces; ++k) {
       // pieces of nearly the same size
       const int t0 = (int)((int64_t)t * k / pieces), t1 = (int)((int64_t)t * (k + 1) / pieces);
@@ -331,56 +391,59 @@ __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__
         slot = sl++;
         a.slots[slot] = make_int4(x, k == 0 ? pieces : 0, 0, 0);
       }
-      a.units[u++] = make_int4(x, first, size, slot);
+      a.units[at++] = make_int4(x, first, size, slot);
     }
-  }
-  if (threadIdx.x == 1023) {
-    a.n_units[0] = u;
-    a.n_units[1] = sl;
   }
 }
 
 // ---- joins --------------------------------------------------------------------
-// dQ of a (query, head): its selected blocks' parts, times the scale.  A warp each.
-template <int D>
+// dQ of a (query, group): its selected blocks' parts, times the scale.  A warp each: an
+// entry's rows are rpe x 32 contiguous bytes per 16 dims.
+template <int D, int RPE>
 __global__ void __launch_bounds__(256) bwd_join_q_kernel(const __grid_constant__ BwdArgs a) {
-  constexpr int PER = D / 32;
+  constexpr int PER = 16 / RPE;                  // 16-dim chunks that a warp's read covers
+  constexpr int N = D / 16 / PER;
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, H = a.s.H;
-  if (w >= (int64_t)a.s.B * a.Tp * H) return;
-  const int h = (int)(w % H), g = h / a.hpg;
-  const int64_t r = w / H;
+  const int lane = threadIdx.x & 31;
+  if (w >= (int64_t)a.s.B * a.Tp * a.s.G) return;
+  const int g = (int)(w % a.s.G);
+  const int64_t r = w / a.s.G;
   const int b = (int)(r / a.Tp), i = a.t0 + (int)(r % a.Tp);
-  const int lb = (int)(((int64_t)a.pos.q_start[b] + i) / kBlock);
-  bool ok = false;
-  if (lane < kTopk) {
-    const int kb = a.sel[(((size_t)b * a.s.T + i) * a.s.G + g) * kTopk + lane];
-    ok = kb >= 0 && kb <= lb;
-  }
-  const uint32_t m = __ballot_sync(0xffffffffu, ok);
-  float acc[PER];
+  const int hh = (lane >> 1) % RPE, ch0 = (lane >> 1) / RPE, d0 = (lane & 1) * 8;
+  int e = -1;
+  if (lane < kTopk) e = a.where[w * kTopk + lane];
+  float acc[N][8];
 #pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  const uint16_t* src = a.part_dq + (size_t)w * kTopk * D + lane * PER;
+  for (int k = 0; k < N; ++k)
 #pragma unroll
+    for (int x = 0; x < 8; ++x) acc[k][x] = 0.f;
+#pragma unroll 2
   for (int j = 0; j < kTopk; ++j) {
-    if (!(m >> j & 1)) continue;
-    if constexpr (PER == 4) {
-      const uint2 u = __ldcs(reinterpret_cast<const uint2*>(src + j * D));
-      acc[0] += bf16lo(u.x);
-      acc[1] += bf16hi(u.x);
-      acc[2] += bf16lo(u.y);
-      acc[3] += bf16hi(u.y);
-    } else {
-      const uint32_t u = __ldcs(reinterpret_cast<const unsigned int*>(src + j * D));
-      acc[0] += bf16lo(u);
-      acc[1] += bf16hi(u);
+    const int ej = __shfl_sync(0xffffffffu, e, j);
+    if (ej < 0 || hh >= a.hpg) continue;
+    const uint16_t* src = a.part_dq +
+                          ((size_t)(ej / a.R) * (D / 16) + ch0) * 2048 + ((ej % a.R) * RPE + hh) * 16 + d0;
+    uint4 v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __ldcs(reinterpret_cast<const uint4*>(src + k * PER * 2048));
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        acc[k][2 * x] += bf16lo(u[x]);
+        acc[k][2 * x + 1] += bf16hi(u[x]);
+      }
     }
   }
-  uint16_t* dst = a.dq + (((size_t)b * a.s.T + i) * H + h) * D + lane * PER;
+  if (hh >= a.hpg) return;
+  const float f = a.s.scale;
+  uint16_t* dst = a.dq + (((size_t)b * a.s.T + i) * a.s.H + g * a.hpg + hh) * D + ch0 * 16 + d0;
 #pragma unroll
-  for (int e = 0; e < PER; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * a.s.scale, acc[e + 1] * a.s.scale);
+  for (int k = 0; k < N; ++k)
+    *reinterpret_cast<uint4*>(dst + k * PER * 16) =
+        make_uint4(pack_bf16(acc[k][0] * f, acc[k][1] * f), pack_bf16(acc[k][2] * f, acc[k][3] * f),
+                   pack_bf16(acc[k][4] * f, acc[k][5] * f), pack_bf16(acc[k][6] * f, acc[k][7] * f));
 }
 
 // dK, dV of a block in several pieces: CTA (slot, part of the rows); the first slot's
@@ -395,7 +458,8 @@ __global__ void __launch_bounds__(256) bwd_join_kv_kernel(const __grid_constant_
   const int kb = d.x & 0x7FFF, g = d.x >> 15 & 7, b = d.x >> 18;
   constexpr int ROWS = 2 * kBlock / kJoinParts, C4 = D / 4;
   for (int e = threadIdx.x; e < ROWS * C4; e += 256) {
-    const int row = blockIdx.y * ROWS + e / C4, c = e % C4 * 4;     // dv's 128 rows, then dk's
+    // dv's 128 rows, then dk's
+    const int row = blockIdx.y * ROWS + e / 2 % ROWS, c = (e / 2 / ROWS * 2 + e % 2) * 4;
     const int tok = row % kBlock;
     const bool is_k = row >= kBlock;
     if ((int64_t)kb * kBlock + tok >= a.pos.kv_len[b]) continue;
@@ -403,7 +467,7 @@ __global__ void __launch_bounds__(256) bwd_join_kv_kernel(const __grid_constant_
 #pragma unroll 4
     for (int k = 0; k < d.y; ++k) {
       const float4 y = __ldcs(reinterpret_cast<const float4*>(
-          a.part_kv + ((size_t)(slot + k) * 2 * kBlock + row) * D + c));
+          a.part_kv + ((((size_t)(slot + k) * 2 + is_k) * (D / 8) + c / 8) * kBlock + tok) * 8 + c % 8));
       x.x += y.x;
       x.y += y.y;
       x.z += y.z;
@@ -434,10 +498,9 @@ __global__ void __launch_bounds__(256) bwd_join_kv_kernel(const __grid_constant_
 cudaError_t launch_bwd_stats(const Shape& s, const Positions& pos, const AttnBwd& t, int rpe,
                              uint8_t* stat, uint32_t stat_groups, cudaStream_t st) {
   StatArgs a{s, pos, t.q, t.k, t.v, t.out, t.dout, t.lse, stat, stat_groups, rpe, 0};
-  const int lpr = s.D / 8, per_cta = kStatThreads / lpr;
-  const int64_t rows = (int64_t)s.B * (rpe ? (int64_t)s.T * s.G * rpe : (int64_t)stat_groups * 8 * s.H);
-  const int64_t ctas = (rows + per_cta - 1) / per_cta;
-  a.row_ctas = (int)(ctas < 8 * kBwdSms ? ctas : 8 * kBwdSms);
+  const int per_cta = kStatThreads / (s.D / 8);
+  const int64_t grps = rpe ? (int64_t)stat_groups : (int64_t)s.B * stat_groups * s.H;
+  a.row_ctas = (int)((grps + per_cta - 1) / per_cta);
   bool early = false;
   for (int b = 0; b < s.B; ++b) early |= pos.q_start[b] < kBlock;
   const int64_t tasks = early ? (int64_t)s.B * s.H * 8 : 0;   // a warp each
@@ -473,10 +536,15 @@ cudaError_t launch_bwd_units(const BwdArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_bwd_join_q(const BwdArgs& a, cudaStream_t st) {
-  const unsigned ctas = (unsigned)(((int64_t)a.s.B * a.Tp * a.s.H + 7) / 8);
+  const unsigned ctas = (unsigned)(((int64_t)a.s.B * a.Tp * a.s.G + 7) / 8);
   note_launches(1);
-  if (a.s.D == 128) bwd_join_q_kernel<128><<<ctas, 256, 0, st>>>(a);
-  else bwd_join_q_kernel<64><<<ctas, 256, 0, st>>>(a);
+  if (a.s.D == 128) {
+    if (a.rpe == 8) bwd_join_q_kernel<128, 8><<<ctas, 256, 0, st>>>(a);
+    else bwd_join_q_kernel<128, 16><<<ctas, 256, 0, st>>>(a);
+  } else {
+    if (a.rpe == 8) bwd_join_q_kernel<64, 8><<<ctas, 256, 0, st>>>(a);
+    else bwd_join_q_kernel<64, 16><<<ctas, 256, 0, st>>>(a);
+  }
   return cudaGetLastError();
 }
 

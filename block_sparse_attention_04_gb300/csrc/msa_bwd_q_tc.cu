@@ -7,8 +7,9 @@
 // last product; K is read K-major by the first product and MN-major by the last.
 //   warp 0       TMA of the item's Q and dO; takes the items from a shared counter
 //   warp 1       TMA of K (3 stages: a block is read until its dQ product) and V (2)
-//   warp 2       tcgen05.mma: dP(n+1), dQ(n), S(n+2), with S in two buffers
-//   warps 3-10   dS: two warpgroups, 64 keys of a block each; an item's dQ
+//   warp 2       tcgen05.mma of dQ and S, S in two buffers
+//   warp 3       tcgen05.mma of dP
+//   warps 4-19   dS: four warpgroups, 32 keys of a block each; an item's dQ
 // The two numbers of a row (lse, delta) stay in registers over an item.
 #include "msa_bwd.h"
 #include "msa_q8.cuh"
@@ -17,14 +18,18 @@
 namespace msa {
 namespace {
 
-constexpr int kMmaW = 2, kSoftW = 3, kThreadsQ = 32 * 11;
-constexpr int kKS = 3, kVS = 2, kRing = 4, kReaders = 10;
+constexpr int kAW = 2, kBW = 3, kSoftW = 4;   // warps: MMA of S and dQ, of dP; dS
+constexpr int kNG = 4;                    // warpgroups for dS ...
+constexpr int kCols = 128 / kNG;          // ... and the keys of a block that each has
+constexpr int kThreadsQ = 32 * (kSoftW + 4 * kNG);
+constexpr int kRing = 4, kReaders = 3 + 4 * kNG;
 
 template <int D>
 struct QCfg {
   static constexpr int kNHalf = D / 64;
   static constexpr int kHalf = 128 * 128;
   static constexpr int kTile = kNHalf * kHalf;
+  static constexpr int kKS = 3, kVS = 2;             // stages of K and V
   static constexpr int kSmem = (2 + kKS + kVS) * kTile + 512;
   // tensor memory columns: S in two buffers, dP, dQ
   static constexpr uint32_t kS = 0, kP = 256, kDQ = 384;
@@ -62,17 +67,19 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   uint8_t* sQ = smem;
   uint8_t* sO = sQ + C::kTile;
   uint8_t* sK = sO + C::kTile;                     // [kKS]
-  uint8_t* sV = sK + kKS * C::kTile;               // [kVS]
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(sV + kVS * C::kTile);
+  uint8_t* sV = sK + C::kKS * C::kTile;            // [kVS]
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sV + C::kVS * C::kTile);
   uint64_t* q_empty = q_full + 1;
   uint64_t* k_full = q_empty + 1;                  // [kKS]
-  uint64_t* k_empty = k_full + kKS;
-  uint64_t* v_full = k_empty + kKS;                // [kVS]
-  uint64_t* v_empty = v_full + kVS;
-  uint64_t* s_full = v_empty + kVS;                // [2] S of the block is in its buffer
+  uint64_t* k_empty = k_full + C::kKS;
+  uint64_t* v_full = k_empty + C::kKS;             // [kVS]
+  uint64_t* v_empty = v_full + C::kVS;
+  uint64_t* s_full = v_empty + C::kVS;                // [2] S of the block is in its buffer
   uint64_t* dp_full = s_full + 2;
-  uint64_t* ds_full = dp_full + 1;                 // dS written over S
-  uint64_t* acc_full = ds_full + 1;                // the item's dQ is complete
+  // [2] dS written over S: one per buffer, as the warp that waits for both (dQ) may fall
+  // behind the one that lets the next dS be made (dP)
+  uint64_t* ds_full = dp_full + 1;
+  uint64_t* acc_full = ds_full + 2;                // the item's dQ is complete
   uint64_t* acc_empty = acc_full + 1;              // ... and read out
   uint64_t* bar_fin = acc_empty + 1;
   uint64_t* it_full = bar_fin + 1;                 // [kRing]
@@ -84,22 +91,23 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    for (int i = 0; i < kKS; ++i) {
+    mbar_init(q_empty, 2);
+    for (int i = 0; i < C::kKS; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
     }
-    for (int i = 0; i < kVS; ++i) {
+    for (int i = 0; i < C::kVS; ++i) {
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 256);
+    mbar_init(&ds_full[0], 128 * kNG);
+    mbar_init(&ds_full[1], 128 * kNG);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 256);
-    mbar_init(bar_fin, 1);
+    mbar_init(acc_empty, 128 * kNG);
+    mbar_init(bar_fin, 2);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&it_full[i], 1);
       mbar_init(&it_empty[i], kReaders);
@@ -111,7 +119,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (warp == kMmaW) tmem_alloc(tmem_slot, 512);
+  if (warp == kAW) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -185,10 +193,10 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     while (next_item(it, ok)) {
       const QItem d = q_item(a, it);
       for (int kb = d.kb0; kb < d.kb1; ++kb, ++n) {
-        const int ks = n % kKS, vs = n % kVS;
+        const int ks = n % C::kKS, vs = n % C::kVS;
         const int row = (int)(((int64_t)d.b * a.s.max_blocks + kb) * kBlock);
         ok = __any_sync(0xffffffffu, *abort_flag != 0) == 0 &&
-             wait_all(&k_empty[ks], ((n / kKS) & 1) ^ 1);
+             wait_all(&k_empty[ks], ((n / C::kKS) & 1) ^ 1);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&k_full[ks], C::kTile);
@@ -198,7 +206,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
                         row);
         }
         __syncwarp();
-        ok = wait_all(&v_empty[vs], ((n / kVS) & 1) ^ 1);
+        ok = wait_all(&v_empty[vs], ((n / C::kVS) & 1) ^ 1);
         if (!ok) {
           k_only = true;
           break;
@@ -216,12 +224,14 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     }
     if (!ok && lane == 0) *abort_flag = 1;
     const int nk = k_only ? n + 1 : n;
-    for (int m = nk - 1; m >= 0 && m >= nk - kKS; --m)
-      mbar_wait(&k_full[m % kKS], (uint32_t)(m / kKS) & 1, nullptr);
-    for (int m = n - 1; m >= 0 && m >= n - kVS; --m)
-      mbar_wait(&v_full[m % kVS], (uint32_t)(m / kVS) & 1, nullptr);
-  } else if (warp == kMmaW) {
-    // ---------------------------------------------------------- MMA (warp 2)
+    for (int m = nk - 1; m >= 0 && m >= nk - C::kKS; --m)
+      mbar_wait(&k_full[m % C::kKS], (uint32_t)(m / C::kKS) & 1, nullptr);
+    for (int m = n - 1; m >= 0 && m >= n - C::kVS; --m)
+      mbar_wait(&v_full[m % C::kVS], (uint32_t)(m / C::kVS) & 1, nullptr);
+  } else if (warp == kAW || warp == kBW) {
+    // ------------------------------------------------------- MMA (warps 2, 3)
+    // Two warps, as issuing takes longer than the products: with one for all three a step
+    // took 2650 cycles, 1536 of them MMAs.
     constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
     constexpr uint32_t idesc_q = idesc_bf16(128, D, false, true);
     const uint64_t qd = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
@@ -238,82 +248,99 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     };
     int it, n = 0, nu = 0;       // blocks and items (with blocks) so far
     bool ok;
-    while (next_item(it, ok)) {
-      const QItem d = q_item(a, it);
-      const int nt = d.kb1 - d.kb0;
-      if (nt == 0) continue;
-      const int64_t t_last = (int64_t)a.pos.q_start[d.b] + T - 1;
-      ok = wait_all(q_full, (uint32_t)nu & 1);
-      if (!ok) break;
-      auto issue_s = [&](int m, int kb) {
-        const int ks = m % kKS;
-        if (!wait_all(&k_full[ks], (uint32_t)(m / kKS) & 1)) return false;
-        const int64_t left = t_last - (int64_t)kb * kBlock;
-        if (left < kBlock - 1) {
-          // rows behind the sequence's last query may hold anything; in dQ's product
-          // they are multiplied by zeros: cleared
-          for (int e = lane; e < C::kNHalf * kBlock * 8; e += 32) {
-            const int row = e >> 3 & 127;
-            if (row > (int)left)
-              sts128(smem_u32(sK) + ks * C::kTile + (e >> 10) * C::kHalf + row * 128 + (e & 7) * 16,
-                     make_uint4(0, 0, 0, 0));
+    if (warp == kAW) {
+      // ---------------------------------------- S(0), S(1); dQ(n), S(n + 2)
+      while (next_item(it, ok)) {
+        const QItem d = q_item(a, it);
+        const int nt = d.kb1 - d.kb0;
+        if (nt == 0) continue;
+        const int64_t t_last = (int64_t)a.pos.q_start[d.b] + T - 1;
+        ok = wait_all(q_full, (uint32_t)nu & 1);
+        if (!ok) break;
+        auto issue_s = [&](int m, int t) {         // of block m, the item's t-th
+          const int ks = m % C::kKS;
+          if (!wait_all(&k_full[ks], (uint32_t)(m / C::kKS) & 1)) return false;
+          const int64_t left = t_last - (int64_t)(d.kb0 + t) * kBlock;
+          if (left < kBlock - 1) {
+            // rows behind the sequence's last query may hold anything; in dQ's product
+            // they are multiplied by zeros: cleared
+            for (int e = lane; e < C::kNHalf * kBlock * 8; e += 32) {
+              const int row = e >> 3 & 127;
+              if (row > (int)left)
+                sts128(smem_u32(sK) + ks * C::kTile + (e >> 10) * C::kHalf + row * 128 + (e & 7) * 16,
+                       make_uint4(0, 0, 0, 0));
+            }
+            fence_async();
+            __syncwarp();
           }
-          fence_async();
+          tc_fence_after();
+          if (elect_one()) {
+            product(C::kS + (m & 1) * 128, qd, kd + (uint64_t)((ks * C::kTile) >> 4));
+            tc_commit(&s_full[m & 1]);
+            if (t + 1 == nt) tc_commit(q_empty);
+          }
+          __syncwarp();
+          return true;
+        };
+        ok = issue_s(n, 0) && (nt == 1 || issue_s(n + 1, 1));
+        for (int t = 0; t < nt && ok; ++t, ++n) {
+          const int ks = n % C::kKS;
+          ok = wait_all(&ds_full[n & 1], (uint32_t)(n >> 1) & 1) &&
+               (t > 0 || nu == 0 || wait_all(acc_empty, (uint32_t)(nu - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            // dS: a warpgroup's keys at the start of its columns of S, two in each
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              tc_mma_f16_ts(tmem + C::kDQ,
+                            tmem + C::kS + (n & 1) * 128 + j * 16 / kCols * kCols + j * 16 % kCols / 2,
+                            kmn + (uint64_t)((ks * C::kTile + j * 2048) >> 4), idesc_q,
+                            t > 0 || j > 0 ? 1u : 0u);
+            tc_commit(&k_empty[ks]);
+            if (t + 1 == nt) tc_commit(acc_full);
+          }
+          __syncwarp();
+          // over dS(n), which dQ(n), issued before, reads
+          if (t + 2 < nt) ok = issue_s(n + 2, t + 2);
+        }
+        if (!ok) break;
+        ++nu;
+      }
+    } else {
+      // ------------------------------------------------------------ dP(n)
+      while (next_item(it, ok)) {
+        const QItem d = q_item(a, it);
+        const int nt = d.kb1 - d.kb0;
+        if (nt == 0) continue;
+        ok = wait_all(q_full, (uint32_t)nu & 1);
+        for (int t = 0; t < nt && ok; ++t, ++n) {
+          const int vs = n % C::kVS;
+          // dP(n - 1) has been read
+          ok = wait_all(&v_full[vs], (uint32_t)(n / C::kVS) & 1) &&
+               (n == 0 || wait_all(&ds_full[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            product(C::kP, od, vd + (uint64_t)((vs * C::kTile) >> 4));
+            tc_commit(dp_full);
+            tc_commit(&v_empty[vs]);
+            if (t + 1 == nt) tc_commit(q_empty);
+          }
           __syncwarp();
         }
-        tc_fence_after();
-        if (elect_one()) {
-          product(C::kS + (m & 1) * 128, qd, kd + (uint64_t)((ks * C::kTile) >> 4));
-          tc_commit(&s_full[m & 1]);
-        }
-        __syncwarp();
-        return true;
-      };
-      auto issue_dp = [&](int m, bool last) {
-        const int vs = m % kVS;
-        if (!wait_all(&v_full[vs], (uint32_t)(m / kVS) & 1)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          product(C::kP, od, vd + (uint64_t)((vs * C::kTile) >> 4));
-          tc_commit(dp_full);
-          tc_commit(&v_empty[vs]);
-          if (last) tc_commit(q_empty);     // every S of the item was issued before
-        }
-        __syncwarp();
-        return true;
-      };
-      ok = issue_s(n, d.kb0) && (nt == 1 || issue_s(n + 1, d.kb0 + 1)) && issue_dp(n, nt == 1);
-      for (int t = 0; t < nt && ok; ++t, ++n) {
-        ok = wait_all(ds_full, (uint32_t)n & 1);
-        if (ok && t + 1 < nt) ok = issue_dp(n + 1, t + 2 == nt);
-        if (ok && t == 0 && nu > 0) ok = wait_all(acc_empty, (uint32_t)(nu - 1) & 1);
         if (!ok) break;
-        tc_fence_after();
-        const int ks = n % kKS;
-        if (elect_one()) {
-          // dS: 64 keys of each warpgroup in 32 columns, at the start of its half of S
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            tc_mma_f16_ts(tmem + C::kDQ, tmem + C::kS + (n & 1) * 128 + (j >> 2) * 64 + (j & 3) * 8,
-                          kmn + (uint64_t)((ks * C::kTile + j * 2048) >> 4), idesc_q,
-                          t > 0 || j > 0 ? 1u : 0u);
-          tc_commit(&k_empty[ks]);
-          if (t + 1 == nt) tc_commit(acc_full);
-        }
-        __syncwarp();
-        if (t + 2 < nt) ok = issue_s(n + 2, d.kb0 + t + 2);
+        ++nu;
       }
-      if (!ok) break;
-      ++nu;
     }
     if (!ok && lane == 0) *abort_flag = 1;
-    // all MMAs done before tensor memory is released
+    // all MMAs of both warps done before tensor memory is released
     if (elect_one()) tc_commit(bar_fin);
     __syncwarp();
     mbar_wait(bar_fin, 0, nullptr);
   } else {
-    // ------------------------------------------------- dS, dQ (warps 3-10)
-    const int c = (warp - kSoftW) >> 2;           // keys 64 c ..; dims c D/2 .. of dQ
+    // ------------------------------------------------- dS, dQ (warps 4-19)
+    const int c = (warp - kSoftW) >> 2;           // keys kCols c ..; dims c D/kNG .. of dQ
     const int quad = warp & 3;
     const int r = quad * 32 + lane;               // query of the tile = TMEM lane
     const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16);
@@ -333,55 +360,49 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       for (int kb = d.kb0; kb < d.kb1; ++kb, ++n) {
         // keys past the query, and rows past the last query, whatever they hold
         const int64_t l64 = min(tq, (int64_t)a.pos.q_start[d.b] + T - 1) - (int64_t)kb * kBlock;
-        const int lim = (int)(l64 < kBlock ? l64 : kBlock) - c * 64;
-        const bool masked = __any_sync(0xffffffffu, lim < 63);
+        const int lim = (int)(l64 < kBlock ? l64 : kBlock) - c * kCols;
+        const bool masked = __any_sync(0xffffffffu, lim < kCols - 1);
         ok = __all_sync(0xffffffffu,
                         *abort_flag == 0 &&
                             mbar_wait(&s_full[n & 1], (uint32_t)(n >> 1) & 1, a.status, a.wait_polls));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t s_at = base + C::kS + (n & 1) * 128 + c * 64;
-        float2 p[32];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        const uint32_t s_at = base + C::kS + (n & 1) * 128 + c * kCols;
+        float2 p[kCols / 2];
+        {
           uint32_t x[32];
-          tmem_ld32(s_at + hf * 32, x);
+          tmem_ld32(s_at, x);
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = ffma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
                                    sl2, nl2);
-            p[hf * 16 + e] = make_float2(ex2(y.x), ex2(y.y));
+            p[e] = make_float2(ex2(y.x), ex2(y.y));
           }
         }
         ok = __all_sync(0xffffffffu, mbar_wait(dp_full, (uint32_t)n & 1, a.status, a.wait_polls));
         if (!ok) break;
         tc_fence_after();
+        uint32_t x[32], w[16];
+        tmem_ld32(base + C::kP + c * kCols, x);
+        tmem_ld_wait();
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t x[32];
-          tmem_ld32(base + C::kP + c * 64 + hf * 32, x);
-          tmem_ld_wait();
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 y = fadd2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), nd2);
-            y = fmul2(p[hf * 16 + e], y);
-            if (masked) {
-              const int col = hf * 32 + 2 * e;
-              y.x = col <= lim ? y.x : 0.f;
-              y.y = col + 1 <= lim ? y.y : 0.f;
-            }
-            w[e] = pack_bf16(y.x, y.y);
+        for (int e = 0; e < 16; ++e) {
+          float2 y = fadd2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), nd2);
+          y = fmul2(p[e], y);
+          if (masked) {
+            y.x = 2 * e <= lim ? y.x : 0.f;
+            y.y = 2 * e + 1 <= lim ? y.y : 0.f;
           }
-          tmem_st16(s_at + hf * 16, w);     // over scores that were read already
+          w[e] = pack_bf16(y.x, y.y);
         }
+        tmem_st16(s_at, w);              // over scores that were read already
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(ds_full);
+        mbar_arrive(&ds_full[n & 1]);
       }
       if (!ok) break;
-      // ---- the item's dQ: half of a query's dims per thread
+      // ---- the item's dQ: a query per thread, a run of dims per warpgroup
       const bool any = d.kb0 < d.kb1;
       if (any) {
         ok = __all_sync(0xffffffffu, mbar_wait(acc_full, (uint32_t)nu & 1, a.status, a.wait_polls));
@@ -389,9 +410,9 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         tc_fence_after();
       }
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
+      for (int cc = 0; cc < D / kNG / 16; ++cc) {
         uint32_t x[16];
-        const int dim = c * (D / 2) + cc * 16;
+        const int dim = c * (D / kNG) + cc * 16;
         if (any) {
           tmem_ld16(base + C::kDQ + dim, x);
           tmem_ld_wait();
@@ -432,7 +453,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaW) {
+  if (warp == kAW) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
