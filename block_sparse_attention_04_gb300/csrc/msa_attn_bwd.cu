@@ -62,7 +62,7 @@ constexpr int kMaxQParts = 4 * kBwdSms;
 int q_items(const Shape& s) { return (s.T + 127) / 128 * s.B * s.H; }
 
 struct Layout {
-  size_t stat, cnt, count, off, entries, where, units, slots, part_dq, part_kv, acc, part_q, total;
+  size_t stat, aug, cnt, count, off, entries, where, units, slots, part_dq, part_kv, acc, part_q, total;
   uint32_t stat_groups;
   int chunks;
 };
@@ -94,6 +94,7 @@ Layout layout(const Shape& s, bool sparse) {
   } else {
     L.stat_groups = (uint32_t)((s.T + 127) / 128 * 16);
     L.stat = take((size_t)s.B * s.H * L.stat_groups * kStatBytes);
+    L.aug = take((size_t)s.B * s.H * L.stat_groups * kAugBytes);
     const int items = q_items(s);
     if (items < kMaxQParts) L.part_q = take((size_t)kMaxQParts * 128 * s.D * sizeof(float));
   }
@@ -122,7 +123,10 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
   a.sel = t.sel;
   a.n_units = reinterpret_cast<int*>(base);
   a.next_unit = a.n_units + 2;
-  a.stat = reinterpret_cast<uint8_t*>(base + L.stat);
+  uint8_t* const stat = reinterpret_cast<uint8_t*>(base + L.stat);
+  uint8_t* const aug = sparse ? nullptr : reinterpret_cast<uint8_t*>(base + L.aug);
+  a.stat = sparse ? stat : aug;
+  a.no_scores = bwd_no_scores(s);
   a.stat_groups = L.stat_groups;
   a.chunks = L.chunks;
   a.cnt = reinterpret_cast<int32_t*>(base + L.cnt);
@@ -144,8 +148,8 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
   for (int b = 0; b < s.B; ++b) max_len = pos.kv_len[b] > max_len ? pos.kv_len[b] : max_len;
   a.nbl = (max_len + kBlock - 1) / kBlock;
   cudaError_t e;
-  if ((e = launch_bwd_stats(s, pos, t, sparse ? a.rpe : 0, reinterpret_cast<uint8_t*>(base + L.stat),
-                            L.stat_groups, st)) != cudaSuccess)
+  if ((e = launch_bwd_stats(s, pos, t, sparse ? a.rpe : 0, stat, aug, L.stat_groups, st)) !=
+      cudaSuccess)
     return e;
   const int tp = sparse ? pass_len(s) : s.T;
   for (int t0 = 0; t0 < s.T; t0 += tp) {
@@ -182,7 +186,7 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
     if (q.splits < 1) q.splits = 1;
   }
   q.next_item = a.n_units + 3;
-  q.stat = a.stat;
+  q.stat = stat;
   q.stat_groups = L.stat_groups;
   q.part = reinterpret_cast<float*>(base + L.part_q);
   q.dq = t.dq;

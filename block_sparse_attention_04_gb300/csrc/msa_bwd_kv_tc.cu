@@ -15,16 +15,23 @@
 // in tensor memory; Q and dO, MN-major, their B operands from the tiles that the first
 // two products read K-major.  Sparse, dS^T goes to shared memory instead, whose
 // [token][row] order is dK's A operand K-major and that of dQ's part MN-major.
-//   warp 0       TMA of Q and dO (five tiles ahead or in use; sparse four), bulk copies
-//                of the rows' statistics; takes the units from a shared counter
+//   warp 0       TMA of Q and dO (four tiles in use or ahead), bulk copies of the rows'
+//                statistics; takes the units from a shared counter
 //   warp 1       TMA of the unit's K and V
-//   warp 2       tcgen05.mma of S and dV
-//   warp 3       tcgen05.mma of dP and dK (and dQ's part)
+//   warp 2       tcgen05.mma; sparse: of S and dV
+//   warp 3       sparse: tcgen05.mma of dP, dK and dQ's part
 //   warps 4-19   P and dS: four warpgroups, 32 columns of a tile each; a unit's dV, dK
 //   warps 20-23  sparse: dQ's parts, bf16, one row of 16 slots x D per (query, head)
 // dS(n) is worked out during dV(n) and S(n+1), P(n+1) during dK(n) and dP(n+1).  Sparse,
 // D = 128: tensor memory holds S, dP, dV and dK (512 columns), so dQ's part takes dP's
 // columns until it has been read out, during dV(n+1) and S(n+2).
+//
+// Shared memory's 128 bytes a cycle are the bound: of a dense tile at D = 128 the
+// products read 192 KB (both operands of S and dP, one of dV and dK), the copies write
+// 64, and a thread per token would read every row's two numbers, 1 KB a warp, whose way to
+// the registers costs as much as 104 KB.  So the dense tiles' numbers come in through the
+// products: a 17th step of S and of dP multiplies ones with them, as three bf16 parts.
+// (4 x 2048 tokens, 48/8 heads: 347 us before.)  A sparse tile has no room left for them.
 #include "msa_bwd.h"
 #include "msa_q8.cuh"
 #include "msa_tma.h"
@@ -40,28 +47,28 @@ template <bool SP>
 constexpr int kv_threads() { return 32 * (kOutW + (SP ? 4 : 0)); }
 constexpr int kRing = 4;                  // unit numbers published by warp 0, ahead of use
 template <bool SP>
-constexpr int ring_readers() { return 3 + 4 * kNG + (SP ? 4 : 0); }
+constexpr int ring_readers() { return 2 + 4 * kNG + (SP ? 5 : 0); }
 
 template <int D, bool SP>
 struct KvCfg {
   static constexpr int kNHalf = D / 64;
   static constexpr int kHalf = 128 * 128;            // 128 rows x 64 dims
   static constexpr int kTile = kNHalf * kHalf;       // K, V, a Q or a dO tile
-  static constexpr int kTiles = SP ? 4 : 5;          // Q and dO tiles in shared memory
+  static constexpr int kTiles = 4;                   // Q and dO tiles in shared memory
   static constexpr int kSS = 2;                      // statistics of tiles
-  static constexpr int kStat = 16 * kStatBytes;      // statistics of a tile
+  static constexpr int kGroupStat = SP ? kStatBytes : kAugBytes;
+  static constexpr int kStat = 16 * kGroupStat;      // statistics of a tile
+  static constexpr int kOnes = SP ? 0 : 2 * kStat;   // dense: their selectors, A operands
   static constexpr int kDs = SP ? 2 * kHalf : 0;     // dS^T [2 x 64 rows][128 tokens]
   static constexpr int kBars = (2 * (kTiles + kSS) + 12 + 2 * kRing) * 8 + kRing * 4 + 8;
   static constexpr int kSmem =
-      (2 + kTiles) * kTile + kDs + kSS * (kStat + 80) + kBars;
+      (2 + kTiles) * kTile + kDs + kOnes + kSS * (kStat + 80) + kBars;
   // Slots of tile n's Q and dO, and the number of times that they were filled before.
-  // Dense: three for Q (held from S(n), a tile ahead, to dK(n)) and two for dO (dP(n) to
-  // dV(n)).  Sparse: dO(n) is free after dP(n), Q(n) after dK(n), and what comes next,
-  // Q(n+2) and dO(n+2), goes into them in that order.
-  __device__ static int q_slot(int n) { return SP ? 2 * (n & 1) + (n >> 1 & 1) : n % 3; }
-  __device__ static int o_slot(int n) { return SP ? 2 * (n & 1) + (~n >> 1 & 1) : 3 + (n & 1); }
-  __device__ static uint32_t q_use(int n) { return (uint32_t)(SP ? n >> 1 : n / 3); }
-  __device__ static uint32_t o_use(int n) { return (uint32_t)(n >> 1); }
+  // dO(n) is free first (after dV(n); sparse dP(n)), Q(n) after dK(n), and what comes
+  // next, Q(n+2) and dO(n+2), goes into them in that order.
+  __device__ static int q_slot(int n) { return 2 * (n & 1) + (n >> 1 & 1); }
+  __device__ static int o_slot(int n) { return 2 * (n & 1) + (~n >> 1 & 1); }
+  __device__ static uint32_t use(int n) { return (uint32_t)(n >> 1); }
   // byte offsets of a tile of rows: sparse tiles hold 8-row groups, half after half
   static constexpr int kGroup = SP ? kNHalf * 1024 : 1024;   // next 8 rows
   static constexpr int kNext = SP ? 1024 : kHalf;            // next 64 dims
@@ -113,7 +120,8 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
   uint8_t* sV = sK + C::kTile;
   uint8_t* sT = sV + C::kTile;                     // [kTiles] Q and dO
   uint8_t* sDs = sT + C::kTiles * C::kTile;
-  uint8_t* sStat = sDs + C::kDs;                   // [kSS] statistics
+  uint8_t* sOnes = sDs + C::kDs;                   // dense: selectors of lse and of delta
+  uint8_t* sStat = sOnes + C::kOnes;               // [kSS] statistics
   // [kSS] per 8-row group of a sparse tile: the last token of the block that its query
   // sees (-1: none), then whether any of them is below 127
   int* sLim = reinterpret_cast<int*>(sStat + C::kSS * C::kStat);
@@ -144,26 +152,24 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kTiles; ++i) {
       mbar_init(&t_full[i], 1);
-      // dO: both MMA warps are done with it; Q: the second one (its dK follows S).  A
-      // sparse slot holds either in turn: Q is given back twice
-      mbar_init(&t_empty[i], SP || i >= 3 ? 2 : 1);
+      mbar_init(&t_empty[i], SP ? 2 : 1);    // sparse: both MMA warps are done with it
     }
     for (int i = 0; i < C::kSS; ++i) {
       mbar_init(&st_full[i], 1);
       mbar_init(&st_empty[i], 1);
     }
     mbar_init(kv_full, 1);
-    mbar_init(kv_empty, 2);
+    mbar_init(kv_empty, SP ? 2 : 1);
     mbar_init(s_full, 1);
     mbar_init(&dp_full[0], 1);
     mbar_init(&dp_full[1], 1);
     mbar_init(p_full, 128 * kNG);
     mbar_init(ds_full, 128 * kNG);
-    mbar_init(acc_full, 2);
+    mbar_init(acc_full, SP ? 2 : 1);
     mbar_init(acc_empty, 128 * kNG);
     mbar_init(dq_full, 1);
     mbar_init(dq_empty, 128);
-    mbar_init(bar_fin, 2);
+    mbar_init(bar_fin, SP ? 2 : 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&it_full[i], 1);
       mbar_init(&it_empty[i], ring_readers<SP>());
@@ -174,6 +180,17 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     tma_prefetch_desc(&tm_o);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
+  }
+  if constexpr (!SP) {
+    // Rows of 16 bf16, K-major without a swizzle: [8 rows][8], then [8 rows][8].  The
+    // statistics' rows hold -lse in three parts at 0..2 and -delta at 8..10 (see
+    // msa_bwd.h): products with ones at those places and zeros elsewhere add them
+    for (int e = threadIdx.x; e < C::kOnes / 16; e += blockDim.x) {
+      const int sel = e / (C::kStat / 16), core = e >> 3 & 1;   // of lse or delta; dims 0.. or 8..
+      const uint32_t one = sel == core ? 0x3F80u : 0u;
+      sts128(smem_u32(sOnes) + e * 16, make_uint4(one | one << 16, one, 0, 0));
+    }
+    fence_async();
   }
   if (warp == kAW) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
@@ -271,10 +288,10 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           }
         };
         ok = __any_sync(0xffffffffu, *abort_flag != 0) == 0 &&
-             wait_all(&t_empty[qs], (C::q_use(n) & 1) ^ 1);
+             wait_all(&t_empty[qs], (C::use(n) & 1) ^ 1);
         if (!ok) break;
         load_tile(dq_, &tm_q, &t_full[qs]);
-        if (lane == qs) last = (int)C::q_use(n);
+        if (lane == qs) last = (int)C::use(n);
         ok = wait_all(&st_empty[ss], ((uint32_t)(n / C::kSS) & 1) ^ 1);
         if (!ok) break;
         if constexpr (SP) {
@@ -287,13 +304,13 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
             bulk_load(st + lane * kStatBytes, a.stat + sg * kStatBytes, kStatBytes, &st_full[ss]);
         } else if (lane == 0) {
           mbar_arrive_expect_tx(&st_full[ss], C::kStat);
-          bulk_load(st, a.stat + sg * kStatBytes, C::kStat, &st_full[ss]);
+          bulk_load(st, a.stat + sg * C::kGroupStat, C::kStat, &st_full[ss]);
         }
         if (lane == C::kTiles + ss) last = n / C::kSS;
-        ok = wait_all(&t_empty[os], (C::o_use(n) & 1) ^ 1);
+        ok = wait_all(&t_empty[os], (C::use(n) & 1) ^ 1);
         if (!ok) break;
         load_tile(do_, &tm_o, &t_full[os]);
-        if (lane == os) last = (int)C::o_use(n);
+        if (lane == os) last = (int)C::use(n);
       }
       cur = nx;
     }
@@ -323,12 +340,8 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     }
     if (!ok && lane == 0) *abort_flag = 1;
     if (n > 0) mbar_wait(kv_full, (uint32_t)(n - 1) & 1, nullptr);
-  } else if (warp == kAW || warp == kBW) {
+  } else if (warp == kAW || (SP && warp == kBW)) {
     // ------------------------------------------------------- MMA (warps 2, 3)
-    // Two warps, each in its own order: issuing a product (a wait, 8 MMAs, a commit)
-    // takes a warp 500 to 800 cycles, of which the pipe is busy 512.  With one warp for
-    // all of them a dense tile took 2830 cycles and a dQ step of the query-outer kernel
-    // 2650, against 2048 and 1536 of MMAs.
     constexpr uint32_t idesc_n = idesc_bf16(128, D, false, true);     // dV, dK
     constexpr uint32_t idesc_q = idesc_bf16(128, D, true, true);      // dQ's part
     const uint64_t kd = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
@@ -338,14 +351,22 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     const uint64_t dsk = smem_desc(smem_u32(sDs), 16, 1024, kSwizzle128B);
     const uint64_t tk = smem_desc(smem_u32(sT), 16, C::kGroup, kSwizzle128B);
     const uint64_t tmn = smem_desc(smem_u32(sT), C::kNext, C::kGroup, kSwizzle128B);
-    // A (128 x D, K-major) times a tile of rows, K-major: `steps` x 16 columns
-    auto rows_product = [&](uint32_t d, uint64_t ad, int slot, int steps) {
+    // A (128 x D, K-major) times a tile of rows, K-major: `steps` x 16 columns.  Dense: on
+    // top of the rows' statistics (sel 0: -lse, 1: -delta)
+    const uint64_t onesd = smem_desc(smem_u32(sOnes), 128, kAugBytes, 0);
+    const uint64_t augd = smem_desc(smem_u32(sStat), 128, kAugBytes, 0);
+    auto rows_product = [&](uint32_t d, uint64_t ad, int slot, int steps, int sel, int ss) {
       const uint32_t idesc = idesc_bf16(128, 0, false, false) | (uint32_t)(2 * steps) << 17;
       const uint64_t bd = tk + (uint64_t)((slot * C::kTile) >> 4);
+      if constexpr (!SP) {
+        tc_mma_f16(tmem + d, onesd + (uint64_t)((sel * C::kStat) >> 4),
+                   augd + (uint64_t)((ss * C::kStat) >> 4), idesc, 0u);
+        if (sel == 0 && a.no_scores) return;
+      }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
         tc_mma_f16(tmem + d, ad + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4),
-                   bd + (uint64_t)(((j >> 2) * C::kNext + (j & 3) * 32) >> 4), idesc, j > 0 ? 1u : 0u);
+                   bd + (uint64_t)(((j >> 2) * C::kNext + (j & 3) * 32) >> 4), idesc, !SP || j > 0 ? 1u : 0u);
     };
     // P^T or dS^T (TMEM at column p, kCols columns of a tile in half as many) times a tile
     auto sum_product = [&](uint32_t d, uint32_t p, int slot, int steps, bool add) {
@@ -363,15 +384,78 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     };
     int it, n = 0, nu = 0;       // tiles and units (with tiles) so far
     bool ok;
-    if (warp == kAW) {
+    if constexpr (!SP) {
+      // -------------- S(0), dP(0); dV(n), S(n + 1) on P(n); dK(n), dP(n + 1) on dS(n)
+      // One warp, in this order: S(n + 1), whose P takes longest, is not held up by the
+      // others (two warps, as below: 4 x 2048 tokens 347 us for 302)
+      while (next_unit(it, ok)) {
+        const KvUnit u = kv_unit<SP>(a, it);
+        if (u.tiles == 0) continue;
+        ok = wait_all(kv_full, (uint32_t)nu & 1) && wait_all(&t_full[C::q_slot(n)], C::use(n) & 1) &&
+             wait_all(&st_full[n % C::kSS], (uint32_t)(n / C::kSS) & 1) &&
+             wait_all(&t_full[C::o_slot(n)], C::use(n) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          rows_product(C::kS, kd, C::q_slot(n), 8, 0, n % C::kSS);
+          tc_commit(s_full);
+          rows_product(C::kP, vd, C::o_slot(n), 8, 1, n % C::kSS);
+          tc_commit(&dp_full[n & 1]);
+          tc_commit(&st_empty[n % C::kSS]);
+          if (u.tiles == 1) tc_commit(kv_empty);
+        }
+        __syncwarp();
+        for (int t = 0; t < u.tiles; ++t, ++n) {
+          const int qs = C::q_slot(n), os = C::o_slot(n), m = n + 1;
+          const bool more = t + 1 < u.tiles;
+          // the next tile's copies first: they have mostly landed
+          ok = (!more || (wait_all(&t_full[C::q_slot(m)], C::use(m) & 1) &&
+                          wait_all(&st_full[m % C::kSS], (uint32_t)(m / C::kSS) & 1))) &&
+               (t > 0 || nu == 0 || wait_all(acc_empty, (uint32_t)(nu - 1) & 1)) &&
+               wait_all(p_full, (uint32_t)n & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            sum_product(C::kDV, C::kS, os, 8, t > 0);
+            tc_commit(&t_empty[os]);
+            if (more) {                           // over P(n), which dV(n) reads
+              rows_product(C::kS, kd, C::q_slot(m), 8, 0, m % C::kSS);
+              tc_commit(s_full);
+            }
+          }
+          __syncwarp();
+          ok = (!more || wait_all(&t_full[C::o_slot(m)], C::use(m) & 1)) &&
+               wait_all(ds_full, (uint32_t)n & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            sum_product(C::kDK, C::kP, qs, 8, t > 0);
+            tc_commit(&t_empty[qs]);
+            if (more) {                           // over dS(n), which dK(n) reads
+              rows_product(C::kP, vd, C::o_slot(m), 8, 1, m % C::kSS);
+              tc_commit(&dp_full[m & 1]);
+              tc_commit(&st_empty[m % C::kSS]);
+              if (t + 2 == u.tiles) tc_commit(kv_empty);
+            } else {
+              tc_commit(acc_full);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        ++nu;
+      }
+    } else if (warp == kAW) {
       // ------------------------------------------------ S(0); dV(n), S(n + 1)
+      // Two warps, as issuing takes long (a product, with its wait and commits, 500 to 800
+      // cycles of a warp), and dQ's part with its readout is what is waited for
       while (next_unit(it, ok)) {
         const KvUnit u = kv_unit<SP>(a, it);
         if (u.tiles == 0) continue;
         ok = wait_all(kv_full, (uint32_t)nu & 1);
         if (!ok) break;
         const int64_t left = (int64_t)a.pos.q_start[u.b] + T - 1 - (int64_t)u.kb * kBlock;
-        if (SP && left < kBlock - 1) {
+        if (left < kBlock - 1) {
           // K rows behind the last query may hold anything; as terms of dQ's part they
           // are multiplied by zeros: cleared
           for (int e = lane; e < C::kNHalf * kBlock * 8; e += 32) {
@@ -385,12 +469,12 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
         }
         auto issue_s = [&](int m, int t) {         // S of tile m, the unit's t-th
           const int qs = C::q_slot(m);
-          if (!wait_all(&t_full[qs], C::q_use(m) & 1)) return false;
+          if (!wait_all(&t_full[qs], C::use(m) & 1)) return false;
           tc_fence_after();
           if (elect_one()) {
-            rows_product(C::kS, kd, qs, SP ? sparse_steps(a, u, t) : 8);
+            rows_product(C::kS, kd, qs, sparse_steps(a, u, t), 0, 0);
             tc_commit(s_full);
-            if (SP) tc_commit(&t_empty[qs]);
+            tc_commit(&t_empty[qs]);
             if (t + 1 == u.tiles) tc_commit(kv_empty);
           }
           __syncwarp();
@@ -401,25 +485,25 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           const int os = C::o_slot(n);
           ok = wait_all(p_full, (uint32_t)n & 1) &&
                (t > 0 || nu == 0 || wait_all(acc_empty, (uint32_t)(nu - 1) & 1)) &&
-               wait_all(&t_full[os], C::o_use(n) & 1);
+               wait_all(&t_full[os], C::use(n) & 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            sum_product(C::kDV, C::kS, os, SP ? sparse_steps(a, u, t) : 8, t > 0);
+            sum_product(C::kDV, C::kS, os, sparse_steps(a, u, t), t > 0);
             tc_commit(&t_empty[os]);
             if (t + 1 == u.tiles) tc_commit(acc_full);
           }
           __syncwarp();
-          // S(n + 1) goes over P(n), which dV(n), issued before, reads.  Sparse: behind dP(n),
-          // which is waited for longer
+          // S(n + 1) goes over P(n), which dV(n), issued before, reads, and behind dP(n), which
+          // is waited for longer
           if (t + 1 < u.tiles)
-            ok = (!SP || wait_all(&dp_full[n & 1], (uint32_t)(n >> 1) & 1)) && issue_s(n + 1, t + 1);
+            ok = wait_all(&dp_full[n & 1], (uint32_t)(n >> 1) & 1) && issue_s(n + 1, t + 1);
         }
         if (!ok) break;
         ++nu;
       }
     } else {
-      // -------- dense: dP(0); dK(n), dP(n + 1).  sparse: dP(n), dK(n), dQ's part(n)
+      // ------------------------------------------ dP(n); dQ's part(n), dK(n)
       while (next_unit(it, ok)) {
         const KvUnit u = kv_unit<SP>(a, it);
         if (u.tiles == 0) continue;
@@ -427,55 +511,45 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
         if (!ok) break;
         auto issue_dp = [&](int m, int t) {
           const int os = C::o_slot(m);
-          if (!wait_all(&t_full[os], C::o_use(m) & 1)) return false;
+          if (!wait_all(&t_full[os], C::use(m) & 1)) return false;
           tc_fence_after();
           if (elect_one()) {
-            rows_product(C::kP, vd, os, SP ? sparse_steps(a, u, t) : 8);
+            rows_product(C::kP, vd, os, sparse_steps(a, u, t), 1, 0);
             tc_commit(&dp_full[m & 1]);
             tc_commit(&t_empty[os]);
-            if (!SP && t + 1 == u.tiles) tc_commit(kv_empty);
           }
           __syncwarp();
           return true;
         };
-        if (!SP) ok = issue_dp(n, 0);
         for (int t = 0; t < u.tiles && ok; ++t, ++n) {
           const int qs = C::q_slot(n);
           const bool more = t + 1 < u.tiles;
-          if constexpr (SP) {
-            // D = 128: dQ's part of the tile before is in dP's place until it is read out
-            if (D == 128 && n > 0) ok = wait_all(dq_empty, (uint32_t)(n - 1) & 1);
-            ok = ok && issue_dp(n, t);
-          }
-          ok = ok && wait_all(ds_full, (uint32_t)n & 1) &&
+          // D = 128: dQ's part of the tile before is in dP's place until it is read out
+          if (D == 128 && n > 0) ok = wait_all(dq_empty, (uint32_t)(n - 1) & 1);
+          ok = ok && issue_dp(n, t) && wait_all(ds_full, (uint32_t)n & 1) &&
                (t > 0 || nu == 0 || wait_all(acc_empty, (uint32_t)(nu - 1) & 1));
-          if (SP && D != 128 && n > 0) ok = ok && wait_all(dq_empty, (uint32_t)(n - 1) & 1);
+          if (D != 128 && n > 0) ok = ok && wait_all(dq_empty, (uint32_t)(n - 1) & 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            if constexpr (SP) {
-              // ---- dQ part = dS K: 128 tokens in 8 steps; read out during dK
+            // dQ's part = dS K: 128 tokens in 8 steps; read out during dK
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                tc_mma_f16(tmem + C::dq(), dsmn + (uint64_t)((j * 2048) >> 4),
-                           kmn + (uint64_t)((j * 2048) >> 4), idesc_q, j > 0 ? 1u : 0u);
-              tc_commit(dq_full);
-              if (!more) tc_commit(kv_empty);
-              const int steps = sparse_steps(a, u, t);
-              const uint64_t bd = tmn + (uint64_t)((qs * C::kTile) >> 4);
-              for (int j = 0; j < steps; ++j)
-                tc_mma_f16(tmem + C::kDK, dsk + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4),
-                           bd + (uint64_t)((j * 2 * C::kGroup) >> 4), idesc_n,
-                           t > 0 || j > 0 ? 1u : 0u);
-            } else {
-              sum_product(C::kDK, C::kP, qs, 8, t > 0);
-            }
+            for (int j = 0; j < 8; ++j)
+              tc_mma_f16(tmem + C::dq(), dsmn + (uint64_t)((j * 2048) >> 4),
+                         kmn + (uint64_t)((j * 2048) >> 4), idesc_q, j > 0 ? 1u : 0u);
+            tc_commit(dq_full);
+            if (!more) tc_commit(kv_empty);
+            const int steps = sparse_steps(a, u, t);
+            const uint64_t bd = tmn + (uint64_t)((qs * C::kTile) >> 4);
+            for (int j = 0; j < steps; ++j)
+              tc_mma_f16(tmem + C::kDK, dsk + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4),
+                         bd + (uint64_t)((j * 2 * C::kGroup) >> 4), idesc_n,
+                         t > 0 || j > 0 ? 1u : 0u);
             tc_commit(&t_empty[qs]);
             tc_commit(&st_empty[n % C::kSS]);    // dS has used the statistics
             if (!more) tc_commit(acc_full);
           }
           __syncwarp();
-          if (!SP && more) ok = issue_dp(n + 1, t + 1);
         }
         if (!ok) break;
         ++nu;
@@ -486,13 +560,13 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     if (elect_one()) tc_commit(bar_fin);
     __syncwarp();
     mbar_wait(bar_fin, 0, nullptr);
-  } else if (warp < kOutW) {
+  } else if (warp >= kSoftW && warp < kOutW) {
     // ------------------------------------------ P, dS; dV and dK (warps 4-19)
     const int c = (warp - kSoftW) >> 2;           // columns kCols c .. of each tile
     const int quad = warp & 3;
     const int r = quad * 32 + lane;               // token of the block = TMEM lane
     const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16);
-    const float sl = a.s.scale * kLog2e;
+    const float sl = !SP && a.no_scores ? 1.f : a.s.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl);
     int it, n = 0, nu = 0;
     bool ok;
@@ -507,7 +581,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
         int lim = 0;                              // dense: columns below see another token
         bool masked;
         ok = *abort_flag == 0 &&
-             mbar_wait(&st_full[ss], (uint32_t)(n / C::kSS) & 1, a.status, a.wait_polls) &&
+             (!SP || mbar_wait(&st_full[ss], (uint32_t)(n / C::kSS) & 1, a.status, a.wait_polls)) &&
              mbar_wait(s_full, (uint32_t)n & 1, a.status, a.wait_polls);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -538,7 +612,8 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           uint32_t w[8];
 #pragma unroll
           for (int g4 = 0; g4 < 4; ++g4) {        // 4 columns
-            const float4 nl = st[(q * 2 + (g4 >> 1)) * 4 + (g4 & 1)];
+            // (dense: -lse is in S already)
+            const float4 nl = SP ? st[(q * 2 + (g4 >> 1)) * 4 + (g4 & 1)] : make_float4(0, 0, 0, 0);
             const float2 y0 = ffma2(make_float2(__uint_as_float(x[4 * g4]), __uint_as_float(x[4 * g4 + 1])),
                                     sl2, make_float2(nl.x, nl.y));
             const float2 y1 = ffma2(make_float2(__uint_as_float(x[4 * g4 + 2]), __uint_as_float(x[4 * g4 + 3])),
@@ -575,11 +650,13 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           uint32_t w[8];
 #pragma unroll
           for (int g4 = 0; g4 < 4; ++g4) {
-            const float4 nd = st[(q * 2 + (g4 >> 1)) * 4 + 2 + (g4 & 1)];
-            float2 d0 = fadd2(make_float2(__uint_as_float(x[4 * g4]), __uint_as_float(x[4 * g4 + 1])),
-                              make_float2(nd.x, nd.y));
-            float2 d1 = fadd2(make_float2(__uint_as_float(x[4 * g4 + 2]), __uint_as_float(x[4 * g4 + 3])),
-                              make_float2(nd.z, nd.w));
+            float2 d0 = make_float2(__uint_as_float(x[4 * g4]), __uint_as_float(x[4 * g4 + 1]));
+            float2 d1 = make_float2(__uint_as_float(x[4 * g4 + 2]), __uint_as_float(x[4 * g4 + 3]));
+            if constexpr (SP) {      // (dense: -delta is in dP already)
+              const float4 nd = st[(q * 2 + (g4 >> 1)) * 4 + 2 + (g4 & 1)];
+              d0 = fadd2(d0, make_float2(nd.x, nd.y));
+              d1 = fadd2(d1, make_float2(nd.z, nd.w));
+            }
             d0 = fmul2(p[q * 8 + 2 * g4], d0);
             d1 = fmul2(p[q * 8 + 2 * g4 + 1], d1);
             if (masked) {      // 0 even where dP is not finite

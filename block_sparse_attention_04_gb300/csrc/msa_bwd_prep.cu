@@ -23,6 +23,8 @@ struct StatArgs {
   const uint16_t *q, *k, *v, *out, *dout;
   const float* lse;
   uint8_t* stat;
+  uint8_t* aug;          // dense: the groups as operands
+  float to_score;        // 1 / (scale log2e), or 1
   uint32_t groups;
   int rpe;               // 0: dense
   int row_ctas;          // CTAs of the first kind
@@ -41,6 +43,18 @@ __device__ __forceinline__ float* stat_row(const StatArgs& a, int b, int i, int 
     r = h % hpg & 7;
   }
   return reinterpret_cast<float*>(a.stat + g * kStatBytes) + r;
+}
+
+// Writes x at its row of an operand group (core 0: lse, 1: delta): three bf16 parts.
+__device__ __forceinline__ void put_aug(uint8_t* group, int core, int row, float x) {
+  const float hi = __uint_as_float(pack_bf16(x, 0.f) << 16);
+  float mid = 0.f, lo = 0.f;
+  if (fabsf(hi) < INFINITY) {              // (a NaN goes on in hi)
+    mid = __uint_as_float(pack_bf16(x - hi, 0.f) << 16);
+    lo = x - hi - mid;
+  }
+  *reinterpret_cast<uint4*>(group + core * 128 + row * 16) =
+      make_uint4(pack_bf16(hi, mid), pack_bf16(lo, 0.f), 0, 0);
 }
 
 template <int D>
@@ -104,8 +118,12 @@ __device__ __forceinline__ void stat_first(const StatArgs& a, int64_t task) {
       sd[u] += __shfl_xor_sync(0xffffffffu, sd[u], o);
     }
     // (a NaN in a row goes on into its delta)
-    if (c == 0 && i0 + r + 8 * u < n)
-      stat_row(a, b, i0 + r + 8 * u, h)[8] = sp[u] == 0.f ? 0.f : -sd[u] / sp[u];
+    if (c == 0 && i0 + r + 8 * u < n) {
+      const float nd = sp[u] == 0.f ? 0.f : -sd[u] / sp[u];
+      const int i = i0 + r + 8 * u;
+      stat_row(a, b, i, h)[8] = nd;
+      if (a.aug) put_aug(a.aug + ((size_t)(b * H + h) * a.groups + (i >> 3)) * kAugBytes, 1, i & 7, nd);
+    }
   }
 }
 
@@ -180,8 +198,16 @@ __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_con
     float* st = reinterpret_cast<float*>(dst) + (l & 7);
     // rows of the second kind leave delta alone
     const int64_t t = (int64_t)a.pos.q_start[b] + i0 + (a.rpe ? 0 : l & 7);
-    if (l < 8) st[0] = -kLog2e * lse;
-    if ((LPR == 8 || l >= 8) && ((l & 7) >= n || t >= kBlock)) st[8] = -mine;
+    const bool lse_lane = l < 8, delta_lane = (LPR == 8 || l >= 8) && ((l & 7) >= n || t >= kBlock);
+    if (lse_lane) st[0] = -kLog2e * lse;
+    if (delta_lane) st[8] = -mine;
+    if (!a.rpe) {
+      uint8_t* ag = a.aug + (dst - a.stat) / kStatBytes * kAugBytes;
+      // rows past the last query: P = 2^-16384 = 0 (and no infinity, which the other
+      // selector's zeros would make NaN)
+      if (lse_lane) put_aug(ag, 0, l & 7, ((l & 7) < n ? -kLog2e * lse : -16384.f) * a.to_score);
+      if (delta_lane) put_aug(ag, 1, l & 7, -mine);
+    }
   }
   if (a.rpe && blockIdx.x == 0 && threadIdx.x < 16)
     reinterpret_cast<float*>(a.stat + (size_t)a.groups * kStatBytes)[threadIdx.x] =
@@ -496,8 +522,9 @@ __global__ void __launch_bounds__(256) bwd_join_kv_kernel(const __grid_constant_
 }  // namespace
 
 cudaError_t launch_bwd_stats(const Shape& s, const Positions& pos, const AttnBwd& t, int rpe,
-                             uint8_t* stat, uint32_t stat_groups, cudaStream_t st) {
-  StatArgs a{s, pos, t.q, t.k, t.v, t.out, t.dout, t.lse, stat, stat_groups, rpe, 0};
+                             uint8_t* stat, uint8_t* aug, uint32_t stat_groups, cudaStream_t st) {
+  const float to_score = bwd_no_scores(s) ? 1.f : 1.f / (s.scale * kLog2e);
+  StatArgs a{s, pos, t.q, t.k, t.v, t.out, t.dout, t.lse, stat, aug, to_score, stat_groups, rpe, 0};
   const int per_cta = kStatThreads / (s.D / 8);
   const int64_t grps = rpe ? (int64_t)stat_groups : (int64_t)s.B * stat_groups * s.H;
   a.row_ctas = (int)((grps + per_cta - 1) / per_cta);
