@@ -9,14 +9,14 @@ namespace msa {
 namespace {
 
 // ---- row statistics -----------------------------------------------------------
-// Rows by CTAs of the first kind, D/8 lanes each: -lse log2e, and -delta = -dout.out.
-// A row whose whole context lies in block 0 (t < 128) leaves delta to CTAs of the
-// second kind, which take it from the probabilities, delta = sum P dP / sum P over its
+// Groups of rows: -lse log2e, and -delta = -dout.out.  A row whose whole context lies in
+// block 0 (t < 128) leaves delta to a second kernel, which takes it from the probabilities, delta = sum P dP / sum P over its
 // keys: with few tokens dS is a small difference of dP and delta, and out carries
 // rounding of 2^-9 (8 tokens, scores of two units: dq 0.35 % off, now 0.25, what
-// rounding dS leaves).  There a warp takes 16 queries of a head against 8 keys at a
-// time on mma.sync; the order of the dims in the products is permuted so that a
-// lane's fragments of two steps are 16 contiguous bytes.
+// rounding dS leaves).  There a CTA takes a head, and a warp 16 of its queries against 8
+// keys at a time on mma.sync, from K and V of block 0 in shared memory; the order of the
+// dims in the products is permuted so that a lane's fragments of two steps are 16
+// contiguous bytes.  (Fragments read from global memory: 45 us for four sequences.)
 struct StatArgs {
   Shape s;
   Positions pos;
@@ -27,7 +27,6 @@ struct StatArgs {
   float to_score;        // 1 / (scale log2e), or 1
   uint32_t groups;
   int rpe;               // 0: dense
-  int row_ctas;          // CTAs of the first kind
 };
 constexpr int kStatThreads = 256;
 
@@ -58,12 +57,26 @@ __device__ __forceinline__ void put_aug(uint8_t* group, int core, int row, float
 }
 
 template <int D>
-__device__ __forceinline__ void stat_first(const StatArgs& a, int64_t task) {
-  // (b, h, 16 queries): the first 128 positions of a sequence are at most 8 such
-  const int lane = threadIdx.x & 31, H = a.s.H, G = a.s.G, g = (int)(task / 8 % H) / (H / G);
-  const int b = (int)(task / 8 / H), h = (int)(task / 8 % H), i0 = (int)(task % 8) * 16;
-  if (b >= a.s.B) return;
+__global__ void __launch_bounds__(256) bwd_stat_first_kernel(const __grid_constant__ StatArgs a) {
+  extern __shared__ __align__(16) uint8_t kv[];      // K, then V: rows of D bf16 and 16 bytes
+  constexpr int PITCH = 2 * D + 16;
+  const int lane = threadIdx.x & 31, H = a.s.H, G = a.s.G;
+  const int b = blockIdx.x / H, h = blockIdx.x % H, g = h / (H / G);
   const int n = min(a.s.T, kBlock - a.pos.q_start[b]);   // rows with t < 128
+  if (n <= 0) return;
+  {
+    // rows behind the last query's hold anything: they are masked below
+    const int rows = min(kBlock, (a.pos.q_start[b] + n + 7) & ~7);
+    for (int e = threadIdx.x; e < 2 * rows * (D / 8); e += 256) {
+      const int ch = e % (D / 8), row = e / (D / 8) % rows;
+      const bool v = e >= rows * (D / 8);
+      const uint16_t* src = (v ? a.v : a.k) + (((size_t)b * a.s.max_blocks * kBlock + row) * G + g) * D;
+      *reinterpret_cast<uint4*>(kv + (v ? kBlock * PITCH : 0) + row * PITCH + ch * 16) =
+          *reinterpret_cast<const uint4*>(src + 8 * ch);
+    }
+    __syncthreads();
+  }
+  const int i0 = (threadIdx.x >> 5) * 16;
   if (i0 >= n) return;
   const int r = lane >> 2, c = lane & 3;
   constexpr int NC = D / 32;
@@ -89,13 +102,12 @@ __device__ __forceinline__ void stat_first(const StatArgs& a, int64_t task) {
   const float sl = a.s.scale * kLog2e;
   const int t_last = a.pos.q_start[b] + min(i0 + 15, n - 1);
   for (int j0 = 0; j0 <= t_last; j0 += 8) {
-    // rows behind the last query's hold anything: they are masked below
-    const size_t at = (((size_t)b * a.s.max_blocks * kBlock + j0 + r) * G + g) * D + 8 * c;
+    const uint8_t* at = kv + (j0 + r) * PITCH + 16 * c;
     float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-      const uint4 fk = *reinterpret_cast<const uint4*>(a.k + at + 32 * k);
-      const uint4 fv = *reinterpret_cast<const uint4*>(a.v + at + 32 * k);
+      const uint4 fk = *reinterpret_cast<const uint4*>(at + 64 * k);
+      const uint4 fv = *reinterpret_cast<const uint4*>(at + kBlock * PITCH + 64 * k);
       mma_bf16_16816(x, fq[0][k].x, fq[1][k].x, fq[0][k].y, fq[1][k].y, fk.x, fk.y);
       mma_bf16_16816(x, fq[0][k].z, fq[1][k].z, fq[0][k].w, fq[1][k].w, fk.z, fk.w);
       mma_bf16_16816(y, fo[0][k].x, fo[1][k].x, fo[0][k].y, fo[1][k].y, fv.x, fv.y);
@@ -134,10 +146,6 @@ template <int D>
 __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_constant__ StatArgs a) {
   constexpr int LPR = D / 8;
   const int H = a.s.H, G = a.s.G, hpg = H / G;
-  if ((int)blockIdx.x >= a.row_ctas) {
-    stat_first<D>(a, (int64_t)(blockIdx.x - a.row_ctas) * (kStatThreads / 32) + (threadIdx.x >> 5));
-    return;
-  }
   const int l = threadIdx.x % LPR;
   const int64_t grp = (int64_t)blockIdx.x * (kStatThreads / LPR) + threadIdx.x / LPR;
   // dense: groups in order (b, 8 queries, h); sparse: (b, query, g, 8 heads)
@@ -196,7 +204,7 @@ __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_con
   }
   if (in) {
     float* st = reinterpret_cast<float*>(dst) + (l & 7);
-    // rows of the second kind leave delta alone
+    // rows of the second kernel leave delta alone
     const int64_t t = (int64_t)a.pos.q_start[b] + i0 + (a.rpe ? 0 : l & 7);
     const bool lse_lane = l < 8, delta_lane = (LPR == 8 || l >= 8) && ((l & 7) >= n || t >= kBlock);
     if (lse_lane) st[0] = -kLog2e * lse;
@@ -524,17 +532,26 @@ __global__ void __launch_bounds__(256) bwd_join_kv_kernel(const __grid_constant_
 cudaError_t launch_bwd_stats(const Shape& s, const Positions& pos, const AttnBwd& t, int rpe,
                              uint8_t* stat, uint8_t* aug, uint32_t stat_groups, cudaStream_t st) {
   const float to_score = bwd_no_scores(s) ? 1.f : 1.f / (s.scale * kLog2e);
-  StatArgs a{s, pos, t.q, t.k, t.v, t.out, t.dout, t.lse, stat, aug, to_score, stat_groups, rpe, 0};
+  StatArgs a{s, pos, t.q, t.k, t.v, t.out, t.dout, t.lse, stat, aug, to_score, stat_groups, rpe};
   const int per_cta = kStatThreads / (s.D / 8);
   const int64_t grps = rpe ? (int64_t)stat_groups : (int64_t)s.B * stat_groups * s.H;
-  a.row_ctas = (int)((grps + per_cta - 1) / per_cta);
+  const unsigned ctas = (unsigned)((grps + per_cta - 1) / per_cta);
+  note_launches(1);
+  if (s.D == 128) bwd_stat_kernel<128><<<ctas, kStatThreads, 0, st>>>(a);
+  else bwd_stat_kernel<64><<<ctas, kStatThreads, 0, st>>>(a);
   bool early = false;
   for (int b = 0; b < s.B; ++b) early |= pos.q_start[b] < kBlock;
-  const int64_t tasks = early ? (int64_t)s.B * s.H * 8 : 0;   // a warp each
-  const unsigned grid = (unsigned)(a.row_ctas + (tasks + kStatThreads / 32 - 1) / (kStatThreads / 32));
-  note_launches(1);
-  if (s.D == 128) bwd_stat_kernel<128><<<grid, kStatThreads, 0, st>>>(a);
-  else bwd_stat_kernel<64><<<grid, kStatThreads, 0, st>>>(a);
+  if (early) {
+    const int smem = 2 * kBlock * (2 * s.D + 16);
+    const cudaError_t e =
+        s.D == 128 ? cudaFuncSetAttribute(bwd_stat_first_kernel<128>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
+                   : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    note_launches(1);
+    if (s.D == 128) bwd_stat_first_kernel<128><<<s.B * s.H, 256, smem, st>>>(a);
+    else bwd_stat_first_kernel<64><<<s.B * s.H, 256, smem, st>>>(a);
+  }
   return cudaGetLastError();
 }
 
