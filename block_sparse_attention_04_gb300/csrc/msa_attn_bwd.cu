@@ -187,6 +187,7 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
   }
   q.next_item = a.n_units + 3;
   q.stat = stat;
+  q.q = t.q;
   q.stat_groups = L.stat_groups;
   q.part = reinterpret_cast<float*>(base + L.part_q);
   q.dq = t.dq;

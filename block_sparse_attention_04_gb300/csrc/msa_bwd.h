@@ -78,6 +78,7 @@ struct BwdQArgs {
   int* next_item;
   const uint8_t* stat;
   uint32_t stat_groups;
+  const uint16_t* q;
   float* part;               // splits > 1: [nitems][splits][128][D] partial dq
   uint16_t* dq;
   int* status;

@@ -19,7 +19,7 @@
 //                statistics; takes the units from a shared counter
 //   warp 1       TMA of the unit's K and V
 //   warp 2       tcgen05.mma; sparse: of S and dV
-//   warp 3       sparse: tcgen05.mma of dP, dK and dQ's part
+//   warp 3       sparse: tcgen05.mma of dP, dK and dQ's part; dense: waits for copies
 //   warps 4-19   P and dS: four warpgroups, 32 columns of a tile each; a unit's dV, dK
 //   warps 20-23  sparse: dQ's parts, bf16, one row of 16 slots x D per (query, head)
 // dS(n) is worked out during dV(n) and S(n+1), P(n+1) during dK(n) and dP(n+1).  Sparse,
@@ -32,6 +32,8 @@
 // the registers costs as much as 104 KB.  So the dense tiles' numbers come in through the
 // products: a 17th step of S and of dP multiplies ones with them, as three bf16 parts.
 // (4 x 2048 tokens, 48/8 heads: 347 us before.)  A sparse tile has no room left for them.
+#include <type_traits>
+
 #include "msa_bwd.h"
 #include "msa_q8.cuh"
 #include "msa_tma.h"
@@ -39,7 +41,9 @@
 namespace msa {
 namespace {
 
-constexpr int kAW = 2, kBW = 3, kSoftW = 4;   // warps: MMA of dV and S, of dP, dK and dQ; P and dS
+// warps: MMA (sparse: of dV and S); dense: the MMA warp's waits, sparse: MMA of dP, dK and
+// dQ's part; P and dS
+constexpr int kAW = 2, kBW = 3, kSoftW = 4;
 constexpr int kNG = 4;                    // warpgroups for P and dS ...
 constexpr int kCols = 128 / kNG;          // ... and the columns of a tile that each has
 constexpr int kOutW = kSoftW + 4 * kNG;
@@ -47,7 +51,7 @@ template <bool SP>
 constexpr int kv_threads() { return 32 * (kOutW + (SP ? 4 : 0)); }
 constexpr int kRing = 4;                  // unit numbers published by warp 0, ahead of use
 template <bool SP>
-constexpr int ring_readers() { return 2 + 4 * kNG + (SP ? 5 : 0); }
+constexpr int ring_readers() { return 3 + 4 * kNG + (SP ? 4 : 0); }
 
 template <int D, bool SP>
 struct KvCfg {
@@ -93,6 +97,10 @@ __device__ __forceinline__ KvUnit kv_unit(const BwdArgs& a, int it) {
   u.slot = d.w;
   u.tiles = SP ? (d.z + a.R - 1) / a.R : d.z;
   return u;
+}
+
+__device__ __forceinline__ float2 pair(const uint32_t* x, int i) {
+  return make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
 }
 
 // Dense: tile of the unit -> head of the group and query tile.
@@ -163,8 +171,8 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     mbar_init(s_full, 1);
     mbar_init(&dp_full[0], 1);
     mbar_init(&dp_full[1], 1);
-    mbar_init(p_full, 128 * kNG);
-    mbar_init(ds_full, 128 * kNG);
+    mbar_init(p_full, 128 * kNG + (SP ? 0 : 1));   // dense: and what comes next has landed
+    mbar_init(ds_full, 128 * kNG + (SP ? 0 : 1));
     mbar_init(acc_full, SP ? 2 : 1);
     mbar_init(acc_empty, 128 * kNG);
     mbar_init(dq_full, 1);
@@ -355,18 +363,25 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     // top of the rows' statistics (sel 0: -lse, 1: -delta)
     const uint64_t onesd = smem_desc(smem_u32(sOnes), 128, kAugBytes, 0);
     const uint64_t augd = smem_desc(smem_u32(sStat), 128, kAugBytes, 0);
+    // (An instruction descriptor that is not a constant costs an MMA 40 cycles: full tiles
+    // have one.)
     auto rows_product = [&](uint32_t d, uint64_t ad, int slot, int steps, int sel, int ss) {
-      const uint32_t idesc = idesc_bf16(128, 0, false, false) | (uint32_t)(2 * steps) << 17;
       const uint64_t bd = tk + (uint64_t)((slot * C::kTile) >> 4);
+      auto all = [&](uint32_t idesc) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+          tc_mma_f16(tmem + d, ad + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4),
+                     bd + (uint64_t)(((j >> 2) * C::kNext + (j & 3) * 32) >> 4), idesc,
+                     !SP || j > 0 ? 1u : 0u);
+      };
+      constexpr uint32_t full = idesc_bf16(128, 128, false, false);
       if constexpr (!SP) {
         tc_mma_f16(tmem + d, onesd + (uint64_t)((sel * C::kStat) >> 4),
-                   augd + (uint64_t)((ss * C::kStat) >> 4), idesc, 0u);
+                   augd + (uint64_t)((ss * C::kStat) >> 4), full, 0u);
         if (sel == 0 && a.no_scores) return;
       }
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-        tc_mma_f16(tmem + d, ad + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4),
-                   bd + (uint64_t)(((j >> 2) * C::kNext + (j & 3) * 32) >> 4), idesc, !SP || j > 0 ? 1u : 0u);
+      if (!SP || steps == 8) all(full);
+      else all(idesc_bf16(128, 0, false, false) | (uint32_t)(2 * steps) << 17);
     };
     // P^T or dS^T (TMEM at column p, kCols columns of a tile in half as many) times a tile
     auto sum_product = [&](uint32_t d, uint32_t p, int slot, int steps, bool add) {
@@ -387,7 +402,9 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     if constexpr (!SP) {
       // -------------- S(0), dP(0); dV(n), S(n + 1) on P(n); dK(n), dP(n + 1) on dS(n)
       // One warp, in this order: S(n + 1), whose P takes longest, is not held up by the
-      // others (two warps, as below: 4 x 2048 tokens 347 us for 302)
+      // others (two warps, as below: 4 x 2048 tokens 347 us for 302).  Few MMAs are
+      // in flight behind an issue, and a wait takes 190 cycles even where it is over, so
+      // that the next warp takes the waits for copies and this one two a tile
       while (next_unit(it, ok)) {
         const KvUnit u = kv_unit<SP>(a, it);
         if (u.tiles == 0) continue;
@@ -408,11 +425,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
         for (int t = 0; t < u.tiles; ++t, ++n) {
           const int qs = C::q_slot(n), os = C::o_slot(n), m = n + 1;
           const bool more = t + 1 < u.tiles;
-          // the next tile's copies first: they have mostly landed
-          ok = (!more || (wait_all(&t_full[C::q_slot(m)], C::use(m) & 1) &&
-                          wait_all(&st_full[m % C::kSS], (uint32_t)(m / C::kSS) & 1))) &&
-               (t > 0 || nu == 0 || wait_all(acc_empty, (uint32_t)(nu - 1) & 1)) &&
-               wait_all(p_full, (uint32_t)n & 1);
+          ok = wait_all(p_full, (uint32_t)n & 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -424,8 +437,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
             }
           }
           __syncwarp();
-          ok = (!more || wait_all(&t_full[C::o_slot(m)], C::use(m) & 1)) &&
-               wait_all(ds_full, (uint32_t)n & 1);
+          ok = wait_all(ds_full, (uint32_t)n & 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -541,10 +553,17 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
             if (!more) tc_commit(kv_empty);
             const int steps = sparse_steps(a, u, t);
             const uint64_t bd = tmn + (uint64_t)((qs * C::kTile) >> 4);
-            for (int j = 0; j < steps; ++j)
+            auto step = [&](int j) {
               tc_mma_f16(tmem + C::kDK, dsk + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4),
                          bd + (uint64_t)((j * 2 * C::kGroup) >> 4), idesc_n,
                          t > 0 || j > 0 ? 1u : 0u);
+            };
+            if (steps == 8) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) step(j);
+            } else {
+              for (int j = 0; j < steps; ++j) step(j);
+            }
             tc_commit(&t_empty[qs]);
             tc_commit(&st_empty[n % C::kSS]);    // dS has used the statistics
             if (!more) tc_commit(acc_full);
@@ -560,6 +579,34 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     if (elect_one()) tc_commit(bar_fin);
     __syncwarp();
     mbar_wait(bar_fin, 0, nullptr);
+  } else if (!SP && warp == kBW) {
+    // -------------------------------------- the MMA warp's waits (dense, warp 3)
+    // Arrives with the softmax warps: at P(n) once the next tile's Q and statistics are in
+    // shared memory (and the last unit's sums have been read out), at dS(n) once its dO is.
+    int it, n = 0, nu = 0;
+    bool ok;
+    while (next_unit(it, ok)) {
+      const KvUnit u = kv_unit<SP>(a, it);
+      if (u.tiles == 0) continue;
+      for (int t = 0; t < u.tiles; ++t, ++n) {
+        const int m = n + 1;
+        const bool more = t + 1 < u.tiles;
+        ok = __any_sync(0xffffffffu, *abort_flag != 0) == 0 &&
+             (!more || (wait_all(&t_full[C::q_slot(m)], C::use(m) & 1) &&
+                        wait_all(&st_full[m % C::kSS], (uint32_t)(m / C::kSS) & 1))) &&
+             (t > 0 || nu == 0 || wait_all(acc_empty, (uint32_t)(nu - 1) & 1)) &&
+             (n == 0 || wait_all(p_full, (uint32_t)(n - 1) & 1));   // not into the phase before
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(p_full);
+        ok = (!more || wait_all(&t_full[C::o_slot(m)], C::use(m) & 1)) &&
+             (n == 0 || wait_all(ds_full, (uint32_t)(n - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(ds_full);
+      }
+      if (!ok) break;
+      ++nu;
+    }
+    if (!ok && lane == 0) *abort_flag = 1;
   } else if (warp >= kSoftW && warp < kOutW) {
     // ------------------------------------------ P, dS; dV and dK (warps 4-19)
     const int c = (warp - kSoftW) >> 2;           // columns kCols c .. of each tile
@@ -596,35 +643,36 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           lim = used ? (int)(d > 0 ? d : 0) - c * kCols : kCols;
           masked = __any_sync(0xffffffffu, lim > 0);
         }
-        // whether token r is not seen by column `col` of this warpgroup
-        auto hidden = [&](int col) { return SP ? r > tl[col >> 3] : col < lim; };
+        // zeros at columns col and col + 1 of this warpgroup, where they do not see token r
+        auto hide = [&](float2& v, int col) {
+          v.x = (SP ? r > tl[col >> 3] : col < lim) ? 0.f : v.x;
+          v.y = (SP ? r > tl[col >> 3] : col + 1 < lim) ? 0.f : v.y;
+        };
         tc_fence_after();
-        // statistics of 8 columns: 64 bytes, -lse log2e then -delta
+        // statistics of 8 columns: 64 bytes, -lse log2e then -delta (dense: S and dP hold them)
         const float4* st =
             reinterpret_cast<const float4*>(sStat + ss * C::kStat + c * (kCols / 8) * kStatBytes);
         float2 p[kCols / 2];
-#pragma unroll
-        for (int q = 0; q < kCols / 16; ++q) {
-          if (SP && q * 16 >= cols) continue;
-          uint32_t x[16];
+        // P of 16 columns, and dS of them, with the masks (few tiles have any) or without
+        auto p_of = [&](auto mask, int q) {
+          uint32_t x[16], w[8];
           tmem_ld16(base + C::kS + c * kCols + q * 16, x);
           tmem_ld_wait();
-          uint32_t w[8];
 #pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {        // 4 columns
-            // (dense: -lse is in S already)
-            const float4 nl = SP ? st[(q * 2 + (g4 >> 1)) * 4 + (g4 & 1)] : make_float4(0, 0, 0, 0);
-            const float2 y0 = ffma2(make_float2(__uint_as_float(x[4 * g4]), __uint_as_float(x[4 * g4 + 1])),
-                                    sl2, make_float2(nl.x, nl.y));
-            const float2 y1 = ffma2(make_float2(__uint_as_float(x[4 * g4 + 2]), __uint_as_float(x[4 * g4 + 3])),
-                                    sl2, make_float2(nl.z, nl.w));
+          for (int g4 = 0; g4 < 4; ++g4) {          // 4 columns
+            float2 y0, y1;
+            if constexpr (SP) {
+              const float4 nl = st[(q * 2 + (g4 >> 1)) * 4 + (g4 & 1)];
+              y0 = ffma2(pair(x, 2 * g4), sl2, make_float2(nl.x, nl.y));
+              y1 = ffma2(pair(x, 2 * g4 + 1), sl2, make_float2(nl.z, nl.w));
+            } else {
+              y0 = fmul2(pair(x, 2 * g4), sl2);
+              y1 = fmul2(pair(x, 2 * g4 + 1), sl2);
+            }
             float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
-            if (masked) {
-              const int col = q * 16 + 4 * g4;
-              p0.x = hidden(col) ? 0.f : p0.x;
-              p0.y = hidden(col + 1) ? 0.f : p0.y;
-              p1.x = hidden(col + 2) ? 0.f : p1.x;
-              p1.y = hidden(col + 3) ? 0.f : p1.y;
+            if constexpr (mask.value) {
+              hide(p0, q * 16 + 4 * g4);
+              hide(p1, q * 16 + 4 * g4 + 2);
             }
             p[q * 8 + 2 * g4] = p0;
             p[q * 8 + 2 * g4 + 1] = p1;
@@ -633,38 +681,24 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           }
           // over columns that were read already
           tmem_st8(base + C::kS + c * kCols + q * 8, w);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(p_full);
-        ok = __all_sync(0xffffffffu, mbar_wait(&dp_full[n & 1], (uint32_t)(n >> 1) & 1, a.status,
-                                               a.wait_polls));
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int q = 0; q < kCols / 16; ++q) {
-          if (SP && q * 16 >= cols) continue;
-          uint32_t x[16];
+        };
+        auto ds_of = [&](auto mask, int q) {
+          uint32_t x[16], w[8];
           tmem_ld16(base + C::kP + c * kCols + q * 16, x);
           tmem_ld_wait();
-          uint32_t w[8];
 #pragma unroll
           for (int g4 = 0; g4 < 4; ++g4) {
-            float2 d0 = make_float2(__uint_as_float(x[4 * g4]), __uint_as_float(x[4 * g4 + 1]));
-            float2 d1 = make_float2(__uint_as_float(x[4 * g4 + 2]), __uint_as_float(x[4 * g4 + 3]));
-            if constexpr (SP) {      // (dense: -delta is in dP already)
+            float2 d0 = pair(x, 2 * g4), d1 = pair(x, 2 * g4 + 1);
+            if constexpr (SP) {
               const float4 nd = st[(q * 2 + (g4 >> 1)) * 4 + 2 + (g4 & 1)];
               d0 = fadd2(d0, make_float2(nd.x, nd.y));
               d1 = fadd2(d1, make_float2(nd.z, nd.w));
             }
             d0 = fmul2(p[q * 8 + 2 * g4], d0);
             d1 = fmul2(p[q * 8 + 2 * g4 + 1], d1);
-            if (masked) {      // 0 even where dP is not finite
-              const int col = q * 16 + 4 * g4;
-              d0.x = hidden(col) ? 0.f : d0.x;
-              d0.y = hidden(col + 1) ? 0.f : d0.y;
-              d1.x = hidden(col + 2) ? 0.f : d1.x;
-              d1.y = hidden(col + 3) ? 0.f : d1.y;
+            if constexpr (mask.value) {             // 0 even where dP is not finite
+              hide(d0, q * 16 + 4 * g4);
+              hide(d1, q * 16 + 4 * g4 + 2);
             }
             w[2 * g4] = pack_bf16(d0.x, d0.y);
             w[2 * g4 + 1] = pack_bf16(d1.x, d1.y);
@@ -679,6 +713,25 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           } else {
             tmem_st8(base + C::kP + c * kCols + q * 8, w);
           }
+        };
+#pragma unroll
+        for (int q = 0; q < kCols / 16; ++q) {
+          if (SP && q * 16 >= cols) continue;
+          if (masked) p_of(std::true_type(), q);
+          else p_of(std::false_type(), q);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_full);
+        ok = __all_sync(0xffffffffu, mbar_wait(&dp_full[n & 1], (uint32_t)(n >> 1) & 1, a.status,
+                                               a.wait_polls));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < kCols / 16; ++q) {
+          if (SP && q * 16 >= cols) continue;
+          if (masked) ds_of(std::true_type(), q);
+          else ds_of(std::false_type(), q);
         }
         if constexpr (SP) fence_async();
         else tmem_st_wait();

@@ -3,14 +3,22 @@
 // whose dQ stays in tensor memory over the key blocks,
 //     S = Q K^T   dP = dO V^T   dS = 2^(S scale log2e - lse log2e) (dP - delta)
 //     dQ += dS K
-// with the queries on the 128 lanes.  dS is written over S as bf16, the A operand of the
-// last product; K is read K-major by the first product and MN-major by the last.
-//   warp 0       TMA of the item's Q and dO; takes the items from a shared counter
-//   warp 1       TMA of K (3 stages: a block is read until its dQ product) and V (2)
-//   warp 2       tcgen05.mma of dQ and S, S in two buffers
-//   warp 3       tcgen05.mma of dP
-//   warps 4-19   dS: four warpgroups, 32 keys of a block each; an item's dQ
+// with the queries on the 128 lanes.  Q and dS are A operands in tensor memory, so that of
+// the products' operands only dO, and K and V as they stream by, are read from shared
+// memory: 128 KB a block at D = 128 and 64 written, as many cycles as the MMAs take.  (With
+// Q in shared memory too and dS over S: 4 x 2048 tokens 278 us.)  K is read K-major by S
+// and MN-major by dQ.
+//   warp 0       TMA of the item's dO; takes the items from a shared counter
+//   warp 1       TMA of K (four stages at D = 128: a block is read from S, two blocks ahead,
+//                to dQ) and V (two)
+//   warp 2       tcgen05.mma: once dS(n) is made dP(n+1), dQ(n), and S(n+2), as S(n+1) has
+//                been read by then
+//   warp 3       waits for the copies in the MMA warp's place
+//   warps 4-19   Q into tensor memory; dS: four warpgroups, 32 keys of a block each; an
+//                item's dQ
 // The two numbers of a row (lse, delta) stay in registers over an item.
+#include <type_traits>
+
 #include "msa_bwd.h"
 #include "msa_q8.cuh"
 #include "msa_tma.h"
@@ -18,7 +26,7 @@
 namespace msa {
 namespace {
 
-constexpr int kAW = 2, kBW = 3, kSoftW = 4;   // warps: MMA of S and dQ, of dP; dS
+constexpr int kMmaW = 2, kWaitW = 3, kSoftW = 4;
 constexpr int kNG = 4;                    // warpgroups for dS ...
 constexpr int kCols = 128 / kNG;          // ... and the keys of a block that each has
 constexpr int kThreadsQ = 32 * (kSoftW + 4 * kNG);
@@ -29,10 +37,10 @@ struct QCfg {
   static constexpr int kNHalf = D / 64;
   static constexpr int kHalf = 128 * 128;
   static constexpr int kTile = kNHalf * kHalf;
-  static constexpr int kKS = 3, kVS = 2;             // stages of K and V
-  static constexpr int kSmem = (2 + kKS + kVS) * kTile + 512;
-  // tensor memory columns: S in two buffers, dP, dQ
-  static constexpr uint32_t kS = 0, kP = 256, kDQ = 384;
+  static constexpr int kKS = D == 128 ? 4 : 8, kVS = D == 128 ? 2 : 4;   // stages of K and V
+  static constexpr int kSmem = (1 + kKS + kVS) * kTile + 512;
+  // tensor memory columns: S, dP, dQ; two bf16 a column: dS, Q
+  static constexpr uint32_t kS = 0, kP = 128, kDQ = 256, kDS = 384, kQ = 448;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -59,27 +67,28 @@ __device__ __forceinline__ QItem q_item(const BwdQArgs& a, int it) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsQ, 1)
-    bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
-                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    bwd_q_kernel(const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ BwdQArgs a) {
   using C = QCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sQ = smem;
-  uint8_t* sO = sQ + C::kTile;
+  uint8_t* sO = smem;
   uint8_t* sK = sO + C::kTile;                     // [kKS]
   uint8_t* sV = sK + C::kKS * C::kTile;            // [kVS]
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(sV + C::kVS * C::kTile);
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* k_full = q_empty + 1;                  // [kKS]
+  uint64_t* o_full = reinterpret_cast<uint64_t*>(sV + C::kVS * C::kTile);
+  uint64_t* o_empty = o_full + 1;
+  uint64_t* k_full = o_empty + 1;                  // [kKS]
   uint64_t* k_empty = k_full + C::kKS;
   uint64_t* v_full = k_empty + C::kKS;             // [kVS]
   uint64_t* v_empty = v_full + C::kVS;
-  uint64_t* s_full = v_empty + C::kVS;                // [2] S of the block is in its buffer
-  uint64_t* dp_full = s_full + 2;
-  // [2] dS written over S: one per buffer, as the warp that waits for both (dQ) may fall
-  // behind the one that lets the next dS be made (dP)
-  uint64_t* ds_full = dp_full + 1;
-  uint64_t* acc_full = ds_full + 2;                // the item's dQ is complete
+  uint64_t* q_full = v_empty + C::kVS;             // the item's Q is in tensor memory
+  uint64_t* s_full = q_full + 1;                   // S of the block
+  uint64_t* s_read = s_full + 1;
+  uint64_t* dp_full = s_read + 1;                  // dP of the block
+  uint64_t* ds_full = dp_full + 1;                 // dP read, dS written; next K and V landed
+  uint64_t* ds_read = ds_full + 1;                 // its dQ product is done
+  uint64_t* first = ds_read + 1;                   // the item's first copies landed
+  uint64_t* acc_full = first + 1;                // the item's dQ is complete
   uint64_t* acc_empty = acc_full + 1;              // ... and read out
   uint64_t* bar_fin = acc_empty + 1;
   uint64_t* it_full = bar_fin + 1;                 // [kRing]
@@ -90,8 +99,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 2);
+    mbar_init(o_full, 1);
+    mbar_init(o_empty, 1);
     for (int i = 0; i < C::kKS; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
@@ -100,26 +109,27 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
+    mbar_init(q_full, 128 * kNG);
+    mbar_init(s_full, 1);
+    mbar_init(s_read, 128 * kNG);
     mbar_init(dp_full, 1);
-    mbar_init(&ds_full[0], 128 * kNG);
-    mbar_init(&ds_full[1], 128 * kNG);
+    mbar_init(ds_full, 128 * kNG + 1);
+    mbar_init(first, 1);
+    mbar_init(ds_read, 1);
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 128 * kNG);
-    mbar_init(bar_fin, 2);
+    mbar_init(bar_fin, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&it_full[i], 1);
       mbar_init(&it_empty[i], kReaders);
     }
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_o);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (warp == kAW) tmem_alloc(tmem_slot, 512);
+  if (warp == kMmaW) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -144,7 +154,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   };
 
   if (warp == 0) {
-    // ----------------------------------------------------- Q and dO (warp 0)
+    // ----------------------------------------------------------- dO (warp 0)
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_first();
       int cur = atomicAdd(a.next_item, 1);
@@ -166,25 +176,22 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         mbar_arrive(&it_full[slot]);
         const QItem d = q_item(a, cur);
         if (d.kb0 < d.kb1) {
-          if (n > 0 && !mbar_wait(q_empty, (uint32_t)(n - 1) & 1, a.status, a.wait_polls)) {
+          if (n > 0 && !mbar_wait(o_empty, (uint32_t)(n - 1) & 1, a.status, a.wait_polls)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(q_full, 2 * C::kTile);
+          mbar_arrive_expect_tx(o_full, C::kTile);
 #pragma unroll
-          for (int hf = 0; hf < C::kNHalf; ++hf) {
-            tma_load_4d_hint(smem_u32(sQ + hf * C::kHalf), &tm_q, q_full, hf * 64, d.h, d.qt * 128,
+          for (int hf = 0; hf < C::kNHalf; ++hf)
+            tma_load_4d_hint(smem_u32(sO + hf * C::kHalf), &tm_o, o_full, hf * 64, d.h, d.qt * 128,
                              d.b, pol);
-            tma_load_4d_hint(smem_u32(sO + hf * C::kHalf), &tm_o, q_full, hf * 64, d.h, d.qt * 128,
-                             d.b, pol);
-          }
           ++n;
         }
         cur = nx;
       }
       if (!ok) *abort_flag = 1;
       // no copy may still be landing when the CTA exits
-      if (n > 0) mbar_wait(q_full, (uint32_t)(n - 1) & 1, nullptr);
+      if (n > 0) mbar_wait(o_full, (uint32_t)(n - 1) & 1, nullptr);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------- K and V (warp 1)
@@ -228,127 +235,160 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       mbar_wait(&k_full[m % C::kKS], (uint32_t)(m / C::kKS) & 1, nullptr);
     for (int m = n - 1; m >= 0 && m >= n - C::kVS; --m)
       mbar_wait(&v_full[m % C::kVS], (uint32_t)(m / C::kVS) & 1, nullptr);
-  } else if (warp == kAW || warp == kBW) {
-    // ------------------------------------------------------- MMA (warps 2, 3)
-    // Two warps, as issuing takes longer than the products: with one for all three a step
-    // took 2650 cycles, 1536 of them MMAs.
+  } else if (warp == kMmaW) {
+    // ---------------------------------------------------------- MMA (warp 2)
     constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
     constexpr uint32_t idesc_q = idesc_bf16(128, D, false, true);
-    const uint64_t qd = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
     const uint64_t od = smem_desc(smem_u32(sO), 16, 1024, kSwizzle128B);
     const uint64_t kd = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
     const uint64_t vd = smem_desc(smem_u32(sV), 16, 1024, kSwizzle128B);
     const uint64_t kmn = smem_desc(smem_u32(sK), C::kHalf, 1024, kSwizzle128B);
-    auto product = [&](uint32_t d, uint64_t ad, uint64_t bd) {
+    // 16 dims: (j & 3) * 32 bytes within a 64-dim half
+    auto dims = [](int j) { return (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4); };
+    auto stage = [](int i) { return (uint64_t)((i * C::kTile) >> 4); };
+    // (inside an elected branch)
+    auto issue_s = [&](int m) {
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        const uint64_t o = (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4);
-        tc_mma_f16(tmem + d, ad + o, bd + o, idesc_s, j > 0 ? 1u : 0u);
-      }
+      for (int j = 0; j < D / 16; ++j)
+        tc_mma_f16_ts(tmem + C::kS, tmem + C::kQ + j * 8, kd + stage(m % C::kKS) + dims(j), idesc_s,
+                      j > 0 ? 1u : 0u);
+      tc_commit(s_full);
+    };
+    auto issue_dp = [&](int m, bool last) {
+      const int vs = m % C::kVS;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+        tc_mma_f16(tmem + C::kP, od + dims(j), vd + stage(vs) + dims(j), idesc_s, j > 0 ? 1u : 0u);
+      tc_commit(dp_full);
+      tc_commit(&v_empty[vs]);
+      if (last) tc_commit(o_empty);
     };
     int it, n = 0, nu = 0;       // blocks and items (with blocks) so far
     bool ok;
-    if (warp == kAW) {
-      // ---------------------------------------- S(0), S(1); dQ(n), S(n + 2)
-      while (next_item(it, ok)) {
-        const QItem d = q_item(a, it);
-        const int nt = d.kb1 - d.kb0;
-        if (nt == 0) continue;
-        const int64_t t_last = (int64_t)a.pos.q_start[d.b] + T - 1;
-        ok = wait_all(q_full, (uint32_t)nu & 1);
+    while (next_item(it, ok)) {
+      const QItem d = q_item(a, it);
+      const int nt = d.kb1 - d.kb0;
+      if (nt == 0) continue;
+      // (S and dP of the item before have been read: its last dQ product waited for that)
+      ok = wait_all(first, (uint32_t)nu & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_s(n);
+        issue_dp(n, nt == 1);
+      }
+      __syncwarp();
+      if (nt > 1) {
+        ok = wait_all(s_read, (uint32_t)n & 1);
         if (!ok) break;
-        auto issue_s = [&](int m, int t) {         // of block m, the item's t-th
-          const int ks = m % C::kKS;
-          if (!wait_all(&k_full[ks], (uint32_t)(m / C::kKS) & 1)) return false;
-          const int64_t left = t_last - (int64_t)(d.kb0 + t) * kBlock;
-          if (left < kBlock - 1) {
-            // rows behind the sequence's last query may hold anything; in dQ's product
-            // they are multiplied by zeros: cleared
-            for (int e = lane; e < C::kNHalf * kBlock * 8; e += 32) {
-              const int row = e >> 3 & 127;
-              if (row > (int)left)
-                sts128(smem_u32(sK) + ks * C::kTile + (e >> 10) * C::kHalf + row * 128 + (e & 7) * 16,
-                       make_uint4(0, 0, 0, 0));
-            }
-            fence_async();
-            __syncwarp();
-          }
-          tc_fence_after();
-          if (elect_one()) {
-            product(C::kS + (m & 1) * 128, qd, kd + (uint64_t)((ks * C::kTile) >> 4));
-            tc_commit(&s_full[m & 1]);
-            if (t + 1 == nt) tc_commit(q_empty);
-          }
-          __syncwarp();
-          return true;
-        };
-        ok = issue_s(n, 0) && (nt == 1 || issue_s(n + 1, 1));
-        for (int t = 0; t < nt && ok; ++t, ++n) {
-          const int ks = n % C::kKS;
-          ok = wait_all(&ds_full[n & 1], (uint32_t)(n >> 1) & 1) &&
-               (t > 0 || nu == 0 || wait_all(acc_empty, (uint32_t)(nu - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            // dS: a warpgroup's keys at the start of its columns of S, two in each
+        tc_fence_after();
+        if (elect_one()) issue_s(n + 1);
+        __syncwarp();
+      }
+      for (int t = 0; t < nt; ++t, ++n) {
+        const int ks = n % C::kKS;
+        ok = wait_all(ds_full, (uint32_t)n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (t + 1 < nt) issue_dp(n + 1, t + 2 == nt);    // first: dS(n + 1) waits for it
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              tc_mma_f16_ts(tmem + C::kDQ,
-                            tmem + C::kS + (n & 1) * 128 + j * 16 / kCols * kCols + j * 16 % kCols / 2,
-                            kmn + (uint64_t)((ks * C::kTile + j * 2048) >> 4), idesc_q,
-                            t > 0 || j > 0 ? 1u : 0u);
-            tc_commit(&k_empty[ks]);
-            if (t + 1 == nt) tc_commit(acc_full);
-          }
-          __syncwarp();
-          // over dS(n), which dQ(n), issued before, reads
-          if (t + 2 < nt) ok = issue_s(n + 2, t + 2);
+          for (int j = 0; j < 8; ++j)
+            tc_mma_f16_ts(tmem + C::kDQ, tmem + C::kDS + j * 8, kmn + stage(ks) + (uint64_t)(j * 128),
+                          idesc_q, t > 0 || j > 0 ? 1u : 0u);
+          tc_commit(ds_read);
+          tc_commit(&k_empty[ks]);
+          if (t + 1 == nt) tc_commit(acc_full);
         }
-        if (!ok) break;
-        ++nu;
-      }
-    } else {
-      // ------------------------------------------------------------ dP(n)
-      while (next_item(it, ok)) {
-        const QItem d = q_item(a, it);
-        const int nt = d.kb1 - d.kb0;
-        if (nt == 0) continue;
-        ok = wait_all(q_full, (uint32_t)nu & 1);
-        for (int t = 0; t < nt && ok; ++t, ++n) {
-          const int vs = n % C::kVS;
-          // dP(n - 1) has been read
-          ok = wait_all(&v_full[vs], (uint32_t)(n / C::kVS) & 1) &&
-               (n == 0 || wait_all(&ds_full[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1));
+        __syncwarp();
+        if (t + 2 < nt) {
+          ok = wait_all(s_read, (uint32_t)(n + 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) {
-            product(C::kP, od, vd + (uint64_t)((vs * C::kTile) >> 4));
-            tc_commit(dp_full);
-            tc_commit(&v_empty[vs]);
-            if (t + 1 == nt) tc_commit(q_empty);
-          }
+          if (elect_one()) issue_s(n + 2);
           __syncwarp();
         }
-        if (!ok) break;
-        ++nu;
       }
+      if (!ok) break;
+      ++nu;
     }
     if (!ok && lane == 0) *abort_flag = 1;
-    // all MMAs of both warps done before tensor memory is released
+    // all MMAs done before tensor memory is released
     if (elect_one()) tc_commit(bar_fin);
     __syncwarp();
     mbar_wait(bar_fin, 0, nullptr);
-  } else {
-    // ------------------------------------------------- dS, dQ (warps 4-19)
-    const int c = (warp - kSoftW) >> 2;           // keys kCols c ..; dims c D/kNG .. of dQ
+  } else if (warp == kWaitW) {
+    // ---------------------------------------------- the MMA warp's waits (warp 3)
+    // A wait takes a warp 190 cycles even where it is over, and few MMAs are in flight
+    // behind an issue: this warp waits for the copies, and arrives with the softmax warps.
+    int it, n = 0, nu = 0;
+    bool ok;
+    while (next_item(it, ok)) {
+      const QItem d = q_item(a, it);
+      const int nt = d.kb1 - d.kb0;
+      if (nt == 0) continue;
+      const int64_t t_last = (int64_t)a.pos.q_start[d.b] + T - 1;
+      auto wait_k = [&](int m, int t) {          // K of block m, the item's t-th
+        const int ks = m % C::kKS;
+        if (!wait_all(&k_full[ks], (uint32_t)(m / C::kKS) & 1)) return false;
+        const int64_t left = t_last - (int64_t)(d.kb0 + t) * kBlock;
+        if (left < kBlock - 1) {
+          // rows behind the sequence's last query may hold anything; in dQ's product
+          // they are multiplied by zeros: cleared
+          for (int e = lane; e < C::kNHalf * kBlock * 8; e += 32) {
+            const int row = e >> 3 & 127;
+            if (row > (int)left)
+              sts128(smem_u32(sK) + ks * C::kTile + (e >> 10) * C::kHalf + row * 128 + (e & 7) * 16,
+                     make_uint4(0, 0, 0, 0));
+          }
+          fence_async();
+          __syncwarp();
+        }
+        return true;
+      };
+      auto wait_v = [&](int m) {
+        return wait_all(&v_full[m % C::kVS], (uint32_t)(m / C::kVS) & 1);
+      };
+      ok = wait_all(q_full, (uint32_t)nu & 1) && wait_all(o_full, (uint32_t)nu & 1) && wait_k(n, 0) &&
+           (nt == 1 || wait_k(n + 1, 1)) && wait_v(n);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(first);
+      for (int t = 0; t < nt; ++t, ++n) {
+        // an arrival must not count for the phase before
+        ok = __any_sync(0xffffffffu, *abort_flag != 0) == 0 && (t + 1 >= nt || wait_v(n + 1)) &&
+             (t + 2 >= nt || wait_k(n + 2, t + 2)) &&
+             (t > 0 || nu == 0 || wait_all(acc_empty, (uint32_t)(nu - 1) & 1)) &&
+             (n == 0 || wait_all(ds_full, (uint32_t)(n - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(ds_full);
+      }
+      if (!ok) break;
+      ++nu;
+    }
+    if (!ok && lane == 0) *abort_flag = 1;
+  } else if (warp >= kSoftW) {
+    // -------------------------------------------- Q, dS, dQ (warps 4-19)
+    // keys kCols c ..; dims c D/kNG .. of Q and dQ
+    const int c = (warp - kSoftW) >> 2;
+    constexpr int kDims = D / kNG;
     const int quad = warp & 3;
     const int r = quad * 32 + lane;               // query of the tile = TMEM lane
     const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16);
     const float sl = a.s.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl);
+    // an item's Q: this thread's dims of its query, read ahead of the item
+    uint4 q[kDims / 8];
+    auto load_q = [&](const QItem& d) {
+      const int i = d.qt * 128 + r;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + (((size_t)d.b * T + (i < T ? i : 0)) * a.s.H + d.h) * D + c * kDims);
+#pragma unroll
+      for (int k = 0; k < kDims / 8; ++k) q[k] = i < T ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+    };
     int it, n = 0, nu = 0;
-    bool ok;
-    while (next_item(it, ok)) {
+    bool ok, some = next_item(it, ok);
+    if (some) load_q(q_item(a, it));
+    while (some) {
       const QItem d = q_item(a, it);
       const int i = d.qt * 128 + r;
       const int64_t tq = (int64_t)a.pos.q_start[d.b] + i;
@@ -357,22 +397,37 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
                         (i & 7);
       const float nl = st[0], nd = st[8];
       const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
+      const bool any = d.kb0 < d.kb1;
+      if (any) {
+        // every S of the item before is done: this thread has read its last one
+        if constexpr (kDims == 32) {
+          const uint32_t w[16] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w,
+                                  q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
+          tmem_st16(base + C::kQ + c * 16, w);
+        } else {
+          const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+          tmem_st8(base + C::kQ + c * 8, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(q_full);
+      }
       for (int kb = d.kb0; kb < d.kb1; ++kb, ++n) {
         // keys past the query, and rows past the last query, whatever they hold
         const int64_t l64 = min(tq, (int64_t)a.pos.q_start[d.b] + T - 1) - (int64_t)kb * kBlock;
         const int lim = (int)(l64 < kBlock ? l64 : kBlock) - c * kCols;
         const bool masked = __any_sync(0xffffffffu, lim < kCols - 1);
-        ok = __all_sync(0xffffffffu,
-                        *abort_flag == 0 &&
-                            mbar_wait(&s_full[n & 1], (uint32_t)(n >> 1) & 1, a.status, a.wait_polls));
+        ok = __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(s_full, (uint32_t)n & 1, a.status,
+                                                                   a.wait_polls));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t s_at = base + C::kS + (n & 1) * 128 + c * kCols;
         float2 p[kCols / 2];
         {
           uint32_t x[32];
-          tmem_ld32(s_at, x);
+          tmem_ld32(base + C::kS + c * kCols, x);
           tmem_ld_wait();
+          tc_fence_before();
+          mbar_arrive(s_read);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = ffma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
@@ -383,36 +438,47 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(dp_full, (uint32_t)n & 1, a.status, a.wait_polls));
         if (!ok) break;
         tc_fence_after();
-        uint32_t x[32], w[16];
-        tmem_ld32(base + C::kP + c * kCols, x);
-        tmem_ld_wait();
+        uint32_t w[16];
+        auto ds_of = [&](auto mask) {
+          uint32_t x[32];
+          tmem_ld32(base + C::kP + c * kCols, x);
+          tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 y = fadd2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), nd2);
-          y = fmul2(p[e], y);
-          if (masked) {
-            y.x = 2 * e <= lim ? y.x : 0.f;
-            y.y = 2 * e + 1 <= lim ? y.y : 0.f;
+          for (int e = 0; e < 16; ++e) {
+            float2 y = fadd2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), nd2);
+            y = fmul2(p[e], y);
+            if constexpr (mask.value) {
+              y.x = 2 * e <= lim ? y.x : 0.f;
+              y.y = 2 * e + 1 <= lim ? y.y : 0.f;
+            }
+            w[e] = pack_bf16(y.x, y.y);
           }
-          w[e] = pack_bf16(y.x, y.y);
-        }
-        tmem_st16(s_at, w);              // over scores that were read already
+        };
+        if (masked) ds_of(std::true_type());
+        else ds_of(std::false_type());
+        ok = __all_sync(0xffffffffu, n == 0 || mbar_wait(ds_read, (uint32_t)(n - 1) & 1, a.status,
+                                                         a.wait_polls));
+        if (!ok) break;
+        tmem_st16(base + C::kDS + c * (kCols / 2), w);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&ds_full[n & 1]);
+        mbar_arrive(ds_full);
       }
       if (!ok) break;
+      const int done = it;
+      some = next_item(it, ok);
+      if (!ok) break;
+      if (some) load_q(q_item(a, it));
       // ---- the item's dQ: a query per thread, a run of dims per warpgroup
-      const bool any = d.kb0 < d.kb1;
       if (any) {
         ok = __all_sync(0xffffffffu, mbar_wait(acc_full, (uint32_t)nu & 1, a.status, a.wait_polls));
         if (!ok) break;
         tc_fence_after();
       }
 #pragma unroll 1
-      for (int cc = 0; cc < D / kNG / 16; ++cc) {
+      for (int cc = 0; cc < kDims / 16; ++cc) {
         uint32_t x[16];
-        const int dim = c * (D / kNG) + cc * 16;
+        const int dim = c * kDims + cc * 16;
         if (any) {
           tmem_ld16(base + C::kDQ + dim, x);
           tmem_ld_wait();
@@ -422,7 +488,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         }
         if (i >= T) continue;
         if (a.splits > 1) {
-          float* dst = a.part + ((size_t)it * 128 + r) * D + dim;
+          float* dst = a.part + ((size_t)done * 128 + r) * D + dim;
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {
             const uint32_t y[8] = {x[e], x[e + 1], x[e + 2], x[e + 3],
@@ -453,7 +519,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kAW) {
+  if (warp == kMmaW) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -488,14 +554,13 @@ template <int D>
 cudaError_t launch_q(const BwdQArgs& a, const AttnBwd& t, cudaStream_t st) {
   using C = QCfg<D>;
   const Shape& s = a.s;
-  CUtensorMap tm_q, tm_o, tm_k, tm_v;
+  CUtensorMap tm_o, tm_k, tm_v;
   {
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)s.H, (cuuint64_t)s.T, (cuuint64_t)s.B};
     cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)s.H * D * 2,
                              (cuuint64_t)s.T * s.H * D * 2};
     cuuint32_t box[4] = {64, 1, 128, 1};
-    if (!encode_bf16_map(&tm_q, t.q, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_bf16_map(&tm_o, t.dout, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_bf16_map(&tm_o, t.dout, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)s.G, (cuuint64_t)(s.cache_blocks() * kBlock)};
@@ -511,7 +576,7 @@ cudaError_t launch_q(const BwdQArgs& a, const AttnBwd& t, cudaStream_t st) {
   const int64_t items = (int64_t)a.nitems * a.splits;
   note_launches(1);
   bwd_q_kernel<D><<<(unsigned)(items < ctas ? items : ctas), kThreadsQ, C::kSmem, st>>>(
-      tm_q, tm_o, tm_k, tm_v, a);
+      tm_o, tm_k, tm_v, a);
   if (a.splits > 1) {
     note_launches(1);
     bwd_q_join_kernel<D><<<(unsigned)(((int64_t)a.nitems * 128 * (D / 4) + 255) / 256), 256, 0, st>>>(a);
