@@ -17,10 +17,12 @@ namespace {
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Tiles per unit: a block's work is divided where it would hold up the others, i.e. is
-// more than a quarter of a CTA's share of all `tiles`, but not below 16 tiles (a piece
-// costs about three tiles' time: K and V, the sums' way out and back).  A divided block
-// of n > piece tiles has ceil(n / piece) <= 2 n / piece slots, so a call has at most 2
-// tiles / piece, and no call of up to `tiles` tiles more than the second bound.
+// more than a quarter of a CTA's share of all `tiles` (the largest units go first), but
+// not below 16 tiles (a piece costs about three tiles' time: K and V, the sums' way out
+// and back).  8192 sparse queries at 48/8 heads: 1093 us with a quarter, 1219 with two
+// thirds.  A divided block of n > piece tiles has ceil(n / piece) <= 2 n / piece slots,
+// so a call has at most 2 tiles / piece, and no call of up to `tiles` tiles more than the
+// second bound.
 constexpr int kMinPiece = 16;
 int piece_tiles(int64_t tiles) {
   const int64_t p = tiles / (4 * kBwdSms) + 1;
@@ -34,17 +36,21 @@ int most_slots(int64_t tiles) {
 
 int rows_per_entry(const Shape& s) { return s.H / s.G <= 8 ? 8 : 16; }
 
-// Tiles of a dense call.
-int64_t dense_tiles(const BwdArgs& a) {
+// Tiles of a dense call, or with `piece` the slots of its divided blocks.
+int64_t dense_tiles(const BwdArgs& a, int piece = 0) {
   int64_t n = 0;
+  auto add = [&](int64_t blocks, int query_tiles) {
+    const int64_t t = (int64_t)query_tiles * a.hpg;
+    n += blocks * a.s.G * (piece == 0 ? t : (t > piece ? (t + piece - 1) / piece : 0));
+  };
   for (int b = 0; b < a.s.B; ++b) {
-    // blocks up to the first query's see every tile, each later one a tile less or the same
+    // blocks up to the first query's see every tile, later ones fewer
     const int first = a.pos.q_start[b] / kBlock;
     const int last = (int)(((int64_t)a.pos.q_start[b] + a.s.T - 1) / kBlock);
-    n += (int64_t)(first + 1) * a.nqt;
-    for (int kb = first + 1; kb <= last; ++kb) n += a.nqt - bwd_first_tile(a, b, kb);
+    add(first + 1, a.nqt);
+    for (int kb = first + 1; kb <= last; ++kb) add(1, a.nqt - bwd_first_tile(a, b, kb));
   }
-  return n * a.s.G * a.hpg;
+  return n;
 }
 
 // Tiles of a call or a pass, at most.
@@ -159,9 +165,7 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
     a.last = t0 + tp >= s.T;
     const int64_t tiles = sparse ? max_tiles(s, true, a.Tp, a.nbl) : dense_tiles(a);
     a.piece = piece_tiles(tiles);
-    a.max_slots = slots_of(tiles);
-    // a group's work for each CTA is less than a few of its largest units
-    a.mixed = tiles / s.G / kBwdSms < 4 * (int64_t)a.piece;
+    a.max_slots = sparse ? slots_of(tiles) : (int)dense_tiles(a, a.piece);
     if ((e = sparse ? launch_bwd_lists(a, st) : launch_bwd_units(a, st)) != cudaSuccess) return e;
     if ((e = launch_bwd_kv(a, t, st)) != cudaSuccess) return e;
     if ((e = launch_bwd_join_kv(a, st)) != cudaSuccess) return e;

@@ -38,7 +38,6 @@ struct BwdArgs {
   int hpg, rpe, R;           // heads per group; sparse: rows per entry, entries per tile
   int nqt;                   // dense: 128-query tiles per sequence
   int piece;                 // tiles per unit (at most)
-  bool mixed;                // units of all groups by size (else group by group)
   const int32_t* sel;        // sparse: the selection
   int32_t* cnt;              // [B][chunks][G][nbl]: entries per chunk, then those before
   int chunks;

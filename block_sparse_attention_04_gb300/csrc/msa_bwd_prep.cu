@@ -326,8 +326,8 @@ __global__ void __launch_bounds__(128) bwd_prefix_kernel(const __grid_constant__
 // ---- units ------------------------------------------------------------------
 // One CTA: every item (g, b, kb) below kv_len as one unit, or as several of at most
 // `piece` tiles, whose sums are joined in their order afterwards.  The units are handed
-// out as CTAs become free, so the large ones come first: in each group (its queries'
-// rows stay in L2 meanwhile), or, where a group has little work for each CTA, of all.
+// out as CTAs become free, so the large ones come first (group by group, which would keep a
+// group's rows in L2, 8192 sparse queries take 1673 us for 1219).
 constexpr int kClasses = 64;               // of sizes, the largest first
 __device__ __forceinline__ int item_tiles(const BwdArgs& a, int64_t L, int* n) {
   const int kb = (int)(L % a.nbl), b = (int)(L / a.nbl % a.s.B);
@@ -338,19 +338,17 @@ __device__ __forceinline__ int item_tiles(const BwdArgs& a, int64_t L, int* n) {
   }
   return *n = (a.nqt - bwd_first_tile(a, b, kb)) * a.hpg;
 }
-__device__ __forceinline__ int item_class(const BwdArgs& a, int64_t L, int tiles) {
-  const int g = a.mixed ? 0 : (int)(L / a.nbl / a.s.B);
-  const int size = (int)((int64_t)min(tiles, a.piece) * (kClasses - 1) / a.piece);
-  return g * kClasses + kClasses - 1 - size;
+__device__ __forceinline__ int item_class(const BwdArgs& a, int tiles) {
+  return kClasses - 1 - (int)((int64_t)min(tiles, a.piece) * (kClasses - 1) / a.piece);
 }
 
 __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__ BwdArgs a) {
   __shared__ int s_s[1024], s_e[1024];
-  __shared__ int s_class[8 * kClasses];    // units of a class, then the next one's place
+  __shared__ int s_class[kClasses];    // units of a class, then the next one's place
   const int64_t n = (int64_t)a.s.G * a.s.B * a.nbl;
   const int64_t per = (n + 1023) / 1024;
   const int64_t lo = min(n, (int64_t)threadIdx.x * per), hi = min(n, lo + per);
-  for (int k = threadIdx.x; k < 8 * kClasses; k += 1024) s_class[k] = 0;
+  for (int k = threadIdx.x; k < kClasses; k += 1024) s_class[k] = 0;
   __syncthreads();
   int sl = 0, en = 0;
   for (int64_t L = lo; L < hi; ++L) {
@@ -359,7 +357,7 @@ __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__
     if (t < 0) continue;
     en += t * a.R;
     const int pieces = t > a.piece ? (t + a.piece - 1) / a.piece : 1;
-    atomicAdd(&s_class[item_class(a, L, t)], pieces);
+    atomicAdd(&s_class[item_class(a, t)], pieces);
     if (pieces > 1) sl += pieces;
   }
   s_s[threadIdx.x] = sl;
@@ -378,23 +376,16 @@ __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__
   }
   sl = s_s[threadIdx.x] - sl;
   en = s_e[threadIdx.x] - en;
-  if (threadIdx.x < 32) {                  // exclusive scan of the classes, 16 a lane
-    int v[8 * kClasses / 32], sum = 0;
-    for (int k = 0; k < 8 * kClasses / 32; ++k) {
-      v[k] = s_class[threadIdx.x * (8 * kClasses / 32) + k];
-      sum += v[k];
-    }
-    int x = sum;
+  if (threadIdx.x < 32) {                  // exclusive scan of the classes, two a lane
+    const int v0 = s_class[2 * threadIdx.x], v1 = s_class[2 * threadIdx.x + 1];
+    int x = v0 + v1;
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
       if ((int)threadIdx.x >= o) x += y;
     }
     if (threadIdx.x == 31) a.n_units[0] = x;
-    x -= sum;
-    for (int k = 0; k < 8 * kClasses / 32; ++k) {
-      s_class[threadIdx.x * (8 * kClasses / 32) + k] = x;
-      x += v[k];
-    }
+    s_class[2 * threadIdx.x] = x - v0 - v1;
+    s_class[2 * threadIdx.x + 1] = x - v1;
   }
   if (threadIdx.x == 1023) {
     a.n_units[1] = s_s[1023];
@@ -412,7 +403,7 @@ __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__
     const int x = kb | g << 15 | b << 18;
     const int pieces = t > a.piece ? (t + a.piece - 1) / a.piece : 1;
     // (the order within a class is the run's own: the units do not depend on one another)
-    int at = atomicAdd(&s_class[item_class(a, L, t)], pieces);
+    int at = atomicAdd(&s_class[item_class(a, t)], pieces);
     for (int k = 0; k < pieces; ++k) {
       // pieces of nearly the same size
       const int t0 = (int)((int64_t)t * k / pieces), t1 = (int)((int64_t)t * (k + 1) / pieces);
@@ -431,44 +422,54 @@ __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__
 }
 
 // ---- joins --------------------------------------------------------------------
-// dQ of a (query, group): its selected blocks' parts, times the scale.  A warp each: an
-// entry's rows are rpe x 32 contiguous bytes per 16 dims.
+// dQ of a (query, group): its selected blocks' parts, times the scale.  A warp for N of the
+// reads that cover an entry's rows, which are rpe x 32 contiguous bytes per 16 dims; the
+// reads of four slots are in flight together.
 template <int D, int RPE>
 __global__ void __launch_bounds__(256) bwd_join_q_kernel(const __grid_constant__ BwdArgs a) {
-  constexpr int PER = 16 / RPE;                  // 16-dim chunks that a warp's read covers
-  constexpr int N = D / 16 / PER;
+  constexpr int PER = 16 / RPE, R = 128 / RPE;   // 16-dim chunks that a warp's read covers
+  constexpr int ALL = D / 16 / PER, N = ALL < 2 ? ALL : 2, U = 4;
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (w >= (int64_t)a.s.B * a.Tp * a.s.G) return;
-  const int g = (int)(w % a.s.G);
-  const int64_t r = w / a.s.G;
+  const int64_t qg = w / (ALL / N);
+  if (qg >= (int64_t)a.s.B * a.Tp * a.s.G) return;
+  const int g = (int)(qg % a.s.G);
+  const int64_t r = qg / a.s.G;
   const int b = (int)(r / a.Tp), i = a.t0 + (int)(r % a.Tp);
-  const int hh = (lane >> 1) % RPE, ch0 = (lane >> 1) / RPE, d0 = (lane & 1) * 8;
+  const int hh = (lane >> 1) % RPE, d0 = (lane & 1) * 8;
+  const int ch0 = (int)(w % (ALL / N)) * N * PER + (lane >> 1) / RPE;
   int e = -1;
-  if (lane < kTopk) e = a.where[w * kTopk + lane];
+  if (lane < kTopk) e = a.where[qg * kTopk + lane];
+  const uint16_t* part = a.part_dq + (size_t)ch0 * 2048 + hh * 16 + d0;
   float acc[N][8];
 #pragma unroll
   for (int k = 0; k < N; ++k)
 #pragma unroll
     for (int x = 0; x < 8; ++x) acc[k][x] = 0.f;
-#pragma unroll 2
-  for (int j = 0; j < kTopk; ++j) {
-    const int ej = __shfl_sync(0xffffffffu, e, j);
-    if (ej < 0 || hh >= a.hpg) continue;
-    const uint16_t* src = a.part_dq +
-                          ((size_t)(ej / a.R) * (D / 16) + ch0) * 2048 + ((ej % a.R) * RPE + hh) * 16 + d0;
-    uint4 v[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = __ldcs(reinterpret_cast<const uint4*>(src + k * PER * 2048));
+  for (int j0 = 0; j0 < kTopk; j0 += U) {
+    uint4 v[U][N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    for (int u = 0; u < U; ++u) {
+      const int ej = __shfl_sync(0xffffffffu, e, j0 + u);
+      const uint16_t* src = part + (size_t)(ej / R) * (D / 16 * 2048) + ej % R * RPE * 16;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        acc[k][2 * x] += bf16lo(u[x]);
-        acc[k][2 * x + 1] += bf16hi(u[x]);
+      for (int k = 0; k < N; ++k) {
+        v[u][k] = make_uint4(0, 0, 0, 0);
+        if (ej >= 0 && hh < a.hpg) v[u][k] = __ldcs(reinterpret_cast<const uint4*>(src + k * PER * 2048));
       }
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const uint32_t y[4] = {v[u][k].x, v[u][k].y, v[u][k].z, v[u][k].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          acc[k][2 * x] += bf16lo(y[x]);
+          acc[k][2 * x + 1] += bf16hi(y[x]);
+        }
+      }
   }
   if (hh >= a.hpg) return;
   const float f = a.s.scale;
@@ -485,15 +486,15 @@ __global__ void __launch_bounds__(256) bwd_join_q_kernel(const __grid_constant__
 constexpr int kJoinParts = 8;
 template <int D>
 __global__ void __launch_bounds__(256) bwd_join_kv_kernel(const __grid_constant__ BwdArgs a) {
-  const int slot = blockIdx.x;
+  constexpr int ROWS = 2 * kBlock / kJoinParts;
+  const int slot = blockIdx.x, part = blockIdx.y;
   if (slot >= a.n_units[1]) return;
   const int4 d = a.slots[slot];
   if (d.y == 0) return;
   const int kb = d.x & 0x7FFF, g = d.x >> 15 & 7, b = d.x >> 18;
-  constexpr int ROWS = 2 * kBlock / kJoinParts, C4 = D / 4;
-  for (int e = threadIdx.x; e < ROWS * C4; e += 256) {
+  for (int e = threadIdx.x; e < ROWS * (D / 4); e += 256) {
     // dv's 128 rows, then dk's
-    const int row = blockIdx.y * ROWS + e / 2 % ROWS, c = (e / 2 / ROWS * 2 + e % 2) * 4;
+    const int row = part * ROWS + e / 2 % ROWS, c = (e / 2 / ROWS * 2 + e % 2) * 4;
     const int tok = row % kBlock;
     const bool is_k = row >= kBlock;
     if ((int64_t)kb * kBlock + tok >= a.pos.kv_len[b]) continue;
@@ -580,7 +581,8 @@ cudaError_t launch_bwd_units(const BwdArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_bwd_join_q(const BwdArgs& a, cudaStream_t st) {
-  const unsigned ctas = (unsigned)(((int64_t)a.s.B * a.Tp * a.s.G + 7) / 8);
+  const int reads = a.s.D / 16 * a.rpe / 16;               // of an entry's rows, two a warp
+  const unsigned ctas = (unsigned)(((int64_t)a.s.B * a.Tp * a.s.G * (reads < 2 ? 1 : reads / 2) + 7) / 8);
   note_launches(1);
   if (a.s.D == 128) {
     if (a.rpe == 8) bwd_join_q_kernel<128, 8><<<ctas, 256, 0, st>>>(a);

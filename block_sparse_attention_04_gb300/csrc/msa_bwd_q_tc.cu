@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       auto wait_v = [&](int m) {
         return wait_all(&v_full[m % C::kVS], (uint32_t)(m / C::kVS) & 1);
       };
-      ok = wait_all(q_full, (uint32_t)nu & 1) && wait_all(o_full, (uint32_t)nu & 1) && wait_k(n, 0) &&
-           (nt == 1 || wait_k(n + 1, 1)) && wait_v(n);
+      ok = wait_all(o_full, (uint32_t)nu & 1) && wait_k(n, 0) && (nt == 1 || wait_k(n + 1, 1)) &&
+           wait_v(n) && wait_all(q_full, (uint32_t)nu & 1);
       if (!ok) break;
       if (lane == 0) mbar_arrive(first);
       for (int t = 0; t < nt; ++t, ++n) {
@@ -376,42 +376,45 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16);
     const float sl = a.s.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl);
-    // an item's Q: this thread's dims of its query, read ahead of the item
-    uint4 q[kDims / 8];
-    auto load_q = [&](const QItem& d) {
+    // An item's Q (this thread's dims of its query) and its row's two numbers are read, and Q
+    // is put into tensor memory, before the item ahead is written out: every S of that one
+    // is done, as this thread has read the last, and the next item's first products run
+    // meanwhile.
+    float nl = 0.f, nd = 0.f;
+    auto begin = [&](const QItem& d) {
       const int i = d.qt * 128 + r;
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + (((size_t)d.b * T + (i < T ? i : 0)) * a.s.H + d.h) * D + c * kDims);
+      uint4 q[kDims / 8];
 #pragma unroll
       for (int k = 0; k < kDims / 8; ++k) q[k] = i < T ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+      const float* st = reinterpret_cast<const float*>(
+                            a.stat + ((size_t)(d.b * a.s.H + d.h) * a.stat_groups + (i >> 3)) * kStatBytes) +
+                        (i & 7);
+      nl = st[0];
+      nd = st[8];
+      if (d.kb0 == d.kb1) return;
+      if constexpr (kDims == 32) {
+        const uint32_t w[16] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w,
+                                q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
+        tmem_st16(base + C::kQ + c * 16, w);
+      } else {
+        const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+        tmem_st8(base + C::kQ + c * 8, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(q_full);
     };
     int it, n = 0, nu = 0;
     bool ok, some = next_item(it, ok);
-    if (some) load_q(q_item(a, it));
+    if (some) begin(q_item(a, it));
     while (some) {
       const QItem d = q_item(a, it);
       const int i = d.qt * 128 + r;
       const int64_t tq = (int64_t)a.pos.q_start[d.b] + i;
-      const float* st = reinterpret_cast<const float*>(
-                            a.stat + ((size_t)(d.b * a.s.H + d.h) * a.stat_groups + (i >> 3)) * kStatBytes) +
-                        (i & 7);
-      const float nl = st[0], nd = st[8];
       const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
       const bool any = d.kb0 < d.kb1;
-      if (any) {
-        // every S of the item before is done: this thread has read its last one
-        if constexpr (kDims == 32) {
-          const uint32_t w[16] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w,
-                                  q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
-          tmem_st16(base + C::kQ + c * 16, w);
-        } else {
-          const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
-          tmem_st8(base + C::kQ + c * 8, w);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(q_full);
-      }
       for (int kb = d.kb0; kb < d.kb1; ++kb, ++n) {
         // keys past the query, and rows past the last query, whatever they hold
         const int64_t l64 = min(tq, (int64_t)a.pos.q_start[d.b] + T - 1) - (int64_t)kb * kBlock;
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       const int done = it;
       some = next_item(it, ok);
       if (!ok) break;
-      if (some) load_q(q_item(a, it));
+      if (some) begin(q_item(a, it));
       // ---- the item's dQ: a query per thread, a run of dims per warpgroup
       if (any) {
         ok = __all_sync(0xffffffffu, mbar_wait(acc_full, (uint32_t)nu & 1, a.status, a.wait_polls));
