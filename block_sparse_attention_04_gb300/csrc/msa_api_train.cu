@@ -131,9 +131,17 @@ int msa_rope_append_bwd(const msa_params* p, const msa_rope* r, const uint16_t* 
       bad_stride(dq_stride, nq) || bad_stride(dk_stride, nk) || bad_stride(dv_stride, nk))
     return MSA_ERR_INVALID_ARG;
   if ((rc = check_ws(ws, ws_bytes, msa_rope_append_bwd_workspace_bytes(p)))) return rc;
-  if (p->T == 0) return MSA_OK;
-  // the status word, and the count of CTAs that are done behind it
-  if (cudaMemsetAsync(ws, 0, 2 * sizeof(int), stream) != cudaSuccess) return MSA_ERR_CUDA;
+  if (p->T == 0) {                           // no tokens: the weights' gradients are zero
+    const size_t bytes = p->D * sizeof(float);
+    if ((q_weight && cudaMemsetAsync(dq_weight, 0, bytes, stream) != cudaSuccess) ||
+        (k_weight && cudaMemsetAsync(dk_weight, 0, bytes, stream) != cudaSuccess))
+      return MSA_ERR_CUDA;
+    return MSA_OK;
+  }
+  // the status word, and the counts of CTAs that are done behind it
+  static_assert((1 + kRopeBwdCounters) * sizeof(int) <= kAlign, "counters in the header");
+  if (cudaMemsetAsync(ws, 0, (1 + kRopeBwdCounters) * sizeof(int), stream) != cudaSuccess)
+    return MSA_ERR_CUDA;
   const RopeIn in{q, k, nullptr, q_stride, k_stride, 0, q_weight, k_weight, nullptr};
   const RopeGrads g{dq_out, dk_cache, dv_cache, dq, dk, dv, dq_stride, dk_stride, dv_stride,
                     dq_weight, dk_weight};

@@ -64,7 +64,8 @@ struct KvCfg {
   static constexpr int kStat = 16 * kGroupStat;      // statistics of a tile
   static constexpr int kOnes = SP ? 0 : 2 * kStat;   // dense: their selectors, A operands
   static constexpr int kDs = SP ? 2 * kHalf : 0;     // dS^T [2 x 64 rows][128 tokens]
-  static constexpr int kBars = (2 * (kTiles + kSS) + 12 + 2 * kRing) * 8 + kRing * 4 + 8;
+  static constexpr int kFills = 2 * kTiles + kSS;
+  static constexpr int kBars = (2 * (kTiles + kSS) + 12 + 2 * kRing) * 8 + (kRing + kFills) * 4 + 8;
   static constexpr int kSmem =
       (2 + kTiles) * kTile + kDs + kOnes + kSS * (kStat + 80) + kBars;
   // Slots of tile n's Q and dO, and the number of times that they were filled before.
@@ -117,6 +118,27 @@ __device__ __forceinline__ int sparse_steps(const BwdArgs& a, const KvUnit& u, i
   return (ne * a.rpe + 15) >> 4;
 }
 
+// Sparse: what a lane of a copying warp knows of its 8-row group of a tile.
+struct SparseRows {
+  int entry, il, z, box_r, boxes;    // entry: of the tile that was fetched
+  int64_t row;
+  bool real;
+  __device__ __forceinline__ void fetch(const BwdArgs& a, const KvUnit& u, int t, int lane) {
+    const int at = t * a.R + (lane & 15) / (a.rpe >> 3);
+    if (at < u.size) entry = a.entries[u.first + at];
+  }
+  __device__ __forceinline__ void place(const BwdArgs& a, const KvUnit& u, int t, int lane) {
+    const int bpe = a.rpe >> 3;
+    boxes = 2 * sparse_steps(a, u, t);
+    real = t * a.R + (lane & 15) / bpe < u.size;
+    il = real ? entry >> 4 : 0;
+    row = (int64_t)u.b * a.s.T + a.t0 + il;
+    // past the end for rows without an entry: zeros
+    z = real ? (int)(row * a.s.G + u.g) : a.s.B * a.s.T * a.s.G;
+    box_r = (lane & 15) % bpe * 8;
+  }
+};
+
 template <int D, bool SP>
 __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
@@ -153,7 +175,9 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
   uint64_t* it_full = bar_fin + 1;                 // [kRing]
   uint64_t* it_empty = it_full + kRing;
   int* ring = reinterpret_cast<int*>(it_empty + kRing);   // unit numbers, -1: no more
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kRing);
+  // the last fill of each tile slot by warp 0, then by warp 1, then of each statistics slot
+  int* last_fill = ring + kRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(last_fill + C::kFills);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -163,7 +187,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
       mbar_init(&t_empty[i], SP ? 2 : 1);    // sparse: both MMA warps are done with it
     }
     for (int i = 0; i < C::kSS; ++i) {
-      mbar_init(&st_full[i], 1);
+      mbar_init(&st_full[i], SP ? 33 : 1);   // sparse: every lane's copies, and what it wrote
       mbar_init(&st_empty[i], 1);
     }
     mbar_init(kv_full, 1);
@@ -183,6 +207,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
       mbar_init(&it_empty[i], ring_readers<SP>());
     }
     *abort_flag = 0;
+    for (int i = 0; i < C::kFills; ++i) last_fill[i] = -1;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_o);
@@ -223,9 +248,22 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status, a.wait_polls));
   };
+  // Sparse: a tile's rows, 8 to a box.
+  auto load_rows = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, const SparseRows& x,
+                       uint64_t pol) {
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(x.boxes * C::kGroup));
+    __syncwarp();
+#pragma unroll 4
+    for (int i = 0; i < x.boxes; ++i) {
+      const int z = __shfl_sync(0xffffffffu, x.z, i), box_r = __shfl_sync(0xffffffffu, x.box_r, i);
+      if (elect_one())
+        tma_load_4d_hint(smem_u32(dst + i * C::kGroup), map, bar, 0, box_r, z, 0, pol);
+    }
+    __syncwarp();
+  };
 
   if (warp == 0) {
-    // ------------------------------------------------ Q, dO, statistics (warp 0)
+    // ------------------------- Q and statistics, dense: dO too (warp 0); takes the units
     const uint64_t pol = l2_policy_evict_last();   // rows are read again by other units
     const int n_units = a.n_units[0];
     int cur = 0;
@@ -237,7 +275,6 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     }
     cur = __shfl_sync(0xffffffffu, cur, 0);
     int n = 0;                     // tiles issued
-    int last = -1;                 // lane: the last fill of tile slot `lane` (then statistics)
     bool ok = true;
     for (int k = 0; cur >= 0 && ok; ++k) {
       // publish the next unit before this one's tiles
@@ -254,86 +291,88 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
       const KvUnit u = kv_unit<SP>(a, cur);
       const int q0 = SP ? 0 : bwd_first_tile(a, u.b, u.kb);
       const int64_t t_last = (int64_t)a.pos.q_start[u.b] + T - 1;
+      SparseRows rows{};
+      if constexpr (SP) rows.fetch(a, u, 0, lane);
       for (int t = 0; t < u.tiles; ++t, ++n) {
         const int qs = C::q_slot(n), os = C::o_slot(n), ss = n % C::kSS;
-        uint8_t *const dq_ = sT + qs * C::kTile, *const do_ = sT + os * C::kTile;
+        uint8_t* const dst = sT + qs * C::kTile;
         const uint32_t st = smem_u32(sStat + ss * C::kStat);
-        // what this lane copies: sparse, its 8-row group of the tile; dense, lane 0 all
-        int boxes = 1, box_r = 0, z = 0, h = 0, qt = 0, lim = 127;
-        size_t sg = 0;
-        bool any = false;
+        if (__any_sync(0xffffffffu, *abort_flag != 0) || !wait_all(&t_empty[qs], (C::use(n) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
         if constexpr (SP) {
-          boxes = 2 * sparse_steps(a, u, t);               // 8-row groups of the tile
-          const int bpe = a.rpe >> 3, at = t * a.R + (lane & 15) / bpe;
-          const bool real = at < u.size;
-          const int il = real ? a.entries[u.first + at] >> 4 : 0;
-          const int64_t row = (int64_t)u.b * T + a.t0 + il;
-          // past the end for rows without an entry: zeros
-          z = real ? (int)(row * a.s.G + u.g) : a.s.B * T * a.s.G;
-          box_r = (lane & 15) % bpe * 8;
-          sg = real ? (size_t)(row * a.s.G + u.g) * bpe + lane % bpe : a.stat_groups;
+          rows.place(a, u, t, lane);
+          load_rows(dst, &tm_q, &t_full[qs], rows, pol);
+          if (lane == 0) last_fill[qs] = (int)C::use(n);
           // a block that the sequence's last query does not reach the end of may hold
           // anything behind it: rows without an entry see none of it
-          const int64_t seen = (int64_t)a.pos.q_start[u.b] + a.t0 + il - (int64_t)u.kb * kBlock;
-          lim = real ? (int)(seen < 127 ? seen : 127)
-                     : (t_last - (int64_t)u.kb * kBlock < 127 ? -1 : 127);
-          any = __any_sync(0xffffffffu, (lane & 15) < boxes && lim < 127);
-        } else {
-          dense_tile(a, u, q0, t, h, qt);
-          h += u.g * a.hpg;
-          sg = (size_t)(u.b * H + h) * a.stat_groups + qt * 16;
-        }
-        auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar) {
-          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(SP ? boxes * C::kGroup : C::kTile));
-          __syncwarp();
-          if constexpr (SP) {
-            if (lane < boxes)
-              tma_load_4d_hint(smem_u32(dst + lane * C::kGroup), map, bar, 0, box_r, z, 0, pol);
-          } else if (lane == 0) {
-#pragma unroll
-            for (int hf = 0; hf < C::kNHalf; ++hf)
-              tma_load_4d_hint(smem_u32(dst + hf * C::kHalf), map, bar, hf * 64, h, qt * 128, u.b, pol);
-          }
-        };
-        ok = __any_sync(0xffffffffu, *abort_flag != 0) == 0 &&
-             wait_all(&t_empty[qs], (C::use(n) & 1) ^ 1);
-        if (!ok) break;
-        load_tile(dq_, &tm_q, &t_full[qs]);
-        if (lane == qs) last = (int)C::use(n);
-        ok = wait_all(&st_empty[ss], ((uint32_t)(n / C::kSS) & 1) ^ 1);
-        if (!ok) break;
-        if constexpr (SP) {
+          const int64_t seen = (int64_t)a.pos.q_start[u.b] + a.t0 + rows.il - (int64_t)u.kb * kBlock;
+          const int lim = rows.real ? (int)(seen < 127 ? seen : 127)
+                                    : (t_last - (int64_t)u.kb * kBlock < 127 ? -1 : 127);
+          const bool any = __any_sync(0xffffffffu, (lane & 15) < rows.boxes && lim < 127);
+          const int bpe = a.rpe >> 3;
+          const size_t sg = rows.real ? (size_t)(rows.row * a.s.G + u.g) * bpe + lane % bpe
+                                      : a.stat_groups;
+          const int boxes = rows.boxes;
+          rows.fetch(a, u, t + 1, lane);           // while waiting for the slot
+          if (!wait_all(&st_empty[ss], ((uint32_t)(n / C::kSS) & 1) ^ 1)) { ok = false; break; }
           if (lane < 16) sLim[ss * 20 + lane] = lim;
           if (lane == 16) sLim[ss * 20 + 16] = any;
+          // 64 bytes of a group by two lanes
+          const char* src = reinterpret_cast<const char*>(a.stat) + sg * kStatBytes + (lane >> 4) * 32;
+          if ((lane & 15) < boxes) {
+            const uint32_t d = st + (lane & 15) * kStatBytes + (lane >> 4) * 32;
+            cp_async_16(d, src);
+            cp_async_16(d + 16, src + 16);
+          }
+          cp_async_arrive(&st_full[ss]);
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&st_full[ss], (uint32_t)(boxes * kStatBytes));
+          if (lane == 0) mbar_arrive(&st_full[ss]);
+        } else {
+          int h, qt;
+          dense_tile(a, u, q0, t, h, qt);
+          h += u.g * a.hpg;
+          const size_t sg = (size_t)(u.b * H + h) * a.stat_groups + qt * 16;
+          auto load_tile = [&](int slot, const CUtensorMap* map) {
+            mbar_arrive_expect_tx(&t_full[slot], C::kTile);
+#pragma unroll
+            for (int hf = 0; hf < C::kNHalf; ++hf)
+              tma_load_4d_hint(smem_u32(sT + slot * C::kTile + hf * C::kHalf), map, &t_full[slot],
+                               hf * 64, h, qt * 128, u.b, pol);
+            last_fill[slot] = (int)C::use(n);
+          };
+          if (lane == 0) load_tile(qs, &tm_q);
           __syncwarp();
-          if (lane < boxes)
-            bulk_load(st + lane * kStatBytes, a.stat + sg * kStatBytes, kStatBytes, &st_full[ss]);
-        } else if (lane == 0) {
-          mbar_arrive_expect_tx(&st_full[ss], C::kStat);
-          bulk_load(st, a.stat + sg * C::kGroupStat, C::kStat, &st_full[ss]);
+          if (!wait_all(&st_empty[ss], ((uint32_t)(n / C::kSS) & 1) ^ 1)) { ok = false; break; }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&st_full[ss], C::kStat);
+            bulk_load(st, a.stat + sg * C::kGroupStat, C::kStat, &st_full[ss]);
+            last_fill[2 * C::kTiles + ss] = n / C::kSS;
+          }
+          __syncwarp();
+          if (!wait_all(&t_empty[os], (C::use(n) & 1) ^ 1)) { ok = false; break; }
+          if (lane == 0) load_tile(os, &tm_o);
+          __syncwarp();
         }
-        if (lane == C::kTiles + ss) last = n / C::kSS;
-        ok = wait_all(&t_empty[os], (C::use(n) & 1) ^ 1);
-        if (!ok) break;
-        load_tile(do_, &tm_o, &t_full[os]);
-        if (lane == os) last = (int)C::use(n);
       }
       cur = nx;
     }
     if (!ok && lane == 0) *abort_flag = 1;
-    // no copy may still be landing when the CTA exits: the last one into each slot
-    if (last >= 0) mbar_wait(lane < C::kTiles ? &t_full[lane] : &st_full[lane - C::kTiles],
-                             (uint32_t)last & 1, nullptr);
+    if constexpr (SP) cp_async_wait_all();
   } else if (warp == 1) {
-    // ------------------------------------------------------ K and V (warp 1)
-    int it, n = 0;
+    // ------------------------------------------- K and V, sparse: dO too (warp 1)
+    // (A box of 8 rows takes a warp some 70 cycles to issue, so that one warp with a tile's
+    // 32 held up the rest: 1093 us for NEWT.)
+    const uint64_t pol = l2_policy_evict_last();
+    int it, n = 0, nu = 0;
     bool ok;
     while (next_unit(it, ok)) {
       const KvUnit u = kv_unit<SP>(a, it);
       if (u.tiles == 0) continue;
-      if (n > 0 && !wait_all(kv_empty, (uint32_t)(n - 1) & 1)) { ok = false; break; }
+      SparseRows rows{};
+      if constexpr (SP) rows.fetch(a, u, 0, lane);
+      if (nu > 0 && !wait_all(kv_empty, (uint32_t)(nu - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
         const int row = (int)(((int64_t)u.b * a.s.max_blocks + u.kb) * kBlock);
         mbar_arrive_expect_tx(kv_full, 2 * C::kTile);
@@ -344,10 +383,24 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
         }
       }
       __syncwarp();
-      ++n;
+      ++nu;
+      if constexpr (SP) {
+        for (int t = 0; t < u.tiles; ++t, ++n) {
+          const int os = C::o_slot(n);
+          if (__any_sync(0xffffffffu, *abort_flag != 0) || !wait_all(&t_empty[os], (C::use(n) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          rows.place(a, u, t, lane);
+          load_rows(sT + os * C::kTile, &tm_o, &t_full[os], rows, pol);
+          if (lane == 0) last_fill[C::kTiles + os] = (int)C::use(n);
+          rows.fetch(a, u, t + 1, lane);
+        }
+        if (!ok) break;
+      }
     }
     if (!ok && lane == 0) *abort_flag = 1;
-    if (n > 0) mbar_wait(kv_full, (uint32_t)(n - 1) & 1, nullptr);
+    if (nu > 0) mbar_wait(kv_full, (uint32_t)(nu - 1) & 1, nullptr);
   } else if (warp == kAW || (SP && warp == kBW)) {
     // ------------------------------------------------------- MMA (warps 2, 3)
     constexpr uint32_t idesc_n = idesc_bf16(128, D, false, true);     // dV, dK
@@ -850,6 +903,15 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
   if (warp == kAW) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  // no copy may still be landing when the CTA exits: the last one into each slot (not an
+  // earlier one, whose phase may be two behind)
+  if (threadIdx.x < C::kTiles + C::kSS) {
+    const int i = threadIdx.x;
+    const int last = i < C::kTiles ? max(last_fill[i], last_fill[i + C::kTiles])
+                                   : last_fill[i + C::kTiles];
+    if (last >= 0) mbar_wait(i < C::kTiles ? &t_full[i] : &st_full[i - C::kTiles],
+                             (uint32_t)last & 1, nullptr);
   }
 }
 

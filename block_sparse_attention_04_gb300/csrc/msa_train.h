@@ -22,10 +22,12 @@ struct RopeGrads {
   int64_t dq_stride, dk_stride, dv_stride;
   float *dq_weight, *dk_weight;
 };
-// base: scratch of rope_bwd_scratch_bytes(); counter: a zeroed word.
+// base: scratch of rope_bwd_scratch_bytes(); counters: kRopeBwdCounters zeroed
+// words.
+constexpr int kRopeBwdCounters = 33;
 size_t rope_bwd_scratch_bytes();
 cudaError_t launch_rope_append_bwd(const Shape& s, const Positions& pos, const msa_rope& r,
-                                   const RopeIn& in, const RopeGrads& g, unsigned* counter,
+                                   const RopeIn& in, const RopeGrads& g, unsigned* counters,
                                    char* base, cudaStream_t st);
 
 // The attention's backward pass.  sel null: dense causal.  base: scratch of
