@@ -88,7 +88,7 @@ Layout layout(const Shape& s, bool sparse) {
   const int slots = most_slots(tiles);
   if (sparse) {
     L.stat_groups = (uint32_t)((size_t)s.B * s.T * s.G * (rpe / 8));
-    L.stat = take(((size_t)L.stat_groups + 1) * kStatBytes);
+    L.aug = take(((size_t)L.stat_groups + 1) * kAugBytes);
     L.chunks = (tp + kChunkRows - 1) / kChunkRows;
     L.cnt = take((size_t)s.B * L.chunks * s.G * nbl * sizeof(int32_t));
     L.count = take(lists * sizeof(int32_t));
@@ -129,9 +129,9 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
   a.sel = t.sel;
   a.n_units = reinterpret_cast<int*>(base);
   a.next_unit = a.n_units + 2;
-  uint8_t* const stat = reinterpret_cast<uint8_t*>(base + L.stat);
-  uint8_t* const aug = sparse ? nullptr : reinterpret_cast<uint8_t*>(base + L.aug);
-  a.stat = sparse ? stat : aug;
+  uint8_t* const stat = sparse ? nullptr : reinterpret_cast<uint8_t*>(base + L.stat);
+  uint8_t* const aug = reinterpret_cast<uint8_t*>(base + L.aug);
+  a.stat = aug;
   a.no_scores = bwd_no_scores(s);
   a.stat_groups = L.stat_groups;
   a.chunks = L.chunks;

@@ -2,13 +2,13 @@
 //
 // Row statistics.  The kernels recompute P = 2^(s scale log2e - lse log2e) and
 // dS = P (dP - delta); the two numbers of a (query, head) row are kept in groups of
-// 8 rows, 64 bytes: eight -lse log2e, then eight -delta.
+// 8 rows, 128 bytes: [8 rows][8 bf16], -lse / scale in three parts at 0..2 and -delta
+// alike at 4..6, zeros at 3 and 7: products with ones add them to S and dP.
+// (-lse log2e where scale log2e is below 2^-100 and scores count for nothing.)
 //   dense    group ((b H + h) ngroups + i/8), a tile's 16 groups in a row; rows past
-//            the last query hold (-inf, 0): their P and dS vanish.  Next to it, for the
-//            KV-outer kernel, 256 bytes a group: [8 rows][8 bf16] with -lse / scale in
-//            three parts at 0..2, then [8 rows][8 bf16] with -delta alike: products with
-//            ones add them to S and dP.  (-lse log2e where scale log2e is below 2^-100
-//            and scores count for nothing.)
+//            the last query hold -16384 (times 1 / scale log2e) and 0: their P and dS
+//            vanish.  Next to it, for the query-outer kernel, 64 bytes a group: eight
+//            -lse log2e, then eight -delta.
 //   sparse   group (((b T + i) G + g) rpe/8 + head/8): an entry's rows; heads past
 //            the group's last as above, and one such group behind all others
 #pragma once
@@ -16,8 +16,8 @@
 
 namespace msa {
 
-constexpr int kStatBytes = 64;          // a group of 8 rows
-constexpr int kAugBytes = 256;          // ... as operands
+constexpr int kStatBytes = 64;          // a group of 8 rows as numbers
+constexpr int kAugBytes = 128;          // ... as operands
 constexpr int kBwdSms = 152;            // what sizes of scratch are made for
 constexpr int kChunkRows = 64;          // query rows whose list entries keep their order
 
@@ -50,7 +50,7 @@ struct BwdArgs {
   int4* slots;               // per slot: (b, g, kb packed as x; its unit's slots, 0 but for the first)
   int max_slots;
   int* next_unit;            // [2] counters of taken units and of taken dQ items
-  const uint8_t* stat;       // dense: as operands
+  const uint8_t* stat;       // as operands
   uint32_t stat_groups;      // dense: groups per (b, h); sparse: index of the neutral group
   bool no_scores;            // scale log2e below 2^-100
   uint16_t* part_dq;         // sparse: dq of each tile, without the scale
@@ -90,7 +90,7 @@ inline bool bwd_no_scores(const Shape& s) {
   return (sl < 0 ? -sl : sl) < 0x1p-100f;
 }
 
-// Preparation: row statistics (aug: dense, as operands), lists (sparse), units.
+// Preparation: row statistics (stat: dense only; aug: as operands), lists (sparse), units.
 cudaError_t launch_bwd_stats(const Shape& s, const Positions& pos, const AttnBwd& a, int rpe,
                              uint8_t* stat, uint8_t* aug, uint32_t stat_groups, cudaStream_t st);
 cudaError_t launch_bwd_lists(const BwdArgs& a, cudaStream_t st);

@@ -59,15 +59,14 @@ struct KvCfg {
   static constexpr int kHalf = 128 * 128;            // 128 rows x 64 dims
   static constexpr int kTile = kNHalf * kHalf;       // K, V, a Q or a dO tile
   static constexpr int kTiles = 4;                   // Q and dO tiles in shared memory
-  static constexpr int kSS = 2;                      // statistics of tiles
-  static constexpr int kGroupStat = SP ? kStatBytes : kAugBytes;
-  static constexpr int kStat = 16 * kGroupStat;      // statistics of a tile
-  static constexpr int kOnes = SP ? 0 : 2 * kStat;   // dense: their selectors, A operands
+  static constexpr int kSS = SP ? 1 : 2;             // statistics of tiles
+  static constexpr int kStat = 16 * kAugBytes;       // statistics of a tile
+  static constexpr int kOnes = 2 * 256;              // their selectors, A operands
   static constexpr int kDs = SP ? 2 * kHalf : 0;     // dS^T [2 x 64 rows][128 tokens]
   static constexpr int kFills = 2 * kTiles + kSS;
   static constexpr int kBars = (2 * (kTiles + kSS) + 12 + 2 * kRing) * 8 + (kRing + kFills) * 4 + 8;
   static constexpr int kSmem =
-      (2 + kTiles) * kTile + kDs + kOnes + kSS * (kStat + 80) + kBars;
+      (2 + kTiles) * kTile + kDs + kOnes + kSS * kStat + 2 * 80 + kBars;
   // Slots of tile n's Q and dO, and the number of times that they were filled before.
   // dO(n) is free first (after dV(n); sparse dP(n)), Q(n) after dK(n), and what comes
   // next, Q(n+2) and dO(n+2), goes into them in that order.
@@ -150,12 +149,12 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
   uint8_t* sV = sK + C::kTile;
   uint8_t* sT = sV + C::kTile;                     // [kTiles] Q and dO
   uint8_t* sDs = sT + C::kTiles * C::kTile;
-  uint8_t* sOnes = sDs + C::kDs;                   // dense: selectors of lse and of delta
+  uint8_t* sOnes = sDs + C::kDs;                   // selectors of lse and of delta
   uint8_t* sStat = sOnes + C::kOnes;               // [kSS] statistics
-  // [kSS] per 8-row group of a sparse tile: the last token of the block that its query
+  // [2] per 8-row group of a sparse tile: the last token of the block that its query
   // sees (-1: none), then whether any of them is below 127
   int* sLim = reinterpret_cast<int*>(sStat + C::kSS * C::kStat);
-  uint64_t* t_full = reinterpret_cast<uint64_t*>(sLim + C::kSS * 20);
+  uint64_t* t_full = reinterpret_cast<uint64_t*>(sLim + 2 * 20);
   uint64_t* t_empty = t_full + C::kTiles;
   uint64_t* st_full = t_empty + C::kTiles;
   uint64_t* st_empty = st_full + C::kSS;
@@ -187,20 +186,21 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
       mbar_init(&t_empty[i], SP ? 2 : 1);    // sparse: both MMA warps are done with it
     }
     for (int i = 0; i < C::kSS; ++i) {
-      mbar_init(&st_full[i], SP ? 33 : 1);   // sparse: every lane's copies, and what it wrote
-      mbar_init(&st_empty[i], 1);
+      mbar_init(&st_full[i], 1);
+      mbar_init(&st_empty[i], SP ? 2 : 1);
     }
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, SP ? 2 : 1);
-    mbar_init(s_full, 1);
+    mbar_init(s_full, SP ? 2 : 1);         // sparse: and the tile's limits are there
     mbar_init(&dp_full[0], 1);
     mbar_init(&dp_full[1], 1);
-    mbar_init(p_full, 128 * kNG + (SP ? 0 : 1));   // dense: and what comes next has landed
-    mbar_init(ds_full, 128 * kNG + (SP ? 0 : 1));
+    // a warp arrives once (512 threads: see below); dense: and what comes next has landed
+    mbar_init(p_full, 4 * kNG + (SP ? 0 : 1));
+    mbar_init(ds_full, 4 * kNG + (SP ? 0 : 1));
     mbar_init(acc_full, SP ? 2 : 1);
-    mbar_init(acc_empty, 128 * kNG);
+    mbar_init(acc_empty, 4 * kNG);
     mbar_init(dq_full, 1);
-    mbar_init(dq_empty, 128);
+    mbar_init(dq_empty, 4);
     mbar_init(bar_fin, SP ? 2 : 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&it_full[i], 1);
@@ -214,15 +214,14 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if constexpr (!SP) {
-    // Rows of 16 bf16, K-major without a swizzle: [8 rows][8], then [8 rows][8].  The
-    // statistics' rows hold -lse in three parts at 0..2 and -delta at 8..10 (see
-    // msa_bwd.h): products with ones at those places and zeros elsewhere add them
-    for (int e = threadIdx.x; e < C::kOnes / 16; e += blockDim.x) {
-      const int sel = e / (C::kStat / 16), core = e >> 3 & 1;   // of lse or delta; dims 0.. or 8..
-      const uint32_t one = sel == core ? 0x3F80u : 0u;
-      sts128(smem_u32(sOnes) + e * 16, make_uint4(one | one << 16, one, 0, 0));
-    }
+  // The statistics' rows are 8 bf16, K-major without a swizzle: -lse in three parts at 0..2,
+  // -delta at 4..6 (see msa_bwd.h).  An MMA is 16 deep: the second 8 are the first again
+  // (a stride of 0), and meet zeros.  The selectors have ones at 0..2 or 4..6; all their
+  // 128 rows are the same 8
+  if (threadIdx.x < C::kOnes / 16) {
+    const int sel = threadIdx.x >> 4, second = threadIdx.x >> 3 & 1;   // of lse or delta; dims 8..
+    const uint32_t one = second ? 0u : 0x3F80u, a0 = sel ? 0u : one, a1 = sel ? one : 0u;
+    sts128(smem_u32(sOnes) + threadIdx.x * 16, make_uint4(a0 | a0 << 16, a0, a1 | a1 << 16, a1));
     fence_async();
   }
   if (warp == kAW) tmem_alloc(tmem_slot, 512);
@@ -247,6 +246,11 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
   };
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status, a.wait_polls));
+  };
+  // One arrival for the lanes' work so far.
+  auto warp_arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
   };
   // Sparse: a tile's rows, 8 to a box.
   auto load_rows = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, const SparseRows& x,
@@ -311,22 +315,27 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           const int lim = rows.real ? (int)(seen < 127 ? seen : 127)
                                     : (t_last - (int64_t)u.kb * kBlock < 127 ? -1 : 127);
           const bool any = __any_sync(0xffffffffu, (lane & 15) < rows.boxes && lim < 127);
-          const int bpe = a.rpe >> 3;
-          const size_t sg = rows.real ? (size_t)(rows.row * a.s.G + u.g) * bpe + lane % bpe
-                                      : a.stat_groups;
-          const int boxes = rows.boxes;
-          rows.fetch(a, u, t + 1, lane);           // while waiting for the slot
-          if (!wait_all(&st_empty[ss], ((uint32_t)(n / C::kSS) & 1) ^ 1)) { ok = false; break; }
-          if (lane < 16) sLim[ss * 20 + lane] = lim;
-          if (lane == 16) sLim[ss * 20 + 16] = any;
-          // 64 bytes of a group by two lanes
-          const char* src = reinterpret_cast<const char*>(a.stat) + sg * kStatBytes + (lane >> 4) * 32;
-          if ((lane & 15) < boxes) {
-            const uint32_t d = st + (lane & 15) * kStatBytes + (lane >> 4) * 32;
-            cp_async_16(d, src);
-            cp_async_16(d + 16, src + 16);
+          const int bpe = a.rpe >> 3, boxes = rows.boxes;
+          const uint32_t sg = rows.real ? (uint32_t)(rows.row * a.s.G + u.g) * bpe + lane % bpe
+                                        : a.stat_groups;
+          // The statistics by way of registers: they are asked for before their slot is free,
+          // which it is when S has to be issued (as bulk copies, 16 to a tile, they held S up
+          // for 3000 cycles)
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t from = __shfl_sync(0xffffffffu, sg, i * 4 + (lane >> 3));
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (i * 4 + (lane >> 3) < boxes)
+              x[i] = __ldg(reinterpret_cast<const uint4*>(a.stat + (size_t)from * kAugBytes) + (lane & 7));
           }
-          cp_async_arrive(&st_full[ss]);
+          rows.fetch(a, u, t + 1, lane);
+          if (!wait_all(&st_empty[ss], ((uint32_t)(n / C::kSS) & 1) ^ 1)) { ok = false; break; }
+          if (lane < 16) sLim[(n & 1) * 20 + lane] = lim;
+          if (lane == 16) sLim[(n & 1) * 20 + 16] = any;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sts128(st + (i * 32 + lane) * 16, x[i]);
+          fence_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&st_full[ss]);
         } else {
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           if (!wait_all(&st_empty[ss], ((uint32_t)(n / C::kSS) & 1) ^ 1)) { ok = false; break; }
           if (lane == 0) {
             mbar_arrive_expect_tx(&st_full[ss], C::kStat);
-            bulk_load(st, a.stat + sg * C::kGroupStat, C::kStat, &st_full[ss]);
+            bulk_load(st, a.stat + sg * kAugBytes, C::kStat, &st_full[ss]);
             last_fill[2 * C::kTiles + ss] = n / C::kSS;
           }
           __syncwarp();
@@ -359,7 +368,6 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
       cur = nx;
     }
     if (!ok && lane == 0) *abort_flag = 1;
-    if constexpr (SP) cp_async_wait_all();
   } else if (warp == 1) {
     // ------------------------------------------- K and V, sparse: dO too (warp 1)
     // (A box of 8 rows takes a warp some 70 cycles to issue, so that one warp with a tile's
@@ -412,28 +420,23 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     const uint64_t dsk = smem_desc(smem_u32(sDs), 16, 1024, kSwizzle128B);
     const uint64_t tk = smem_desc(smem_u32(sT), 16, C::kGroup, kSwizzle128B);
     const uint64_t tmn = smem_desc(smem_u32(sT), C::kNext, C::kGroup, kSwizzle128B);
-    // A (128 x D, K-major) times a tile of rows, K-major: `steps` x 16 columns.  Dense: on
-    // top of the rows' statistics (sel 0: -lse, 1: -delta)
-    const uint64_t onesd = smem_desc(smem_u32(sOnes), 128, kAugBytes, 0);
-    const uint64_t augd = smem_desc(smem_u32(sStat), 128, kAugBytes, 0);
-    // (An instruction descriptor that is not a constant costs an MMA 40 cycles: full tiles
-    // have one.)
+    // A (128 x D, K-major) times a tile of rows, K-major: `steps` x 16 columns, on top of
+    // the rows' statistics (sel 0: -lse, 1: -delta).  (An instruction descriptor that is
+    // not a constant costs an MMA 40 cycles: full tiles have one.)
+    const uint64_t onesd = smem_desc(smem_u32(sOnes), 128, 0, 0);
+    const uint64_t augd = smem_desc(smem_u32(sStat), 0, kAugBytes, 0);
     auto rows_product = [&](uint32_t d, uint64_t ad, int slot, int steps, int sel, int ss) {
       const uint64_t bd = tk + (uint64_t)((slot * C::kTile) >> 4);
       auto all = [&](uint32_t idesc) {
+        tc_mma_f16(tmem + d, onesd + (uint64_t)((sel * 256) >> 4),
+                   augd + (uint64_t)((ss * C::kStat) >> 4), idesc, 0u);
+        if (sel == 0 && a.no_scores) return;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
           tc_mma_f16(tmem + d, ad + (uint64_t)(((j >> 2) * C::kHalf + (j & 3) * 32) >> 4),
-                     bd + (uint64_t)(((j >> 2) * C::kNext + (j & 3) * 32) >> 4), idesc,
-                     !SP || j > 0 ? 1u : 0u);
+                     bd + (uint64_t)(((j >> 2) * C::kNext + (j & 3) * 32) >> 4), idesc, 1u);
       };
-      constexpr uint32_t full = idesc_bf16(128, 128, false, false);
-      if constexpr (!SP) {
-        tc_mma_f16(tmem + d, onesd + (uint64_t)((sel * C::kStat) >> 4),
-                   augd + (uint64_t)((ss * C::kStat) >> 4), full, 0u);
-        if (sel == 0 && a.no_scores) return;
-      }
-      if (!SP || steps == 8) all(full);
+      if (!SP || steps == 8) all(idesc_bf16(128, 128, false, false));
       else all(idesc_bf16(128, 0, false, false) | (uint32_t)(2 * steps) << 17);
     };
     // P^T or dS^T (TMEM at column p, kCols columns of a tile in half as many) times a tile
@@ -533,13 +536,19 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           __syncwarp();
         }
         auto issue_s = [&](int m, int t) {         // S of tile m, the unit's t-th
-          const int qs = C::q_slot(m);
-          if (!wait_all(&t_full[qs], C::use(m) & 1)) return false;
+          const int qs = C::q_slot(m), ss = m % C::kSS;
+          if (!wait_all(&t_full[qs], C::use(m) & 1) ||
+              !wait_all(&st_full[ss], (uint32_t)(m / C::kSS) & 1))
+            return false;
+          // hands on what warp 0 wrote: the limits.  (They are kept for two tiles: dP of the
+          // tile between, which frees the statistics, is issued behind dS of the first)
+          if (lane == 0) mbar_arrive(s_full);
           tc_fence_after();
           if (elect_one()) {
-            rows_product(C::kS, kd, qs, sparse_steps(a, u, t), 0, 0);
+            rows_product(C::kS, kd, qs, sparse_steps(a, u, t), 0, ss);
             tc_commit(s_full);
             tc_commit(&t_empty[qs]);
+            tc_commit(&st_empty[ss]);
             if (t + 1 == u.tiles) tc_commit(kv_empty);
           }
           __syncwarp();
@@ -574,24 +583,23 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
         if (u.tiles == 0) continue;
         ok = wait_all(kv_full, (uint32_t)nu & 1);
         if (!ok) break;
-        auto issue_dp = [&](int m, int t) {
-          const int os = C::o_slot(m);
-          if (!wait_all(&t_full[os], C::use(m) & 1)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-            rows_product(C::kP, vd, os, sparse_steps(a, u, t), 1, 0);
-            tc_commit(&dp_full[m & 1]);
-            tc_commit(&t_empty[os]);
-          }
-          __syncwarp();
-          return true;
-        };
         for (int t = 0; t < u.tiles && ok; ++t, ++n) {
-          const int qs = C::q_slot(n);
+          const int qs = C::q_slot(n), os = C::o_slot(n), ss = n % C::kSS;
           const bool more = t + 1 < u.tiles;
           // D = 128: dQ's part of the tile before is in dP's place until it is read out
-          if (D == 128 && n > 0) ok = wait_all(dq_empty, (uint32_t)(n - 1) & 1);
-          ok = ok && issue_dp(n, t) && wait_all(ds_full, (uint32_t)n & 1) &&
+          ok = wait_all(&t_full[os], C::use(n) & 1) &&
+               wait_all(&st_full[ss], (uint32_t)(n / C::kSS) & 1) &&
+               (D != 128 || n == 0 || wait_all(dq_empty, (uint32_t)(n - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            rows_product(C::kP, vd, os, sparse_steps(a, u, t), 1, ss);
+            tc_commit(&dp_full[n & 1]);
+            tc_commit(&t_empty[os]);
+            tc_commit(&st_empty[ss]);
+          }
+          __syncwarp();
+          ok = wait_all(ds_full, (uint32_t)n & 1) &&
                (t > 0 || nu == 0 || wait_all(acc_empty, (uint32_t)(nu - 1) & 1));
           if (D != 128 && n > 0) ok = ok && wait_all(dq_empty, (uint32_t)(n - 1) & 1);
           if (!ok) break;
@@ -618,7 +626,6 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
               for (int j = 0; j < steps; ++j) step(j);
             }
             tc_commit(&t_empty[qs]);
-            tc_commit(&st_empty[n % C::kSS]);    // dS has used the statistics
             if (!more) tc_commit(acc_full);
           }
           __syncwarp();
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     const int quad = warp & 3;
     const int r = quad * 32 + lane;               // token of the block = TMEM lane
     const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16);
-    const float sl = !SP && a.no_scores ? 1.f : a.s.scale * kLog2e;
+    const float sl = a.no_scores ? 1.f : a.s.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl);
     int it, n = 0, nu = 0;
     bool ok;
@@ -676,19 +683,17 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
       const int64_t t_key = (int64_t)u.kb * kBlock + r;
       const bool used = t_key <= (int64_t)a.pos.q_start[u.b] + T - 1;  // by the last query
       for (int t = 0; t < u.tiles; ++t, ++n) {
-        const int ss = n % C::kSS;
         int cols = kCols;                         // of this warpgroup's that the tile has
         int lim = 0;                              // dense: columns below see another token
         bool masked;
         ok = *abort_flag == 0 &&
-             (!SP || mbar_wait(&st_full[ss], (uint32_t)(n / C::kSS) & 1, a.status, a.wait_polls)) &&
              mbar_wait(s_full, (uint32_t)n & 1, a.status, a.wait_polls);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const int* tl = sLim + ss * 20 + c * (kCols / 8);
+        const int* tl = sLim + (n & 1) * 20 + c * (kCols / 8);
         if constexpr (SP) {
           cols = sparse_steps(a, u, t) * 16 - c * kCols;
-          masked = sLim[ss * 20 + 16] != 0;
+          masked = sLim[(n & 1) * 20 + 16] != 0;
         } else {
           int h, qt;
           dense_tile(a, u, q0, t, h, qt);
@@ -702,9 +707,6 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           v.y = (SP ? r > tl[col >> 3] : col + 1 < lim) ? 0.f : v.y;
         };
         tc_fence_after();
-        // statistics of 8 columns: 64 bytes, -lse log2e then -delta (dense: S and dP hold them)
-        const float4* st =
-            reinterpret_cast<const float4*>(sStat + ss * C::kStat + c * (kCols / 8) * kStatBytes);
         float2 p[kCols / 2];
         // P of 16 columns, and dS of them, with the masks (few tiles have any) or without
         auto p_of = [&](auto mask, int q) {
@@ -713,15 +715,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           tmem_ld_wait();
 #pragma unroll
           for (int g4 = 0; g4 < 4; ++g4) {          // 4 columns
-            float2 y0, y1;
-            if constexpr (SP) {
-              const float4 nl = st[(q * 2 + (g4 >> 1)) * 4 + (g4 & 1)];
-              y0 = ffma2(pair(x, 2 * g4), sl2, make_float2(nl.x, nl.y));
-              y1 = ffma2(pair(x, 2 * g4 + 1), sl2, make_float2(nl.z, nl.w));
-            } else {
-              y0 = fmul2(pair(x, 2 * g4), sl2);
-              y1 = fmul2(pair(x, 2 * g4 + 1), sl2);
-            }
+            const float2 y0 = fmul2(pair(x, 2 * g4), sl2), y1 = fmul2(pair(x, 2 * g4 + 1), sl2);
             float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
             if constexpr (mask.value) {
               hide(p0, q * 16 + 4 * g4);
@@ -741,14 +735,8 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           tmem_ld_wait();
 #pragma unroll
           for (int g4 = 0; g4 < 4; ++g4) {
-            float2 d0 = pair(x, 2 * g4), d1 = pair(x, 2 * g4 + 1);
-            if constexpr (SP) {
-              const float4 nd = st[(q * 2 + (g4 >> 1)) * 4 + 2 + (g4 & 1)];
-              d0 = fadd2(d0, make_float2(nd.x, nd.y));
-              d1 = fadd2(d1, make_float2(nd.z, nd.w));
-            }
-            d0 = fmul2(p[q * 8 + 2 * g4], d0);
-            d1 = fmul2(p[q * 8 + 2 * g4 + 1], d1);
+            float2 d0 = fmul2(p[q * 8 + 2 * g4], pair(x, 2 * g4));
+            float2 d1 = fmul2(p[q * 8 + 2 * g4 + 1], pair(x, 2 * g4 + 1));
             if constexpr (mask.value) {             // 0 even where dP is not finite
               hide(d0, q * 16 + 4 * g4);
               hide(d1, q * 16 + 4 * g4 + 2);
@@ -775,7 +763,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(p_full);
+        warp_arrive(p_full);
         ok = __all_sync(0xffffffffu, mbar_wait(&dp_full[n & 1], (uint32_t)(n >> 1) & 1, a.status,
                                                a.wait_polls));
         if (!ok) break;
@@ -789,7 +777,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
         if constexpr (SP) fence_async();
         else tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(ds_full);
+        warp_arrive(ds_full);
       }
       if (!ok) break;
       // ---- the unit's dV (the first half of the warpgroups) and dK, a token per thread
@@ -852,7 +840,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
       }
       if (u.tiles > 0) {
         tc_fence_before();
-        mbar_arrive(acc_empty);
+        warp_arrive(acc_empty);
         ++nu;
       }
     }
@@ -891,7 +879,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           }
         }
         tc_fence_before();
-        mbar_arrive(dq_empty);
+        warp_arrive(dq_empty);
       }
       if (!ok) break;
     }

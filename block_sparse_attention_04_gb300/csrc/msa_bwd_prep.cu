@@ -22,38 +22,37 @@ struct StatArgs {
   Positions pos;
   const uint16_t *q, *k, *v, *out, *dout;
   const float* lse;
-  uint8_t* stat;
-  uint8_t* aug;          // dense: the groups as operands
+  uint8_t* stat;         // dense: the groups as numbers
+  uint8_t* aug;          // the groups as operands
   float to_score;        // 1 / (scale log2e), or 1
   uint32_t groups;
   int rpe;               // 0: dense
 };
 constexpr int kStatThreads = 256;
-
-__device__ __forceinline__ float* stat_row(const StatArgs& a, int b, int i, int h) {
-  const int hpg = a.s.H / a.s.G;
-  size_t g;
-  int r;
-  if (a.rpe == 0) {
-    g = (size_t)(b * a.s.H + h) * a.groups + (i >> 3);
-    r = i & 7;
-  } else {
-    g = (((size_t)b * a.s.T + i) * a.s.G + h / hpg) * (a.rpe >> 3) + (h % hpg >> 3);
-    r = h % hpg & 7;
-  }
-  return reinterpret_cast<float*>(a.stat + g * kStatBytes) + r;
-}
-
-// Writes x at its row of an operand group (core 0: lse, 1: delta): three bf16 parts.
-__device__ __forceinline__ void put_aug(uint8_t* group, int core, int row, float x) {
+// Writes x at its row of an operand group (0: lse, 1: delta): three bf16 parts.
+__device__ __forceinline__ void put_aug(uint8_t* group, int which, int row, float x) {
   const float hi = __uint_as_float(pack_bf16(x, 0.f) << 16);
   float mid = 0.f, lo = 0.f;
   if (fabsf(hi) < INFINITY) {              // (a NaN goes on in hi)
     mid = __uint_as_float(pack_bf16(x - hi, 0.f) << 16);
     lo = x - hi - mid;
   }
-  *reinterpret_cast<uint4*>(group + core * 128 + row * 16) =
-      make_uint4(pack_bf16(hi, mid), pack_bf16(lo, 0.f), 0, 0);
+  *reinterpret_cast<uint2*>(group + row * 16 + which * 8) =
+      make_uint2(pack_bf16(hi, mid), pack_bf16(lo, 0.f));
+}
+
+// -delta of row (b, query i, head h).
+__device__ __forceinline__ void put_delta(const StatArgs& a, int b, int i, int h, float x) {
+  const int hpg = a.s.H / a.s.G;
+  if (a.rpe == 0) {
+    const size_t g = (size_t)(b * a.s.H + h) * a.groups + (i >> 3);
+    reinterpret_cast<float*>(a.stat + g * kStatBytes)[8 + (i & 7)] = x;
+    put_aug(a.aug + g * kAugBytes, 1, i & 7, x);
+  } else {
+    const size_t g =
+        (((size_t)b * a.s.T + i) * a.s.G + h / hpg) * (a.rpe >> 3) + (h % hpg >> 3);
+    put_aug(a.aug + g * kAugBytes, 1, h % hpg & 7, x);
+  }
 }
 
 template <int D>
@@ -133,8 +132,7 @@ __global__ void __launch_bounds__(256) bwd_stat_first_kernel(const __grid_consta
     if (c == 0 && i0 + r + 8 * u < n) {
       const float nd = sp[u] == 0.f ? 0.f : -sd[u] / sp[u];
       const int i = i0 + r + 8 * u;
-      stat_row(a, b, i, h)[8] = nd;
-      if (a.aug) put_aug(a.aug + ((size_t)(b * H + h) * a.groups + (i >> 3)) * kAugBytes, 1, i & 7, nd);
+      put_delta(a, b, i, h, nd);
     }
   }
 }
@@ -153,7 +151,7 @@ __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_con
   int64_t row;                       // the first row, of rows [B][T][H]
   const int step = a.rpe ? 1 : H;    // to the next
   bool in;
-  uint8_t* dst;
+  size_t dst;                        // group
   if (a.rpe) {
     const int sub = a.rpe >> 3;
     in = grp < (int64_t)a.s.B * a.s.T * G * sub;
@@ -164,7 +162,7 @@ __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_con
     h0 = x / sub * hpg + x % sub * 8;
     n = min(8, hpg - x % sub * 8);
     row = q * H + h0;
-    dst = a.stat + grp * kStatBytes;
+    dst = (size_t)grp;
   } else {
     const int64_t q = grp / H;
     h0 = (int)(grp - q * H);
@@ -173,7 +171,7 @@ __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_con
     i0 = (int)(q - (int64_t)b * a.groups) * 8;
     n = min(8, a.s.T - i0);
     row = ((int64_t)b * a.s.T + i0) * H + h0;
-    dst = a.stat + ((size_t)(b * H + h0) * a.groups + (i0 >> 3)) * kStatBytes;
+    dst = (size_t)(b * H + h0) * a.groups + (i0 >> 3);
   }
   if (!in) n = 0;
   uint4 o[8], g[8];
@@ -203,23 +201,23 @@ __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_con
     if ((l & 7) == k) mine = d;
   }
   if (in) {
-    float* st = reinterpret_cast<float*>(dst) + (l & 7);
     // rows of the second kernel leave delta alone
     const int64_t t = (int64_t)a.pos.q_start[b] + i0 + (a.rpe ? 0 : l & 7);
     const bool lse_lane = l < 8, delta_lane = (LPR == 8 || l >= 8) && ((l & 7) >= n || t >= kBlock);
-    if (lse_lane) st[0] = -kLog2e * lse;
-    if (delta_lane) st[8] = -mine;
     if (!a.rpe) {
-      uint8_t* ag = a.aug + (dst - a.stat) / kStatBytes * kAugBytes;
-      // rows past the last query: P = 2^-16384 = 0 (and no infinity, which the other
-      // selector's zeros would make NaN)
-      if (lse_lane) put_aug(ag, 0, l & 7, ((l & 7) < n ? -kLog2e * lse : -16384.f) * a.to_score);
-      if (delta_lane) put_aug(ag, 1, l & 7, -mine);
+      float* st = reinterpret_cast<float*>(a.stat + dst * kStatBytes) + (l & 7);
+      if (lse_lane) st[0] = -kLog2e * lse;
+      if (delta_lane) st[8] = -mine;
     }
+    // rows that there are none of: P = 2^-16384 = 0 (and no infinity, which the other
+    // selector's zeros would make NaN)
+    uint8_t* ag = a.aug + dst * kAugBytes;
+    if (lse_lane) put_aug(ag, 0, l & 7, ((l & 7) < n ? -kLog2e * lse : -16384.f) * a.to_score);
+    if (delta_lane) put_aug(ag, 1, l & 7, -mine);
   }
   if (a.rpe && blockIdx.x == 0 && threadIdx.x < 16)
-    reinterpret_cast<float*>(a.stat + (size_t)a.groups * kStatBytes)[threadIdx.x] =
-        threadIdx.x < 8 ? -INFINITY : 0.f;
+    put_aug(a.aug + (size_t)a.groups * kAugBytes, threadIdx.x >> 3, threadIdx.x & 7,
+            threadIdx.x < 8 ? -16384.f * a.to_score : 0.f);
 }
 
 // ---- inverted lists -------------------------------------------------------------

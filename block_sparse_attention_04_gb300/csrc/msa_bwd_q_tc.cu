@@ -109,15 +109,15 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
-    mbar_init(q_full, 128 * kNG);
+    mbar_init(q_full, 4 * kNG);     // one arrival a warp
     mbar_init(s_full, 1);
-    mbar_init(s_read, 128 * kNG);
+    mbar_init(s_read, 4 * kNG);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 128 * kNG + 1);
+    mbar_init(ds_full, 4 * kNG + 1);
     mbar_init(first, 1);
     mbar_init(ds_read, 1);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 128 * kNG);
+    mbar_init(acc_empty, 4 * kNG);
     mbar_init(bar_fin, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&it_full[i], 1);
@@ -151,6 +151,11 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   };
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status, a.wait_polls));
+  };
+  // One arrival for the lanes' work so far.
+  auto warp_arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
   };
 
   if (warp == 0) {
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(q_full);
+      warp_arrive(q_full);
     };
     int it, n = 0, nu = 0;
     bool ok, some = next_item(it, ok);
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           tmem_ld32(base + C::kS + c * kCols, x);
           tmem_ld_wait();
           tc_fence_before();
-          mbar_arrive(s_read);
+          warp_arrive(s_read);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = ffma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         tmem_st16(base + C::kDS + c * (kCols / 2), w);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(ds_full);
+        warp_arrive(ds_full);
       }
       if (!ok) break;
       const int done = it;
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       }
       if (any) {
         tc_fence_before();
-        mbar_arrive(acc_empty);
+        warp_arrive(acc_empty);
         ++nu;
       }
     }
