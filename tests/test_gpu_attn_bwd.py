@@ -323,3 +323,102 @@ def test_reach_of_a_nan_is_bounded(msa):
         assert torch.isfinite(dk[:600, 0].float()).all()
         assert torch.isfinite(c.dk.view(2, -1, 2, 64)[0, :300].float()).all()
         assert torch.isfinite(dk[512:600, 1].float()).all()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=3, T=2790, H=4, G=1, D=64, starts=[0, 500, 77]),
+    dict(B=9, T=950, H=3, G=1, D=128, starts=[0, 1, 100, 127, 128, 129, 300, 400, 500])])
+def test_more_rows_than_one_pass(msa, kw):
+    """Sparse calls of more than 8192 query rows go in passes, which add up dK and dV."""
+    c = Case(sparse=True, **kw)
+    c.forward_ref()
+    ws = c.backward(msa)
+    msa.msa_workspace_status(ws)
+    c.verify()
+
+
+def test_offsets_beyond_32_bits(msa):
+    """The second sequence's caches begin 2.1e9 elements in: the bits of a small cache."""
+    G, D, mb = 8, 128, 16500
+    for sparse in (False, True):
+        c = Case(B=2, T=40, H=16, G=G, D=D, starts=[3, 300], sparse=sparse)
+        c.forward_ref()
+        c.backward(msa)
+        want = [c.dq, c.dk, c.dv]
+        small = c.mb
+        c.k, c.v = ([x, torch.empty(2, mb, 128, G, D, dtype=torch.bfloat16, device="cuda")]
+                    for x in (c.k, c.v))
+        for x in (c.k, c.v):
+            x[1][:, :small] = x[0]
+        c.k, c.v, c.mb = c.k[1], c.v[1], mb
+        p = c.params(msa)
+        ws = msa.sparse_bwd_workspace(p) if sparse else msa.dense_bwd_workspace(p)
+        dq, dk, dv = torch.empty_like(c.q), torch.empty_like(c.k), torch.empty_like(c.v)
+        dk[:, :small], dv[:, :small] = NAN, NAN
+        head = (p, c.q, c.k, c.v) + ((c.sel,) if sparse else ())
+        fn = msa.msa_sparse_attn_bwd if sparse else msa.msa_dense_attn_bwd
+        fn(*head, c.out, c.lse, c.dout, c.starts, c.kv_len, dq, dk, dv, ws)
+        msa.msa_workspace_status(ws)
+        for got, x in zip((dq, dk[:, :small], dv[:, :small]), want):
+            assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(x))
+        del dk, dv
+        c.k = c.v = None
+
+
+def test_two_graphs_on_one_workspace(msa):
+    """Replayed in turn, each finds the workspace as the other left it."""
+    cases = [Case(B=1, T=150, H=12, G=2, D=128, starts=[70], sparse=s, seed=5) for s in (False, True)]
+    cases.append(Case(B=2, T=90, H=4, G=1, D=64, starts=[0, 400], sparse=True, seed=6))
+    sizes = []
+    for c in cases:
+        c.forward_ref()
+        sizes.append(c.backward(msa).numel())
+    ws = torch.empty(max(sizes), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    graphs = []
+    torch.cuda.synchronize()
+    for c in cases:
+        p = c.params(msa)
+        head = (p, c.q, c.k, c.v) + (() if c.sel is None else (c.sel,))
+        fn = msa.msa_dense_attn_bwd if c.sel is None else msa.msa_sparse_attn_bwd
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            fn(*head, c.out, c.lse, c.dout, c.starts, c.kv_len, c.dq, c.dk, c.dv, ws)
+    for order in ((0, 1, 2), (2, 1, 0), (1, 1, 0)):
+        for c in cases:
+            c.dq.fill_(NAN)
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in set(order):
+            cases[i].verify()
+
+
+@pytest.mark.parametrize("sparse,D", [(False, 128), (False, 64), (True, 128), (True, 64)])
+def test_wait_expiry_is_reported_then_next_call_is_exact(msa, sparse, D):
+    """With a cap of one poll (as in tests/test_gpu_wait_expiry.py) the waits between the
+    warps run out on copies that land a moment later: the call reports it, ends, and
+    leaves the context and the workspace usable.  Dense, the K and V of a CTA's next unit
+    wait for all of its tiles, tens of microseconds; sparse, the same warp copies the tiles'
+    rows, so that no wait is longer than two tiles (5 us), which one poll may outlast."""
+    c = Case(B=2, T=2000, H=12, G=2, D=D, starts=[500, 0], sparse=sparse)
+    c.forward_ref()
+    ws = c.backward(msa)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    seen = []
+    try:
+        msa.msa_debug_set_wait_polls(1)
+        for i in range(4):
+            flush.fill_(i)
+            c.backward(msa, ws)
+            try:
+                msa.msa_workspace_status(ws)
+                seen.append(0)
+            except msa.MsaError as e:
+                seen.append(e.status)
+    finally:
+        msa.msa_debug_set_wait_polls(0)
+    torch.cuda.synchronize()
+    assert set(seen) <= {0, -5} and (sparse or -5 in seen), seen
+    c.backward(msa, ws)
+    msa.msa_workspace_status(ws)
+    c.verify()

@@ -261,3 +261,21 @@ def test_graph_and_streams(msa):
     torch.cuda.synchronize()
     for c in cases:
         c.verify(c.keep[1])
+
+
+def test_no_tokens(msa):
+    """A call without tokens writes nothing but the weights' gradients: zeros."""
+    p = msa.params(2, 0, 4, 2, 64, 32, 3)
+    r = msa.rope(64)
+    e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    cache = [torch.full((2, 3, 128, 2, 64), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    dqw, dkw = torch.full((64,), NAN, device="cuda"), torch.full((64,), NAN, device="cuda")
+    some = e(64)          # tensors without elements have no address
+    ws = msa.rope_append_bwd_workspace(p)
+    a = [x.data_ptr() for x in (some, some)]
+    msa.msa_rope_append_bwd(p, r, a[0], a[1], w, w, [0, 5], some.data_ptr(), *cache, some.data_ptr(),
+                            some.data_ptr(), some.data_ptr(), dqw, dkw, ws)
+    torch.cuda.synchronize()
+    assert (dqw == 0).all() and (dkw == 0).all()
+    assert all((x == 3).all() for x in cache)
