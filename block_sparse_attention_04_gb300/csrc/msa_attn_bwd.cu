@@ -16,19 +16,21 @@ namespace {
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Tiles per unit: a block's work is divided where it would hold up the others, i.e. is
-// more than a quarter of a CTA's share of all `tiles` (the largest units go first), but
-// not below 16 tiles (a piece costs about three tiles' time: K and V, the sums' way out
-// and back).  8192 sparse queries at 48/8 heads: 1093 us with a quarter, 1219 with two
-// thirds.  A divided block of n > piece tiles has ceil(n / piece) <= 2 n / piece slots,
-// so a call has at most 2 tiles / piece, and no call of up to `tiles` tiles more than the
-// second bound.
+// Tiles per unit: a block's work is divided where it would hold up the others (the largest
+// units go first): sparse, where it is more than a quarter of a CTA's share of all `tiles`
+// (most of the tiles there might be; 8192 queries at 48/8 heads: the KV-outer kernel 1005 us,
+// 1131 with two thirds, 976 with an eighth, whose joins take that back; 2048 of 32K 336,
+// 339, 357).  Dense, two thirds: the tiles are known and the sizes go down evenly
+// (4 x 2048 tokens 642 us in all, 665 with a quarter).  Not below 16 tiles: a piece costs
+// about three tiles' time, K and V, the sums' way out and back.  A divided block of
+// n > piece tiles has ceil(n / piece) <= 2 n / piece slots, so a call has at most
+// 2 tiles / piece, and no call of up to `tiles` tiles more than the second bound.
 constexpr int kMinPiece = 16;
-int piece_tiles(int64_t tiles) {
-  const int64_t p = tiles / (4 * kBwdSms) + 1;
+int piece_tiles(int64_t tiles, bool sparse) {
+  const int64_t p = (sparse ? tiles / (4 * kBwdSms) : tiles * 2 / (3 * kBwdSms)) + 1;
   return (int)(p < kMinPiece ? kMinPiece : (p > (1 << 28) ? 1 << 28 : p));
 }
-int slots_of(int64_t tiles) { return (int)(2 * tiles / piece_tiles(tiles)); }
+int sparse_slots(int64_t tiles) { return (int)(2 * tiles / piece_tiles(tiles, true)); }
 int most_slots(int64_t tiles) {
   const int64_t n = 2 * tiles / kMinPiece;
   return (int)(n < 8 * kBwdSms ? n : 8 * kBwdSms);
@@ -164,8 +166,8 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
     a.first = t0 == 0;
     a.last = t0 + tp >= s.T;
     const int64_t tiles = sparse ? max_tiles(s, true, a.Tp, a.nbl) : dense_tiles(a);
-    a.piece = piece_tiles(tiles);
-    a.max_slots = sparse ? slots_of(tiles) : (int)dense_tiles(a, a.piece);
+    a.piece = piece_tiles(tiles, sparse);
+    a.max_slots = sparse ? sparse_slots(tiles) : (int)dense_tiles(a, a.piece);
     if ((e = sparse ? launch_bwd_lists(a, st) : launch_bwd_units(a, st)) != cudaSuccess) return e;
     if ((e = launch_bwd_kv(a, t, st)) != cudaSuccess) return e;
     if ((e = launch_bwd_join_kv(a, st)) != cudaSuccess) return e;

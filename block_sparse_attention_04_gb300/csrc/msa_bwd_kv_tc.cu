@@ -15,9 +15,9 @@
 // in tensor memory; Q and dO, MN-major, their B operands from the tiles that the first
 // two products read K-major.  Sparse, dS^T goes to shared memory instead, whose
 // [token][row] order is dK's A operand K-major and that of dQ's part MN-major.
-//   warp 0       TMA of Q and dO (four tiles in use or ahead), bulk copies of the rows'
-//                statistics; takes the units from a shared counter
-//   warp 1       TMA of the unit's K and V
+//   warp 0       TMA of Q and dO (four tiles in use or ahead), the rows' statistics; takes
+//                the units from a shared counter.  Sparse: of Q alone
+//   warp 1       TMA of the unit's K and V; sparse: of dO
 //   warp 2       tcgen05.mma; sparse: of S and dV
 //   warp 3       sparse: tcgen05.mma of dP, dK and dQ's part; dense: waits for copies
 //   warps 4-19   P and dS: four warpgroups, 32 columns of a tile each; a unit's dV, dK
@@ -26,12 +26,25 @@
 // D = 128: tensor memory holds S, dP, dV and dK (512 columns), so dQ's part takes dP's
 // columns until it has been read out, during dV(n+1) and S(n+2).
 //
+// What is rounded: P and dS to bf16, as operands; dQ's parts, one for each of the 16
+// selected blocks, to bf16 (2^-8 each, summed in fp32 afterwards): as fp32 they would be
+// 4 GB written and read again for 8192 tokens of 48 heads, 600 us more for 1420.
+//
 // Shared memory's 128 bytes a cycle are the bound: of a dense tile at D = 128 the
 // products read 192 KB (both operands of S and dP, one of dV and dK), the copies write
 // 64, and a thread per token would read every row's two numbers, 1 KB a warp, whose way to
-// the registers costs as much as 104 KB.  So the dense tiles' numbers come in through the
-// products: a 17th step of S and of dP multiplies ones with them, as three bf16 parts.
-// (4 x 2048 tokens, 48/8 heads: 347 us before.)  A sparse tile has no room left for them.
+// the registers costs as much as 104 KB.  So these come in through the products: a step of
+// S and of dP on top of the others multiplies ones with them, as three bf16 parts
+// (4 x 2048 tokens, 48/8 heads: 293 us, 347 with the numbers read by the threads).  A
+// sparse tile's products read 288 KB (dS, too, and K once more), 64 are copied and 32
+// written: 3000 cycles of the 4600 that a tile takes (8192 tokens: 1001 us, the tensor
+// pipe at 0.48 of its cycles).
+//
+// Tried for the sparse tiles, 8192 tokens: all MMAs from one warp in a fixed order, as for
+// the dense ones, 1107 us (D = 64, 2 x 101 tokens: 40 for 44); the parts read out by the
+// P and dS warps, 1059; dS over dO's slot, with two sets of statistics, 1098; a group's
+// units together, so that its Q and dO stay in L2, 1030 to 1090; rows prefetched into L2
+// three tiles ahead, 1600.
 #include <type_traits>
 
 #include "msa_bwd.h"
@@ -144,6 +157,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ BwdArgs a) {
   using C = KvCfg<D, SP>;
+  after_previous();
   extern __shared__ __align__(1024) uint8_t smem[];   // the swizzled tiles' alignment
   uint8_t* sK = smem;
   uint8_t* sV = sK + C::kTile;
@@ -371,7 +385,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
   } else if (warp == 1) {
     // ------------------------------------------- K and V, sparse: dO too (warp 1)
     // (A box of 8 rows takes a warp some 70 cycles to issue, so that one warp with a tile's
-    // 32 held up the rest: 1093 us for NEWT.)
+    // 32 held up the rest: 8192 tokens 1093 us for 1011.)
     const uint64_t pol = l2_policy_evict_last();
     int it, n = 0, nu = 0;
     bool ok;
@@ -938,9 +952,8 @@ cudaError_t launch_kv(const BwdArgs& a, const AttnBwd& t, cudaStream_t st) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   // one CTA per SM (it takes all of tensor memory, also where shared memory has room for two)
-  note_launches(1);
-  bwd_kv_kernel<D, SP><<<sm_count(), kv_threads<SP>(), C::kSmem, st>>>(tm_q, tm_o, tm_k, tm_v, a);
-  return cudaGetLastError();
+  return launch_behind(bwd_kv_kernel<D, SP>, sm_count(), kv_threads<SP>(), C::kSmem, st, tm_q, tm_o, tm_k,
+                       tm_v, a);
 }
 
 }  // namespace

@@ -57,6 +57,8 @@ __device__ __forceinline__ void put_delta(const StatArgs& a, int b, int i, int h
 
 template <int D>
 __global__ void __launch_bounds__(256) bwd_stat_first_kernel(const __grid_constant__ StatArgs a) {
+  let_next();
+  after_previous();
   extern __shared__ __align__(16) uint8_t kv[];      // K, then V: rows of D bf16 and 16 bytes
   constexpr int PITCH = 2 * D + 16;
   const int lane = threadIdx.x & 31, H = a.s.H, G = a.s.G;
@@ -142,6 +144,7 @@ __global__ void __launch_bounds__(256) bwd_stat_first_kernel(const __grid_consta
 // queries of 48 heads, 403 MB.)
 template <int D>
 __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_constant__ StatArgs a) {
+  let_next();
   constexpr int LPR = D / 8;
   const int H = a.s.H, G = a.s.G, hpg = H / G;
   const int l = threadIdx.x % LPR;
@@ -252,6 +255,8 @@ __device__ __forceinline__ void chunk_ids(const BwdArgs& a, int b, int il, int g
 // CTA (one warp): chunk, group; FILL false: counts, true: entries.
 template <bool FILL>
 __global__ void __launch_bounds__(32) bwd_lists_kernel(const __grid_constant__ BwdArgs a) {
+  let_next();
+  after_previous();
   extern __shared__ int32_t s_cnt[];
   const int lane = threadIdx.x, g = blockIdx.x % a.s.G;
   const int ch = blockIdx.x / a.s.G % a.chunks, b = blockIdx.x / a.s.G / a.chunks;
@@ -296,6 +301,8 @@ __global__ void __launch_bounds__(32) bwd_lists_kernel(const __grid_constant__ B
 
 // Thread per list: its entries, and for each chunk those of the chunks before.
 __global__ void __launch_bounds__(128) bwd_prefix_kernel(const __grid_constant__ BwdArgs a) {
+  let_next();
+  after_previous();
   const int64_t L = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (L >= (int64_t)a.s.G * a.s.B * a.nbl) return;
   const int kb = (int)(L % a.nbl), b = (int)(L / a.nbl % a.s.B), g = (int)(L / a.nbl / a.s.B);
@@ -324,8 +331,8 @@ __global__ void __launch_bounds__(128) bwd_prefix_kernel(const __grid_constant__
 // ---- units ------------------------------------------------------------------
 // One CTA: every item (g, b, kb) below kv_len as one unit, or as several of at most
 // `piece` tiles, whose sums are joined in their order afterwards.  The units are handed
-// out as CTAs become free, so the large ones come first (group by group, which would keep a
-// group's rows in L2, 8192 sparse queries take 1673 us for 1219).
+// out as CTAs become free, so the large ones come first (with a group's large ones together, whose rows
+// would stay in L2, 8192 sparse queries take 3 to 5 % longer).
 constexpr int kClasses = 64;               // of sizes, the largest first
 __device__ __forceinline__ int item_tiles(const BwdArgs& a, int64_t L, int* n) {
   const int kb = (int)(L % a.nbl), b = (int)(L / a.nbl % a.s.B);
@@ -341,7 +348,9 @@ __device__ __forceinline__ int item_class(const BwdArgs& a, int tiles) {
 }
 
 __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__ BwdArgs a) {
-  __shared__ int s_s[1024], s_e[1024];
+  let_next();
+  after_previous();
+  __shared__ int s_s[32], s_e[32];
   __shared__ int s_class[kClasses];    // units of a class, then the next one's place
   const int64_t n = (int64_t)a.s.G * a.s.B * a.nbl;
   const int64_t per = (n + 1023) / 1024;
@@ -358,22 +367,34 @@ __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__
     atomicAdd(&s_class[item_class(a, t)], pieces);
     if (pieces > 1) sl += pieces;
   }
-  s_s[threadIdx.x] = sl;
-  s_e[threadIdx.x] = en;
-  __syncthreads();
-  for (int d = 1; d < 1024; d <<= 1) {
-    int y = 0, z = 0;
-    if ((int)threadIdx.x >= d) {
-      y = s_s[threadIdx.x - d];
-      z = s_e[threadIdx.x - d];
+  // exclusive sums over the threads: in each warp, then of the warps'
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int sl_in = sl, en_in = en;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, sl_in, o), z = __shfl_up_sync(0xffffffffu, en_in, o);
+    if (lane >= o) {
+      sl_in += y;
+      en_in += z;
     }
-    __syncthreads();
-    s_s[threadIdx.x] += y;
-    s_e[threadIdx.x] += z;
-    __syncthreads();
   }
-  sl = s_s[threadIdx.x] - sl;
-  en = s_e[threadIdx.x] - en;
+  if (lane == 31) {
+    s_s[warp] = sl_in;
+    s_e[warp] = en_in;
+  }
+  __syncthreads();
+  int sl_all = s_s[lane], en_all = s_e[lane];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, sl_all, o), z = __shfl_up_sync(0xffffffffu, en_all, o);
+    if (lane >= o) {
+      sl_all += y;
+      en_all += z;
+    }
+  }
+  const int slots = __shfl_sync(0xffffffffu, sl_all, 31);
+  const int sl_before = __shfl_sync(0xffffffffu, sl_all, max(warp - 1, 0));
+  const int en_before = __shfl_sync(0xffffffffu, en_all, max(warp - 1, 0));
+  sl = (warp > 0 ? sl_before : 0) + sl_in - sl;
+  en = (warp > 0 ? en_before : 0) + en_in - en;
   if (threadIdx.x < 32) {                  // exclusive scan of the classes, two a lane
     const int v0 = s_class[2 * threadIdx.x], v1 = s_class[2 * threadIdx.x + 1];
     int x = v0 + v1;
@@ -386,7 +407,7 @@ __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__
     s_class[2 * threadIdx.x + 1] = x - v1;
   }
   if (threadIdx.x == 1023) {
-    a.n_units[1] = s_s[1023];
+    a.n_units[1] = slots;
     a.next_unit[0] = a.next_unit[1] = 0;   // taken units; dense: taken items of dQ
   }
   __syncthreads();
@@ -425,6 +446,8 @@ __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__
 // reads of four slots are in flight together.
 template <int D, int RPE>
 __global__ void __launch_bounds__(256) bwd_join_q_kernel(const __grid_constant__ BwdArgs a) {
+  let_next();
+  after_previous();
   constexpr int PER = 16 / RPE, R = 128 / RPE;   // 16-dim chunks that a warp's read covers
   constexpr int ALL = D / 16 / PER, N = ALL < 2 ? ALL : 2, U = 4;
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -484,6 +507,8 @@ __global__ void __launch_bounds__(256) bwd_join_q_kernel(const __grid_constant__
 constexpr int kJoinParts = 8;
 template <int D>
 __global__ void __launch_bounds__(256) bwd_join_kv_kernel(const __grid_constant__ BwdArgs a) {
+  let_next();
+  after_previous();
   constexpr int ROWS = 2 * kBlock / kJoinParts;
   const int slot = blockIdx.x, part = blockIdx.y;
   if (slot >= a.n_units[1]) return;
@@ -538,6 +563,7 @@ cudaError_t launch_bwd_stats(const Shape& s, const Positions& pos, const AttnBwd
   note_launches(1);
   if (s.D == 128) bwd_stat_kernel<128><<<ctas, kStatThreads, 0, st>>>(a);
   else bwd_stat_kernel<64><<<ctas, kStatThreads, 0, st>>>(a);
+  if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
   bool early = false;
   for (int b = 0; b < s.B; ++b) early |= pos.q_start[b] < kBlock;
   if (early) {
@@ -547,11 +573,10 @@ cudaError_t launch_bwd_stats(const Shape& s, const Positions& pos, const AttnBwd
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
                    : cudaSuccess;
     if (e != cudaSuccess) return e;
-    note_launches(1);
-    if (s.D == 128) bwd_stat_first_kernel<128><<<s.B * s.H, 256, smem, st>>>(a);
-    else bwd_stat_first_kernel<64><<<s.B * s.H, 256, smem, st>>>(a);
+    return launch_behind(s.D == 128 ? bwd_stat_first_kernel<128> : bwd_stat_first_kernel<64>,
+                         s.B * s.H, 256, smem, st, a);
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 cudaError_t launch_bwd_lists(const BwdArgs& a, cudaStream_t st) {
@@ -564,41 +589,32 @@ cudaError_t launch_bwd_lists(const BwdArgs& a, cudaStream_t st) {
     return e;
   const unsigned ctas = (unsigned)((int64_t)a.s.B * a.chunks * a.s.G);
   const int64_t lists = (int64_t)a.s.G * a.s.B * a.nbl;
-  note_launches(3);
-  bwd_lists_kernel<false><<<ctas, 32, smem, st>>>(a);
-  bwd_prefix_kernel<<<(unsigned)((lists + 127) / 128), 128, 0, st>>>(a);
-  if ((e = launch_bwd_units(a, st)) != cudaSuccess) return e;
-  bwd_lists_kernel<true><<<ctas, 32, smem, st>>>(a);
-  return cudaGetLastError();
+  if ((e = launch_behind(bwd_lists_kernel<false>, ctas, 32, smem, st, a)) != cudaSuccess ||
+      (e = launch_behind(bwd_prefix_kernel, (unsigned)((lists + 127) / 128), 128, 0, st, a)) !=
+          cudaSuccess ||
+      (e = launch_bwd_units(a, st)) != cudaSuccess)
+    return e;
+  return launch_behind(bwd_lists_kernel<true>, ctas, 32, smem, st, a);
 }
 
 cudaError_t launch_bwd_units(const BwdArgs& a, cudaStream_t st) {
-  note_launches(1);
-  bwd_units_kernel<<<1, 1024, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_behind(bwd_units_kernel, 1, 1024, 0, st, a);
 }
 
 cudaError_t launch_bwd_join_q(const BwdArgs& a, cudaStream_t st) {
   const int reads = a.s.D / 16 * a.rpe / 16;               // of an entry's rows, two a warp
   const unsigned ctas = (unsigned)(((int64_t)a.s.B * a.Tp * a.s.G * (reads < 2 ? 1 : reads / 2) + 7) / 8);
-  note_launches(1);
-  if (a.s.D == 128) {
-    if (a.rpe == 8) bwd_join_q_kernel<128, 8><<<ctas, 256, 0, st>>>(a);
-    else bwd_join_q_kernel<128, 16><<<ctas, 256, 0, st>>>(a);
-  } else {
-    if (a.rpe == 8) bwd_join_q_kernel<64, 8><<<ctas, 256, 0, st>>>(a);
-    else bwd_join_q_kernel<64, 16><<<ctas, 256, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  return launch_behind(a.s.D == 128
+                           ? (a.rpe == 8 ? bwd_join_q_kernel<128, 8> : bwd_join_q_kernel<128, 16>)
+                           : (a.rpe == 8 ? bwd_join_q_kernel<64, 8> : bwd_join_q_kernel<64, 16>),
+                       ctas, 256, 0, st, a);
 }
 
 cudaError_t launch_bwd_join_kv(const BwdArgs& a, cudaStream_t st) {
   if (a.max_slots == 0) return cudaSuccess;
   const dim3 grid((unsigned)a.max_slots, kJoinParts);
-  note_launches(1);
-  if (a.s.D == 128) bwd_join_kv_kernel<128><<<grid, 256, 0, st>>>(a);
-  else bwd_join_kv_kernel<64><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_behind(a.s.D == 128 ? bwd_join_kv_kernel<128> : bwd_join_kv_kernel<64>, grid, 256, 0,
+                       st, a);
 }
 
 }  // namespace msa

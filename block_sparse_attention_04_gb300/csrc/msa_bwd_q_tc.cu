@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     bwd_q_kernel(const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ BwdQArgs a) {
+  after_previous();
   using C = QCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sO = smem;
@@ -536,6 +537,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
 // dQ of items in several splits: their sums in order.  A thread per 4 dims of a row.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_q_join_kernel(const __grid_constant__ BwdQArgs a) {
+  after_previous();
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = e / (D / 4);
   if (row >= (int64_t)a.nitems * 128) return;
@@ -582,14 +584,12 @@ cudaError_t launch_q(const BwdQArgs& a, const AttnBwd& t, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int ctas = sm_count();
   const int64_t items = (int64_t)a.nitems * a.splits;
-  note_launches(1);
-  bwd_q_kernel<D><<<(unsigned)(items < ctas ? items : ctas), kThreadsQ, C::kSmem, st>>>(
-      tm_o, tm_k, tm_v, a);
-  if (a.splits > 1) {
-    note_launches(1);
-    bwd_q_join_kernel<D><<<(unsigned)(((int64_t)a.nitems * 128 * (D / 4) + 255) / 256), 256, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  if ((e = launch_behind(bwd_q_kernel<D>, (unsigned)(items < ctas ? items : ctas), kThreadsQ, C::kSmem,
+                         st, tm_o, tm_k, tm_v, a)) != cudaSuccess ||
+      a.splits == 1)
+    return e;
+  return launch_behind(bwd_q_join_kernel<D>,
+                       (unsigned)(((int64_t)a.nitems * 128 * (D / 4) + 255) / 256), 256, 0, st, a);
 }
 
 }  // namespace

@@ -154,6 +154,11 @@ __device__ __forceinline__ void stg256(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
+// Launches in programmatic order: the next kernel of the stream may be made resident (it
+// begins with after_previous), and the one before has ended and its writes are there.
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void cp_async_16(uint32_t saddr, const void* g) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr), "l"(g));
 }
