@@ -71,26 +71,35 @@ struct KvCfg {
   static constexpr int kNHalf = D / 64;
   static constexpr int kHalf = 128 * 128;            // 128 rows x 64 dims
   static constexpr int kTile = kNHalf * kHalf;       // K, V, a Q or a dO tile
-  static constexpr int kTiles = 4;                   // Q and dO tiles in shared memory
-  static constexpr int kSS = SP ? 1 : 2;             // statistics of tiles
+  // Dense, D = 64: tensor memory has room for a second S, so that S(n+2) is made on dS(n)
+  // and no P waits for its S (3 chunks of 1000 queries, 64/4 heads: 922 -> 812 us
+  // in all)
+  static constexpr bool kTwoS = !SP && D == 64;
+  static constexpr int kTiles = kTwoS ? 8 : 4;       // Q and dO tiles in shared memory
+  static constexpr int kSS = SP ? 1 : kTwoS ? 4 : 2; // statistics of tiles
   static constexpr int kStat = 16 * kAugBytes;       // statistics of a tile
   static constexpr int kOnes = 2 * 256;              // their selectors, A operands
   static constexpr int kDs = SP ? 2 * kHalf : 0;     // dS^T [2 x 64 rows][128 tokens]
   static constexpr int kFills = 2 * kTiles + kSS;
-  static constexpr int kBars = (2 * (kTiles + kSS) + 12 + 2 * kRing) * 8 + (kRing + kFills) * 4 + 8;
+  static constexpr int kBars = (2 * (kTiles + kSS) + 13 + 2 * kRing) * 8 + (kRing + kFills) * 4 + 8;
   static constexpr int kSmem =
       (2 + kTiles) * kTile + kDs + kOnes + kSS * kStat + 2 * 80 + kBars;
   // Slots of tile n's Q and dO, and the number of times that they were filled before.
   // dO(n) is free first (after dV(n); sparse dP(n)), Q(n) after dK(n), and what comes
   // next, Q(n+2) and dO(n+2), goes into them in that order.
-  __device__ static int q_slot(int n) { return 2 * (n & 1) + (n >> 1 & 1); }
-  __device__ static int o_slot(int n) { return 2 * (n & 1) + (~n >> 1 & 1); }
-  __device__ static uint32_t use(int n) { return (uint32_t)(n >> 1); }
+  // (Eight slots: each its own.)
+  __device__ static int q_slot(int n) { return kTwoS ? 2 * (n & 3) : 2 * (n & 1) + (n >> 1 & 1); }
+  __device__ static int o_slot(int n) { return kTwoS ? 2 * (n & 3) + 1 : 2 * (n & 1) + (~n >> 1 & 1); }
+  __device__ static uint32_t use(int n) { return (uint32_t)(kTwoS ? n >> 2 : n >> 1); }
+  // S of tile n: its columns (the second behind all others), its barrier and its parity
+  __device__ static uint32_t s_at(int n) { return kTwoS && (n & 1) ? 256 + 2 * D : 0; }
+  __device__ static int s_bar(int n) { return kTwoS ? n & 1 : 0; }
+  __device__ static uint32_t s_use(int n) { return (uint32_t)(kTwoS ? n >> 1 : n) & 1; }
   // byte offsets of a tile of rows: sparse tiles hold 8-row groups, half after half
   static constexpr int kGroup = SP ? kNHalf * 1024 : 1024;   // next 8 rows
   static constexpr int kNext = SP ? 1024 : kHalf;            // next 64 dims
   // tensor memory columns: S, dP, dV, dK, dQ's part (D = 128: in dP's place)
-  static constexpr uint32_t kS = 0, kP = 128, kDV = 256, kDK = 256 + D;
+  static constexpr uint32_t kP = 128, kDV = 256, kDK = 256 + D;
   static constexpr uint32_t dq() { return D == 128 ? kP : 256 + 2 * D; }
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
@@ -174,10 +183,10 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
   uint64_t* st_empty = st_full + C::kSS;
   uint64_t* kv_full = st_empty + C::kSS;           // K and V of the unit landed
   uint64_t* kv_empty = kv_full + 1;                // its last product that reads them is done
-  uint64_t* s_full = kv_empty + 1;                 // S of the tile is in tensor memory
+  uint64_t* s_full = kv_empty + 1;                 // [2] S of the tile is in tensor memory
   // [2] dP of the tile: one for even and odd tiles, as the warp that issues S waits for it
   // too and may fall behind
-  uint64_t* dp_full = s_full + 1;
+  uint64_t* dp_full = s_full + 2;
   uint64_t* p_full = dp_full + 2;                  // P written over S
   uint64_t* ds_full = p_full + 1;                  // dS written over dP (and to shared memory)
   uint64_t* acc_full = ds_full + 1;                // the unit's dV and dK are complete
@@ -205,7 +214,8 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
     }
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, SP ? 2 : 1);
-    mbar_init(s_full, SP ? 2 : 1);         // sparse: and the tile's limits are there
+    mbar_init(&s_full[0], SP ? 2 : 1);     // sparse: and the tile's limits are there
+    mbar_init(&s_full[1], 1);
     mbar_init(&dp_full[0], 1);
     mbar_init(&dp_full[1], 1);
     // a warp arrives once (512 threads: see below); dense: and what comes next has landed
@@ -478,33 +488,40 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
       while (next_unit(it, ok)) {
         const KvUnit u = kv_unit<SP>(a, it);
         if (u.tiles == 0) continue;
-        ok = wait_all(kv_full, (uint32_t)nu & 1) && wait_all(&t_full[C::q_slot(n)], C::use(n) & 1) &&
-             wait_all(&st_full[n % C::kSS], (uint32_t)(n / C::kSS) & 1) &&
-             wait_all(&t_full[C::o_slot(n)], C::use(n) & 1);
+        auto issue_s = [&](int m) {
+          rows_product(C::s_at(m), kd, C::q_slot(m), 8, 0, m % C::kSS);
+          tc_commit(&s_full[C::s_bar(m)]);
+        };
+        auto issue_dp = [&](int m) {
+          rows_product(C::kP, vd, C::o_slot(m), 8, 1, m % C::kSS);
+          tc_commit(&dp_full[m & 1]);
+          tc_commit(&st_empty[m % C::kSS]);
+        };
+        const bool two = C::kTwoS && u.tiles > 1;
+        ok = wait_all(kv_full, (uint32_t)nu & 1);
+        for (int m = n; m <= n + two && ok; ++m)
+          ok = wait_all(&t_full[C::q_slot(m)], C::use(m) & 1) &&
+               wait_all(&st_full[m % C::kSS], (uint32_t)(m / C::kSS) & 1);
+        ok = ok && wait_all(&t_full[C::o_slot(n)], C::use(n) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          rows_product(C::kS, kd, C::q_slot(n), 8, 0, n % C::kSS);
-          tc_commit(s_full);
-          rows_product(C::kP, vd, C::o_slot(n), 8, 1, n % C::kSS);
-          tc_commit(&dp_full[n & 1]);
-          tc_commit(&st_empty[n % C::kSS]);
+          issue_s(n);
+          issue_dp(n);
+          if (two) issue_s(n + 1);
           if (u.tiles == 1) tc_commit(kv_empty);
         }
         __syncwarp();
         for (int t = 0; t < u.tiles; ++t, ++n) {
-          const int qs = C::q_slot(n), os = C::o_slot(n), m = n + 1;
+          const int qs = C::q_slot(n), os = C::o_slot(n);
           const bool more = t + 1 < u.tiles;
           ok = wait_all(p_full, (uint32_t)n & 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            sum_product(C::kDV, C::kS, os, 8, t > 0);
+            sum_product(C::kDV, C::s_at(n), os, 8, t > 0);
             tc_commit(&t_empty[os]);
-            if (more) {                           // over P(n), which dV(n) reads
-              rows_product(C::kS, kd, C::q_slot(m), 8, 0, m % C::kSS);
-              tc_commit(s_full);
-            }
+            if (!C::kTwoS && more) issue_s(n + 1);   // over P(n), which dV(n) reads
           }
           __syncwarp();
           ok = wait_all(ds_full, (uint32_t)n & 1);
@@ -513,10 +530,9 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           if (elect_one()) {
             sum_product(C::kDK, C::kP, qs, 8, t > 0);
             tc_commit(&t_empty[qs]);
-            if (more) {                           // over dS(n), which dK(n) reads
-              rows_product(C::kP, vd, C::o_slot(m), 8, 1, m % C::kSS);
-              tc_commit(&dp_full[m & 1]);
-              tc_commit(&st_empty[m % C::kSS]);
+            if (more) {                              // over dS(n), which dK(n) reads
+              issue_dp(n + 1);
+              if (C::kTwoS && t + 2 < u.tiles) issue_s(n + 2);
               if (t + 2 == u.tiles) tc_commit(kv_empty);
             } else {
               tc_commit(acc_full);
@@ -559,7 +575,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           if (lane == 0) mbar_arrive(s_full);
           tc_fence_after();
           if (elect_one()) {
-            rows_product(C::kS, kd, qs, sparse_steps(a, u, t), 0, ss);
+            rows_product(C::s_at(0), kd, qs, sparse_steps(a, u, t), 0, ss);
             tc_commit(s_full);
             tc_commit(&t_empty[qs]);
             tc_commit(&st_empty[ss]);
@@ -577,7 +593,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            sum_product(C::kDV, C::kS, os, sparse_steps(a, u, t), t > 0);
+            sum_product(C::kDV, C::s_at(0), os, sparse_steps(a, u, t), t > 0);
             tc_commit(&t_empty[os]);
             if (t + 1 == u.tiles) tc_commit(acc_full);
           }
@@ -665,14 +681,17 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
       for (int t = 0; t < u.tiles; ++t, ++n) {
         const int m = n + 1;
         const bool more = t + 1 < u.tiles;
-        ok = __any_sync(0xffffffffu, *abort_flag != 0) == 0 &&
-             (!more || (wait_all(&t_full[C::q_slot(m)], C::use(m) & 1) &&
-                        wait_all(&st_full[m % C::kSS], (uint32_t)(m / C::kSS) & 1))) &&
+        auto wait_q = [&](int x) {
+          return wait_all(&t_full[C::q_slot(x)], C::use(x) & 1) &&
+                 wait_all(&st_full[x % C::kSS], (uint32_t)(x / C::kSS) & 1);
+        };
+        ok = __any_sync(0xffffffffu, *abort_flag != 0) == 0 && (C::kTwoS || !more || wait_q(m)) &&
              (t > 0 || nu == 0 || wait_all(acc_empty, (uint32_t)(nu - 1) & 1)) &&
              (n == 0 || wait_all(p_full, (uint32_t)(n - 1) & 1));   // not into the phase before
         if (!ok) break;
         if (lane == 0) mbar_arrive(p_full);
         ok = (!more || wait_all(&t_full[C::o_slot(m)], C::use(m) & 1)) &&
+             (!C::kTwoS || t + 2 >= u.tiles || wait_q(n + 2)) &&
              (n == 0 || wait_all(ds_full, (uint32_t)(n - 1) & 1));
         if (!ok) break;
         if (lane == 0) mbar_arrive(ds_full);
@@ -701,7 +720,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
         int lim = 0;                              // dense: columns below see another token
         bool masked;
         ok = *abort_flag == 0 &&
-             mbar_wait(s_full, (uint32_t)n & 1, a.status, a.wait_polls);
+             mbar_wait(&s_full[C::s_bar(n)], C::s_use(n), a.status, a.wait_polls);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int* tl = sLim + (n & 1) * 20 + c * (kCols / 8);
@@ -725,7 +744,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
         // P of 16 columns, and dS of them, with the masks (few tiles have any) or without
         auto p_of = [&](auto mask, int q) {
           uint32_t x[16], w[8];
-          tmem_ld16(base + C::kS + c * kCols + q * 16, x);
+          tmem_ld16(base + C::s_at(n) + c * kCols + q * 16, x);
           tmem_ld_wait();
 #pragma unroll
           for (int g4 = 0; g4 < 4; ++g4) {          // 4 columns
@@ -741,7 +760,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
             w[2 * g4 + 1] = pack_bf16(p1.x, p1.y);
           }
           // over columns that were read already
-          tmem_st8(base + C::kS + c * kCols + q * 8, w);
+          tmem_st8(base + C::s_at(n) + c * kCols + q * 8, w);
         };
         auto ds_of = [&](auto mask, int q) {
           uint32_t x[16], w[8];
