@@ -131,13 +131,7 @@ int msa_rope_append_bwd(const msa_params* p, const msa_rope* r, const uint16_t* 
       bad_stride(dq_stride, nq) || bad_stride(dk_stride, nk) || bad_stride(dv_stride, nk))
     return MSA_ERR_INVALID_ARG;
   if ((rc = check_ws(ws, ws_bytes, msa_rope_append_bwd_workspace_bytes(p)))) return rc;
-  if (p->T == 0) {                           // no tokens: the weights' gradients are zero
-    const size_t bytes = p->D * sizeof(float);
-    if ((q_weight && cudaMemsetAsync(dq_weight, 0, bytes, stream) != cudaSuccess) ||
-        (k_weight && cudaMemsetAsync(dk_weight, 0, bytes, stream) != cudaSuccess))
-      return MSA_ERR_CUDA;
-    return MSA_OK;
-  }
+  if (p->T == 0) return MSA_OK;
   // the status word, and the counts of CTAs that are done behind it
   static_assert((1 + kRopeBwdCounters) * sizeof(int) <= kAlign, "counters in the header");
   if (cudaMemsetAsync(ws, 0, (1 + kRopeBwdCounters) * sizeof(int), stream) != cudaSuccess)

@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
             const uint32_t from = __shfl_sync(0xffffffffu, sg, i * 4 + (lane >> 3));
             x[i] = make_uint4(0, 0, 0, 0);
             if (i * 4 + (lane >> 3) < boxes)
-              x[i] = __ldg(reinterpret_cast<const uint4*>(a.stat + (size_t)from * kAugBytes) + (lane & 7));
+              x[i] = __ldcg(reinterpret_cast<const uint4*>(a.stat + (size_t)from * kAugBytes) + (lane & 7));
           }
           rows.fetch(a, u, t + 1, lane);
           if (!wait_all(&st_empty[ss], ((uint32_t)(n / C::kSS) & 1) ^ 1)) { ok = false; break; }
