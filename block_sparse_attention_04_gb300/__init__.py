@@ -564,18 +564,21 @@ def yarn_mscale(factor):
 def _row_stride(t, p, heads, what):
     """Elements between consecutive tokens of [B][T][heads][D] (a plain address: the
     row itself)."""
-    row = heads * p.D
-    if t is None or isinstance(t, int) or not hasattr(t, "stride"):
-        return row
-    if tuple(t.shape) not in ((p.B, p.T, heads, p.D), (p.B, p.T, row)):
-        raise ValueError("%s must be [B][T][%d][%d], got %s" % (what, heads, p.D, tuple(t.shape)))
-    st = t.stride()
-    step = st[1] if p.T > 1 else st[0]
-    ok = st[-1] == 1 and (t.dim() == 3 or heads == 1 or st[2] == p.D)
-    ok = ok and (p.B == 1 or st[0] == p.T * step)
-    if p.B == 1 and p.T == 1:
-        step = row
-    if not ok:
+    if t is None or type(t) is int:
+        return heads * p.D
+    B, T, D = p.B, p.T, p.D
+    try:
+        shape, st = t.shape, t.stride()
+    except AttributeError:
+        return heads * D
+    if shape == (B, T, heads, D):
+        ok = heads == 1 or st[2] == D
+    elif shape == (B, T, heads * D):
+        ok = True
+    else:
+        raise ValueError("%s must be [B][T][%d][%d], got %s" % (what, heads, D, tuple(shape)))
+    step = st[1] if T > 1 else st[0] if B > 1 else heads * D
+    if not ok or st[-1] != 1 or (B > 1 and st[0] != T * step):
         raise ValueError("%s: the rows of a token must be contiguous and the tokens evenly "
                          "spaced" % what)
     return step
