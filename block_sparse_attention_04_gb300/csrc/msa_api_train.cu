@@ -65,7 +65,6 @@ int attn_bwd(const msa_params* p, const AttnBwd& a, bool sparse, const int32_t* 
     return MSA_ERR_INVALID_ARG;
   if ((rc = check_ws(ws, ws_bytes, bwd_bytes(p, sparse)))) return rc;
   if (p->T == 0) return MSA_OK;
-  if (cudaMemsetAsync(ws, 0, kAlign, stream) != cudaSuccess) return MSA_ERR_CUDA;
   return cuda_status(launch_attn_bwd(shape_of(p), pos, a, static_cast<int*>(ws),
                                      static_cast<char*>(ws) + kAlign, stream));
 }
@@ -98,11 +97,9 @@ int msa_rope_append(const msa_params* p, const msa_rope* r, const int32_t* block
     return MSA_ERR_INVALID_ARG;
   if ((rc = check_ws(ws, ws_bytes, kAlign))) return rc;
   if (p->T == 0) return MSA_OK;
-  int* status = static_cast<int*>(ws);
-  if (cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return MSA_ERR_CUDA;
   const RopeIn in{q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, k_idx_new};
   return cuda_status(launch_rope_append(shape_of(p, block_table, num_pool_blocks), pos, *r, in,
-                                        q_out, k_cache, v_cache, k_idx_cache, status, stream));
+                                        q_out, k_cache, v_cache, k_idx_cache, static_cast<int*>(ws), stream));
 }
 
 size_t msa_rope_append_bwd_workspace_bytes(const msa_params* p) {
@@ -132,15 +129,11 @@ int msa_rope_append_bwd(const msa_params* p, const msa_rope* r, const uint16_t* 
     return MSA_ERR_INVALID_ARG;
   if ((rc = check_ws(ws, ws_bytes, msa_rope_append_bwd_workspace_bytes(p)))) return rc;
   if (p->T == 0) return MSA_OK;
-  // the status word, and the counts of CTAs that are done behind it
-  static_assert((1 + kRopeBwdCounters) * sizeof(int) <= kAlign, "counters in the header");
-  if (cudaMemsetAsync(ws, 0, (1 + kRopeBwdCounters) * sizeof(int), stream) != cudaSuccess)
-    return MSA_ERR_CUDA;
   const RopeIn in{q, k, nullptr, q_stride, k_stride, 0, q_weight, k_weight, nullptr};
   const RopeGrads g{dq_out, dk_cache, dv_cache, dq, dk, dv, dq_stride, dk_stride, dv_stride,
                     dq_weight, dk_weight};
   return cuda_status(launch_rope_append_bwd(shape_of(p), pos, *r, in, g,
-                                            static_cast<unsigned*>(ws) + 1,
+                                            static_cast<int*>(ws),
                                             static_cast<char*>(ws) + kAlign, stream));
 }
 

@@ -156,7 +156,8 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
   for (int b = 0; b < s.B; ++b) max_len = pos.kv_len[b] > max_len ? pos.kv_len[b] : max_len;
   a.nbl = (max_len + kBlock - 1) / kBlock;
   cudaError_t e;
-  if ((e = launch_bwd_stats(s, pos, t, sparse ? a.rpe : 0, stat, aug, L.stat_groups, st)) !=
+  if ((e = launch_bwd_stats(s, pos, t, sparse ? a.rpe : 0, stat, aug, L.stat_groups, status,
+                            st)) !=
       cudaSuccess)
     return e;
   const int tp = sparse ? pass_len(s) : s.T;

@@ -90,31 +90,10 @@ inline bool bwd_no_scores(const Shape& s) {
   return (sl < 0 ? -sl : sl) < 0x1p-100f;
 }
 
-// Launches a kernel that begins with after_previous() behind another of the same call, so
-// that its launch overlaps that one: a call has five to nine kernels, and where they are
-// short the gaps between them count (dense, 77 tokens: 41 -> 32 us; sparse, 2 x 101: 90 ->
-// 78).  Only the short ones let the next in before they end: behind the KV-outer kernel,
-// the waiting CTAs of a join cost 100 us of 1410.
-template <typename... P, typename... A>
-cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
-                          cudaStream_t st, const A&... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  note_launches(1);
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// Preparation: row statistics (stat: dense only; aug: as operands), lists (sparse), units.
+// Preparation: row statistics (stat: dense only; aug: as operands; clears *status), lists (sparse), units.
 cudaError_t launch_bwd_stats(const Shape& s, const Positions& pos, const AttnBwd& a, int rpe,
-                             uint8_t* stat, uint8_t* aug, uint32_t stat_groups, cudaStream_t st);
+                             uint8_t* stat, uint8_t* aug, uint32_t stat_groups, int* status,
+                             cudaStream_t st);
 cudaError_t launch_bwd_lists(const BwdArgs& a, cudaStream_t st);
 cudaError_t launch_bwd_units(const BwdArgs& a, cudaStream_t st);
 // dK and dV (and, sparse, dQ's parts), one owner per KV block.

@@ -27,6 +27,7 @@ struct StatArgs {
   float to_score;        // 1 / (scale log2e), or 1
   uint32_t groups;
   int rpe;               // 0: dense
+  int* status;
 };
 constexpr int kStatThreads = 256;
 // Writes x at its row of an operand group (0: lse, 1: delta): three bf16 parts.
@@ -145,6 +146,7 @@ __global__ void __launch_bounds__(256) bwd_stat_first_kernel(const __grid_consta
 template <int D>
 __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_constant__ StatArgs a) {
   let_next();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;   // the others are launched behind
   constexpr int LPR = D / 8;
   const int H = a.s.H, G = a.s.G, hpg = H / G;
   const int l = threadIdx.x % LPR;
@@ -554,9 +556,11 @@ __global__ void __launch_bounds__(256) bwd_join_kv_kernel(const __grid_constant_
 }  // namespace
 
 cudaError_t launch_bwd_stats(const Shape& s, const Positions& pos, const AttnBwd& t, int rpe,
-                             uint8_t* stat, uint8_t* aug, uint32_t stat_groups, cudaStream_t st) {
+                             uint8_t* stat, uint8_t* aug, uint32_t stat_groups, int* status,
+                             cudaStream_t st) {
   const float to_score = bwd_no_scores(s) ? 1.f : 1.f / (s.scale * kLog2e);
-  StatArgs a{s, pos, t.q, t.k, t.v, t.out, t.dout, t.lse, stat, aug, to_score, stat_groups, rpe};
+  StatArgs a{s, pos, t.q, t.k, t.v, t.out, t.dout, t.lse, stat, aug, to_score, stat_groups, rpe,
+             status};
   const int per_cta = kStatThreads / (s.D / 8);
   const int64_t grps = rpe ? (int64_t)stat_groups : (int64_t)s.B * stat_groups * s.H;
   const unsigned ctas = (unsigned)((grps + per_cta - 1) / per_cta);

@@ -29,7 +29,6 @@ constexpr int kRopeThreads = 128;
 constexpr int kRows = 5;                    // rows of a token that a thread has, at most
 constexpr int kFwdCtas = 8, kBwdCtas = 4;   // of an SM
 constexpr int kBwdMaxCtas = 1024;
-constexpr int kJoinGroups = kRopeBwdCounters - 1;   // of CTAs whose sums are added up together
 constexpr int kHalfRot = MSA_MAX_ROT / 2;
 
 struct RopeArgs {
@@ -44,7 +43,6 @@ struct RopeArgs {
   int* status;
   int parts;                   // CTAs that share a run of tokens (each a part of its rows)
   float* part_w;               // backward: [CTAs][2][D] sums of the weights' gradients
-  unsigned* counters;          // backward: [1 + kJoinGroups], zeroed
 };
 
 // 16 bytes to shared memory, without waiting; copies_done waits for all of the thread's but
@@ -238,8 +236,8 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas) rope_append_kernel(
     }
     if (threadIdx.x == kRopeThreads - 65) {  // of a warp without angles
       const int64_t pos = (int64_t)a.pos.q_start[tw.b] + tw.i;
-      const int64_t pb = cache_block(a.s, tw.b, (int)(pos / kBlock), a.status);
-      t.slot = pb < 0 ? -1 : pb * kBlock + pos % kBlock;   // flagged: nothing written
+      const int64_t pb = cache_block(a.s, tw.b, (int)(pos / kBlock), nullptr);
+      t.slot = pb < 0 ? -1 : pb * kBlock + pos % kBlock;   // outside the pool: not written
     }
   };
 #pragma unroll
@@ -262,7 +260,20 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas) rope_append_kernel(
     }
   }
   fill(ts[0]);
-  __syncthreads();
+  // The first CTA looks through the call's table entries and writes the status, so that
+  // nothing has to clear it before the launch (a memset: 3 us of 15).
+  bool outside = false;
+  if (blockIdx.x == 0 && a.s.bt) {
+    const int blocks = (a.s.T + kBlock - 1) / kBlock + 1;      // of a sequence, at most
+    for (int64_t e = threadIdx.x; e < (int64_t)a.s.B * blocks; e += kRopeThreads) {
+      const int b = (int)(e / blocks);
+      const int64_t kb = a.pos.q_start[b] / kBlock + e % blocks;
+      if (kb * kBlock < (int64_t)a.pos.q_start[b] + a.s.T)
+        outside |= cache_block(a.s, b, (int)kb, nullptr) < 0;
+    }
+  }
+  outside = __syncthreads_or(outside);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = outside ? kDevInvalid : 0;
   for (int buf = 0, st = 0;; buf ^= 1, st = st + 1 == kStages ? 0 : st + 1) {
     const int64_t tok = tw.tok;
     load(st == 0 ? kStages - 1 : st - 1);    // read by every thread before the last barrier
@@ -320,27 +331,15 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas) rope_append_kernel(
   }
 }
 
-// Counts this CTA in; true in the one that makes `n`, which sees what the others wrote.
-__device__ __forceinline__ bool is_last(unsigned* counter, int n, bool* shared) {
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) *shared = atomicAdd(counter, 1u) == (unsigned)n - 1;
-  __syncthreads();
-  __threadfence();
-  return *shared;
-}
-
 // ---- backward ---------------------------------------------------------------
 // The same walk over the tokens.  A thread sums the weights' gradients of its 8 dims over
-// all its rows; the CTA's sums go to part_w in a fixed order, and the last CTA to finish
-// adds the CTAs' up, again in a fixed order.
+// all its rows; the CTA's sums go to part_w, which a second kernel adds up, in fixed orders.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) rope_append_bwd_kernel(
     const __grid_constant__ RopeArgs a) {
   constexpr int LPR = D / 8, ROWS = kRopeThreads / LPR, U = kRows;
   __shared__ TokenTable<D, 1> ts[2];
   __shared__ float4 w[2][2][LPR];
-  __shared__ bool last;
   const int n_tok = (int)((int64_t)a.s.B * a.s.T);
   const int step = gridDim.x / a.parts, part = blockIdx.x % a.parts;
   const int H = a.s.H, G = a.s.G, heads = H + 2 * G;
@@ -356,6 +355,8 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) rope_append_bwd_kernel
   const int at = (r0 + row) * D + 8 * l;
   TokenWalk tw(blockIdx.x / a.parts, step, a.s.T);
   extern __shared__ uint4 stage[];           // [kStages][gradients, inputs][U][threads]
+  let_next();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
   TokenWalk lw = tw;                         // the token to load next
   const uint16_t* q = a.in.q + lw.tok * a.in.q_stride + at;
   const uint16_t* k = a.in.k + lw.tok * a.in.k_stride + at - H * D;
@@ -494,31 +495,27 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) rope_append_bwd_kernel
     for (int wp = 0; wp < kRopeThreads / 32; ++wp) x += red[wp][d / D][d % D];
     a.part_w[(size_t)blockIdx.x * 2 * D + d] = x;
   }
-  // the last CTA of a group adds its CTAs' sums up, the last group the groups' sums
-  const int size = ((int)gridDim.x + kJoinGroups - 1) / kJoinGroups;
-  const int group = blockIdx.x / size, groups = ((int)gridDim.x + size - 1) / size;
-  const int first = group * size, n = min(size, (int)gridDim.x - first);
-  float2 x;
-  auto add_up = [&](int c0, int count, int every) {
-    x = make_float2(0.f, 0.f);
-    if ((int)threadIdx.x >= D) return;
-    const float2* part = reinterpret_cast<const float2*>(a.part_w) + (size_t)c0 * D + threadIdx.x;
+}
+
+// The CTAs' sums of 32 columns (q's D, then k's): each warp every 32nd CTA's, then the warps.
+template <int D>
+__global__ void __launch_bounds__(1024) rope_join_weights_kernel(const __grid_constant__ RopeArgs a,
+                                                                 int ctas) {
+  __shared__ float sum[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int d = blockIdx.x * 32 + lane;
+  after_previous();
+  float x = 0.f;
 #pragma unroll 8
-    for (int c = 0; c < count; ++c) x = fadd2(x, __ldcg(part + (size_t)c * every * D));
-  };
-  if (!is_last(a.counters + 1 + group, n, &last)) return;
-  add_up(first, n, 1);
-  if ((int)threadIdx.x < D)
-    reinterpret_cast<float2*>(a.part_w)[(size_t)first * D + threadIdx.x] = x;
-  if (!is_last(a.counters, groups, &last)) return;
-  add_up(0, groups, size);
-  const int d = 2 * threadIdx.x;
-  if (d >= 2 * D) return;
-  float* dst = d < D ? a.g.dq_weight : a.g.dk_weight;
-  if (d < D ? q_norm : k_norm) {
-    dst[d % D] = x.x;
-    dst[d % D + 1] = x.y;
-  }
+  for (int c = warp; c < ctas; c += 32) x += __ldcg(a.part_w + (size_t)c * 2 * D + d);
+  sum[warp][lane] = x;
+  __syncthreads();
+  if (warp > 0) return;
+  x = 0.f;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) x += sum[w][lane];
+  if (d < D ? a.in.q_weight != nullptr : a.in.k_weight != nullptr)
+    (d < D ? a.g.dq_weight : a.g.dk_weight)[d % D] = x;
 }
 
 RopeArgs rope_args(const Shape& s, const Positions& pos, const msa_rope& r, const RopeIn& in) {
@@ -586,21 +583,26 @@ cudaError_t launch_rope_append(const Shape& s, const Positions& pos, const msa_r
 size_t rope_bwd_scratch_bytes() { return (size_t)kBwdMaxCtas * 2 * 128 * sizeof(float); }
 
 cudaError_t launch_rope_append_bwd(const Shape& s, const Positions& pos, const msa_rope& r,
-                                   const RopeIn& in, const RopeGrads& g, unsigned* counters,
+                                   const RopeIn& in, const RopeGrads& g, int* status,
                                    char* base, cudaStream_t st) {
   RopeArgs a = rope_args(s, pos, r, in);
   a.g = g;
-  a.counters = counters;
+  a.status = status;
   a.part_w = reinterpret_cast<float*>(base);
   const unsigned ctas = rope_grid(a, std::min<int64_t>((int64_t)sm_count() * kBwdCtas, kBwdMaxCtas), kRopeThreads, kRows);
   constexpr int smem = kStages * 2 * kRows * kRopeThreads * (int)sizeof(uint4);
-  if (s.D == 128)
-    return r.interleaved
-               ? launch_rows(rope_append_bwd_kernel<128, true>, ctas, kRopeThreads, smem, a, st)
-               : launch_rows(rope_append_bwd_kernel<128, false>, ctas, kRopeThreads, smem, a, st);
-  return r.interleaved
-             ? launch_rows(rope_append_bwd_kernel<64, true>, ctas, kRopeThreads, smem, a, st)
-             : launch_rows(rope_append_bwd_kernel<64, false>, ctas, kRopeThreads, smem, a, st);
+  const cudaError_t e =
+      s.D == 128
+          ? (r.interleaved
+                 ? launch_rows(rope_append_bwd_kernel<128, true>, ctas, kRopeThreads, smem, a, st)
+                 : launch_rows(rope_append_bwd_kernel<128, false>, ctas, kRopeThreads, smem, a, st))
+          : (r.interleaved
+                 ? launch_rows(rope_append_bwd_kernel<64, true>, ctas, kRopeThreads, smem, a, st)
+                 : launch_rows(rope_append_bwd_kernel<64, false>, ctas, kRopeThreads, smem, a, st));
+  if (e != cudaSuccess || (!in.q_weight && !in.k_weight)) return e;
+  return s.D == 128
+             ? launch_behind(rope_join_weights_kernel<128>, 8, 1024, 0, st, a, (int)ctas)
+             : launch_behind(rope_join_weights_kernel<64>, 4, 1024, 0, st, a, (int)ctas);
 }
 
 }  // namespace msa

@@ -277,3 +277,19 @@ def test_no_tokens(msa):
                             msa.rope_append_bwd_workspace(p))
     torch.cuda.synchronize()
     assert all((x == 3).all() for x in (*cache, dqw, dkw, some))
+
+
+def test_only_the_entries_of_the_call_count(msa):
+    """Table entries that no token of the call falls into may hold anything; one bad entry
+    of the last sequence's last block is found."""
+    c = Case(B=70, T=130, H=4, G=2, D=64, Di=32, starts=[7 * b for b in range(70)], rot=64, paged=True)
+    first = torch.tensor(c.starts, device="cuda") // 128
+    last = (torch.tensor(c.starts, device="cuda") + 129) // 128
+    kb = torch.arange(c.table.shape[1], device="cuda")
+    c.table[(kb < first[:, None]) | (kb > last[:, None])] = -5
+    ws, _ = c.run(msa)
+    msa.msa_workspace_status(ws)
+    c.table[69, last[69]] = 2 ** 31 - 1
+    ws, _ = c.run(msa)
+    with pytest.raises(msa.MsaError):
+        msa.msa_workspace_status(ws)
