@@ -57,9 +57,7 @@ __device__ __forceinline__ void put_delta(const StatArgs& a, int b, int i, int h
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) bwd_stat_first_kernel(const __grid_constant__ StatArgs a) {
-  let_next();
-  after_previous();
+__device__ __forceinline__ void stat_first(const StatArgs& a) {
   extern __shared__ __align__(16) uint8_t kv[];      // K, then V: rows of D bf16 and 16 bytes
   constexpr int PITCH = 2 * D + 16;
   const int lane = threadIdx.x & 31, H = a.s.H, G = a.s.G;
@@ -140,13 +138,27 @@ __global__ void __launch_bounds__(256) bwd_stat_first_kernel(const __grid_consta
   }
 }
 
+// It reads nothing that the kernel before it writes, and writes other words: it runs beside
+// that and waits for it in the end, as the kernel behind waits for this one alone.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_stat_first_kernel(const __grid_constant__ StatArgs a) {
+  let_next();
+  stat_first<D>(a);
+  after_previous();
+}
+
 // A group of 8 rows per D/8 lanes: its 16 row reads are in flight together, and it is
 // written whole.  (One row at a time, with its two numbers stored singly: 438 us for 16K
 // queries of 48 heads, 403 MB.)
 template <int D>
 __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_constant__ StatArgs a) {
-  let_next();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;   // the others are launched behind
+  if (threadIdx.x == 0) {
+    if (blockIdx.x == 0) {
+      *a.status = 0;                 // before the next kernel, which may report, can start
+      __threadfence();
+    }
+    let_next();
+  }
   constexpr int LPR = D / 8;
   const int H = a.s.H, G = a.s.G, hpg = H / G;
   const int l = threadIdx.x % LPR;
@@ -258,7 +270,8 @@ __device__ __forceinline__ void chunk_ids(const BwdArgs& a, int b, int il, int g
 template <bool FILL>
 __global__ void __launch_bounds__(32) bwd_lists_kernel(const __grid_constant__ BwdArgs a) {
   let_next();
-  after_previous();
+  // the first pass's counts need nothing of the call: beside the statistics (see above)
+  if (FILL || !a.first) after_previous();
   extern __shared__ int32_t s_cnt[];
   const int lane = threadIdx.x, g = blockIdx.x % a.s.G;
   const int ch = blockIdx.x / a.s.G % a.chunks, b = blockIdx.x / a.s.G / a.chunks;
@@ -297,8 +310,10 @@ __global__ void __launch_bounds__(32) bwd_lists_kernel(const __grid_constant__ B
     }
   }
   __syncwarp();
-  if (!FILL)
+  if (!FILL) {
     for (int k = lane; k < a.nbl; k += 32) cnt[k] = s_cnt[k];
+    after_previous();
+  }
 }
 
 // Thread per list: its entries, and for each chunk those of the chunks before.
@@ -351,7 +366,7 @@ __device__ __forceinline__ int item_class(const BwdArgs& a, int tiles) {
 
 __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__ BwdArgs a) {
   let_next();
-  after_previous();
+  if (a.sel) after_previous();             // dense units come from the shape: as above
   __shared__ int s_s[32], s_e[32];
   __shared__ int s_class[kClasses];    // units of a class, then the next one's place
   const int64_t n = (int64_t)a.s.G * a.s.B * a.nbl;
@@ -440,6 +455,7 @@ __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__
       a.units[at++] = make_int4(x, first, size, slot);
     }
   }
+  after_previous();
 }
 
 // ---- joins --------------------------------------------------------------------
