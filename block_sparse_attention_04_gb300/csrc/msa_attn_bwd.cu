@@ -113,6 +113,36 @@ Layout layout(const Shape& s, bool sparse) {
   return L;
 }
 
+cudaError_t launch_dense_q(const BwdArgs& a, const AttnBwd& t, const uint8_t* stat, char* part,
+                           cudaStream_t st) {
+  BwdQArgs q{};
+  q.s = a.s;
+  q.pos = a.pos;
+  q.nqt = a.nqt;
+  q.nitems = q_items(a.s);
+  // few items: the key blocks of each over several CTAs, at least 4 blocks a split
+  q.splits = 1;
+  if (q.nitems < kMaxQParts) {
+    int blocks = 1;
+    for (int b = 0; b < a.s.B; ++b) {
+      const int n = (int)(((int64_t)a.pos.q_start[b] + a.s.T - 1) / kBlock) + 1;
+      blocks = n > blocks ? n : blocks;
+    }
+    const int by_parts = kMaxQParts / q.nitems, by_blocks = blocks / 4;
+    q.splits = by_parts < by_blocks ? by_parts : by_blocks;
+    if (q.splits < 1) q.splits = 1;
+  }
+  q.next_item = a.n_units + 3;
+  q.stat = stat;
+  q.q = t.q;
+  q.stat_groups = a.stat_groups;
+  q.part = reinterpret_cast<float*>(part);
+  q.dq = t.dq;
+  q.status = a.status;
+  q.wait_polls = a.wait_polls;
+  return launch_bwd_q(q, t, st);
+}
+
 }  // namespace
 
 size_t attn_bwd_scratch_bytes(const Shape& s, bool sparse) { return layout(s, sparse).total; }
@@ -171,36 +201,12 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
     a.max_slots = sparse ? sparse_slots(tiles) : (int)dense_tiles(a, a.piece);
     if ((e = sparse ? launch_bwd_lists(a, st) : launch_bwd_units(a, st)) != cudaSuccess) return e;
     if ((e = launch_bwd_kv(a, t, st)) != cudaSuccess) return e;
+    // (dQ's kernel directly behind the KV-outer one: it starts as that leaves SMs)
+    if (!sparse && (e = launch_dense_q(a, t, stat, base + L.part_q, st)) != cudaSuccess) return e;
     if ((e = launch_bwd_join_kv(a, st)) != cudaSuccess) return e;
     if (sparse && (e = launch_bwd_join_q(a, st)) != cudaSuccess) return e;
   }
-  if (sparse) return cudaSuccess;
-  BwdQArgs q{};
-  q.s = s;
-  q.pos = pos;
-  q.nqt = a.nqt;
-  q.nitems = q_items(s);
-  // few items: the key blocks of each over several CTAs, at least 4 blocks a split
-  q.splits = 1;
-  if (q.nitems < kMaxQParts) {
-    int blocks = 1;
-    for (int b = 0; b < s.B; ++b) {
-      const int n = (int)(((int64_t)pos.q_start[b] + s.T - 1) / kBlock) + 1;
-      blocks = n > blocks ? n : blocks;
-    }
-    const int by_parts = kMaxQParts / q.nitems, by_blocks = blocks / 4;
-    q.splits = by_parts < by_blocks ? by_parts : by_blocks;
-    if (q.splits < 1) q.splits = 1;
-  }
-  q.next_item = a.n_units + 3;
-  q.stat = stat;
-  q.q = t.q;
-  q.stat_groups = L.stat_groups;
-  q.part = reinterpret_cast<float*>(base + L.part_q);
-  q.dq = t.dq;
-  q.status = status;
-  q.wait_polls = a.wait_polls;
-  return launch_bwd_q(q, t, st);
+  return cudaSuccess;
 }
 
 }  // namespace msa

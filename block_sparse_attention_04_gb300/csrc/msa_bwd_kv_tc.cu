@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
                   const __grid_constant__ BwdArgs a) {
   using C = KvCfg<D, SP>;
   after_previous();
+  if (!SP) let_next();       // dQ's kernel takes the SMs as they come free
   extern __shared__ __align__(1024) uint8_t smem[];   // the swizzled tiles' alignment
   uint8_t* sK = smem;
   uint8_t* sV = sK + C::kTile;

@@ -70,7 +70,6 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     bwd_q_kernel(const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ BwdQArgs a) {
-  after_previous();
   using C = QCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sO = smem;
@@ -397,8 +396,9 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       const float* st = reinterpret_cast<const float*>(
                             a.stat + ((size_t)(d.b * a.s.H + d.h) * a.stat_groups + (i >> 3)) * kStatBytes) +
                         (i & 7);
-      nl = st[0];
-      nd = st[8];
+      // (past L1: the kernel that wrote them has ended, but no wait of this one says so)
+      nl = __ldcg(st);
+      nd = __ldcg(st + 8);
       if (d.kb0 == d.kb1) return;
       if constexpr (kDims == 32) {
         const uint32_t w[16] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w,
@@ -532,6 +532,10 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // The KV-outer kernel lets this one in when its own CTAs are all there, i.e. behind the
+  // preparation, of which alone this one reads: it fills the SMs as they come free, and
+  // ends when that has ended.
+  after_previous();
 }
 
 // dQ of items in several splits: their sums in order.  A thread per 4 dims of a row.
