@@ -10,10 +10,18 @@
 // Bound by HBM: a token's rows are read once and written once.  A row (one head of
 // a token) is spread over D/8 lanes of 8 dims: 16-byte accesses, the norm's sum by
 // log2(D/8) shuffles, and with halves rotated (i with i + rot/2) the partner's 8
-// values come from the lane rot/16 away.  The angles of a token are made once per
+// values from the lane rot/16 away.  The angles of a token are made once per
 // CTA for all of its heads: t * inv_freq in turns and its fraction in fp64 (fp32
 // would leave 2^-24 * t turns of error: a third of a radian at t = 1M), sine and
 // cosine of the fraction in fp32.
+//
+// What holds it up is the arithmetic of a row, so a row is C x + S y, y its partners, with
+// the norm's weights inside C and S (one table per token for the queries, one for K), in
+// packed fp32; a thread has the same rows of each token, and the next token's come by
+// cp.async while one is worked on.  Many small CTAs, as each waits at a barrier per token.
+// 8192 tokens, 48/8 heads of 128, half rotated: 47.5 us (302 MB, 0.84 of HBM's floor; rows
+// in registers, index arithmetic per row and tables of angles: 84).  Backward, 8192 tokens:
+// 70 us and 3 for the weights' join (386 MB; 168 before).
 #include <algorithm>
 #include <type_traits>
 
@@ -25,7 +33,7 @@ namespace msa {
 namespace {
 
 constexpr int kStages = 2;                  // tokens in shared memory
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 128;           // (256: 46 and 87 us; 3 x 1000 tokens 15 for 11)
 constexpr int kRows = 5;                    // rows of a token that a thread has, at most
 constexpr int kFwdCtas = 8, kBwdCtas = 4;   // of an SM
 constexpr int kBwdMaxCtas = 1024;
