@@ -38,11 +38,11 @@
 // (4 x 2048 tokens, 48/8 heads: 293 us, 347 with the numbers read by the threads).  A
 // sparse tile's products read 288 KB (dS, too, and K once more), 64 are copied and 32
 // written: 3000 cycles of the 4600 that a tile takes (8192 tokens: 1001 us, the tensor
-// pipe at 0.48 of its cycles).
+// pipe at 0.55 of its cycles).
 //
 // Tried for the sparse tiles, 8192 tokens: all MMAs from one warp in a fixed order, as for
 // the dense ones, 1107 us (D = 64, 2 x 101 tokens: 40 for 44); the parts read out by the
-// P and dS warps, 1059; dS over dO's slot, with two sets of statistics, 1098; a group's
+// P and dS warps, 1059 (with warp 2's waits by another warp 1270); dS over dO's slot, with two sets of statistics, 1098; a group's
 // units together, so that its Q and dO stay in L2, 1030 to 1090; rows prefetched into L2
 // three tiles ahead, 1600.
 #include <type_traits>

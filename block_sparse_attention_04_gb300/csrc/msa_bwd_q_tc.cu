@@ -5,9 +5,11 @@
 //     dQ += dS K
 // with the queries on the 128 lanes.  Q and dS are A operands in tensor memory, so that of
 // the products' operands only dO, and K and V as they stream by, are read from shared
-// memory: 128 KB a block at D = 128 and 64 written, as many cycles as the MMAs take.  (With
-// Q in shared memory too and dS over S: 4 x 2048 tokens 278 us.)  K is read K-major by S
-// and MN-major by dQ.
+// memory: 128 KB a block at D = 128 and 64 written, as many cycles as the MMAs take (with
+// Q in shared memory too and dS over S one sequence of 16K tokens took 4 % longer).  K is
+// read K-major by S and MN-major by dQ.  4 x 2048 tokens, 48/8 heads: 282 us, the tensor
+// pipe at 0.50 of its cycles; what it waits for is the softmax of a block, as a second S
+// does not fit into tensor memory at D = 128.
 //   warp 0       TMA of the item's dO; takes the items from a shared counter
 //   warp 1       TMA of K (four stages at D = 128: a block is read from S, two blocks ahead,
 //                to dQ) and V (two)
