@@ -422,3 +422,15 @@ def test_wait_expiry_is_reported_then_next_call_is_exact(msa, sparse, D):
     c.backward(msa, ws)
     msa.msa_workspace_status(ws)
     c.verify()
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(B=256, T=1, H=16, G=8, D=64, starts=[(61 * i) % 700 for i in range(256)]),
+    dict(B=2, T=150, H=128, G=8, D=128, starts=[0, 77])])
+def test_most_sequences_and_heads(msa, kw, sparse):
+    c = Case(sparse=sparse, **kw)
+    c.forward_ref()
+    ws = c.backward(msa)
+    msa.msa_workspace_status(ws)
+    c.verify()

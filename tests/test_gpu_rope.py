@@ -293,3 +293,14 @@ def test_only_the_entries_of_the_call_count(msa):
     ws, _ = c.run(msa)
     with pytest.raises(msa.MsaError):
         msa.msa_workspace_status(ws)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=256, T=1, H=16, G=8, D=64, Di=32, starts=[(61 * i) % 700 for i in range(256)], rot=64),
+    dict(B=3, T=70, H=128, G=8, D=128, Di=64, starts=[0, 60, 127], rot=128)])
+def test_most_sequences_and_heads(msa, kw):
+    c = Case(paged=True, **kw)
+    ws, r = c.run(msa)
+    msa.msa_workspace_status(ws)
+    c.verify(r)
+    test_append_backward(msa, kw)
