@@ -912,8 +912,8 @@ __global__ void __launch_bounds__(256) attn_tc_merge_kernel(AttnPass a, uint16_t
     }
   }
   uint16_t* dst = out + (((size_t)b * a.s.T + i) * H + h) * D + lane * PER;
-  // a selection without a visible token: zeros (8-bit calls)
-  const float inv = Q8 && W == 0.f ? 0.f : back / W;
+  // a selection without a visible token: zeros
+  const float inv = W == 0.f ? 0.f : back / W;
 #pragma unroll
   for (int e = 0; e < PER; e += 2)
     *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);

@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(
   if constexpr (DENSE) {
     dense_fold<PER>(ds, (size_t)(b * T + i) * s.H + h, M, L, acc, lane, dst, lse);
   } else {
-    const float inv = 1.f / L;
+    const float inv = L == 0.f ? 0.f : 1.f / L;          // nothing visible: zeros
 #pragma unroll
     for (int e = 0; e < PER; e += 2) {
       *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);

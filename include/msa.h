@@ -122,7 +122,8 @@ int msa_index_topk(const msa_params *p, const uint16_t *q_idx, const uint16_t *k
 
 /* Step 4 for a caller-given selection sel[B][T][G][16] (ids ascending or
  * not, -1 entries ignored, every id in [0, lb]).  Writes out[B][T][H][D]
- * bf16 (round to nearest even) from fp32 accumulation. */
+ * bf16 (round to nearest even) from fp32 accumulation; zeros where a
+ * (query, group) has no id to attend to. */
 int msa_sparse_attn(const msa_params *p, const uint16_t *q, const uint16_t *k_cache,
                     const uint16_t *v_cache, const int32_t *sel, const int32_t *q_start,
                     const int32_t *kv_len, uint16_t *out, void *ws, size_t ws_bytes,
@@ -498,7 +499,7 @@ int msa_rope_append_bwd(const msa_params *p, const msa_rope *r, const uint16_t *
  * msa_sparse_attn and msa_dense_attn that also return what the backward pass needs
  * of the softmax: lse[B][T][H] (fp32), the natural logarithm of the sum of
  * exp(scale * s) over the tokens that the (query, head) attends to (-inf where
- * there is none).  out and ws are as without it. */
+ * there is none: out is zeros there).  out and ws are as without it. */
 int msa_sparse_attn_lse(const msa_params *p, const uint16_t *q, const uint16_t *k_cache,
                         const uint16_t *v_cache, const int32_t *sel, const int32_t *q_start,
                         const int32_t *kv_len, uint16_t *out, float *lse, void *ws,
