@@ -561,6 +561,13 @@ def yarn_mscale(factor):
     return 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
 
 
+def _no_row_ptr(t):
+    """The address of an array of the tokens of a call without any: torch gives a tensor
+    without elements none, and the library, which asks for one, reads nothing there."""
+    a = _ptr(t)
+    return a if a != 0 or type(t) is int else 256
+
+
 def _row_stride(t, p, heads, what):
     """Elements between consecutive tokens of [B][T][heads][D] (a plain address: the
     row itself)."""
@@ -577,6 +584,8 @@ def _row_stride(t, p, heads, what):
         ok = True
     else:
         raise ValueError("%s must be [B][T][%d][%d], got %s" % (what, heads, D, tuple(shape)))
+    if T == 0:
+        return heads * D
     step = st[1] if T > 1 else st[0] if B > 1 else heads * D
     if not ok or st[-1] != 1 or (B > 1 and st[0] != T * step):
         raise ValueError("%s: the rows of a token must be contiguous and the tokens evenly "
@@ -589,11 +598,12 @@ def msa_rope_append(p, r, q, k, v, k_idx_new, q_weight, k_weight, q_start, q_out
     """Norm and rotation of q and k, and the rows of K, V and K_idx into the caches
     (see msa.h).  q, k and v may be parts of one tensor; the weights and k_idx_new
     (with k_idx_cache) may be None."""
+    row = _ptr if p.T else _no_row_ptr
     _call(load().msa_rope_append(ctypes.byref(p), ctypes.byref(r), _ptr(block_table),
-                                 int(num_pool_blocks), _ptr(q), _ptr(k), _ptr(v),
+                                 int(num_pool_blocks), row(q), row(k), row(v),
                                  _row_stride(q, p, p.H, "q"), _row_stride(k, p, p.G, "k"),
                                  _row_stride(v, p, p.G, "v"), _ptr(q_weight), _ptr(k_weight),
-                                 _ptr(k_idx_new), _host_i32(q_start, p.B), _ptr(q_out),
+                                 row(k_idx_new), _host_i32(q_start, p.B), row(q_out),
                                  _ptr(k_cache), _ptr(v_cache), _ptr(k_idx_cache), _ptr(ws),
                                  _nbytes(ws), _stream(stream)), "msa_rope_append")
 
@@ -612,11 +622,12 @@ def msa_rope_append_bwd(p, r, q, k, q_weight, k_weight, q_start, dq_out, dk_cach
                         dv, dq_weight, dk_weight, ws, stream=None):
     """From the gradients of q_out and of the caches to those of the projections and of
     the norms' weights (see msa.h)."""
-    _call(load().msa_rope_append_bwd(ctypes.byref(p), ctypes.byref(r), _ptr(q), _ptr(k),
+    row = _ptr if p.T else _no_row_ptr
+    _call(load().msa_rope_append_bwd(ctypes.byref(p), ctypes.byref(r), row(q), row(k),
                                      _row_stride(q, p, p.H, "q"), _row_stride(k, p, p.G, "k"),
                                      _ptr(q_weight), _ptr(k_weight), _host_i32(q_start, p.B),
-                                     _ptr(dq_out), _ptr(dk_cache), _ptr(dv_cache), _ptr(dq), _ptr(dk),
-                                     _ptr(dv), _row_stride(dq, p, p.H, "dq"),
+                                     row(dq_out), _ptr(dk_cache), _ptr(dv_cache), row(dq), row(dk),
+                                     row(dv), _row_stride(dq, p, p.H, "dq"),
                                      _row_stride(dk, p, p.G, "dk"), _row_stride(dv, p, p.G, "dv"),
                                      _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), _nbytes(ws),
                                      _stream(stream)), "msa_rope_append_bwd")
@@ -624,17 +635,19 @@ def msa_rope_append_bwd(p, r, q, k, q_weight, k_weight, q_start, dq_out, dk_cach
 
 def msa_sparse_attn_lse(p, q, k_cache, v_cache, sel, q_start, kv_len, out, lse, ws, stream=None):
     """msa_sparse_attn that also writes lse [B][T][H] (see msa.h)."""
-    _call(load().msa_sparse_attn_lse(ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                     _ptr(sel), _host_i32(q_start, p.B), _host_i32(kv_len, p.B),
-                                     _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)),
+    row = _ptr if p.T else _no_row_ptr
+    _call(load().msa_sparse_attn_lse(ctypes.byref(p), row(q), _ptr(k_cache), _ptr(v_cache),
+                                     row(sel), _host_i32(q_start, p.B), _host_i32(kv_len, p.B),
+                                     row(out), row(lse), _ptr(ws), _nbytes(ws), _stream(stream)),
           "msa_sparse_attn_lse")
 
 
 def msa_dense_attn_lse(p, q, k_cache, v_cache, q_start, kv_len, out, lse, ws, stream=None):
     """msa_dense_attn that also writes lse [B][T][H] (see msa.h)."""
-    _call(load().msa_dense_attn_lse(ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                    _host_i32(q_start, p.B), _host_i32(kv_len, p.B), _ptr(out),
-                                    _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)),
+    row = _ptr if p.T else _no_row_ptr
+    _call(load().msa_dense_attn_lse(ctypes.byref(p), row(q), _ptr(k_cache), _ptr(v_cache),
+                                    _host_i32(q_start, p.B), _host_i32(kv_len, p.B), row(out),
+                                    row(lse), _ptr(ws), _nbytes(ws), _stream(stream)),
           "msa_dense_attn_lse")
 
 
@@ -650,9 +663,10 @@ def sparse_bwd_workspace(p, device="cuda"):
 def msa_sparse_attn_bwd(p, q, k_cache, v_cache, sel, out, lse, dout, q_start, kv_len, dq, dk, dv, ws,
                         stream=None):
     """dq, and the rows of dk and dv in the caches' layout, of msa_sparse_attn (see msa.h)."""
-    _call(load().msa_sparse_attn_bwd(ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                     _ptr(sel), _ptr(out), _ptr(lse), _ptr(dout),
-                                     _host_i32(q_start, p.B), _host_i32(kv_len, p.B), _ptr(dq),
+    row = _ptr if p.T else _no_row_ptr
+    _call(load().msa_sparse_attn_bwd(ctypes.byref(p), row(q), _ptr(k_cache), _ptr(v_cache),
+                                     row(sel), row(out), row(lse), row(dout),
+                                     _host_i32(q_start, p.B), _host_i32(kv_len, p.B), row(dq),
                                      _ptr(dk), _ptr(dv), _ptr(ws), _nbytes(ws), _stream(stream)),
           "msa_sparse_attn_bwd")
 
@@ -669,9 +683,10 @@ def dense_bwd_workspace(p, device="cuda"):
 def msa_dense_attn_bwd(p, q, k_cache, v_cache, out, lse, dout, q_start, kv_len, dq, dk, dv, ws,
                        stream=None):
     """dq, and the rows of dk and dv in the caches' layout, of msa_dense_attn (see msa.h)."""
-    _call(load().msa_dense_attn_bwd(ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out),
-                                    _ptr(lse), _ptr(dout), _host_i32(q_start, p.B),
-                                    _host_i32(kv_len, p.B), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
+    row = _ptr if p.T else _no_row_ptr
+    _call(load().msa_dense_attn_bwd(ctypes.byref(p), row(q), _ptr(k_cache), _ptr(v_cache), row(out),
+                                    row(lse), row(dout), _host_i32(q_start, p.B),
+                                    _host_i32(kv_len, p.B), row(dq), _ptr(dk), _ptr(dv), _ptr(ws),
                                     _nbytes(ws), _stream(stream)), "msa_dense_attn_bwd")
 
 
