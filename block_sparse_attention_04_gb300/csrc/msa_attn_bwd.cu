@@ -1,10 +1,10 @@
 // The attention's backward pass (msa_sparse_attn_bwd, msa_dense_attn_bwd): its scratch
 // and the sequence of its kernels.
-//   dense    statistics; units; dK and dV (KV-outer); dQ (query-outer)
+//   dense    statistics; units; dK and dV (KV-outer) and dQ (query-outer) in one launch
 //   sparse   statistics; per pass of at most 8192 query rows: lists, units; dK, dV and
 //            dQ's parts (KV-outer); the parts' sums.  Several passes add dK and dV up
 //            in fp32.
-// Dense takes two kernels of four and three products where one of five would do: dQ
+// Dense takes two passes of four and three products where one of five would do: dQ
 // would then need one sum per (query, head) over all key blocks, i.e. atomic adds (whose
 // order changes the bits) of 128 x D fp32 per tile.
 #include "msa_bwd.h"
@@ -113,34 +113,17 @@ Layout layout(const Shape& s, bool sparse) {
   return L;
 }
 
-cudaError_t launch_dense_q(const BwdArgs& a, const AttnBwd& t, const uint8_t* stat, char* part,
-                           cudaStream_t st) {
-  BwdQArgs q{};
-  q.s = a.s;
-  q.pos = a.pos;
-  q.nqt = a.nqt;
-  q.nitems = q_items(a.s);
-  // few items: the key blocks of each over several CTAs, at least 4 blocks a split
-  q.splits = 1;
-  if (q.nitems < kMaxQParts) {
-    int blocks = 1;
-    for (int b = 0; b < a.s.B; ++b) {
-      const int n = (int)(((int64_t)a.pos.q_start[b] + a.s.T - 1) / kBlock) + 1;
-      blocks = n > blocks ? n : blocks;
-    }
-    const int by_parts = kMaxQParts / q.nitems, by_blocks = blocks / 4;
-    q.splits = by_parts < by_blocks ? by_parts : by_blocks;
-    if (q.splits < 1) q.splits = 1;
+// Few items: the key blocks of each over several CTAs, at least 4 blocks a split.
+int dense_q_splits(const BwdArgs& a) {
+  if (a.q_items >= kMaxQParts) return 1;
+  int blocks = 1;
+  for (int b = 0; b < a.s.B; ++b) {
+    const int n = (int)(((int64_t)a.pos.q_start[b] + a.s.T - 1) / kBlock) + 1;
+    blocks = n > blocks ? n : blocks;
   }
-  q.next_item = a.n_units + 3;
-  q.stat = stat;
-  q.q = t.q;
-  q.stat_groups = a.stat_groups;
-  q.part = reinterpret_cast<float*>(part);
-  q.dq = t.dq;
-  q.status = a.status;
-  q.wait_polls = a.wait_polls;
-  return launch_bwd_q(q, t, st);
+  const int by_parts = kMaxQParts / a.q_items, by_blocks = blocks / 4;
+  const int n = by_parts < by_blocks ? by_parts : by_blocks;
+  return n < 1 ? 1 : n;
 }
 
 }  // namespace
@@ -161,6 +144,7 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
   a.sel = t.sel;
   a.n_units = reinterpret_cast<int*>(base);
   a.next_unit = a.n_units + 2;
+  a.next_item = a.n_units + 3;
   uint8_t* const stat = sparse ? nullptr : reinterpret_cast<uint8_t*>(base + L.stat);
   uint8_t* const aug = reinterpret_cast<uint8_t*>(base + L.aug);
   a.stat = aug;
@@ -182,6 +166,13 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
   a.dv = t.dv;
   a.status = status;
   a.wait_polls = debug_wait_polls();
+  if (!sparse) {
+    a.q_items = q_items(s);
+    a.q_splits = dense_q_splits(a);
+    a.nums = stat;
+    a.q = t.q;
+    a.part_q = reinterpret_cast<float*>(base + L.part_q);
+  }
   int max_len = 1;
   for (int b = 0; b < s.B; ++b) max_len = pos.kv_len[b] > max_len ? pos.kv_len[b] : max_len;
   a.nbl = (max_len + kBlock - 1) / kBlock;
@@ -201,8 +192,6 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
     a.max_slots = sparse ? sparse_slots(tiles) : (int)dense_tiles(a, a.piece);
     if ((e = sparse ? launch_bwd_lists(a, st) : launch_bwd_units(a, st)) != cudaSuccess) return e;
     if ((e = launch_bwd_kv(a, t, st)) != cudaSuccess) return e;
-    // (dQ's kernel directly behind the KV-outer one: it starts as that leaves SMs)
-    if (!sparse && (e = launch_dense_q(a, t, stat, base + L.part_q, st)) != cudaSuccess) return e;
     if ((e = launch_bwd_join_kv(a, st)) != cudaSuccess) return e;
     if (sparse && (e = launch_bwd_join_q(a, st)) != cudaSuccess) return e;
   }

@@ -49,7 +49,7 @@ struct BwdArgs {
   int* n_units;              // [2]: units, partial slots
   int4* slots;               // per slot: (b, g, kb packed as x; its unit's slots, 0 but for the first)
   int max_slots;
-  int* next_unit;            // [2] counters of taken units and of taken dQ items
+  int* next_unit;            // counter of taken units
   const uint8_t* stat;       // as operands
   uint32_t stat_groups;      // dense: groups per (b, h); sparse: index of the neutral group
   bool no_scores;            // scale log2e below 2^-100
@@ -60,6 +60,13 @@ struct BwdArgs {
   uint16_t *dq, *dk, *dv;
   int* status;
   uint32_t wait_polls;       // poll cap of the pipeline waits (0: wall-clock bound only)
+  // dense: dQ by (query tile, head) items x splits of their key blocks
+  int kv_ctas;               // CTAs of the launch that work on units; those behind take items
+  int q_items, q_splits;
+  int* next_item;            // counter of taken items
+  const uint8_t* nums;       // statistics as numbers
+  const uint16_t* q;
+  float* part_q;             // q_splits > 1: [items][splits][128][D] partial dq
 };
 
 // Dense: the first query tile that sees block kb of sequence b (nqt: none does).
@@ -68,21 +75,6 @@ __host__ __device__ inline int bwd_first_tile(const BwdArgs& a, int b, int kb) {
   if (i0 >= a.s.T) return a.nqt;
   return i0 > 0 ? (int)(i0 / 128) : 0;
 }
-
-// Units of the dense call: (query tile, head) items x splits of the key blocks.
-struct BwdQArgs {
-  Shape s;
-  Positions pos;
-  int nqt, nitems, splits;
-  int* next_item;
-  const uint8_t* stat;
-  uint32_t stat_groups;
-  const uint16_t* q;
-  float* part;               // splits > 1: [nitems][splits][128][D] partial dq
-  uint16_t* dq;
-  int* status;
-  uint32_t wait_polls;
-};
 
 // Whether scores are scaled to nothing.
 inline bool bwd_no_scores(const Shape& s) {
@@ -96,10 +88,8 @@ cudaError_t launch_bwd_stats(const Shape& s, const Positions& pos, const AttnBwd
                              cudaStream_t st);
 cudaError_t launch_bwd_lists(const BwdArgs& a, cudaStream_t st);
 cudaError_t launch_bwd_units(const BwdArgs& a, cudaStream_t st);
-// dK and dV (and, sparse, dQ's parts), one owner per KV block.
+// dK and dV, one owner per KV block; sparse: dQ's parts, dense: dQ.
 cudaError_t launch_bwd_kv(const BwdArgs& a, const AttnBwd& t, cudaStream_t st);
-// Dense dQ.
-cudaError_t launch_bwd_q(const BwdQArgs& a, const AttnBwd& t, cudaStream_t st);
 // Joins: dQ from the selected blocks' parts; dK and dV of blocks in several pieces.
 cudaError_t launch_bwd_join_q(const BwdArgs& a, cudaStream_t st);
 cudaError_t launch_bwd_join_kv(const BwdArgs& a, cudaStream_t st);

@@ -48,6 +48,7 @@
 #include <type_traits>
 
 #include "msa_bwd.h"
+#include "msa_bwd_q_tc.cuh"
 #include "msa_q8.cuh"
 #include "msa_tma.h"
 
@@ -161,13 +162,10 @@ struct SparseRows {
 };
 
 template <int D, bool SP>
-__global__ void __launch_bounds__(kv_threads<SP>(), 1)
-    bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
-                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ BwdArgs a) {
+__device__ __forceinline__ void kv_cta(const CUtensorMap& tm_q, const CUtensorMap& tm_o,
+                                       const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                       const BwdArgs& a) {
   using C = KvCfg<D, SP>;
-  after_previous();
-  if (!SP) let_next();       // dQ's kernel takes the SMs as they come free
   extern __shared__ __align__(1024) uint8_t smem[];   // the swizzled tiles' alignment
   uint8_t* sK = smem;
   uint8_t* sV = sK + C::kTile;
@@ -937,9 +935,32 @@ __global__ void __launch_bounds__(kv_threads<SP>(), 1)
   }
 }
 
+template <int D>
+__global__ void __launch_bounds__(kv_threads<true>(), 1)
+    bwd_sparse_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ BwdArgs a) {
+  after_previous();
+  kv_cta<D, true>(tm_q, tm_o, tm_k, tm_v, a);
+}
+
+// Dense: dQ's CTAs are the last of the launch, so that they take the SMs as the KV-outer ones
+// leave them (two launches, the second behind the end of the first: 4 x 2048 tokens 632 us for
+// 603).  Neither kind waits for the other.
+template <int D>
+__global__ void __launch_bounds__(kv_threads<false>(), 1)
+    bwd_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ BwdArgs a) {
+  static_assert(kv_threads<false>() == dq::kThreadsQ, "both kinds of CTA have the same threads");
+  after_previous();
+  if ((int)blockIdx.x < a.kv_ctas) kv_cta<D, false>(tm_q, tm_o, tm_k, tm_v, a);
+  else dq::q_cta<D>(tm_o, tm_k, tm_v, a);
+}
+
 template <int D, bool SP>
-cudaError_t launch_kv(const BwdArgs& a, const AttnBwd& t, cudaStream_t st) {
-  using C = KvCfg<D, SP>;
+cudaError_t launch_kv(const BwdArgs& args, const AttnBwd& t, cudaStream_t st) {
+  BwdArgs a = args;
   const Shape& s = a.s;
   CUtensorMap tm_q, tm_o, tm_k, tm_v;
   if (SP) {
@@ -968,12 +989,31 @@ cudaError_t launch_kv(const BwdArgs& a, const AttnBwd& t, cudaStream_t st) {
   if (!encode_bf16_map(&tm_k, t.k, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_bf16_map(&tm_v, t.v, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(bwd_kv_kernel<D, SP>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
   // one CTA per SM (it takes all of tensor memory, also where shared memory has room for two)
-  return launch_behind(bwd_kv_kernel<D, SP>, sm_count(), kv_threads<SP>(), C::kSmem, st, tm_q, tm_o, tm_k,
-                       tm_v, a);
+  const int ctas = sm_count();
+  cudaError_t e;
+  if constexpr (SP) {
+    constexpr int smem = KvCfg<D, true>::kSmem;
+    if ((e = cudaFuncSetAttribute(bwd_sparse_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  smem)) != cudaSuccess)
+      return e;
+    return launch_behind(bwd_sparse_kernel<D>, ctas, kv_threads<true>(), smem, st, tm_q, tm_o, tm_k,
+                         tm_v, a);
+  } else {
+    constexpr int smem = KvCfg<D, false>::kSmem > dq::QCfg<D>::kSmem ? KvCfg<D, false>::kSmem
+                                                                     : dq::QCfg<D>::kSmem;
+    a.kv_ctas = ctas;
+    const int64_t items = (int64_t)a.q_items * a.q_splits;
+    const int q_ctas = (int)(items < ctas ? items : ctas);
+    if ((e = cudaFuncSetAttribute(bwd_dense_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  smem)) != cudaSuccess ||
+        (e = launch_behind(bwd_dense_kernel<D>, (unsigned)(ctas + q_ctas), kv_threads<false>(), smem, st,
+                           tm_q, tm_o, tm_k, tm_v, a)) != cudaSuccess ||
+        a.q_splits == 1)
+      return e;
+    return launch_behind(dq::bwd_q_join_kernel<D>,
+                         (unsigned)(((int64_t)a.q_items * 128 * (D / 4) + 255) / 256), 256, 0, st, a);
+  }
 }
 
 }  // namespace

@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(1024) bwd_units_kernel(const __grid_constant__
   }
   if (threadIdx.x == 1023) {
     a.n_units[1] = slots;
-    a.next_unit[0] = a.next_unit[1] = 0;   // taken units; dense: taken items of dQ
+    *a.next_unit = *a.next_item = 0;
   }
   __syncthreads();
   for (int64_t L = lo; L < hi; ++L) {

@@ -1,4 +1,5 @@
-// dQ of the dense attention's backward pass on tensor cores, query-outer: an item is a
+// dQ of the dense attention's backward pass on tensor cores, query-outer (the CTAs of
+// msa_bwd_kv_tc.cu's dense kernel that are not KV-outer ones): an item is a
 // 128-query tile of one head (or a split of its key blocks, where there are few items),
 // whose dQ stays in tensor memory over the key blocks,
 //     S = Q K^T   dP = dO V^T   dS = 2^(S scale log2e - lse log2e) (dP - delta)
@@ -7,7 +8,7 @@
 // the products' operands only dO, and K and V as they stream by, are read from shared
 // memory: 128 KB a block at D = 128 and 64 written, as many cycles as the MMAs take (with
 // Q in shared memory too and dS over S one sequence of 16K tokens took 4 % longer).  K is
-// read K-major by S and MN-major by dQ.  4 x 2048 tokens, 48/8 heads: 282 us, the tensor
+// read K-major by S and MN-major by dQ.  4 x 2048 tokens, 48/8 heads: 282 us alone, the tensor
 // pipe at 0.50 of its cycles; what it waits for is the softmax of a block, as a second S
 // does not fit into tensor memory at D = 128.
 //   warp 0       TMA of the item's dO; takes the items from a shared counter
@@ -19,6 +20,7 @@
 //   warps 4-19   Q into tensor memory; dS: four warpgroups, 32 keys of a block each; an
 //                item's dQ
 // The two numbers of a row (lse, delta) stay in registers over an item.
+#pragma once
 #include <type_traits>
 
 #include "msa_bwd.h"
@@ -27,6 +29,7 @@
 
 namespace msa {
 namespace {
+namespace dq {
 
 constexpr int kMmaW = 2, kWaitW = 3, kSoftW = 4;
 constexpr int kNG = 4;                    // warpgroups for dS ...
@@ -50,10 +53,10 @@ struct QCfg {
 struct QItem {
   int b, h, g, qt, kb0, kb1;     // key blocks [kb0, kb1)
 };
-__device__ __forceinline__ QItem q_item(const BwdQArgs& a, int it) {
+__device__ __forceinline__ QItem q_item(const BwdArgs& a, int it) {
   QItem d;
-  const int split = it % a.splits;
-  int r = it / a.splits;
+  const int split = it % a.q_splits;
+  int r = it / a.q_splits;
   const int per = a.s.B * a.s.H;
   d.qt = a.nqt - 1 - r / per;
   r %= per;
@@ -62,16 +65,14 @@ __device__ __forceinline__ QItem q_item(const BwdQArgs& a, int it) {
   d.g = d.h / (a.s.H / a.s.G);
   const int i_last = min(a.s.T - 1, d.qt * 128 + 127);
   const int n = (int)(((int64_t)a.pos.q_start[d.b] + i_last) / kBlock) + 1;
-  d.kb0 = (int)((int64_t)n * split / a.splits);
-  d.kb1 = (int)((int64_t)n * (split + 1) / a.splits);
+  d.kb0 = (int)((int64_t)n * split / a.q_splits);
+  d.kb1 = (int)((int64_t)n * (split + 1) / a.q_splits);
   return d;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreadsQ, 1)
-    bwd_q_kernel(const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v,
-                 const __grid_constant__ BwdQArgs a) {
+__device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap& tm_k,
+                                      const CUtensorMap& tm_v, const BwdArgs& a) {
   using C = QCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sO = smem;
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_first();
       int cur = atomicAdd(a.next_item, 1);
-      if (cur >= a.nitems * a.splits) cur = -1;
+      if (cur >= a.q_items * a.q_splits) cur = -1;
       ring[0] = cur;
       mbar_arrive(&it_full[0]);
       int n = 0;                 // items with key blocks, loaded
@@ -177,8 +178,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           ok = false;
           break;
         }
-        int nx = *abort_flag ? a.nitems * a.splits : atomicAdd(a.next_item, 1);
-        if (nx >= a.nitems * a.splits) nx = -1;
+        int nx = *abort_flag ? a.q_items * a.q_splits : atomicAdd(a.next_item, 1);
+        if (nx >= a.q_items * a.q_splits) nx = -1;
         ring[slot] = nx;
         mbar_arrive(&it_full[slot]);
         const QItem d = q_item(a, cur);
@@ -396,9 +397,9 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
 #pragma unroll
       for (int k = 0; k < kDims / 8; ++k) q[k] = i < T ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
       const float* st = reinterpret_cast<const float*>(
-                            a.stat + ((size_t)(d.b * a.s.H + d.h) * a.stat_groups + (i >> 3)) * kStatBytes) +
+                            a.nums + ((size_t)(d.b * a.s.H + d.h) * a.stat_groups + (i >> 3)) * kStatBytes) +
                         (i & 7);
-      // (past L1: the kernel that wrote them has ended, but no wait of this one says so)
+      // (past L1: the kernels that write them may still run when this one is launched)
       nl = __ldcg(st);
       nd = __ldcg(st + 8);
       if (d.kb0 == d.kb1) return;
@@ -498,8 +499,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           for (int e = 0; e < 16; ++e) x[e] = 0;
         }
         if (i >= T) continue;
-        if (a.splits > 1) {
-          float* dst = a.part + ((size_t)done * 128 + r) * D + dim;
+        if (a.q_splits > 1) {
+          float* dst = a.part_q + ((size_t)done * 128 + r) * D + dim;
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {
             const uint32_t y[8] = {x[e], x[e + 1], x[e + 2], x[e + 3],
@@ -534,28 +535,24 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // The KV-outer kernel lets this one in when its own CTAs are all there, i.e. behind the
-  // preparation, of which alone this one reads: it fills the SMs as they come free, and
-  // ends when that has ended.
-  after_previous();
 }
 
 // dQ of items in several splits: their sums in order.  A thread per 4 dims of a row.
 template <int D>
-__global__ void __launch_bounds__(256) bwd_q_join_kernel(const __grid_constant__ BwdQArgs a) {
+__global__ void __launch_bounds__(256) bwd_q_join_kernel(const __grid_constant__ BwdArgs a) {
   after_previous();
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = e / (D / 4);
-  if (row >= (int64_t)a.nitems * 128) return;
+  if (row >= (int64_t)a.q_items * 128) return;
   const int item = (int)(row / 128), r = (int)(row % 128), dim = (int)(e % (D / 4)) * 4;
-  const QItem d = q_item(a, item * a.splits);
+  const QItem d = q_item(a, item * a.q_splits);
   const int i = d.qt * 128 + r;
   if (i >= a.s.T) return;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int k = 0; k < a.splits; ++k) {
+  for (int k = 0; k < a.q_splits; ++k) {
     const float4 y = __ldcs(reinterpret_cast<const float4*>(
-        a.part + (((size_t)item * a.splits + k) * 128 + r) * D + dim));
+        a.part_q + (((size_t)item * a.q_splits + k) * 128 + r) * D + dim));
     x.x += y.x;
     x.y += y.y;
     x.z += y.z;
@@ -566,42 +563,6 @@ __global__ void __launch_bounds__(256) bwd_q_join_kernel(const __grid_constant__
       make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
 }
 
-template <int D>
-cudaError_t launch_q(const BwdQArgs& a, const AttnBwd& t, cudaStream_t st) {
-  using C = QCfg<D>;
-  const Shape& s = a.s;
-  CUtensorMap tm_o, tm_k, tm_v;
-  {
-    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)s.H, (cuuint64_t)s.T, (cuuint64_t)s.B};
-    cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)s.H * D * 2,
-                             (cuuint64_t)s.T * s.H * D * 2};
-    cuuint32_t box[4] = {64, 1, 128, 1};
-    if (!encode_bf16_map(&tm_o, t.dout, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
-  }
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)s.G, (cuuint64_t)(s.cache_blocks() * kBlock)};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)s.G * D * 2};
-  cuuint32_t box[3] = {64, 1, (cuuint32_t)kBlock};
-  if (!encode_bf16_map(&tm_k, t.k, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_bf16_map(&tm_v, t.v, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(bwd_q_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::kSmem);
-  if (e != cudaSuccess) return e;
-  const int ctas = sm_count();
-  const int64_t items = (int64_t)a.nitems * a.splits;
-  if ((e = launch_behind(bwd_q_kernel<D>, (unsigned)(items < ctas ? items : ctas), kThreadsQ, C::kSmem,
-                         st, tm_o, tm_k, tm_v, a)) != cudaSuccess ||
-      a.splits == 1)
-    return e;
-  return launch_behind(bwd_q_join_kernel<D>,
-                       (unsigned)(((int64_t)a.nitems * 128 * (D / 4) + 255) / 256), 256, 0, st, a);
-}
-
+}  // namespace dq
 }  // namespace
-
-cudaError_t launch_bwd_q(const BwdQArgs& a, const AttnBwd& t, cudaStream_t st) {
-  return a.s.D == 128 ? launch_q<128>(a, t, st) : launch_q<64>(a, t, st);
-}
-
 }  // namespace msa

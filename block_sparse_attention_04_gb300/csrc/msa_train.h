@@ -6,11 +6,12 @@
 namespace msa {
 
 // Launches a kernel that begins with after_previous() behind another of the same call, so
-// that its launch overlaps that one: a call has five to nine kernels, and where they are
+// that its launch overlaps that one: a call has four to nine kernels, and where they are
 // short the gaps between them count (dense, 77 tokens: 41 -> 32 us; sparse, 2 x 101: 90 ->
 // 78).  The short ones let the next in when they start; behind the sparse KV-outer kernel,
 // the waiting CTAs of a join would cost 100 us of 1410.  A kernel that needs nothing of the
-// one before it waits in its end instead (dense, 77 tokens: 30 -> 20; 4 x 2048: 642 -> 603).
+// one before it waits in its end instead (dense, 77 tokens: 30 -> 25.5; 4 x 2048: 642 -> 632):
+// it then reads only what the caller gave, and writes what no kernel before it reads.
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
                           cudaStream_t st, const A&... args) {
