@@ -153,10 +153,7 @@ __global__ void __launch_bounds__(256) bwd_stat_first_kernel(const __grid_consta
 template <int D>
 __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_constant__ StatArgs a) {
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) {
-      *a.status = 0;                 // before the next kernel, which may report, can start
-      __threadfence();
-    }
+    if (blockIdx.x == 0) *a.status = 0;    // (a kernel that may report waits for this one first)
     let_next();
   }
   constexpr int LPR = D / 8;
@@ -244,9 +241,9 @@ __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(const __grid_con
 // meet in a list take their places in lane order.  Counts per chunk, then the entries
 // of the chunks before, come from a first pass.
 
-// The 16 ids of lane's row of a chunk of 32, -1 where they are not to be used.
-__device__ __forceinline__ void chunk_ids(const BwdArgs& a, int b, int il, int g, bool flag,
-                                          int (&id)[kTopk]) {
+// The 16 ids of lane's row of a chunk of 32, -1 where they are not to be used.  Whether one
+// is past the local block.
+__device__ __forceinline__ bool chunk_ids(const BwdArgs& a, int b, int il, int g, int (&id)[kTopk]) {
   const bool in = il < a.Tp;
   const int i = a.t0 + (in ? il : 0);
   const int4* sr =
@@ -263,7 +260,7 @@ __device__ __forceinline__ void chunk_ids(const BwdArgs& a, int b, int il, int g
       bad |= in && x[u] > lb;
     }
   }
-  if (flag && bad) flag_invalid(a.status);
+  return bad;
 }
 
 // CTA (one warp): chunk, group; FILL false: counts, true: entries.
@@ -280,10 +277,11 @@ __global__ void __launch_bounds__(32) bwd_lists_kernel(const __grid_constant__ B
   // (off and cnt are not used yet where a list is empty: any value will do)
   for (int k = lane; k < a.nbl; k += 32) s_cnt[k] = FILL ? off[k] + cnt[k] : 0;
   __syncwarp();
+  bool bad = false;
   for (int r0 = ch * kChunkRows; r0 < min(a.Tp, (ch + 1) * kChunkRows); r0 += 32) {
     const int il = r0 + lane;
     int id[kTopk];
-    chunk_ids(a, b, il, g, !FILL, id);
+    bad |= chunk_ids(a, b, il, g, id);
     int place[kTopk];
 #pragma unroll
     for (int j = 0; j < kTopk; ++j) {
@@ -313,6 +311,7 @@ __global__ void __launch_bounds__(32) bwd_lists_kernel(const __grid_constant__ B
   if (!FILL) {
     for (int k = lane; k < a.nbl; k += 32) cnt[k] = s_cnt[k];
     after_previous();
+    if (bad) flag_invalid(a.status);       // behind the kernel that clears it
   }
 }
 
