@@ -18,7 +18,8 @@ from . import _build
 __all__ = ["MsaParams", "MsaError", "params", "load", "msa_workspace_bytes", "msa_index_topk",
            "msa_sparse_attn", "msa_forward", "msa_workspace_status", "msa_status_string",
            "msa_kernel_launch_count", "msa_index_topk_noalloc", "msa_debug_set_wait_polls",
-           "msa_quality_workspace_bytes", "msa_selection_quality", "quality_workspace",
+           "msa_debug_delay_copies", "msa_quality_workspace_bytes", "msa_selection_quality",
+           "quality_workspace",
            "msa_cache_append", "msa_forward_paged", "msa_dense_workspace_bytes",
            "msa_dense_attn", "dense_workspace", "msa_index_kl_workspace_bytes", "msa_index_kl",
            "kl_workspace", "msa_cache_append_q8", "msa_q8_workspace_bytes", "q8_workspace",
@@ -38,8 +39,9 @@ MAX_ROT = 128
 KERNELS = {"auto": 0, "streaming": 1, "tensorcore": 2}
 EXPORTS = ("msa_workspace_bytes", "msa_index_topk", "msa_sparse_attn", "msa_forward",
            "msa_workspace_status", "msa_status_string", "msa_kernel_launch_count",
-           "msa_index_topk_noalloc", "msa_debug_set_wait_polls", "msa_quality_workspace_bytes",
-           "msa_selection_quality", "msa_cache_append", "msa_forward_paged",
+           "msa_index_topk_noalloc", "msa_debug_set_wait_polls", "msa_debug_delay_copies",
+           "msa_quality_workspace_bytes", "msa_selection_quality", "msa_cache_append",
+           "msa_forward_paged",
            "msa_dense_workspace_bytes", "msa_dense_attn", "msa_index_kl_workspace_bytes",
            "msa_index_kl", "msa_cache_append_q8", "msa_q8_workspace_bytes",
            "msa_sparse_attn_q8", "msa_forward_q8", "msa_window_workspace_bytes",
@@ -143,6 +145,8 @@ def load(path=None):
         getattr(L, name).restype = sz
     L.msa_debug_set_wait_polls.argtypes = [ctypes.c_uint32]
     L.msa_debug_set_wait_polls.restype = None
+    L.msa_debug_delay_copies.argtypes = [ci, ci, ctypes.c_uint32]
+    L.msa_debug_delay_copies.restype = None
     L.msa_kernel_launch_count.argtypes = []
     L.msa_kernel_launch_count.restype = ctypes.c_uint64
     L.msa_status_string.argtypes = [ci]
@@ -238,6 +242,12 @@ def msa_debug_set_wait_polls(polls):
     """Test-only: cap the tensor-core kernels' pipeline waits at `polls` polls
     (0 restores the default wall-clock bound)."""
     load().msa_debug_set_wait_polls(int(polls))
+
+
+def msa_debug_delay_copies(kind, at, us):
+    """Test-only: the backward attention's CTAs of one kind (1: KV-outer, 2: dQ) wait `us`
+    microseconds before their K and V copy number `at` (us 0: none; see msa.h)."""
+    load().msa_debug_delay_copies(int(kind), int(at), int(us))
 
 
 def msa_workspace_bytes(p):

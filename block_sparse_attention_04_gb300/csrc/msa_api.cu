@@ -18,6 +18,14 @@ void note_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_
 static std::atomic<uint32_t> g_wait_polls{0};
 uint32_t debug_wait_polls() { return g_wait_polls.load(std::memory_order_relaxed); }
 
+static std::atomic<int> g_delay_kind{0}, g_delay_at{0};
+static std::atomic<uint32_t> g_delay_ns{0};
+CopyDelay debug_copy_delay() {
+  const uint32_t ns = g_delay_ns.load(std::memory_order_relaxed);
+  return {ns == 0 ? 0 : g_delay_kind.load(std::memory_order_relaxed),
+          g_delay_at.load(std::memory_order_relaxed), ns};
+}
+
 constexpr int kMaxContextBlocks = 32768;
 
 int validate_params(const msa_params* p) {
@@ -499,6 +507,12 @@ uint64_t msa_kernel_launch_count(void) { return g_launches.load(std::memory_orde
 
 void msa_debug_set_wait_polls(uint32_t polls) {
   g_wait_polls.store(polls, std::memory_order_relaxed);
+}
+
+void msa_debug_delay_copies(int kind, int at, uint32_t us) {
+  g_delay_kind.store(kind, std::memory_order_relaxed);
+  g_delay_at.store(at, std::memory_order_relaxed);
+  g_delay_ns.store((us < 100000 ? us : 100000) * 1000, std::memory_order_relaxed);
 }
 
 const char* msa_status_string(int status) {

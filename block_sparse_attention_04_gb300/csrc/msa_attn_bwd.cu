@@ -165,7 +165,9 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
   a.dk = t.dk;
   a.dv = t.dv;
   a.status = status;
-  a.wait_polls = debug_wait_polls();
+  a.delay = debug_copy_delay();
+  a.wait_polls = a.delay.kind == MSA_DEBUG_BWD_DQ ? 0 : debug_wait_polls();
+  a.q_wait_polls = a.delay.kind == MSA_DEBUG_BWD_KV ? 0 : debug_wait_polls();
   if (!sparse) {
     a.q_items = q_items(s);
     a.q_splits = dense_q_splits(a);

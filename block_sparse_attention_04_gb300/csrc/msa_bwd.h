@@ -59,7 +59,9 @@ struct BwdArgs {
   bool first, last;          // pass
   uint16_t *dq, *dk, *dv;
   int* status;
-  uint32_t wait_polls;       // poll cap of the pipeline waits (0: wall-clock bound only)
+  // poll caps of the pipeline waits, KV-outer and dQ's (0: wall-clock bound only)
+  uint32_t wait_polls, q_wait_polls;
+  CopyDelay delay;           // tests of waits that run out
   // dense: dQ by (query tile, head) items x splits of their key blocks
   int kv_ctas;               // CTAs of the launch that work on units; those behind take items
   int q_items, q_splits;

@@ -404,6 +404,7 @@ __device__ __forceinline__ void kv_cta(const CUtensorMap& tm_q, const CUtensorMa
       SparseRows rows{};
       if constexpr (SP) rows.fetch(a, u, 0, lane);
       if (nu > 0 && !wait_all(kv_empty, (uint32_t)(nu - 1) & 1)) { ok = false; break; }
+      if (!SP) copy_delay(a.delay, MSA_DEBUG_BWD_KV, nu);
       if (lane == 0) {
         const int row = (int)(((int64_t)u.b * a.s.max_blocks + u.kb) * kBlock);
         mbar_arrive_expect_tx(kv_full, 2 * C::kTile);
@@ -422,6 +423,7 @@ __device__ __forceinline__ void kv_cta(const CUtensorMap& tm_q, const CUtensorMa
             ok = false;
             break;
           }
+          copy_delay(a.delay, MSA_DEBUG_BWD_KV, n);
           rows.place(a, u, t, lane);
           load_rows(sT + os * C::kTile, &tm_o, &t_full[os], rows, pol);
           if (lane == 0) last_fill[C::kTiles + os] = (int)C::use(n);

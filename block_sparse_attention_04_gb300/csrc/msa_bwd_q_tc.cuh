@@ -144,7 +144,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
   auto next_item = [&](int& it, bool& ok) {
     const int slot = ki % kRing;
     ok = __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(&it_full[slot], (ki / kRing) & 1,
-                                                               a.status, a.wait_polls));
+                                                               a.status, a.q_wait_polls));
     if (!ok) return false;
     // read by every lane before the slot is handed back
     it = __shfl_sync(0xffffffffu, ring[slot], 0);
@@ -153,7 +153,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
     return it >= 0;
   };
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status, a.wait_polls));
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status, a.q_wait_polls));
   };
   // One arrival for the lanes' work so far.
   auto warp_arrive = [&](uint64_t* bar) {
@@ -174,7 +174,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
       for (int k = 0; cur >= 0; ++k) {
         // publish the next item before this one's tiles, so that its K and V can start
         const int r = k + 1, slot = r % kRing;
-        if (r >= kRing && !mbar_wait(&it_empty[slot], ((r / kRing) - 1) & 1, a.status, a.wait_polls)) {
+        if (r >= kRing && !mbar_wait(&it_empty[slot], ((r / kRing) - 1) & 1, a.status, a.q_wait_polls)) {
           ok = false;
           break;
         }
@@ -184,7 +184,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
         mbar_arrive(&it_full[slot]);
         const QItem d = q_item(a, cur);
         if (d.kb0 < d.kb1) {
-          if (n > 0 && !mbar_wait(o_empty, (uint32_t)(n - 1) & 1, a.status, a.wait_polls)) {
+          if (n > 0 && !mbar_wait(o_empty, (uint32_t)(n - 1) & 1, a.status, a.q_wait_polls)) {
             ok = false;
             break;
           }
@@ -213,6 +213,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
         ok = __any_sync(0xffffffffu, *abort_flag != 0) == 0 &&
              wait_all(&k_empty[ks], ((n / C::kKS) & 1) ^ 1);
         if (!ok) break;
+        copy_delay(a.delay, MSA_DEBUG_BWD_DQ, n);
         if (lane == 0) {
           mbar_arrive_expect_tx(&k_full[ks], C::kTile);
 #pragma unroll
@@ -430,7 +431,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
         const int lim = (int)(l64 < kBlock ? l64 : kBlock) - c * kCols;
         const bool masked = __any_sync(0xffffffffu, lim < kCols - 1);
         ok = __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(s_full, (uint32_t)n & 1, a.status,
-                                                                   a.wait_polls));
+                                                                   a.q_wait_polls));
         if (!ok) break;
         tc_fence_after();
         float2 p[kCols / 2];
@@ -447,7 +448,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
             p[e] = make_float2(ex2(y.x), ex2(y.y));
           }
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(dp_full, (uint32_t)n & 1, a.status, a.wait_polls));
+        ok = __all_sync(0xffffffffu, mbar_wait(dp_full, (uint32_t)n & 1, a.status, a.q_wait_polls));
         if (!ok) break;
         tc_fence_after();
         uint32_t w[16];
@@ -469,7 +470,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
         if (masked) ds_of(std::true_type());
         else ds_of(std::false_type());
         ok = __all_sync(0xffffffffu, n == 0 || mbar_wait(ds_read, (uint32_t)(n - 1) & 1, a.status,
-                                                         a.wait_polls));
+                                                         a.q_wait_polls));
         if (!ok) break;
         tmem_st16(base + C::kDS + c * (kCols / 2), w);
         tmem_st_wait();
@@ -483,7 +484,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
       if (some) begin(q_item(a, it));
       // ---- the item's dQ: a query per thread, a run of dims per warpgroup
       if (any) {
-        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, (uint32_t)nu & 1, a.status, a.wait_polls));
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, (uint32_t)nu & 1, a.status, a.q_wait_polls));
         if (!ok) break;
         tc_fence_after();
       }

@@ -22,6 +22,12 @@ constexpr int kDevNoPages = 3;        // status word value: no free page left
 // Poll cap of the kernels' pipeline waits (0: the wall-clock bound alone);
 // set only through msa_debug_set_wait_polls.
 uint32_t debug_wait_polls();
+// Set only through msa_debug_delay_copies: kind of CTA (0: none), number of the copy, time.
+struct CopyDelay {
+  int kind, at;
+  uint32_t ns;
+};
+CopyDelay debug_copy_delay();
 
 // Adds n to the library-wide count of enqueued kernels.
 void note_launches(int n);

@@ -577,6 +577,14 @@ uint64_t msa_kernel_launch_count(void);
  * launches made after the call, from any thread; not for production use. */
 void msa_debug_set_wait_polls(uint32_t polls);
 
+/* Diagnostics, for the same tests: the warp of each CTA that copies K and V in the
+ * attention's backward pass waits `us` microseconds (at most 100,000; 0, the default:
+ * no wait) before its copy number `at` (0: the first; a sparse call's tiles, a dense
+ * call's units, dQ's key blocks), and the poll cap holds for that kind of CTA alone, so
+ * that a wait of the others of its CTA is sure to run out there. */
+typedef enum { MSA_DEBUG_BWD_KV = 1, MSA_DEBUG_BWD_DQ = 2 } msa_debug_kind;
+void msa_debug_delay_copies(int kind, int at, uint32_t us);
+
 #ifdef __cplusplus
 }
 #endif
