@@ -165,9 +165,12 @@ cudaError_t launch_attn_bwd(const Shape& s, const Positions& pos, const AttnBwd&
   a.dk = t.dk;
   a.dv = t.dv;
   a.status = status;
-  a.delay = debug_copy_delay();
-  a.wait_polls = a.delay.kind == MSA_DEBUG_BWD_DQ ? 0 : debug_wait_polls();
-  a.q_wait_polls = a.delay.kind == MSA_DEBUG_BWD_KV ? 0 : debug_wait_polls();
+  const CopyDelay delay = debug_copy_delay();
+  a.late_kv = delay.kind == MSA_DEBUG_BWD_KV ? delay.at : -1;
+  a.late_q = delay.kind == MSA_DEBUG_BWD_DQ ? delay.at : -1;
+  a.late_ns = delay.ns;
+  a.wait_polls = delay.kind == MSA_DEBUG_BWD_DQ ? 0 : debug_wait_polls();
+  a.q_wait_polls = delay.kind == MSA_DEBUG_BWD_KV ? 0 : debug_wait_polls();
   if (!sparse) {
     a.q_items = q_items(s);
     a.q_splits = dense_q_splits(a);

@@ -61,7 +61,10 @@ struct BwdArgs {
   int* status;
   // poll caps of the pipeline waits, KV-outer and dQ's (0: wall-clock bound only)
   uint32_t wait_polls, q_wait_polls;
-  CopyDelay delay;           // tests of waits that run out
+  // tests of waits that run out: the copy of a KV-outer CTA, of a dQ CTA that is late
+  // (-1: none), and by how much
+  int late_kv, late_q;
+  uint32_t late_ns;
   // dense: dQ by (query tile, head) items x splits of their key blocks
   int kv_ctas;               // CTAs of the launch that work on units; those behind take items
   int q_items, q_splits;

@@ -396,6 +396,7 @@ __device__ __forceinline__ void kv_cta(const CUtensorMap& tm_q, const CUtensorMa
     // (A box of 8 rows takes a warp some 70 cycles to issue, so that one warp with a tile's
     // 32 held up the rest: 8192 tokens 1093 us for 1011.)
     const uint64_t pol = l2_policy_evict_last();
+    const int late = a.late_kv;
     int it, n = 0, nu = 0;
     bool ok;
     while (next_unit(it, ok)) {
@@ -404,7 +405,7 @@ __device__ __forceinline__ void kv_cta(const CUtensorMap& tm_q, const CUtensorMa
       SparseRows rows{};
       if constexpr (SP) rows.fetch(a, u, 0, lane);
       if (nu > 0 && !wait_all(kv_empty, (uint32_t)(nu - 1) & 1)) { ok = false; break; }
-      if (!SP) copy_delay(a.delay, MSA_DEBUG_BWD_KV, nu);
+      if (!SP && nu == late) copy_delay(a.late_ns);
       if (lane == 0) {
         const int row = (int)(((int64_t)u.b * a.s.max_blocks + u.kb) * kBlock);
         mbar_arrive_expect_tx(kv_full, 2 * C::kTile);
@@ -423,7 +424,7 @@ __device__ __forceinline__ void kv_cta(const CUtensorMap& tm_q, const CUtensorMa
             ok = false;
             break;
           }
-          copy_delay(a.delay, MSA_DEBUG_BWD_KV, n);
+          if (n == late) copy_delay(a.late_ns);
           rows.place(a, u, t, lane);
           load_rows(sT + os * C::kTile, &tm_o, &t_full[os], rows, pol);
           if (lane == 0) last_fill[C::kTiles + os] = (int)C::use(n);

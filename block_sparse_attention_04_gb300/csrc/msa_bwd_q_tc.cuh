@@ -204,6 +204,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
   } else if (warp == 1) {
     // ------------------------------------------------------- K and V (warp 1)
     int it, n = 0;
+    const int late = a.late_q;
     bool ok, k_only = false;     // k_only: block n's K is on its way, its V is not
     while (next_item(it, ok)) {
       const QItem d = q_item(a, it);
@@ -213,7 +214,7 @@ __device__ __forceinline__ void q_cta(const CUtensorMap& tm_o, const CUtensorMap
         ok = __any_sync(0xffffffffu, *abort_flag != 0) == 0 &&
              wait_all(&k_empty[ks], ((n / C::kKS) & 1) ^ 1);
         if (!ok) break;
-        copy_delay(a.delay, MSA_DEBUG_BWD_DQ, n);
+        if (n == late) copy_delay(a.late_ns);
         if (lane == 0) {
           mbar_arrive_expect_tx(&k_full[ks], C::kTile);
 #pragma unroll

@@ -223,11 +223,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* s
   }
 }
 
-// Waits before copy `n` of a CTA of this kind, where a test asks for that.
-__device__ __forceinline__ void copy_delay(const CopyDelay& d, int kind, int n) {
-  if (d.kind != kind || d.at != n) return;
+// A copy that a test delays (msa_debug_delay_copies).
+__device__ __forceinline__ void copy_delay(uint32_t ns) {
   const uint64_t t0 = globaltimer_ns();
-  while (globaltimer_ns() - t0 < d.ns) __nanosleep(1000);
+  while (globaltimer_ns() - t0 < ns) __nanosleep(1000);
 }
 
 // Records an invalid selected id (or block-table entry) in the status word
