@@ -42,7 +42,7 @@ constexpr int kHalfRot = MSA_MAX_ROT / 2;
 struct RopeArgs {
   Shape s;
   Positions pos;
-  int rot, interleaved;
+  int rot;
   float eps, mscale;
   double turns[kHalfRot];      // inv_freq / 2 pi
   RopeIn in;
@@ -53,17 +53,6 @@ struct RopeArgs {
   float* part_w;               // backward: [CTAs][2][D] sums of the weights' gradients
 };
 
-// 16 bytes to shared memory, without waiting; copies_done waits for all of the thread's but
-// the newest N tokens'.
-__device__ __forceinline__ void copy16(uint4* dst, const uint16_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_done() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // Sum over the LPR lanes of a row (LPR a power of two, rows aligned in the warp).
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
@@ -217,17 +206,17 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas) rope_append_kernel(
       for (int u = 0; u < U; ++u) {
         const int r = u * ROWS + row;
         uint4* dst = stage + (st * U + u) * kRopeThreads + threadIdx.x;
-        if ((u + 1) * ROWS <= q_rows) copy16(dst, q + u * ROWS * D);
-        else if (r < n_rows) copy16(dst, (r < n_q ? q : r < n_qk ? k : v) + u * ROWS * D);
+        if ((u + 1) * ROWS <= q_rows) cp_async_16(smem_u32(dst), q + u * ROWS * D);
+        else if (r < n_rows) cp_async_16(smem_u32(dst), (r < n_q ? q : r < n_qk ? k : v) + u * ROWS * D);
       }
-      if (ki) copy16(idx_stage + st * 16 + threadIdx.x, ki);
+      if (ki) cp_async_16(smem_u32(idx_stage + st * 16 + threadIdx.x), ki);
       q += step * a.in.q_stride;
       k += step * a.in.k_stride;
       v += step * a.in.v_stride;
       if (ki) ki += (int64_t)step * a.s.Di;
       load_tok += step;
     }
-    copies_end();
+    cp_async_commit();
   };
   const int2 pd = pair_dims<INTER>(a);
   float pw[2][2] = {};
@@ -285,7 +274,7 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas) rope_append_kernel(
   for (int buf = 0, st = 0;; buf ^= 1, st = st + 1 == kStages ? 0 : st + 1) {
     const int64_t tok = tw.tok;
     load(st == 0 ? kStages - 1 : st - 1);    // read by every thread before the last barrier
-    copies_done<kStages - 1>();
+    cp_async_wait<kStages - 1>();            // for all but the newest token's
     __syncwarp();                            // a row's copies are its warp's
     tw.next(step);
     const bool more = tw.tok < n_tok;
@@ -380,12 +369,12 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) rope_append_bwd_kernel
         const int r = u * ROWS + row;
         uint4* dst = stage + (st * 2 * U + u) * kRopeThreads + threadIdx.x;
         if ((u + 1) * ROWS <= q_rows) {
-          copy16(dst, gq + u * ROWS * D);
-          if (q_norm) copy16(dst + U * kRopeThreads, q + u * ROWS * D);
+          cp_async_16(smem_u32(dst), gq + u * ROWS * D);
+          if (q_norm) cp_async_16(smem_u32(dst + U * kRopeThreads), q + u * ROWS * D);
         } else if (r < n_rows) {
-          copy16(dst, (r < n_q ? gq : r < n_qk ? gk : gv) + u * ROWS * D);
+          cp_async_16(smem_u32(dst), (r < n_q ? gq : r < n_qk ? gk : gv) + u * ROWS * D);
           if (r < n_q ? q_norm : r < n_qk && k_norm)
-            copy16(dst + U * kRopeThreads, (r < n_q ? q : k) + u * ROWS * D);
+            cp_async_16(smem_u32(dst + U * kRopeThreads), (r < n_q ? q : k) + u * ROWS * D);
         }
       }
       q += step * a.in.q_stride;
@@ -393,7 +382,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) rope_append_bwd_kernel
       gq += (int64_t)step * H * D;
       lw.next(step);
     }
-    copies_end();
+    cp_async_commit();
   };
   const int2 pd = pair_dims<INTER>(a);
   auto fill = [&](TokenTable<D, 1>& t) {
@@ -424,7 +413,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) rope_append_bwd_kernel
   for (int buf = 0, st = 0;; buf ^= 1, st = st + 1 == kStages ? 0 : st + 1) {
     const int64_t tok = tw.tok;
     load(st == 0 ? kStages - 1 : st - 1);
-    copies_done<kStages - 1>();
+    cp_async_wait<kStages - 1>();            // for all but the newest token's
     __syncwarp();
     tw.next(step);
     const bool more = tw.tok < n_tok;
@@ -531,7 +520,6 @@ RopeArgs rope_args(const Shape& s, const Positions& pos, const msa_rope& r, cons
   a.s = s;
   a.pos = pos;
   a.rot = r.rot;
-  a.interleaved = r.interleaved;
   a.eps = r.eps;
   a.mscale = r.mscale;
   for (int i = 0; i < r.rot / 2; ++i) a.turns[i] = r.inv_freq[i] / 6.283185307179586476925;
