@@ -7,7 +7,7 @@
 // (-lse log2e where scale log2e is below 2^-100 and scores count for nothing.)
 //   dense    group ((b H + h) ngroups + i/8), a tile's 16 groups in a row; rows past
 //            the last query hold -16384 (times 1 / scale log2e) and 0: their P and dS
-//            vanish.  Next to it, for the query-outer kernel, 64 bytes a group: eight
+//            vanish.  Next to it, for dQ's CTAs, 64 bytes a group: eight
 //            -lse log2e, then eight -delta.
 //   sparse   group (((b T + i) G + g) rpe/8 + head/8): an entry's rows; heads past
 //            the group's last as above, and one such group behind all others

@@ -19,7 +19,7 @@
 // the norm's weights inside C and S (one table per token for the queries, one for K), in
 // packed fp32; a thread has the same rows of each token, and the next token's come by
 // cp.async while one is worked on.  Many small CTAs, as each waits at a barrier per token.
-// 8192 tokens, 48/8 heads of 128, half rotated: 47.5 us (302 MB, 0.84 of HBM's floor; rows
+// 8192 tokens, 48/8 heads of 128, half rotated: 47.5 us (270 MB, 0.84 of the copy rate; rows
 // in registers, index arithmetic per row and tables of angles: 84).  Backward, 8192 tokens:
 // 70 us and 3 for the weights' join (386 MB; 168 before).
 #include <algorithm>

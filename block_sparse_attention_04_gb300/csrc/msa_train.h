@@ -6,7 +6,7 @@
 namespace msa {
 
 // Launches a kernel that begins with after_previous() behind another of the same call, so
-// that its launch overlaps that one: a call has four to nine kernels, and where they are
+// that its launch overlaps that one: a call has three to nine kernels, and where they are
 // short the gaps between them count (dense, 77 tokens: 41 -> 32 us; sparse, 2 x 101: 90 ->
 // 78).  The short ones let the next in when they start; behind the sparse KV-outer kernel,
 // the waiting CTAs of a join would cost 100 us of 1410.  A kernel that needs nothing of the

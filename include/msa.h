@@ -484,7 +484,8 @@ int msa_rope_append(const msa_params *p, const msa_rope *r, const int32_t *block
  * q_weight (k_weight) is NULL, and dq_weight (dk_weight) is then not written.
  * Sums are in fp32 in an order that the shape alone decides (calls with the same
  * inputs on the same device give the same bits).  A call with T = 0 writes nothing,
- * as everywhere: not the weights' gradients either.  ws: at least
+ * as everywhere: not the weights' gradients either.  Outputs must not overlap
+ * inputs.  ws: at least
  * msa_rope_append_bwd_workspace_bytes(p) bytes, 256-byte aligned. */
 size_t msa_rope_append_bwd_workspace_bytes(const msa_params *p);
 int msa_rope_append_bwd(const msa_params *p, const msa_rope *r, const uint16_t *q,
@@ -521,13 +522,12 @@ int msa_dense_attn_lse(const msa_params *p, const uint16_t *q, const uint16_t *k
  * as they were.  Products are of bf16 operands (P and dS rounded to nearest) and
  * sums in fp32, in an order that inputs and shape decide (no atomics: calls with
  * the same inputs on the same device give the same bits); msa_sparse_attn_bwd
- * rounds dq's part of each selected block to bf16 before it adds them up.  Where a
- * query's whole context lies in one block, delta is taken from P and dP, which keeps
- * the difference exact where few tokens are seen.  out and lse are the forward
- * call's;
+ * rounds dq's part of each selected block to bf16 before it adds them up.  At the
+ * first 128 positions of a sequence delta is taken from P and dP, which keeps the
+ * difference exact where few tokens are seen.  out and lse are the forward call's;
  * sel and an id's meaning are as in msa_sparse_attn (an id listed twice counts
- * twice; ids outside [0, lb] are reported and skipped; a query without a visible
- * token gets dq = 0).  Cache rows behind the last query of a sequence may hold
+ * twice; negative ids are ignored, ids past lb reported and skipped; a query without
+ * a visible token gets dq = 0).  Outputs must not overlap inputs.  Cache rows behind the last query of a sequence may hold
  * anything; a NaN or an infinity in q, out, dout or lse of one query may also reach, in
  * the gradients of the heads of its group, dk and dv of tokens of the blocks that it
  * attends to which it does not see itself, and one in k or v of a token dq of
