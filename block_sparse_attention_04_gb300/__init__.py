@@ -544,11 +544,11 @@ def msa_pages_compact(pools, num_pool_blocks, block_table, refs, table_out, refs
 
 def rope(rot, base=10000.0, interleaved=False, eps=1e-6, linear=1.0, yarn=None, mscale=1.0):
     """How positions rotate the first `rot` dims of every head (the library's calls take
-    multiples of 16), and the norm's eps (see msa.h).  Frequencies base^(-2i/rot) / linear, the position divided by
-    `linear`.  yarn=(factor, trained_length[, beta_fast, beta_slow]): each frequency
-    between itself and its `factor`-th part by how often it turns within the trained
-    length (all of itself from beta_fast turns on, 32; the part below beta_slow, 1);
-    the usual factor of cos and sin goes with it as mscale=yarn_mscale(factor)."""
+    multiples of 16), and the norm's eps (see msa.h).  Frequencies base^(-2i/rot) /
+    linear, the position divided by `linear`.  yarn=(factor, trained_length[, beta_fast,
+    beta_slow]): each frequency between itself and its `factor`-th part by how often it
+    turns within the trained length (all of itself from beta_fast turns on, 32; the part
+    below beta_slow, 1); the usual factor of cos and sin goes with it as mscale=yarn_mscale(factor)."""
     if not 0 <= rot <= MAX_ROT or rot % 2:
         raise ValueError("rot must be even and in 0 .. %d" % MAX_ROT)
     f = [base ** (-2.0 * i / rot) / linear for i in range(rot // 2)]
